@@ -430,6 +430,176 @@ sab_status sab_block_causal_attention(const void* Q, const void* K, const void* 
                                       size_t ws_bytes, void* stream);
 
 /*
+ * Rotary positions of queries and keys outside the ring producer (training
+ * sequences, prompts, decoded tokens), and their gradient.  The method's
+ * fused rotary kernel ("Matrix-Game 4.0", section 实验结果) has no stated
+ * formulas; the common ones are used.  Every head's leading `dims` dimensions
+ * are cut into up to three bands, one per position axis (frame, row, column;
+ * one band for a plain token index).  Pair i (0 <= i < n/2) of a band of n
+ * dimensions turns by p * f_i, p being the token's position on that axis:
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos),  f_i = base^(-2i/n).
+ * Dimensions dims .. D-1 are copied.
+ * layout     which two elements form pair j of the dims/2 pairs (the bands'
+ *            pairs one after the other): INTERLEAVED 2j and 2j+1, HALF j and
+ *            j + dims/2.
+ * scaling    longer contexts than `base` was chosen for, by factor s >= 1:
+ *            LINEAR  f_i / s;
+ *            BASE    base * s^(n/(n-2)) in place of base (n > 2);
+ *            RAMP    f_i (w + (1 - w) / s) with w = (c f_i / 2 pi -
+ *                    ramp_slow) / (ramp_fast - ramp_slow) clamped to [0, 1]:
+ *                    pairs that turn often within original_context = c tokens
+ *                    keep their frequency, slow ones are stretched
+ *                    ("YaRN: Efficient Context Window Extension of Large
+ *                    Language Models", section 3.2; the paper's temperature
+ *                    is `magnitude`).
+ *            NONE takes s = 1.
+ * Angles are exact for positions of any size: a frequency is held in turns
+ * per position as a 64-bit fraction, so position * frequency modulo one turn
+ * is one wrapping integer product (its error is position * 2^-65 turns, next
+ * to the 2^-53 relative error of the fp64 frequency).  Sine, cosine and
+ * products are fp32; one rounding to the element type.
+ */
+typedef enum { SAB_ROTARY_INTERLEAVED = 0, SAB_ROTARY_HALF = 1 } sab_rotary_layout;
+typedef enum {
+  SAB_ROTARY_SCALE_NONE = 0,
+  SAB_ROTARY_SCALE_LINEAR = 1,
+  SAB_ROTARY_SCALE_BASE = 2,
+  SAB_ROTARY_SCALE_RAMP = 3
+} sab_rotary_scaling;
+typedef enum { SAB_DTYPE_BF16 = 0, SAB_DTYPE_FP32 = 1 } sab_dtype;
+
+typedef struct {
+  int layout;               /* sab_rotary_layout                                        */
+  int axes;                 /* position axes, 1..3                                      */
+  int band[3];              /* even dimensions per axis (>= 2 for an axis in use)       */
+  int scaling;              /* sab_rotary_scaling                                       */
+  double base;              /* > 1                                                      */
+  double factor;            /* s >= 1                                                   */
+  double original_context;  /* RAMP: c > 0                                              */
+  double ramp_fast;         /* RAMP: turns from which a pair keeps its frequency        */
+  double ramp_slow;         /* RAMP: turns up to which it is stretched fully (< fast)   */
+  double magnitude;         /* factor on the rotated pairs, finite, > 0                 */
+} sab_rotary_desc;
+
+#define SAB_ROTARY_MAX_DIMS 256
+/* Filled by sab_rotary_plan_init; plain data, no pointers, free to copy. */
+typedef struct {
+  unsigned int magic;
+  int layout;
+  int axes;
+  int dims;                                            /* rotated dimensions        */
+  float magnitude;
+  unsigned char axis[SAB_ROTARY_MAX_DIMS / 2];         /* position axis of a pair   */
+  unsigned long long step[SAB_ROTARY_MAX_DIMS / 2];    /* turns per position, 2^-64 */
+} sab_rotary_plan;
+
+/*
+ * Work out the frequencies of `desc` (host only, no CUDA call).  Errors:
+ * INVALID_ARG (null, bad layout, axes, bands not even or summing past
+ * SAB_ROTARY_MAX_DIMS, a value out of the ranges above).
+ */
+sab_status sab_rotary_plan_init(const sab_rotary_desc* desc, sab_rotary_plan* plan);
+
+/*
+ * Rows of one tensor: token (b, t) holds heads * D contiguous elements at
+ * in + b * in_batch + t * in_token (strides in elements; likewise out), so a
+ * slice of a fused QKV projection or of a longer buffer needs no copy.
+ * out may be in with the same strides (rotated in place); otherwise it must
+ * not overlap it.  The strides must keep distinct output tokens apart.
+ */
+typedef struct {
+  const void* in;
+  void* out;
+  int heads;
+  long long in_batch, in_token, out_batch, out_token;
+} sab_rotary_rows;
+
+/*
+ * Rotate B x L tokens of q and (unless k is NULL) of k, which may have
+ * another number of heads, in one launch.
+ * positions  device int64 [axes, B, L], 8-byte aligned, any sign; or NULL for
+ *            one axis: token t of every sequence is at first_position + t.
+ * D          head dimension, a multiple of 8, plan->dims <= D <= 256.
+ * dtype      sab_dtype of all in and out tensors; pointers 16-byte aligned,
+ *            strides multiples of 16 bytes.
+ * sab_rotary_backward: the gradient with respect to `in` given the gradient
+ * with respect to `out` (the transposed rotation, same magnitude); its `in`
+ * is the gradient of the rotated tensor, its `out` the gradient of the input.
+ * Errors: INVALID_ARG (pointers, alignment, strides, sizes, a plan that
+ * sab_rotary_plan_init did not fill, NULL positions with several axes), CUDA.
+ */
+sab_status sab_rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, const sab_rotary_rows* k,
+                      const long long* positions, long long first_position, int B, int L, int D, int dtype,
+                      void* stream);
+sab_status sab_rotary_backward(const sab_rotary_plan* plan, const sab_rotary_rows* dq, const sab_rotary_rows* dk,
+                               const long long* positions, long long first_position, int B, int L, int D,
+                               int dtype, void* stream);
+
+/*
+ * Decay attention: linear attention with a decay per head, the memory of
+ * what has left the ring's window in constant space (no counterpart in the
+ * method).  Per (b, h), with g = exp(log_decay[h]) and a state S of D x D
+ * (key dimension x value dimension) fp32:
+ *   S_t = g S_{t-1} + k_t v_t^T,   O_t = scale * q_t S_t.
+ * Causal by token.  A stream is fed chunk by chunk (sab_decay_attention with
+ * the state of the chunks before it) or token by token
+ * (sab_decay_attention_step); both leave the same state.
+ * Q, K, V, O  device, token-major [B, L, H, D] bf16; O overlaps no input.
+ * log_decay   device fp32 [H], <= 0: the natural log of the decay, a constant
+ *             of the model (no gradient).  Values above 0 are taken as 0,
+ *             values below -10^4 as -10^4 (a decay to exactly 0).
+ * seq_len     device int32 [B] or NULL (all L): tokens of sequence b, clamped
+ *             to [0, L] on the device.  Tokens past it are padding: never
+ *             used (whatever they hold), O = 0 there, and they neither decay
+ *             nor change the state.
+ * state_in    device fp32 [B, H, D, D] or NULL (zeros).
+ * state_out   device fp32 [B, H, D, D] or NULL (not wanted): the state after
+ *             the last token.  May be state_in.
+ * scale       > 0, usually 1/sqrt(D).
+ * workspace   device scratch of sab_decay_attention_workspace bytes (0: may
+ *             be NULL), 256-byte aligned; no zero-fill needed.  Calls that
+ *             can overlap on the GPU need one each.
+ * Products run on bf16 tensor cores with fp32 accumulation: q, k, v as they
+ * are, the masked scores and the state's copy that multiplies q rounded to
+ * bf16, the state itself held in fp32 and fed by k rounded to 16 bits of
+ * mantissa.  D must be 64 or 128.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+size_t sab_decay_attention_workspace(int B, int L, int H, int D);
+sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
+                               const int* seq_len, const float* state_in, int B, int L, int H, int D, float scale,
+                               void* O, float* state_out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * One token of every sequence: Q, K, V, O are [B, H, D] bf16, otherwise as
+ * sab_decay_attention; everything in fp32.  active: device int32 [B] or NULL
+ * (all): sequences with active[b] == 0 keep their state (state_out = state_in)
+ * and get O = 0.  state_in NULL: zeros; state_out is required and may be
+ * state_in (the usual in-place step).  No workspace.
+ */
+sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V, const float* log_decay,
+                                    const int* active, const float* state_in, int B, int H, int D, float scale,
+                                    void* O, float* state_out, void* stream);
+
+/*
+ * Gradients of sab_decay_attention for a loss with gradient dO with respect
+ * to O and d_state_out (NULL: zeros) with respect to state_out.  With X_t the
+ * gradient reaching S_t from later tokens (X_{L-1} = d_state_out):
+ *   R_t = X_t + scale q_t dO_t^T,  dK_t = R_t v_t,  dV_t = R_t^T k_t,
+ *   X_{t-1} = g R_t,  dQ_t = scale S_t dO_t,  d_state_in = X_{-1}.
+ * dQ, dK, dV  device, token-major [B, L, H, D] bf16 (outputs; 0 on padding);
+ * they overlap no input and not one another.
+ * d_state_in  device fp32 [B, H, D, D] or NULL; may be d_state_out.
+ * The other arguments as in the forward call; the workspace is of
+ * sab_decay_attention_backward_workspace bytes.  Roundings as in the forward.
+ */
+size_t sab_decay_attention_backward_workspace(int B, int L, int H, int D);
+sab_status sab_decay_attention_backward(const void* Q, const void* K, const void* V, const void* dO,
+                                        const float* log_decay, const int* seq_len, const float* state_in,
+                                        const float* d_state_out, int B, int L, int H, int D, float scale, void* dQ,
+                                        void* dK, void* dV, float* d_state_in, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/*
  * Synchronise `stream`, then report and clear the device error word that
  * bounded pipeline waits set when they give up (SAB_ERR_TIMEOUT) and that the
  * index checks of a debug build set (SAB_ERR_BOUNDS, reported first when both

@@ -89,6 +89,14 @@ def library() -> ctypes.CDLL:
         "sab_chunk_attention_fp8mma": (I, [P, I, LL, P, I, I, I, F, P, P, P, SZ, P]),
         "sab_memory_prefix_attention_backward": (I, [P, P, P, P, P, P, I, I, I, I, I, P, I, I, F, P, P, P, P, SZ,
                                                      P]),
+        "sab_rotary_plan_init": (I, [P, P]),
+        "sab_rotary": (I, [P, P, P, P, LL, I, I, I, I, P]),
+        "sab_rotary_backward": (I, [P, P, P, P, LL, I, I, I, I, P]),
+        "sab_decay_attention_workspace": (SZ, [I, I, I, I]),
+        "sab_decay_attention": (I, [P, P, P, P, P, P, I, I, I, I, F, P, P, P, SZ, P]),
+        "sab_decay_attention_step": (I, [P, P, P, P, P, P, I, I, I, F, P, P, P]),
+        "sab_decay_attention_backward_workspace": (SZ, [I, I, I, I]),
+        "sab_decay_attention_backward": (I, [P] * 8 + [I, I, I, I, F] + [P] * 5 + [SZ, P]),
         "sab_status_string": (ctypes.c_char_p, [I]),
         "sab_version": (ctypes.c_char_p, []),
     }
@@ -422,6 +430,217 @@ def qk_norm_rope(handle, layer: int, chunk: int, Q, K, V, rope: RopeDesc, Q_out,
         _ptr(V, torch.bfloat16, "V"), _ptr(gamma_q, torch.float32, "gamma_q"), _ptr(gamma_k, torch.float32, "gamma_k"),
         ctypes.byref(rope), _ptr(Q_out, torch.bfloat16, "Q_out"), _ptr(K_out, torch.bfloat16, "K_out"),
         _ptr(V_out, torch.bfloat16, "V_out"), int(bool(append)), _stream(stream)), "qk_norm_rope")
+
+
+# ---------------------------------------------------------------- rotary
+
+ROTARY_INTERLEAVED = 0
+ROTARY_HALF = 1
+ROTARY_SCALE_NONE = 0
+ROTARY_SCALE_LINEAR = 1
+ROTARY_SCALE_BASE = 2
+ROTARY_SCALE_RAMP = 3
+DTYPE_BF16 = 0
+DTYPE_FP32 = 1
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("axes", ctypes.c_int), ("band", ctypes.c_int * 3),
+                ("scaling", ctypes.c_int)] + [(n, ctypes.c_double) for n in (
+                    "base", "factor", "original_context", "ramp_fast", "ramp_slow", "magnitude")]
+
+
+class RotaryPlan(ctypes.Structure):
+    """Frequencies of one rotary embedding (plain host data, see ``rotary_plan``)."""
+
+    _fields_ = [("magic", ctypes.c_uint), ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("dims", ctypes.c_int),
+                ("magnitude", ctypes.c_float), ("axis", ctypes.c_ubyte * 128), ("step", ctypes.c_ulonglong * 128)]
+
+
+class RotaryRows(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int)] + [
+        (n, ctypes.c_longlong) for n in ("in_batch", "in_token", "out_batch", "out_token")]
+
+
+def rotary_plan(bands, layout: int = ROTARY_INTERLEAVED, base: float = 10000.0, scaling: int = ROTARY_SCALE_NONE,
+                factor: float = 1.0, original_context: float = 0.0, ramp_fast: float = 32.0, ramp_slow: float = 1.0,
+                magnitude: float = 1.0) -> RotaryPlan:
+    """sab_rotary_plan_init: the frequencies of one rotary embedding.
+    ``bands``: rotated dimensions per position axis (one to three even
+    numbers; their sum may be less than the head dimension).  Keep the plan
+    and pass it to every call (see include/sab.h)."""
+    bands = tuple(int(n) for n in bands)
+    if not 1 <= len(bands) <= 3:
+        raise SabError(1, "rotary_plan: one to three bands")
+    d = RotaryDesc(int(layout), len(bands), (ctypes.c_int * 3)(*bands), int(scaling), float(base), float(factor),
+                   float(original_context), float(ramp_fast), float(ramp_slow), float(magnitude))
+    plan = RotaryPlan()
+    _check(library().sab_rotary_plan_init(ctypes.byref(d), ctypes.byref(plan)), "rotary_plan")
+    return plan
+
+
+def _on_current_device(t, name):
+    if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rotary_rows(x, out, name):
+    """Token rows of ``x`` and ``out`` ([B, L, H, D] with contiguous heads)."""
+    for t, n in ((x, name), (out, name + "_out")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise TypeError(f"{n}: expected a [B, L, H, D] torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{n}: must be a CUDA tensor")
+        _on_current_device(t, n)
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{n}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+        if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+            raise ValueError(f"{n}: a token's heads must be contiguous")
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name}_out: expected the shape and type of {name}")
+    B, L, H, D = x.shape
+    st = [t.stride(d) if t.shape[d] > 1 else H * D for t in (x, out) for d in (0, 1)]
+    return RotaryRows(x.data_ptr(), out.data_ptr(), H, *st)
+
+
+def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, stream):
+    q = _rotary_rows(Q, Q_out, "Q")
+    B, L, _, D = Q.shape
+    k = None
+    if K is not None:
+        k = _rotary_rows(K, K_out, "K")
+        if (K.shape[0], K.shape[1], K.shape[3]) != (B, L, D) or K.dtype != Q.dtype:
+            raise ValueError("K: expected Q's batch, length, head dimension and type")
+    if positions is not None:
+        _on_current_device(positions, "positions")
+        if positions.numel() != plan.axes * B * L:
+            raise ValueError("positions: expected int64 [axes, B, L]")
+    _check(fn(ctypes.byref(plan), ctypes.byref(q), None if k is None else ctypes.byref(k),
+              _ptr(positions, torch.int64, "positions"), int(first_position), B, L, D, _DTYPES[Q.dtype],
+              _stream(stream)), what)
+
+
+def rotary(plan: RotaryPlan, Q, K, Q_out, K_out=None, positions=None, first_position: int = 0, stream=None):
+    """sab_rotary: rotate queries ``Q`` [B, L, Hq, D] and keys ``K``
+    [B, L, Hk, D] (or None) into ``Q_out``, ``K_out``; an output may be its
+    input.  Batch and token strides are free, a token's heads contiguous.
+    ``positions``: int64 [axes, B, L] ([B, L] for one axis), or None for
+    first_position + t (see include/sab.h)."""
+    _rotary(library().sab_rotary, "rotary", plan, Q, K, Q_out, K_out, positions, first_position, stream)
+
+
+def rotary_backward(plan: RotaryPlan, dQ_out, dK_out, dQ, dK=None, positions=None, first_position: int = 0,
+                    stream=None):
+    """sab_rotary_backward: gradients of ``rotary``'s inputs (``dQ``, ``dK``)
+    from those of its outputs; shapes, strides and positions as there."""
+    _rotary(library().sab_rotary_backward, "rotary_backward", plan, dQ_out, dK_out, dQ, dK, positions,
+            first_position, stream)
+
+
+# -------------------------------------------------------- decay attention
+
+def decay_attention_workspace(B: int, L: int, H: int, D: int) -> int:
+    return int(library().sab_decay_attention_workspace(int(B), int(L), int(H), int(D)))
+
+
+def decay_attention_backward_workspace(B: int, L: int, H: int, D: int) -> int:
+    return int(library().sab_decay_attention_backward_workspace(int(B), int(L), int(H), int(D)))
+
+
+def _scratch(nbytes, like, stream):
+    """``nbytes`` of device scratch for one call on ``stream`` (None: 0 bytes)."""
+    if nbytes == 0:
+        return None
+    mem = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:  # the allocator must not hand it out again before that stream is done
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        mem.record_stream(s)
+    return mem
+
+
+def _shaped(t, shape, dtype, name):
+    if t is not None and not isinstance(t, int):
+        p = _ptr(t, dtype, name)
+        _on_current_device(t, name)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        return p
+    return _ptr(t, dtype, name)
+
+
+def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_out=None, seq_len=None,
+                    workspace=None, stream=None):
+    """sab_decay_attention: linear attention of [B, L, H, D] bf16 sequences with
+    a decay per head, from the state [B, H, D, D] fp32 ``state_in`` to
+    ``state_out`` (see include/sab.h)."""
+    B, L, H, D = Q.shape
+    if workspace is None:
+        workspace = _scratch(decay_attention_workspace(B, L, H, D), Q, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
+    _check(library().sab_decay_attention(
+        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(log_decay, (H,), f4, "log_decay"),
+        _shaped(seq_len, (B,), torch.int32, "seq_len"), _shaped(state_in, st, f4, "state_in"), B, L, H, D,
+        float(scale), _shaped(O, x, bf, "O"), _shaped(state_out, st, f4, "state_out"), _ptr(workspace, None, "workspace"),
+        ws_bytes, _stream(stream)), "decay_attention")
+
+
+def decay_attention_step(Q, K, V, log_decay, scale: float, state_in, state_out, O, active=None, stream=None):
+    """sab_decay_attention_step: one token [B, H, D] of every sequence;
+    ``state_out`` may be ``state_in`` (see include/sab.h)."""
+    B, H, D = Q.shape
+    x, st, bf, f4 = (B, H, D), (B, H, D, D), torch.bfloat16, torch.float32
+    _check(library().sab_decay_attention_step(
+        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(log_decay, (H,), f4, "log_decay"),
+        _shaped(active, (B,), torch.int32, "active"), _shaped(state_in, st, f4, "state_in"), B, H, D, float(scale),
+        _shaped(O, x, bf, "O"), _shaped(state_out, st, f4, "state_out"), _stream(stream)), "decay_attention_step")
+
+
+def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, state_in=None, d_state_out=None,
+                             d_state_in=None, seq_len=None, workspace=None, stream=None):
+    """sab_decay_attention_backward: (dQ, dK, dV) and d_state_in of
+    decay_attention (see include/sab.h)."""
+    B, L, H, D = Q.shape
+    if workspace is None:
+        workspace = _scratch(decay_attention_backward_workspace(B, L, H, D), Q, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
+    _check(library().sab_decay_attention_backward(
+        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(dO, x, bf, "dO"),
+        _shaped(log_decay, (H,), f4, "log_decay"), _shaped(seq_len, (B,), torch.int32, "seq_len"),
+        _shaped(state_in, st, f4, "state_in"), _shaped(d_state_out, st, f4, "d_state_out"), B, L, H, D, float(scale),
+        _shaped(dQ, x, bf, "dQ"), _shaped(dK, x, bf, "dK"), _shaped(dV, x, bf, "dV"),
+        _shaped(d_state_in, st, f4, "d_state_in"), _ptr(workspace, None, "workspace"), ws_bytes, _stream(stream)),
+        "decay_attention_backward")
+
+
+class DecayState:
+    """The carried state of one decay-attention layer for ``batch`` streams,
+    the constant-size companion of a ``KVRing``: ``attention`` feeds a chunk,
+    ``step`` a token, both in place."""
+
+    def __init__(self, log_decay, batch, head_dim):
+        if log_decay.dim() != 1:
+            raise ValueError("log_decay: expected [heads]")
+        self.log_decay = log_decay
+        self.state = torch.zeros((batch, log_decay.numel(), head_dim, head_dim), dtype=torch.float32,
+                                 device=log_decay.device)
+
+    def reset(self):
+        self.state.zero_()
+
+    def attention(self, Q, K, V, scale=None, O=None, seq_len=None, workspace=None, stream=None):
+        O = torch.empty_like(Q) if O is None else O
+        decay_attention(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, O, self.state,
+                        self.state, seq_len, workspace, stream)
+        return O
+
+    def step(self, Q, K, V, scale=None, O=None, active=None, stream=None):
+        O = torch.empty_like(Q) if O is None else O
+        decay_attention_step(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, self.state,
+                             self.state, O, active, stream)
+        return O
 
 
 class KVRing:

@@ -20,6 +20,7 @@ using namespace sab;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr unsigned kRotaryMagic = 0x53524f54u;  // a plan that sab_rotary_plan_init filled
 
 // Debug builds: the kind of launch whose next instance carries a forged index
 // (sab_debug_inject_bounds_error); 0 when none is pending.
@@ -785,6 +786,260 @@ sab_status sab_memory_prefix_attention_backward(const void* Q, const void* K, co
                                                 size_t ws_bytes, void* stream) {
   return attention_backward(Q, K, V, O, dO, LSE, B, L, H, D, mem_pad, mem_len, chunk_tokens, window, softmax_scale,
                             dQ, dK, dV, workspace, ws_bytes, stream);
+}
+
+sab_status sab_rotary_plan_init(const sab_rotary_desc* desc, sab_rotary_plan* plan) {
+  if (desc == nullptr || plan == nullptr) return SAB_ERR_INVALID_ARG;
+  const sab_rotary_desc& d = *desc;
+  if (d.layout != SAB_ROTARY_INTERLEAVED && d.layout != SAB_ROTARY_HALF) return SAB_ERR_INVALID_ARG;
+  if (d.axes < 1 || d.axes > 3) return SAB_ERR_INVALID_ARG;
+  long long dims = 0;
+  for (int a = 0; a < d.axes; ++a) {
+    if (d.band[a] < 2 || (d.band[a] & 1)) return SAB_ERR_INVALID_ARG;
+    dims += d.band[a];
+  }
+  if (dims > SAB_ROTARY_MAX_DIMS) return SAB_ERR_INVALID_ARG;
+  if (!(d.base > 1.0) || !isfinite(d.base) || !(d.magnitude > 0.0) || !isfinite((float)d.magnitude))
+    return SAB_ERR_INVALID_ARG;
+  double s = 1.0;
+  if (d.scaling != SAB_ROTARY_SCALE_NONE) {
+    if (d.scaling < 0 || d.scaling > SAB_ROTARY_SCALE_RAMP) return SAB_ERR_INVALID_ARG;
+    if (!(d.factor >= 1.0) || !isfinite(d.factor)) return SAB_ERR_INVALID_ARG;
+    s = d.factor;
+  }
+  if (d.scaling == SAB_ROTARY_SCALE_RAMP &&
+      (!(d.original_context > 0.0) || !isfinite(d.original_context) || !isfinite(d.ramp_fast) ||
+       !isfinite(d.ramp_slow) || !(d.ramp_slow < d.ramp_fast)))
+    return SAB_ERR_INVALID_ARG;
+  if (d.scaling == SAB_ROTARY_SCALE_BASE)
+    for (int a = 0; a < d.axes; ++a)
+      if (d.band[a] == 2) return SAB_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  memset(plan, 0, sizeof(*plan));
+  int j = 0;
+  for (int a = 0; a < d.axes; ++a) {
+    const double n = d.band[a];
+    const double base = d.scaling == SAB_ROTARY_SCALE_BASE ? d.base * pow(s, n / (n - 2.0)) : d.base;
+    if (!isfinite(base)) return SAB_ERR_INVALID_ARG;
+    for (int i = 0; i < d.band[a] / 2; ++i, ++j) {
+      double f = pow(base, -2.0 * i / n);
+      if (d.scaling == SAB_ROTARY_SCALE_LINEAR) f /= s;
+      if (d.scaling == SAB_ROTARY_SCALE_RAMP) {
+        const double w = (d.original_context * f / kTwoPi - d.ramp_slow) / (d.ramp_fast - d.ramp_slow);
+        const double keep = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+        f *= keep + (1.0 - keep) / s;
+      }
+      // f <= 1 radian per position, so below 1/6 of a turn
+      plan->axis[j] = (unsigned char)a;
+      plan->step[j] = (unsigned long long)(ldexp(f / kTwoPi, 64) + 0.5);
+    }
+  }
+  plan->layout = d.layout;
+  plan->axes = d.axes;
+  plan->dims = (int)dims;
+  plan->magnitude = (float)d.magnitude;
+  plan->magic = kRotaryMagic;
+  return SAB_OK;
+}
+
+// Rows of one rotary tensor: pointers, strides, and that no two output
+// tokens share an element.
+static bool rotary_rows_ok(const sab_rotary_rows* r, int B, int L, int D, int esize) {
+  if (r->in == nullptr || r->out == nullptr || !aligned16(r->in) || !aligned16(r->out) || r->heads < 1) return false;
+  if ((long long)r->heads * D > (1LL << 30)) return false;
+  const long long st[4] = {r->in_batch, r->in_token, r->out_batch, r->out_token};
+  for (long long x : st)
+    if (x < 0 || x > (1LL << 40) || (x * esize) % 16 != 0) return false;
+  if (r->in == r->out && (r->in_batch != r->out_batch || r->in_token != r->out_token) && (long long)B * L > 1)
+    return false;
+  const long long row = (long long)r->heads * D;
+  const bool token_apart = L == 1 || r->out_token >= row, batch_apart = B == 1 || r->out_batch >= row;
+  const bool token_inner = B == 1 || r->out_batch >= (L - 1) * r->out_token + row;
+  const bool batch_inner = L == 1 || r->out_token >= (B - 1) * r->out_batch + row;
+  return token_apart && batch_apart && (token_inner || batch_inner);
+}
+
+static sab_status rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, const sab_rotary_rows* k,
+                         const long long* positions, long long first_position, int B, int L, int D, int dtype,
+                         bool backward, void* stream) {
+  if (plan == nullptr || plan->magic != kRotaryMagic || q == nullptr) return SAB_ERR_INVALID_ARG;
+  if (dtype != SAB_DTYPE_BF16 && dtype != SAB_DTYPE_FP32) return SAB_ERR_INVALID_ARG;
+  if (B < 1 || L < 1 || L > (1 << 30) || (long long)B * L > (1LL << 31) || D < 8 || D % 8 != 0 ||
+      D > SAB_ROTARY_MAX_DIMS || plan->dims > D)
+    return SAB_ERR_INVALID_ARG;
+  if (positions == nullptr ? plan->axes != 1 : (reinterpret_cast<uintptr_t>(positions) & 7u) != 0)
+    return SAB_ERR_INVALID_ARG;
+  const int esize = dtype == SAB_DTYPE_BF16 ? 2 : 4;
+  if (!rotary_rows_ok(q, B, L, D, esize) || (k != nullptr && !rotary_rows_ok(k, B, L, D, esize)))
+    return SAB_ERR_INVALID_ARG;
+  RotaryParams p;
+  memset(&p, 0, sizeof(p));
+  for (int w = 0; w < 2; ++w) {
+    const sab_rotary_rows* r = w == 0 ? q : k;
+    if (r != nullptr)
+      p.rows[w] = RotaryRows{r->in, r->out, r->heads, r->in_batch, r->in_token, r->out_batch, r->out_token};
+  }
+  p.positions = positions;
+  p.first_position = first_position;
+  p.B = B;
+  p.L = L;
+  p.D = D;
+  p.dims = plan->dims;
+  p.half_layout = plan->layout == SAB_ROTARY_HALF;
+  p.magnitude = plan->magnitude;
+  p.sine = backward ? -plan->magnitude : plan->magnitude;
+  memcpy(p.axis, plan->axis, sizeof(p.axis));
+  memcpy(p.step, plan->step, sizeof(p.step));
+  return launch_rotary(p, dtype == SAB_DTYPE_FP32, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
+                                                                                                   : SAB_ERR_CUDA;
+}
+
+sab_status sab_rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, const sab_rotary_rows* k,
+                      const long long* positions, long long first_position, int B, int L, int D, int dtype,
+                      void* stream) {
+  return rotary(plan, q, k, positions, first_position, B, L, D, dtype, false, stream);
+}
+
+sab_status sab_rotary_backward(const sab_rotary_plan* plan, const sab_rotary_rows* dq, const sab_rotary_rows* dk,
+                               const long long* positions, long long first_position, int B, int L, int D,
+                               int dtype, void* stream) {
+  return rotary(plan, dq, dk, positions, first_position, B, L, D, dtype, true, stream);
+}
+
+// Arguments common to the decay attention calls.
+static bool decay_shape_ok(int B, int L, int H, int D) {
+  return B >= 1 && L >= 1 && H >= 1 && (D == 64 || D == 128) && L <= (1 << 30) && (long long)B * H <= (1LL << 24) &&
+         (long long)B * L <= (1LL << 38) / ((long long)H * D);
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t sab_decay_attention_workspace(int B, int L, int H, int D) {
+  (void)B, (void)L, (void)H, (void)D;
+  return 0;
+}
+
+sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
+                               const int* seq_len, const float* state_in, int B, int L, int H, int D, float scale,
+                               void* O, float* state_out, void* workspace, size_t ws_bytes, void* stream) {
+  const void* ptrs[] = {Q, K, V, O};
+  for (const void* x : ptrs)
+    if (x == nullptr || !aligned16(x)) return SAB_ERR_INVALID_ARG;
+  if (O == Q || O == K || O == V) return SAB_ERR_INVALID_ARG;
+  if (log_decay == nullptr || !aligned4(log_decay) || !aligned4(seq_len) || !aligned16(state_in) ||
+      !aligned16(state_out))
+    return SAB_ERR_INVALID_ARG;
+  if (!decay_shape_ok(B, L, H, D) || !(scale > 0.f) || !isfinite(scale)) return SAB_ERR_INVALID_ARG;
+  const size_t need = sab_decay_attention_workspace(B, L, H, D);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
+    return SAB_ERR_WORKSPACE;
+  DecayParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(Q);
+  p.k = static_cast<const uint16_t*>(K);
+  p.v = static_cast<const uint16_t*>(V);
+  p.o = static_cast<uint16_t*>(O);
+  p.log_decay = log_decay;
+  p.seq_len = seq_len;
+  p.state_in = state_in;
+  p.state_out = state_out;
+  p.B = B;
+  p.L = L;
+  p.H = H;
+  p.D = D;
+  p.kv_mul = 1.f;
+  p.o_mul = scale;
+  return launch_decay_run(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+}
+
+sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V, const float* log_decay,
+                                    const int* active, const float* state_in, int B, int H, int D, float scale,
+                                    void* O, float* state_out, void* stream) {
+  const void* ptrs[] = {Q, K, V, O, state_out};
+  for (const void* x : ptrs)
+    if (x == nullptr || !aligned16(x)) return SAB_ERR_INVALID_ARG;
+  if (O == Q || O == K || O == V) return SAB_ERR_INVALID_ARG;
+  if (log_decay == nullptr || !aligned4(log_decay) || !aligned4(active) || !aligned16(state_in))
+    return SAB_ERR_INVALID_ARG;
+  if (!decay_shape_ok(B, 1, H, D) || !(scale > 0.f) || !isfinite(scale)) return SAB_ERR_INVALID_ARG;
+  DecayStepParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(Q);
+  p.k = static_cast<const uint16_t*>(K);
+  p.v = static_cast<const uint16_t*>(V);
+  p.o = static_cast<uint16_t*>(O);
+  p.log_decay = log_decay;
+  p.active = active;
+  p.state_in = state_in;
+  p.state_out = state_out;
+  p.B = B;
+  p.H = H;
+  p.D = D;
+  p.scale = scale;
+  return launch_decay_step(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+}
+
+size_t sab_decay_attention_backward_workspace(int B, int L, int H, int D) {
+  (void)B, (void)L, (void)H, (void)D;
+  return 0;
+}
+
+sab_status sab_decay_attention_backward(const void* Q, const void* K, const void* V, const void* dO,
+                                        const float* log_decay, const int* seq_len, const float* state_in,
+                                        const float* d_state_out, int B, int L, int H, int D, float scale, void* dQ,
+                                        void* dK, void* dV, float* d_state_in, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+  const void* ptrs[] = {Q, K, V, dO, dQ, dK, dV};
+  for (int i = 0; i < 7; ++i) {
+    if (ptrs[i] == nullptr || !aligned16(ptrs[i])) return SAB_ERR_INVALID_ARG;
+    for (int j = 4; j < 7; ++j)
+      if (j != i && ptrs[i] == ptrs[j]) return SAB_ERR_INVALID_ARG;
+  }
+  if (log_decay == nullptr || !aligned4(log_decay) || !aligned4(seq_len) || !aligned16(state_in) ||
+      !aligned16(d_state_out) || !aligned16(d_state_in))
+    return SAB_ERR_INVALID_ARG;
+  if (d_state_in != nullptr && d_state_in == state_in) return SAB_ERR_INVALID_ARG;
+  if (!decay_shape_ok(B, L, H, D) || !(scale > 0.f) || !isfinite(scale)) return SAB_ERR_INVALID_ARG;
+  const size_t need = sab_decay_attention_backward_workspace(B, L, H, D);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
+    return SAB_ERR_WORKSPACE;
+  const uint16_t* q = static_cast<const uint16_t*>(Q);
+  const uint16_t* k = static_cast<const uint16_t*>(K);
+  const uint16_t* v = static_cast<const uint16_t*>(V);
+  const uint16_t* g = static_cast<const uint16_t*>(dO);
+  DecayParams p;
+  memset(&p, 0, sizeof(p));
+  p.log_decay = log_decay;
+  p.seq_len = seq_len;
+  p.B = B;
+  p.L = L;
+  p.H = H;
+  p.D = D;
+  struct Run {
+    const uint16_t *q, *k, *v;
+    void* o;
+    const float* in;
+    float* out;
+    int reverse, state_t;
+    float kv_mul, o_mul;
+  };
+  // d_state_in (which may be d_state_out) is written by the last run
+  const Run runs[3] = {{g, v, k, dQ, state_in, nullptr, 0, 1, 1.f, scale},
+                       {v, g, q, dK, d_state_out, nullptr, 1, 1, scale, 1.f},
+                       {k, q, g, dV, d_state_out, d_state_in, 1, 0, scale, 1.f}};
+  for (const Run& r : runs) {
+    p.q = r.q;
+    p.k = r.k;
+    p.v = r.v;
+    p.o = static_cast<uint16_t*>(r.o);
+    p.state_in = r.in;
+    p.state_out = r.out;
+    p.reverse = r.reverse;
+    p.state_t = r.state_t;
+    p.kv_mul = r.kv_mul;
+    p.o_mul = r.o_mul;
+    if (launch_decay_run(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SAB_ERR_CUDA;
+  }
+  return SAB_OK;
 }
 
 sab_status sab_selftest_split_abort(const sab_ring* ring, int layer, long long chunk, const void* Q,

@@ -210,12 +210,69 @@ struct BwdParams {
   float scale_log2;       // scale * log2(e)
 };
 
+// Rotary positions (token rows of one or two tensors, see sab_rotary).
+constexpr int kRotaryMaxPairs = 128;
+struct RotaryRows {
+  const void* in;
+  void* out;
+  int heads;              // 0: no second tensor
+  long long in_batch, in_token, out_batch, out_token;  // strides in elements
+};
+struct RotaryParams {
+  RotaryRows rows[2];     // q, k
+  const long long* positions;  // [axes, B, L] or null
+  long long first_position;
+  int B, L, D;
+  int dims;               // rotated leading dimensions of a head
+  int half_layout;
+  float magnitude;        // factor of the cosines
+  float sine;             // factor of the sines: +magnitude forward, -magnitude backward
+  int units, tokens;      // set by the launcher: threads per head, tokens per block
+  unsigned char axis[kRotaryMaxPairs];
+  unsigned long long step[kRotaryMaxPairs];
+};
+
+// One run of the decay recurrence over [B, L, H, D] rows (see
+// sab_decay_attention): forward, S = g S + (kv_mul k) v^T then o = o_mul q S;
+// reversed in time, S += (kv_mul k) v^T, o = o_mul q S, then S *= g.
+struct DecayParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* o;
+  const float* log_decay;   // [H]
+  const int* seq_len;       // [B] or null
+  const float* state_in;    // [B, H, D, D] or null
+  float* state_out;         // or null
+  int B, L, H, D;
+  int reverse;
+  int state_t;              // states in memory are [v dimension][k dimension]
+  float kv_mul, o_mul;
+};
+
+// One token of every sequence.
+struct DecayStepParams {
+  const uint16_t* q;        // [B, H, D]
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* o;
+  const float* log_decay;
+  const int* active;        // [B] or null
+  const float* state_in;    // [B, H, D, D] or null
+  float* state_out;
+  int B, H, D;
+  float scale;
+};
+
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_append_bf16(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_append_fp8(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_counter_add(long long* counter, long long delta, cudaStream_t s);
 cudaError_t launch_qk_rope(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_attention_backward(const BwdParams& p, cudaStream_t s);
+cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
+cudaError_t launch_decay_run(const DecayParams& p, cudaStream_t s);
+cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
 // One query tile per CTA, key-half softmax warpgroups; unsplit KV only.
 cudaError_t launch_chunk_attention_kh(const AttnParams& p, cudaStream_t s);
