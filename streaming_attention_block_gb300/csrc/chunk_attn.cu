@@ -30,6 +30,7 @@
 // copies and MMAs (again with bounded waits), frees TMEM and returns.
 #include <math.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -1791,10 +1792,14 @@ cudaError_t noalloc_scratch(void** ptr, size_t* bytes) {
 }
 
 unsigned int* device_error_word() {
-  static unsigned int* ptr = nullptr;
+  static std::atomic<unsigned int*> ptrs[64];  // per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  unsigned int* ptr = ptrs[dev].load();
   if (ptr == nullptr) {
     void* a = nullptr;
     if (cudaGetSymbolAddress(&a, g_sab_error_word) == cudaSuccess) ptr = static_cast<unsigned int*>(a);
+    ptrs[dev].store(ptr);
   }
   return ptr;
 }

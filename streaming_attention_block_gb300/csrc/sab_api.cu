@@ -913,9 +913,58 @@ static bool decay_shape_ok(int B, int L, int H, int D) {
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Segments a decay attention run cuts each sequence into, so that B * H
+// sequences fill the SMs with one CTA each: tiles per segment.
+static int decay_segment_tiles(int B, int L, int H) {
+  const int tiles = (L + kTileM - 1) / kTileM;
+  const long long want = device_sms() / ((long long)B * H);
+  if (want < 2) return tiles;
+  return (int)((tiles + want - 1) / want);
+}
+static int decay_segments(int B, int L, int H) {
+  const int tiles = (L + kTileM - 1) / kTileM, per = decay_segment_tiles(B, L, H);
+  return (tiles + per - 1) / per;
+}
+
 size_t sab_decay_attention_workspace(int B, int L, int H, int D) {
-  (void)B, (void)L, (void)H, (void)D;
-  return 0;
+  if (!decay_shape_ok(B, L, H, D)) return 0;
+  const int n = decay_segments(B, L, H);
+  return n == 1 ? 0 : align_up((size_t)B * H * n * D * D * sizeof(float), kAlign);
+}
+
+struct DecayRun {
+  const void *q, *k, *v;
+  void* o;
+  const float* in;
+  float* out;
+  int reverse, state_t;
+  float kv_mul, o_mul;
+};
+static sab_status decay_run(const DecayRun& r, const float* log_decay, const int* seq_len, int B, int L, int H, int D,
+                            void* workspace, void* stream) {
+  DecayTileParams p;
+  memset(&p, 0, sizeof(p));
+  if (!encode_token_major(&p.q_map, r.q, B, L, H, D) || !encode_token_major(&p.k_map, r.k, B, L, H, D) ||
+      !encode_token_major(&p.v_map, r.v, B, L, H, D) || !encode_token_major(&p.o_map, r.o, B, L, H, D))
+    return SAB_ERR_CUDA;
+  p.o = static_cast<uint16_t*>(r.o);
+  p.log_decay = log_decay;
+  p.seq_len = seq_len;
+  p.state_in = r.in;
+  p.state_out = r.out;
+  p.carry = static_cast<float*>(workspace);
+  p.B = B;
+  p.L = L;
+  p.H = H;
+  p.D = D;
+  p.seg_tiles = decay_segment_tiles(B, L, H);
+  p.nseg = decay_segments(B, L, H);
+  p.reverse = r.reverse;
+  p.state_t = r.state_t;
+  p.kv_mul = r.kv_mul;
+  p.o_mul = r.o_mul;
+  p.err_word = device_error_word();
+  return launch_decay_tiles(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 
 sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -932,23 +981,8 @@ sab_status sab_decay_attention(const void* Q, const void* K, const void* V, cons
   const size_t need = sab_decay_attention_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  DecayParams p;
-  memset(&p, 0, sizeof(p));
-  p.q = static_cast<const uint16_t*>(Q);
-  p.k = static_cast<const uint16_t*>(K);
-  p.v = static_cast<const uint16_t*>(V);
-  p.o = static_cast<uint16_t*>(O);
-  p.log_decay = log_decay;
-  p.seq_len = seq_len;
-  p.state_in = state_in;
-  p.state_out = state_out;
-  p.B = B;
-  p.L = L;
-  p.H = H;
-  p.D = D;
-  p.kv_mul = 1.f;
-  p.o_mul = scale;
-  return launch_decay_run(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale}, log_decay, seq_len, B, L, H, D, workspace,
+                   stream);
 }
 
 sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -979,8 +1013,7 @@ sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V,
 }
 
 size_t sab_decay_attention_backward_workspace(int B, int L, int H, int D) {
-  (void)B, (void)L, (void)H, (void)D;
-  return 0;
+  return sab_decay_attention_workspace(B, L, H, D);  // its three runs use it one after the other
 }
 
 sab_status sab_decay_attention_backward(const void* Q, const void* K, const void* V, const void* dO,
@@ -1002,42 +1035,13 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   const size_t need = sab_decay_attention_backward_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  const uint16_t* q = static_cast<const uint16_t*>(Q);
-  const uint16_t* k = static_cast<const uint16_t*>(K);
-  const uint16_t* v = static_cast<const uint16_t*>(V);
-  const uint16_t* g = static_cast<const uint16_t*>(dO);
-  DecayParams p;
-  memset(&p, 0, sizeof(p));
-  p.log_decay = log_decay;
-  p.seq_len = seq_len;
-  p.B = B;
-  p.L = L;
-  p.H = H;
-  p.D = D;
-  struct Run {
-    const uint16_t *q, *k, *v;
-    void* o;
-    const float* in;
-    float* out;
-    int reverse, state_t;
-    float kv_mul, o_mul;
-  };
   // d_state_in (which may be d_state_out) is written by the last run
-  const Run runs[3] = {{g, v, k, dQ, state_in, nullptr, 0, 1, 1.f, scale},
-                       {v, g, q, dK, d_state_out, nullptr, 1, 1, scale, 1.f},
-                       {k, q, g, dV, d_state_out, d_state_in, 1, 0, scale, 1.f}};
-  for (const Run& r : runs) {
-    p.q = r.q;
-    p.k = r.k;
-    p.v = r.v;
-    p.o = static_cast<uint16_t*>(r.o);
-    p.state_in = r.in;
-    p.state_out = r.out;
-    p.reverse = r.reverse;
-    p.state_t = r.state_t;
-    p.kv_mul = r.kv_mul;
-    p.o_mul = r.o_mul;
-    if (launch_decay_run(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SAB_ERR_CUDA;
+  const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale},
+                            {V, dO, Q, dK, d_state_out, nullptr, 1, 1, scale, 1.f},
+                            {K, Q, dO, dV, d_state_out, d_state_in, 1, 0, scale, 1.f}};
+  for (const DecayRun& r : runs) {
+    const sab_status st = decay_run(r, log_decay, seq_len, B, L, H, D, workspace, stream);
+    if (st != SAB_OK) return st;
   }
   return SAB_OK;
 }

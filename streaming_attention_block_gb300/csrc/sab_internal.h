@@ -235,19 +235,20 @@ struct RotaryParams {
 // One run of the decay recurrence over [B, L, H, D] rows (see
 // sab_decay_attention): forward, S = g S + (kv_mul k) v^T then o = o_mul q S;
 // reversed in time, S += (kv_mul k) v^T, o = o_mul q S, then S *= g.
-struct DecayParams {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  uint16_t* o;
+struct DecayTileParams {
+  CUtensorMap q_map, k_map, v_map, o_map;  // dims (D, L, H, B), box (64, 128, 1, 1), SW128
+  uint16_t* o;              // tiles without a live token are zeroed directly
   const float* log_decay;   // [H]
   const int* seq_len;       // [B] or null
   const float* state_in;    // [B, H, D, D] or null
   float* state_out;         // or null
+  float* carry;             // [B, H, nseg, D, D] scratch when nseg > 1
   int B, L, H, D;
+  int nseg, seg_tiles;      // segments per sequence, 128-token tiles per segment
   int reverse;
-  int state_t;              // states in memory are [v dimension][k dimension]
+  int state_t;              // the caller's states are [v dimension][k dimension]
   float kv_mul, o_mul;
+  unsigned int* err_word;   // the library's device error word
 };
 
 // One token of every sequence.
@@ -271,7 +272,7 @@ cudaError_t launch_counter_add(long long* counter, long long delta, cudaStream_t
 cudaError_t launch_qk_rope(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_attention_backward(const BwdParams& p, cudaStream_t s);
 cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
-cudaError_t launch_decay_run(const DecayParams& p, cudaStream_t s);
+cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
 // One query tile per CTA, key-half softmax warpgroups; unsplit KV only.
