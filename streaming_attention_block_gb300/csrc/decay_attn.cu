@@ -37,6 +37,8 @@ struct Decay {
   }
   __device__ __forceinline__ float operator()(float s) const { return fmaf(s, hi, s * lo); }
 };
+// over n tokens
+__device__ __noinline__ Decay decay_over(int n, float ln) { return Decay((float)n * ln); }
 
 // One token: the state passes once through registers.  One CTA per (b, h)
 // and W value columns; W / 4 lanes hold a row's columns as 16-byte vectors, so
@@ -132,8 +134,9 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
 //
 // Roundings: P (decay applied in fp32) and the state's copy that multiplies
 // q go to bf16, as every tensor-core operand must; the state itself stays in
-// fp32 registers.  W K would lose the state 8 bits, so it is split into a bf16
-// part and the bf16 rest, two products: 16 bits.
+// fp32 registers.  W K in bf16 would cost the state 8 bits, so it is split into
+// TERMS bf16 parts, one product each: three (24 bits) for a state that the
+// caller gets, two (16 bits) for one that only feeds bf16 outputs.
 //
 // One CTA owns a run of tiles of one (b, h).  When B H leaves SMs idle a
 // sequence is cut into segments: decay_segment_kernel sums each segment's own
@@ -151,9 +154,9 @@ __device__ __forceinline__ uint64_t global_ns() {
 
 // Bounded mbarrier wait: gives up after kTimeoutNs or when another warp of
 // the CTA has (see chunk_attn.cu); records the site in the device error word.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
-                                             unsigned* err_word) {
-  if (mbar_test_wait(bar, parity)) return true;
+// Out of line, as is all rare code here: four roles share the instruction cache.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
+                                       unsigned* err_word) {
   const uint64_t t0 = global_ns();
 #pragma unroll 1
   for (uint32_t it = 1;; ++it) {
@@ -168,7 +171,11 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
     }
   }
 }
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned* err_word) {
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
+                                             unsigned* err_word) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, site, err_word);
+}
+__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned* err_word) {
   const uint64_t t0 = global_ns();
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
@@ -204,90 +211,116 @@ struct Run {
   }
 };
 
-// k rows of a tile times mul * g^(e0 + sg * row), in place as bf16 with the
-// bf16 rest in `rest`; rows from n on become zero.  Both tiles are 128-byte
-// swizzled; a row's 16-byte pieces keep their places, so they need no
-// unscrambling.  `v`, if given, also loses its rows from n on: they may hold
-// anything, and 0 * NaN would reach every output.
-template <int D>
-__device__ __forceinline__ void scale_rows(uint8_t* k, uint8_t* rest, uint8_t* v, int tid, int n, float mul, float ld2,
-                                           int e0, int sg) {
-  constexpr int kPieces = D / 8;  // per row
-#pragma unroll 4
-  for (int i = tid; i < kC * kPieces; i += 256) {
-    const int row = i / kPieces, c = i % kPieces;
-    const uint32_t off = (uint32_t)((c >> 3) * (kC * 128) + row * 128 + (c & 7) * 16);
-    uint32_t hi[4], lo[4];
+// Pieces of 16 bytes (8 elements) of a 128-byte swizzled tile of ROWS rows.  A
+// row's pieces keep their places, so row-wise work needs no unscrambling.
+template <int ROWS>
+__device__ __forceinline__ uint32_t piece_off(int row, int c) {
+  return (uint32_t)((c >> 3) * (ROWS * 128) + row * 128 + (c & 7) * 16);
+}
+
+// Rows of a k tile times f * w[row], as TERMS bf16 parts that add up to it:
+// the first in place, the others (the rounded rest of the one before) in tiles
+// of `rest_bytes` behind `rest`.  Rows from n on become zero; so do those of
+// `v`, if given: they may hold anything, and 0 * NaN would reach every sum.
+template <int D, int ROWS, int TERMS>
+__device__ __forceinline__ void scale_rows(uint8_t* k, uint8_t* rest, uint32_t rest_bytes, uint8_t* v, int tid, int n,
+                                           float f, const float* w) {
+  constexpr int kPieces = D / 8;             // per row
+  constexpr int kStep = 256 / kPieces;       // rows between a thread's pieces
+  uint32_t off = piece_off<ROWS>(tid / kPieces, tid % kPieces);
+#pragma unroll 2
+  for (int row = tid / kPieces; row < ROWS; row += kStep, off += kStep * 128) {
+    uint32_t part[TERMS][4];
     if (row < n) {
-      const float w = mul * ex2((float)(e0 + sg * row) * ld2);
+      const float wr = f * w[row];
       const uint4 x = *reinterpret_cast<const uint4*>(k + off);
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = __uint_as_float(xs[j] << 16) * w, b = __uint_as_float(xs[j] & 0xFFFF0000u) * w;
-        hi[j] = pack_bf16(a, b);
-        lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16), b - __uint_as_float(hi[j] & 0xFFFF0000u));
+        float2 r = __fmul2_rn(make_float2(__uint_as_float(xs[j] << 16), __uint_as_float(xs[j] & 0xFFFF0000u)),
+                              make_float2(wr, wr));
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const uint32_t q = pack_bf16(r.x, r.y);
+          part[t][j] = q;
+          if (t + 1 < TERMS)
+            r = __fadd2_rn(r, make_float2(-__uint_as_float(q << 16), -__uint_as_float(q & 0xFFFF0000u)));
+        }
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) hi[j] = lo[j] = 0u;
+      for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[t][j] = 0u;
       if (v != nullptr) *reinterpret_cast<uint4*>(v + off) = make_uint4(0u, 0u, 0u, 0u);
     }
-    *reinterpret_cast<uint4*>(k + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(rest + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(k + off) = make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]);
+#pragma unroll
+    for (int t = 1; t < TERMS; ++t)
+      *reinterpret_cast<uint4*>(rest + (t - 1) * rest_bytes + off) =
+          make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
   }
 }
 template <int D>
-__device__ __forceinline__ void zero_rows(uint8_t* v, int tid, int n) {
+__device__ __noinline__ void zero_rows(uint8_t* v, int tid, int n) {
   constexpr int kPieces = D / 8;
-  for (int i = n * kPieces + tid; i < kC * kPieces; i += 256) {
-    const int row = i / kPieces, c = i % kPieces;
-    *reinterpret_cast<uint4*>(v + (c >> 3) * (kC * 128) + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+#pragma unroll 1
+  for (int i = n * kPieces + tid; i < kC * kPieces; i += 256)
+    *reinterpret_cast<uint4*>(v + piece_off<kC>(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-major
 
-template <int D_>
+// The tile kernel's warps: 0 loads, 1 issues MMAs, 2-9 ("rows") turn scores
+// into P and accumulators into output rows, 10-17 ("state") scale k and carry
+// the state, 18 stores.  The two element groups work on the same tile at once:
+// neither needs the other within a tile, and each alone takes about half of
+// the time HBM needs for a tile.
+// A tile's output is staged over its v once the update has read it.
+template <int D_, int TERMS_>
 struct TileCfg {
-  static constexpr int D = D_;
+  static constexpr int D = D_, TERMS = TERMS_;
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = kC * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
-  static constexpr int kVStages = D == 128 ? 1 : 2;
+  static constexpr int kQStages = D == 128 ? 1 : 2;
+  static constexpr int kVStages = D == 128 && TERMS == 3 ? 1 : 2;
   // (D = 64: the update's A operand, M = 128, takes its upper 64 rows from the
   // box behind a k tile; they land in accumulator rows that nothing reads)
-  static constexpr uint32_t kQOff = 0;                                   // [2]; the output is staged over q
-  static constexpr uint32_t kKOff = kQOff + 2 * kTileBytes;              // [2]; scaled in place
-  static constexpr uint32_t kRestOff = kKOff + 2 * kTileBytes;
-  static constexpr uint32_t kVOff = kRestOff + kTileBytes;
-  static constexpr uint32_t kStOff = kVOff + kVStages * kTileBytes;      // bf16 state [D][D]
+  static constexpr uint32_t kKOff = 0;                                       // [2]; scaled in place
+  static constexpr uint32_t kRestOff = kKOff + 2 * kTileBytes;               // [TERMS - 1]
+  static constexpr uint32_t kQOff = kRestOff + (TERMS - 1) * kTileBytes;
+  static constexpr uint32_t kVOff = kQOff + kQStages * kTileBytes;
+  static constexpr uint32_t kStOff = kVOff + kVStages * kTileBytes;          // bf16 state [D][D]
   static constexpr uint32_t kStBoxBytes = D * 128u;
   static constexpr uint32_t kBarOff = kStOff + kBoxes * kStBoxBytes;
-  static constexpr int kFullQ = 0, kFullK = 2, kFullV = 4;               // [2] each
-  static constexpr int kEmptyQ = 6, kEmptyK = 8, kEmptyV = 10;           // [2] each
-  static constexpr int kSFull = 12, kPFull = 13, kKwFull = 14, kOFull = 15, kUFull = 16, kStFull = 17, kOut = 18 /* [2] */,
-                       kDrain = 20, kNumBars = 21;
-  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;           // tmem address, abort flag
-  static constexpr uint32_t kTabOff = (kMiscOff + 16 + 15) & ~15u;        // 32 decay powers, read 16 bytes at a time
-  static constexpr uint32_t kSmemBytes = kTabOff + 128 + 1024;
-  static constexpr int kThreads = 352;  // producer, MMA, 8 element warps, store
+  static constexpr int kFullQ = 0, kFullK = 2, kFullV = 4;                   // [2] each
+  static constexpr int kEmptyQ = 6, kEmptyK = 8, kEmptyV = 10, kOut = 12;    // [2] each
+  static constexpr int kSFull = 14, kPFull = 15, kKwFull = 16, kOFull = 17, kORead = 18, kUFull = 19, kStFull = 20,
+                       kDrain = 21, kNumBars = 22;
+  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;               // tmem address, abort flag
+  static constexpr uint32_t kTabOff = kMiscOff + 16;                         // decay powers: of P [256], of k [128]
+  static constexpr uint32_t kSmemBytes = kTabOff + 4 * (256 + 128) + 1024;
+  static constexpr int kThreads = 608;
   static constexpr uint32_t kS = 0, kIntra = 128, kInter = 128 + D, kUpd = 128 + 2 * D;  // TMEM columns
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static_assert(kTabOff % 16 == 0 && kStOff % 1024 == 0, "alignment");
+  static_assert(kTabOff % 4 == 0 && kStOff % 1024 == 0, "alignment");
 };
 
-template <int D>
-__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
+template <int D, int TERMS>
+__global__ void __launch_bounds__(TileCfg<D, TERMS>::kThreads, 1)
 decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
-  using C = TileCfg<D>;
+  using C = TileCfg<D, TERMS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u32 - raw_u32);
   uint32_t* misc = reinterpret_cast<uint32_t*>(base + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  float* tab = reinterpret_cast<float*>(base + C::kTabOff);
+  // p_tab[127 + i - j]: factor of the score of row i and column j (0 where
+  // masked); w_tab[j]: factor of k row j of a full tile
+  float* p_tab = reinterpret_cast<float*>(base + C::kTabOff);
+  float* w_tab = p_tab + 256;
   auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = blockIdx.x % p.nseg;
@@ -296,7 +329,10 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i)
-      mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kStFull || i == C::kOut || i == C::kOut + 1 ? 256 : 1);
+      mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kORead || i == C::kStFull || i == C::kOut ||
+                                i == C::kOut + 1
+                            ? 256
+                            : 1);
     misc[1] = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -309,7 +345,13 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   griddep_wait();
   const Run run(p, b, seg);
   const float ln = decay_ln(p.log_decay, h), ld2 = ln * kLog2e;
-  if (threadIdx.x < 32) tab[lane] = ex2((float)(p.reverse ? lane : 31 - lane) * ld2);
+  if (threadIdx.x < 256) {
+    const int d = p.reverse ? 127 - (int)threadIdx.x : (int)threadIdx.x - 127;
+    p_tab[threadIdx.x] = d >= 0 ? p.o_mul * p.kv_mul * ex2((float)d * ld2) : 0.f;
+  } else if (threadIdx.x < 384) {
+    const int j = threadIdx.x - 256;
+    w_tab[j] = p.kv_mul * ex2((float)(p.reverse ? j + 1 : 127 - j) * ld2);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -324,31 +366,35 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0 && nt > 0) {
-      auto load = [&](const CUtensorMap* m, uint32_t off, int fb, int row) {
-        mbar_arrive_expect_tx(bar(fb), C::kTileBytes);
+      int nq = 0, nk = 0, nv = 0;
+      // load number n of a stream of `stages` slots
+      auto load = [&](const CUtensorMap* m, uint32_t off, int full, int empty, int stages, int& n, int it) {
+        const int s = n % stages;
+        if (n >= stages && !wait(empty + s, (n / stages - 1) & 1u, 9)) return false;
+        mbar_arrive_expect_tx(bar(full + s), C::kTileBytes);
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_4d(base_u32 + off + bx * C::kBoxBytes, m, bar(fb), bx * 64, row, h, b);
+          tma_load_4d(base_u32 + off + s * C::kTileBytes + bx * C::kBoxBytes, m, bar(full + s), bx * 64,
+                      run.tile(run.a + it) * kC, h, b);
+        ++n;
+        return true;
       };
-      int nq = 0, nk = 0, nv = 0;
-      bool ok = true;
+      // q first for the first tile, then in the order in which the slots come free
+      auto load_q = [&](int it) { return load(&p.q_map, C::kQOff, C::kFullQ, C::kEmptyQ, C::kQStages, nq, it); };
+      bool ok = load_q(0);
       for (int it = 0; ok && it < nt; ++it) {
-        const int s = it & 1, row = run.tile(run.a + it) * kC, sv = it % C::kVStages;
-        if (it >= 2) ok = wait(C::kEmptyK + s, (it / 2 - 1) & 1u, 9);
-        if (!ok) break;
-        load(&p.k_map, C::kKOff + s * C::kTileBytes, C::kFullK + s, row), ++nk;
-        if (it >= 2) ok = wait(C::kEmptyQ + s, (it / 2 - 1) & 1u, 9);
-        if (!ok) break;
-        load(&p.q_map, C::kQOff + s * C::kTileBytes, C::kFullQ + s, row), ++nq;
-        if (it >= C::kVStages) ok = wait(C::kEmptyV + sv, (it / C::kVStages - 1) & 1u, 9);
-        if (!ok) break;
-        load(&p.v_map, C::kVOff + sv * C::kTileBytes, C::kFullV + sv, row), ++nv;
+        ok = load(&p.k_map, C::kKOff, C::kFullK, C::kEmptyK, 2, nk, it) &&
+             (it == 0 || C::kVStages > 1 || load_q(it)) &&
+             load(&p.v_map, C::kVOff, C::kFullV, C::kEmptyV, C::kVStages, nv, it) &&
+             (it == 0 || C::kVStages == 1 || load_q(it));
       }
       if (*abort_flag) {
-        for (int i = max(0, nk - 2); i < nk; ++i) wait_drain(bar(C::kFullK + (i & 1)), (i / 2) & 1u, p.err_word);
-        for (int i = max(0, nq - 2); i < nq; ++i) wait_drain(bar(C::kFullQ + (i & 1)), (i / 2) & 1u, p.err_word);
-        for (int i = max(0, nv - C::kVStages); i < nv; ++i)
-          wait_drain(bar(C::kFullV + i % C::kVStages), (i / C::kVStages) & 1u, p.err_word);
+        auto drain = [&](int full, int stages, int n) {
+          for (int i = max(0, n - stages); i < n; ++i) wait_drain(bar(full + i % stages), (i / stages) & 1u, p.err_word);
+        };
+        drain(C::kFullK, 2, nk);
+        drain(C::kFullQ, C::kQStages, nq);
+        drain(C::kFullV, C::kVStages, nv);
       }
     }
     __syncwarp();
@@ -367,230 +413,237 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       if (r) tc_fence_after();
       return r;
     };
-    bool ok = true;
-    for (int it = 0; ok && it < nt; ++it) {
-      const int s = it & 1, sv = it % C::kVStages;
-      const uint32_t q = C::kQOff + s * C::kTileBytes, k = C::kKOff + s * C::kTileBytes,
-                     v = C::kVOff + sv * C::kTileBytes;
-      ok = wait_all(C::kFullQ + s, (it / 2) & 1u, 10) && wait_all(C::kFullK + s, (it / 2) & 1u, 10);
-      if (!ok) break;
+    auto scores = [&](int it) {
+      const int s = it & 1, sq = it % C::kQStages;
+      if (!wait_all(C::kFullQ + sq, (it / C::kQStages) & 1u, 10) || !wait_all(C::kFullK + s, (it / 2) & 1u, 10))
+        return false;
+      const uint32_t q = C::kQOff + sq * C::kTileBytes, k = C::kKOff + s * C::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_ss_e(tmem + C::kS, at(kmaj, q + k_off(kk)), at(kmaj, k + k_off(kk)), id_s, kk > 0);
       mma_commit_e(bar(C::kSFull));
-      if (!(ok = wait_all(C::kStFull, it & 1u, 11))) break;
+      return true;
+    };
+    bool ok = nt > 0 && scores(0);
+    for (int it = 0; ok && it < nt; ++it) {
+      const int s = it & 1, sv = it % C::kVStages, sq = it % C::kQStages;
+      const uint32_t q = C::kQOff + sq * C::kTileBytes, k = C::kKOff + s * C::kTileBytes,
+                     v = C::kVOff + sv * C::kTileBytes;
+      // the state before the tile is published, the previous output rows are read
+      ok = wait_all(C::kStFull, it & 1u, 11) && (it == 0 || wait_all(C::kORead, (it - 1) & 1u, 11));
+      if (!ok) break;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_ss_e(tmem + C::kInter, at(kmaj, q + k_off(kk)), at(mn_st, C::kStOff + kk * 2048u), id_o, kk > 0);
+      mma_commit_e(bar(C::kEmptyQ + sq));
       ok = wait_all(C::kPFull, it & 1u, 12) && wait_all(C::kFullV + sv, (it / C::kVStages) & 1u, 10);
       if (!ok) break;
 #pragma unroll
       for (int kk = 0; kk < kC / 16; ++kk)
         mma_ts_e(tmem + C::kIntra, tmem + C::kS + (kk >> 2) * 64 + (kk & 3) * 8, at(mn, v + kk * 2048u), id_o, kk > 0);
       mma_commit_e(bar(C::kOFull));
-      if (it >= n_upd) break;
-      if (!(ok = wait_all(C::kKwFull, it & 1u, 13))) break;
+      if (it < n_upd) {
+        if (!(ok = wait_all(C::kKwFull, it & 1u, 13))) break;
 #pragma unroll
-      for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ss_e(tmem + C::kUpd, at(mn, k + kk * 2048u), at(mn, v + kk * 2048u), id_u, kk > 0);
+        for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-      for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ss_e(tmem + C::kUpd, at(mn, C::kRestOff + kk * 2048u), at(mn, v + kk * 2048u), id_u, 1u);
-      mma_commit_e(bar(C::kUFull));
-      mma_commit_e(bar(C::kEmptyK + s));
-      mma_commit_e(bar(C::kEmptyV + sv));
+          for (int kk = 0; kk < kC / 16; ++kk)
+            mma_ss_e(tmem + C::kUpd, at(mn, (t == 0 ? k : C::kRestOff + (t - 1) * C::kTileBytes) + kk * 2048u),
+                     at(mn, v + kk * 2048u), id_u, t > 0 || kk > 0);
+        mma_commit_e(bar(C::kUFull));
+        mma_commit_e(bar(C::kEmptyK + s));
+      }
+      if (it + 1 < nt) ok = scores(it + 1);
     }
-    if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
+    if (__any_sync(0xffffffffu, (nt > 0 && !ok) || *abort_flag)) {
       mma_commit_e(bar(C::kDrain));
       if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // --------------------------------------------------------- output store
     if (lane == 0) {
       for (int it = 0; it < nt; ++it) {
-        if (!wait(C::kOut + (it & 1), (it / 2) & 1u, 14)) break;
-        const int row = run.tile(run.a + it) * kC;
+        const int sv = it % C::kVStages;
+        if (!wait(C::kOut + sv, (it / C::kVStages) & 1u, 14)) break;
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_store_4d(&p.o_map, base_u32 + C::kQOff + (it & 1) * C::kTileBytes + bx * C::kBoxBytes, bx * 64, row, h, b);
+          tma_store_4d(&p.o_map, base_u32 + C::kVOff + sv * C::kTileBytes + bx * C::kBoxBytes, bx * 64,
+                       run.tile(run.a + it) * kC, h, b);
         tma_store_commit_and_wait_read();
-        mbar_arrive(bar(C::kEmptyQ + (it & 1)));
+        mbar_arrive(bar(C::kEmptyV + sv));
       }
     }
     __syncwarp();
   } else {
-    // -------------------------------------------------------- element work
-    const int tid = threadIdx.x - 64;
-    const int hf = (warp - 2) >> 2, quad = warp & 3;
+    const int quad = warp & 3, hf = ((warp - 2) >> 2) & 1;
     const int row = quad * 32 + lane;  // token of the tile; key dimension of the state
     const uint32_t lane_off = tmem + ((uint32_t)(quad * 32) << 16);
-    constexpr int kCols = D / 2;       // state and output columns of this thread: [hf D/2, (hf + 1) D/2)
+    constexpr int kCols = D / 2;       // columns of this thread: [hf D/2, (hf + 1) D/2)
     const bool rev = p.reverse != 0;
-    const float p_mul = p.o_mul * p.kv_mul;
-    float st[kCols];
-    // offset of 16-byte piece c (8 columns) of a row in a swizzled tile
+    // offset of 16-byte piece c (8 columns) of this thread's row in a swizzled tile
     auto piece = [&](int c, uint32_t box_bytes) {
       const int cc = hf * (kCols / 8) + c;
       return (uint32_t)((cc >> 3) * box_bytes + row * 128 + (((cc & 7) ^ (row & 7)) << 4));
     };
-    auto publish_state = [&]() {
-      if (row < D) {
-#pragma unroll
-        for (int c = 0; c < kCols / 8; ++c)
-          *reinterpret_cast<uint4*>(base + C::kStOff + piece(c, C::kStBoxBytes)) =
-              make_uint4(pack_bf16(st[8 * c], st[8 * c + 1]), pack_bf16(st[8 * c + 2], st[8 * c + 3]),
-                         pack_bf16(st[8 * c + 4], st[8 * c + 5]), pack_bf16(st[8 * c + 6], st[8 * c + 7]));
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(bar(C::kStFull));
-    };
-    // the state before the segment: carried ones are stored as this run holds
-    // them, the caller's possibly transposed
-    const float* in = p.nseg > 1 ? p.carry + (bh * p.nseg + seg) * D * D
-                                 : p.state_in != nullptr ? p.state_in + bh * D * D : nullptr;
-    const bool in_t = p.nseg == 1 && p.state_t;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) st[c] = 0.f;
-    if (in != nullptr && row < D && nt > 0) {
-      if (in_t) {
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) st[c] = in[(long long)(hf * kCols + c) * D + row];
-      } else {
-#pragma unroll
-        for (int c = 0; c < kCols / 4; ++c) {
-          const float4 x = *reinterpret_cast<const float4*>(in + (long long)row * D + hf * kCols + 4 * c);
-          st[4 * c] = x.x, st[4 * c + 1] = x.y, st[4 * c + 2] = x.z, st[4 * c + 3] = x.w;
-        }
-      }
-    }
-    if (nt > 0) publish_state();
     bool ok = true;
-    for (int it = 0; it < nt; ++it) {
-      const int s = it & 1, n = run.tokens(run.a + it);
-      uint8_t* kt = base + C::kKOff + s * C::kTileBytes;
-      uint8_t* vt = base + C::kVOff + (it % C::kVStages) * C::kTileBytes;
-      // 1. P = decayed, masked scores, bf16, over the scores
-      ok = __all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 15));
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        const int c0 = hf * 64 + 32 * pass;
-        const uint32_t src = lane_off + C::kS + c0, dst = lane_off + C::kS + hf * 64 + 16 * pass;
-        uint32_t pk[16];
-        const bool none = (rev ? c0 + 31 < quad * 32 : c0 > quad * 32 + 31) || c0 >= n;
-        if (none) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = 0u;
-        } else {
-          uint32_t sv[32];
-          tmem_ld32(src, sv);
-          tmem_wait_ld();
-          if (n == kC && c0 != quad * 32) {
-            // whole block on the visible side: g^|i - j| as the distance to the
-            // block's near edge times the table's powers, both at most 1
-            const float f = p_mul * ex2((float)(rev ? c0 - row : row - c0 - 31) * ld2);
-#pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4) {
-              const float4 t = *reinterpret_cast<const float4*>(tab + 4 * c4);
-              pk[2 * c4] = pack_bf16(__uint_as_float(sv[4 * c4]) * (f * t.x), __uint_as_float(sv[4 * c4 + 1]) * (f * t.y));
-              pk[2 * c4 + 1] =
-                  pack_bf16(__uint_as_float(sv[4 * c4 + 2]) * (f * t.z), __uint_as_float(sv[4 * c4 + 3]) * (f * t.w));
-            }
-          } else {
-            auto one = [&](int c) {
-              const int j = c0 + c, d = rev ? j - row : row - j;
-              return d >= 0 && j < n ? __uint_as_float(sv[c]) * (p_mul * ex2((float)d * ld2)) : 0.f;
-            };
-#pragma unroll
-            for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(one(2 * c), one(2 * c + 1));
-          }
-        }
-        tmem_st16(dst, pk);
-      }
-      tmem_wait_st();
-      if (n < kC) {  // padding of v must not meet the zeros of P
-        ok = __all_sync(0xffffffffu, wait(C::kFullV + it % C::kVStages, (it / C::kVStages) & 1u, 15));
-        if (!ok) break;
-        zero_rows<D>(vt, tid, n);
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      mbar_arrive(bar(C::kPFull));
-      // 2. scaled k for the update
-      if (it < n_upd) {
-        ok = __all_sync(0xffffffffu, wait(C::kFullK + s, (it / 2) & 1u, 15));
-        if (!ok) break;
-        scale_rows<D>(kt, base + C::kRestOff, nullptr, tid, n, p.kv_mul, ld2, rev ? 1 : n - 1, rev ? 1 : -1);
-        fence_proxy_async_smem();
-        mbar_arrive(bar(C::kKwFull));
-      }
-      // 3. output rows, staged over q
-      ok = __all_sync(0xffffffffu, wait(C::kOFull, it & 1u, 15));
-      if (!ok) break;
-      tc_fence_after();
-      {
-        const float f = p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2);
-        uint8_t* ot = base + C::kQOff + s * C::kTileBytes;
-#pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          uint32_t x[32], y[32];
-          tmem_ld32(lane_off + C::kIntra + hf * kCols + c0, x);
-          tmem_ld32(lane_off + C::kInter + hf * kCols + c0, y);
-          tmem_wait_ld();
-          uint32_t o[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            o[c] = row < n ? pack_bf16(fmaf(__uint_as_float(y[2 * c]), f, __uint_as_float(x[2 * c])),
-                                       fmaf(__uint_as_float(y[2 * c + 1]), f, __uint_as_float(x[2 * c + 1])))
-                           : 0u;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(ot + piece(c0 / 8 + c, C::kBoxBytes)) =
-                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-        }
-      }
-      tc_fence_before();
-      fence_proxy_async_smem();
-      mbar_arrive(bar(C::kOut + s));
-      // 4. the state after the tile
-      if (it < n_upd) {
-        ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 15));
+    if (warp < 10) {
+      // ------------------------------------------------------------- rows
+      const int tid = threadIdx.x - 64;
+      for (int it = 0; it < nt; ++it) {
+        const int n = run.tokens(run.a + it), sv = it % C::kVStages;
+        uint8_t* vt = base + C::kVOff + sv * C::kTileBytes;
+        // P = decayed, masked scores, bf16, over the scores
+        ok = __all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 15));
         if (!ok) break;
         tc_fence_after();
-        const Decay decay((float)n * ln);
+#pragma unroll 1
+        for (int pass = 0; pass < 4; ++pass) {
+          const int c0 = hf * 64 + 16 * pass;
+          uint32_t pk[8];
+          if ((rev ? c0 + 15 < quad * 32 : c0 > quad * 32 + 31) || c0 >= n) {  // nothing visible
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          uint32_t x[32];
-          tmem_ld32(lane_off + C::kUpd + hf * kCols + c0, x);
+            for (int c = 0; c < 8; ++c) pk[c] = 0u;
+          } else {
+            uint32_t x[16];
+            tmem_ld16(lane_off + C::kS + c0, x);
+            tmem_wait_ld();
+            if (c0 + 16 > n) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (c0 + c >= n) x[c] = 0u;
+            }
+            const float* t = p_tab + 127 + row - c0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              pk[c] = pack_bf16(__uint_as_float(x[2 * c]) * t[-2 * c], __uint_as_float(x[2 * c + 1]) * t[-2 * c - 1]);
+          }
+          tmem_st8(lane_off + C::kS + hf * 64 + 8 * pass, pk);
+        }
+        tmem_wait_st();
+        if (n < kC) {  // padding of v must not meet the zeros of P
+          ok = __all_sync(0xffffffffu, wait(C::kFullV + sv, (it / C::kVStages) & 1u, 15));
+          if (!ok) break;
+          zero_rows<D>(vt, tid, n);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::kPFull));
+        // output rows
+        const float f = p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2);
+        ok = __all_sync(0xffffffffu, wait(C::kOFull, it & 1u, 15));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t o[kCols / 2];
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 16) {
+          uint32_t x[16], y[16];
+          tmem_ld16(lane_off + C::kIntra + hf * kCols + c0, x);
+          tmem_ld16(lane_off + C::kInter + hf * kCols + c0, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) st[c0 + c] = decay(st[c0 + c]) + __uint_as_float(x[c]);
+          for (int c = 0; c < 8; ++c) {
+            const float2 r = __ffma2_rn(make_float2(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])),
+                                        make_float2(f, f),
+                                        make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])));
+            o[c0 / 2 + c] = row < n ? pack_bf16(r.x, r.y) : 0u;
+          }
         }
-        if (it + 1 < nt) publish_state();
+        tc_fence_before();
+        mbar_arrive(bar(C::kORead));
+        if (it < n_upd) {  // v is free once the update has read it
+          ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 15));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c)
+          *reinterpret_cast<uint4*>(vt + piece(c, C::kBoxBytes)) =
+              make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::kOut + sv));
       }
-    }
-    // an aborted CTA stores no state; its outputs are not valid either
-    if (ok && !*abort_flag && p.state_out != nullptr && row < D) {
-      float* out = p.state_out + bh * D * D;
-      if (nt == 0 && in != nullptr) {  // nothing live: the state passes through
+      // tiles of the segment without a live token
+      for (int r = run.r0; r < run.r1; ++r) {
+        if (r >= run.a && r < run.b) continue;
+        const int t0 = run.tile(r) * kC, rows = min(kC, p.L - t0);
+        for (int i = tid; i < rows * (D / 8); i += 256) {
+          const long long e = (((long long)b * p.L + t0 + i / (D / 8)) * p.H + h) * D + i % (D / 8) * 8;
+          *reinterpret_cast<uint4*>(p.o + e) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ state
+      const int tid = threadIdx.x - 320;
+      float st[kCols];
+      auto publish = [&]() {
+        if (row < D) {
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c)
+            *reinterpret_cast<uint4*>(base + C::kStOff + piece(c, C::kStBoxBytes)) =
+                make_uint4(pack_bf16(st[8 * c], st[8 * c + 1]), pack_bf16(st[8 * c + 2], st[8 * c + 3]),
+                           pack_bf16(st[8 * c + 4], st[8 * c + 5]), pack_bf16(st[8 * c + 6], st[8 * c + 7]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(C::kStFull));
+      };
+      // the state before the segment
+      const float* in = p.nseg > 1 ? p.carry + (bh * p.nseg + seg) * D * D
+                                   : p.state_in != nullptr ? p.state_in + bh * D * D : nullptr;
+      const bool in_t = p.nseg > 1 ? p.carry_t : p.state_t;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) st[c] = 0.f;
+      if (in != nullptr && row < D) {
+        if (in_t) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) st[c] = in[(long long)(hf * kCols + c) * D + row];
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols / 4; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(in + (long long)row * D + hf * kCols + 4 * c);
+            st[4 * c] = x.x, st[4 * c + 1] = x.y, st[4 * c + 2] = x.z, st[4 * c + 3] = x.w;
+          }
+        }
+      }
+      if (nt > 0) publish();
+      Decay decay = decay_over(kC, ln);
+      for (int it = 0; it < n_upd; ++it) {
+        const int s = it & 1, n = run.tokens(run.a + it);
+        // the scores have read k; its scaled form replaces it
+        ok = __all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 8) && wait(C::kFullK + s, (it / 2) & 1u, 8));
+        if (!ok) break;
+        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes, base + C::kRestOff, C::kTileBytes, nullptr, tid, n, 1.f,
+                                 rev ? w_tab : w_tab + kC - n);
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::kKwFull));
+        ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 8));
+        if (!ok) break;
+        tc_fence_after();
+        if (n != kC) decay = decay_over(n, ln);
+        const float2 hi = make_float2(decay.hi, decay.hi), lo = make_float2(decay.lo, decay.lo);
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 16) {
+          uint32_t x[16];
+          tmem_ld16(lane_off + C::kUpd + hf * kCols + c0, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float2 s2 = make_float2(st[c0 + c], st[c0 + c + 1]);
+            const float2 r = __fadd2_rn(__ffma2_rn(s2, hi, __fmul2_rn(s2, lo)),
+                                        make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+            st[c0 + c] = r.x;
+            st[c0 + c + 1] = r.y;
+          }
+        }
+        if (n != kC) decay = decay_over(kC, ln);
+        if (it + 1 < nt) publish();
+      }
+      // an aborted CTA stores no state; its outputs are not valid either
+      if (ok && !*abort_flag && p.state_out != nullptr && row < D) {
+        float* out = p.state_out + bh * D * D;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          st[c] = in_t ? in[(long long)(hf * kCols + c) * D + row] : in[(long long)row * D + hf * kCols + c];
-      }
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        out[p.state_t ? (long long)(hf * kCols + c) * D + row : (long long)row * D + hf * kCols + c] = st[c];
-    }
-    // tiles of the segment without a live token
-    for (int r = run.r0; r < run.r1; ++r) {
-      if (r >= run.a && r < run.b) continue;
-      const int t0 = run.tile(r) * kC, rows = min(kC, p.L - t0);
-      for (int i = tid; i < rows * (D / 8); i += 256) {
-        const long long e = (((long long)b * p.L + t0 + i / (D / 8)) * p.H + h) * D + i % (D / 8) * 8;
-        *reinterpret_cast<uint4*>(p.o + e) = make_uint4(0u, 0u, 0u, 0u);
+          out[p.state_t ? (long long)(hf * kCols + c) * D + row : (long long)row * D + hf * kCols + c] = st[c];
       }
     }
   }
@@ -602,27 +655,36 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   }
 }
 
-// A segment's own contribution to the state after it: the tiles' updates with
-// the decays to the segment's end, accumulated in TMEM over the segment.
-template <int D_>
+// A segment's own contribution to the state after it: its tokens' updates with
+// the decays to the segment's end, accumulated in TMEM over the segment, 64
+// tokens at a time.  Nothing but the loads and the scaling of k runs per
+// step, so the loads are kept many steps ahead.
+template <int D_, int TERMS_>
 struct SegCfg {
-  static constexpr int D = D_;
+  static constexpr int D = D_, TERMS = TERMS_;
+  static constexpr int kRows = 64;
   static constexpr int kBoxes = D / 64;
-  static constexpr uint32_t kBoxBytes = kC * 128u;
+  static constexpr uint32_t kBoxBytes = kRows * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
-  static constexpr int kStages = 2;
-  static constexpr uint32_t kStageBytes = 3 * kTileBytes;  // k (scaled in place), its rest, v
-  static constexpr uint32_t kBarOff = kStages * kStageBytes;
-  static constexpr int kFull = 0, kScaled = 2, kEmpty = 4, kFinal = 6, kDrain = 7, kNumBars = 8;
+  static constexpr int kStages = TERMS == 3 ? 5 : 6;
+  static constexpr uint32_t kStageBytes = 2 * kTileBytes;                   // k (scaled in place), v
+  static constexpr uint32_t kRestOff = kStages * kStageBytes;               // [2][TERMS - 1]
+  static constexpr uint32_t kRestBytes = (TERMS - 1) * kTileBytes;
+  static constexpr uint32_t kPadOff = kRestOff + 2 * kRestBytes;            // D = 64: behind the last A operand
+  static constexpr uint32_t kBarOff = kPadOff + (D == 64 ? kTileBytes : 0);
+  static constexpr int kFull = 0, kEmpty = kStages, kScaled = 2 * kStages, kFinal = kScaled + 2, kDrain = kFinal + 1,
+                       kNumBars = kDrain + 1;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kSmemBytes = kMiscOff + 16 + 1024;
+  static constexpr uint32_t kTabOff = kMiscOff + 16;                        // decay powers of k
+  static constexpr uint32_t kSmemBytes = kTabOff + 4 * kRows + 1024;
   static constexpr int kThreads = 320;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-template <int D>
-__global__ void __launch_bounds__(SegCfg<D>::kThreads, 1)
+template <int D, int TERMS>
+__global__ void __launch_bounds__(SegCfg<D, TERMS>::kThreads, 1)
 decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
-  using C = SegCfg<D>;
+  using C = SegCfg<D, TERMS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
@@ -649,11 +711,15 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   griddep_wait();
   const Run run(p, b, seg);
   const float ld2 = decay_ln(p.log_decay, h) * kLog2e;
+  float* w_tab = reinterpret_cast<float*>(base + C::kTabOff);  // factor of k row j of a full step next to the end
+  if (threadIdx.x < C::kRows)
+    w_tab[threadIdx.x] = p.kv_mul * ex2((float)(p.reverse ? (int)threadIdx.x + 1 : C::kRows - 1 - (int)threadIdx.x) * ld2);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int nt = run.b - run.a;
+  const int first = run.first(), count = run.count();
+  const int nt = (count + C::kRows - 1) / C::kRows;
   auto wait = [&](int i, uint32_t parity, unsigned site) {
     return wait_bounded(bar(i), parity, abort_flag, site, p.err_word);
   };
@@ -661,19 +727,20 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     if (lane == 0) {
       int issued = 0;
       for (int it = 0; it < nt; ++it) {
-        const int s = it & 1, row = run.tile(run.a + it) * kC;
-        if (it >= 2 && !wait(C::kEmpty + s, (it / 2 - 1) & 1u, 9)) break;
-        mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kTileBytes);
+        const int s = it % C::kStages;
+        if (it >= C::kStages && !wait(C::kEmpty + s, (it / C::kStages - 1) & 1u, 9)) break;
+        mbar_arrive_expect_tx(bar(C::kFull + s), C::kStageBytes);
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx) {
           const uint32_t dst = base_u32 + s * C::kStageBytes + bx * C::kBoxBytes;
-          tma_load_4d(dst, &p.k_map, bar(C::kFull + s), bx * 64, row, h, b);
-          tma_load_4d(dst + 2 * C::kTileBytes, &p.v_map, bar(C::kFull + s), bx * 64, row, h, b);
+          tma_load_4d(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + it * C::kRows, h, b);
+          tma_load_4d(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + it * C::kRows, h, b);
         }
         ++issued;
       }
       if (*abort_flag)
-        for (int i = max(0, issued - 2); i < issued; ++i) wait_drain(bar(C::kFull + (i & 1)), (i / 2) & 1u, p.err_word);
+        for (int i = max(0, issued - C::kStages); i < issued; ++i)
+          wait_drain(bar(C::kFull + i % C::kStages), (i / C::kStages) & 1u, p.err_word);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -682,17 +749,18 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     auto at = [](uint64_t d, uint32_t off) { return make_desc((uint32_t)d + (off >> 4), (uint32_t)(d >> 32)); };
     bool ok = true;
     for (int it = 0; it < nt; ++it) {
-      const int s = it & 1;
-      ok = __all_sync(0xffffffffu, wait(C::kScaled + s, (it / 2) & 1u, 13) && wait(C::kFull + s, (it / 2) & 1u, 13));
+      const int s = it % C::kStages;
+      ok = __all_sync(0xffffffffu, wait(C::kScaled + (it & 1), (it / 2) & 1u, 13) &&
+                                       wait(C::kFull + s, (it / C::kStages) & 1u, 13));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t k = s * C::kStageBytes, v = k + 2 * C::kTileBytes;
+      const uint32_t k = s * C::kStageBytes, v = k + C::kTileBytes, rest = C::kRestOff + (it & 1) * C::kRestBytes;
 #pragma unroll
-      for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ss_e(tmem, at(mn, k + kk * 2048u), at(mn, v + kk * 2048u), id_u, it > 0 || kk > 0);
+      for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-      for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ss_e(tmem, at(mn, k + C::kTileBytes + kk * 2048u), at(mn, v + kk * 2048u), id_u, 1u);
+        for (int kk = 0; kk < C::kRows / 16; ++kk)
+          mma_ss_e(tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u), at(mn, v + kk * 2048u), id_u,
+                   it > 0 || t > 0 || kk > 0);
       mma_commit_e(bar(C::kEmpty + s));
     }
     mma_commit_e(bar(ok ? C::kFinal : C::kDrain));
@@ -701,17 +769,21 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   } else {
     const int tid = threadIdx.x - 64, hf = (warp - 2) >> 2, quad = warp & 3, row = quad * 32 + lane;
     constexpr int kCols = D / 2;
-    const int first = run.first(), end = first + run.count();
     bool ok = true;
     for (int it = 0; it < nt; ++it) {
-      const int s = it & 1, t0 = run.tile(run.a + it) * kC;
-      ok = __all_sync(0xffffffffu, wait(C::kFull + s, (it / 2) & 1u, 15));
+      const int s = it % C::kStages, t0 = it * C::kRows;  // from the segment's first token
+      ok = __all_sync(0xffffffffu, wait(C::kFull + s, (it / C::kStages) & 1u, 15));
+      // the parts' tiles are free once the step before the last has been multiplied
+      if (ok && it >= 2)
+        ok = __all_sync(0xffffffffu, wait(C::kEmpty + (it - 2) % C::kStages, ((it - 2) / C::kStages) & 1u, 15));
       if (!ok) break;
       uint8_t* k = base + s * C::kStageBytes;
-      scale_rows<D>(k, k + C::kTileBytes, k + 2 * C::kTileBytes, tid, run.tokens(run.a + it), p.kv_mul, ld2,
-                    p.reverse ? t0 - first + 1 : end - 1 - t0, p.reverse ? 1 : -1);
+      const int after = count - t0 - C::kRows;  // tokens behind the step (forward); missing ones if negative
+      scale_rows<D, C::kRows, TERMS>(k, base + C::kRestOff + (it & 1) * C::kRestBytes, C::kTileBytes, k + C::kTileBytes,
+                                     tid, count - t0, ex2((float)(p.reverse ? t0 : max(after, 0)) * ld2),
+                                     p.reverse ? w_tab : w_tab + max(-after, 0));
       fence_proxy_async_smem();
-      mbar_arrive(bar(C::kScaled + s));
+      mbar_arrive(bar(C::kScaled + (it & 1)));
     }
     if (ok) ok = __all_sync(0xffffffffu, wait(C::kFinal, 0, 15));
     ok = ok && !*abort_flag;
@@ -745,27 +817,49 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
 }
 
 // Chains the segments' contributions, in place, into the state before every
-// segment; the state after the last goes to state_out.  One thread per element.
+// segment; the state after the last goes to state_out.  One thread per four
+// elements; the contributions are fetched kAhead segments ahead.
 template <int D>
-__global__ void __launch_bounds__(256) decay_carry_kernel(const __grid_constant__ DecayTileParams p) {
+__global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayTileParams p) {
+  constexpr int kAhead = 8, kBlocks = D * D / 512;
   griddep_launch_dependents();
   griddep_wait();
-  const long long bh = blockIdx.x / (D * D / 256);
-  const int e = (int)(blockIdx.x % (D * D / 256)) * 256 + threadIdx.x;
+  const long long bh = blockIdx.x / kBlocks;
+  const int e = ((int)(blockIdx.x % kBlocks) * 128 + threadIdx.x) * 4;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   const float ln = decay_ln(p.log_decay, h);
-  const int e_io = p.state_t ? (e % D) * D + e / D : e;  // the caller's orientation
-  float s = p.state_in != nullptr ? p.state_in[bh * D * D + e_io] : 0.f;
-  float* c = p.carry + bh * p.nseg * D * D + e;
   const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
-  float next = nrun > 0 ? c[0] : 0.f;
-  for (int seg = 0; seg < p.nseg; ++seg) {
-    const float add = next;
-    if (seg + 1 < nrun) next = c[(long long)(seg + 1) * D * D];
-    c[(long long)seg * D * D] = s;
-    if (seg < nrun) s = Decay((float)Run(p, b, seg).count() * ln)(s) + add;
+  float* c = p.carry + bh * p.nseg * D * D + e;
+  // the caller's orientation: element (r, col) of a run may be held at (col, r)
+  const int step = p.state_t ? D : 1;
+  const long long io = bh * D * D + (p.state_t ? (e % D) * D + e / D : e);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.state_in != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = p.state_in[io + i * step];
   }
-  if (p.state_out != nullptr) p.state_out[bh * D * D + e_io] = s;
+  float4 add[kAhead];
+  for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (s0 + i < nrun) add[i] = *reinterpret_cast<const float4*>(c + (long long)(s0 + i) * D * D);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i >= p.nseg) break;
+      *reinterpret_cast<float4*>(c + (long long)(s0 + i) * D * D) = make_float4(s[0], s[1], s[2], s[3]);
+      if (s0 + i < nrun) {
+        const Decay decay((float)Run(p, b, s0 + i).count() * ln);
+        s[0] = decay(s[0]) + add[i].x;
+        s[1] = decay(s[1]) + add[i].y;
+        s[2] = decay(s[2]) + add[i].z;
+        s[3] = decay(s[3]) + add[i].w;
+      }
+    }
+  }
+  if (p.state_out != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.state_out[io + i * step] = s[i];
+  }
 }
 
 template <typename P>
@@ -783,38 +877,52 @@ cudaError_t launch(void (*kernel)(P), unsigned grid, unsigned threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int D>
-cudaError_t launch_tiles(const DecayTileParams& p, cudaStream_t s) {
-  static std::atomic<unsigned long long> ready{0};  // devices whose kernels have their shared-memory limit raised
+// Raises a kernel's shared-memory limit, once per device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<unsigned long long>& ready) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev <= 63 && (ready.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev <= 63) ready.fetch_or(1ull << dev);
+  return e;
+}
+
+template <int D, int TERMS>
+cudaError_t launch_segments(const DecayTileParams& p, cudaStream_t s) {
+  using C = SegCfg<D, TERMS>;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem(decay_segment_kernel<D, TERMS>, C::kSmemBytes, ready);
   if (e != cudaSuccess) return e;
-  if (dev > 63 || !(ready.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(decay_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)TileCfg<D>::kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decay_segment_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)SegCfg<D>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(1ull << dev);
-  }
   const long long bh = (long long)p.B * p.H;
-  DecayTileParams q = p;
-  if (p.nseg > 1) {
-    const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
-    e = launch(decay_segment_kernel<D>, (unsigned)(bh * nrun), SegCfg<D>::kThreads, SegCfg<D>::kSmemBytes, p, s);
-    if (e != cudaSuccess) return e;
-    e = launch(decay_carry_kernel<D>, (unsigned)(bh * (D * D / 256)), 256, 0, p, s);
-    if (e != cudaSuccess) return e;
-    q.state_out = nullptr;  // written by the carry kernel
-  }
-  return launch(decay_tile_kernel<D>, (unsigned)(bh * p.nseg), TileCfg<D>::kThreads, TileCfg<D>::kSmemBytes, q, s);
+  const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
+  e = launch(decay_segment_kernel<D, TERMS>, (unsigned)(bh * nrun), C::kThreads, C::kSmemBytes, p, s);
+  if (e != cudaSuccess) return e;
+  return launch(decay_carry_kernel<D>, (unsigned)(bh * (D * D / 512)), 128, 0, p, s);
+}
+
+template <int D, int TERMS>
+cudaError_t launch_tiles(const DecayTileParams& p, cudaStream_t s) {
+  using C = TileCfg<D, TERMS>;
+  static std::atomic<unsigned long long> ready{0};
+  const cudaError_t e = allow_smem(decay_tile_kernel<D, TERMS>, C::kSmemBytes, ready);
+  if (e != cudaSuccess) return e;
+  return launch(decay_tile_kernel<D, TERMS>, (unsigned)((long long)p.B * p.H * p.nseg), C::kThreads, C::kSmemBytes, p,
+                s);
 }
 
 }  // namespace
 
+// k enters a state that the caller gets as three bf16 parts (24 bits), a state
+// that only feeds bf16 outputs as two (16 bits).
+cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s) {
+  if (p.state_out != nullptr) return p.D == 128 ? launch_segments<128, 3>(p, s) : launch_segments<64, 3>(p, s);
+  return p.D == 128 ? launch_segments<128, 2>(p, s) : launch_segments<64, 2>(p, s);
+}
+
 cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s) {
-  return p.D == 128 ? launch_tiles<128>(p, s) : launch_tiles<64>(p, s);
+  if (p.state_out != nullptr) return p.D == 128 ? launch_tiles<128, 3>(p, s) : launch_tiles<64, 3>(p, s);
+  return p.D == 128 ? launch_tiles<128, 2>(p, s) : launch_tiles<64, 2>(p, s);
 }
 
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s) {

@@ -932,6 +932,8 @@ size_t sab_decay_attention_workspace(int B, int L, int H, int D) {
   return n == 1 ? 0 : align_up((size_t)B * H * n * D * D * sizeof(float), kAlign);
 }
 
+// One run of the recurrence.  chain: work out the states before the segments
+// first; otherwise the workspace holds them from the run before, transposed.
 struct DecayRun {
   const void *q, *k, *v;
   void* o;
@@ -939,13 +941,19 @@ struct DecayRun {
   float* out;
   int reverse, state_t;
   float kv_mul, o_mul;
+  bool chain;
 };
 static sab_status decay_run(const DecayRun& r, const float* log_decay, const int* seq_len, int B, int L, int H, int D,
                             void* workspace, void* stream) {
   DecayTileParams p;
   memset(&p, 0, sizeof(p));
+  p.seg_tiles = decay_segment_tiles(B, L, H);
+  p.nseg = decay_segments(B, L, H);
+  const bool sums = p.nseg > 1 && r.chain;
   if (!encode_token_major(&p.q_map, r.q, B, L, H, D) || !encode_token_major(&p.k_map, r.k, B, L, H, D) ||
-      !encode_token_major(&p.v_map, r.v, B, L, H, D) || !encode_token_major(&p.o_map, r.o, B, L, H, D))
+      !encode_token_major(&p.v_map, r.v, B, L, H, D) || !encode_token_major(&p.o_map, r.o, B, L, H, D) ||
+      (sums && (!encode_token_major(&p.k_map_h, r.k, B, L, H, D, 64) ||
+                !encode_token_major(&p.v_map_h, r.v, B, L, H, D, 64))))
     return SAB_ERR_CUDA;
   p.o = static_cast<uint16_t*>(r.o);
   p.log_decay = log_decay;
@@ -953,18 +961,20 @@ static sab_status decay_run(const DecayRun& r, const float* log_decay, const int
   p.state_in = r.in;
   p.state_out = r.out;
   p.carry = static_cast<float*>(workspace);
+  p.carry_t = !r.chain;
   p.B = B;
   p.L = L;
   p.H = H;
   p.D = D;
-  p.seg_tiles = decay_segment_tiles(B, L, H);
-  p.nseg = decay_segments(B, L, H);
   p.reverse = r.reverse;
   p.state_t = r.state_t;
   p.kv_mul = r.kv_mul;
   p.o_mul = r.o_mul;
   p.err_word = device_error_word();
-  return launch_decay_tiles(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (sums && launch_decay_segments(p, s) != cudaSuccess) return SAB_ERR_CUDA;
+  if (p.nseg > 1) p.state_out = nullptr;  // written with the segments' states
+  return launch_decay_tiles(p, s) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 
 sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -981,7 +991,7 @@ sab_status sab_decay_attention(const void* Q, const void* K, const void* V, cons
   const size_t need = sab_decay_attention_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale}, log_decay, seq_len, B, L, H, D, workspace,
+  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, true}, log_decay, seq_len, B, L, H, D, workspace,
                    stream);
 }
 
@@ -1035,10 +1045,13 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   const size_t need = sab_decay_attention_backward_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  // d_state_in (which may be d_state_out) is written by the last run
-  const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale},
-                            {V, dO, Q, dK, d_state_out, nullptr, 1, 1, scale, 1.f},
-                            {K, Q, dO, dV, d_state_out, d_state_in, 1, 0, scale, 1.f}};
+  // dV before dK: one chain of states serves both (dK's run holds them
+  // transposed).  d_state_in, which may be d_state_out, is written by the last
+  // run to read d_state_out: with the chain, or else by dK's run.
+  const bool cut = decay_segments(B, L, H) > 1;
+  const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale, true},
+                            {K, Q, dO, dV, d_state_out, cut ? d_state_in : nullptr, 1, 0, scale, 1.f, true},
+                            {V, dO, Q, dK, d_state_out, cut ? nullptr : d_state_in, 1, 1, scale, 1.f, false}};
   for (const DecayRun& r : runs) {
     const sab_status st = decay_run(r, log_decay, seq_len, B, L, H, D, workspace, stream);
     if (st != SAB_OK) return st;

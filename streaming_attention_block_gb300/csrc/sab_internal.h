@@ -237,12 +237,14 @@ struct RotaryParams {
 // reversed in time, S += (kv_mul k) v^T, o = o_mul q S, then S *= g.
 struct DecayTileParams {
   CUtensorMap q_map, k_map, v_map, o_map;  // dims (D, L, H, B), box (64, 128, 1, 1), SW128
+  CUtensorMap k_map_h, v_map_h;            // the same with 64-row boxes (segment sums)
   uint16_t* o;              // tiles without a live token are zeroed directly
   const float* log_decay;   // [H]
   const int* seq_len;       // [B] or null
   const float* state_in;    // [B, H, D, D] or null
   float* state_out;         // or null
   float* carry;             // [B, H, nseg, D, D] scratch when nseg > 1
+  int carry_t;              // the carried states are [v dimension][k dimension]
   int B, L, H, D;
   int nseg, seg_tiles;      // segments per sequence, 128-token tiles per segment
   int reverse;
@@ -272,6 +274,10 @@ cudaError_t launch_counter_add(long long* counter, long long delta, cudaStream_t
 cudaError_t launch_qk_rope(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_attention_backward(const BwdParams& p, cudaStream_t s);
 cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
+// the state before every segment, into p.carry (nseg > 1); the state after the
+// last, if p.state_out is given
+cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s);
+// the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);

@@ -121,7 +121,9 @@ def test_forward(case, with_state):
         for b, n in enumerate(lens):
             assert not bool(O[b, min(max(n, 0), L):].any())
     O2, none = _forward(q, k, v, ld, D ** -0.5, S, dl, want_state=False)
-    assert torch.equal(O2, O) and none is None
+    # (k enters a state that nobody asked for with 16 bits instead of 24: other bits, same bounds)
+    _check(O2, o, oa, "O without state_out")
+    assert none is None
     if with_state:
         O3, S3 = _forward(q, k, v, ld, D ** -0.5, S, dl, inplace=True)
         assert torch.equal(O3, O) and torch.equal(S3, So)
