@@ -269,6 +269,13 @@ __device__ __noinline__ void zero_rows(uint8_t* v, int tid, int n) {
     *reinterpret_cast<uint4*>(v + piece_off<kC>(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// One arrival per warp, after its lanes' writes (each lane fences its own): 32
+// arrivals on one word cost as much as the work they report.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-major
 
 // The tile kernel's warps: 0 loads, 1 issues MMAs, 2-9 ("rows") turn scores
@@ -331,7 +338,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     for (int i = 0; i < C::kNumBars; ++i)
       mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kORead || i == C::kStFull || i == C::kOut ||
                                 i == C::kOut + 1
-                            ? 256
+                            ? 8
                             : 1);
     misc[1] = 0;
     fence_mbar_init();
@@ -528,7 +535,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(bar(C::kPFull));
+        warp_arrive(bar(C::kPFull), lane);
         // output rows
         const float f = p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2);
         ok = __all_sync(0xffffffffu, wait(C::kOFull, it & 1u, 15));
@@ -550,7 +557,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
           }
         }
         tc_fence_before();
-        mbar_arrive(bar(C::kORead));
+        warp_arrive(bar(C::kORead), lane);
         if (it < n_upd) {  // v is free once the update has read it
           ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 15));
           if (!ok) break;
@@ -560,7 +567,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
           *reinterpret_cast<uint4*>(vt + piece(c, C::kBoxBytes)) =
               make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::kOut + sv));
+        warp_arrive(bar(C::kOut + sv), lane);
       }
       // tiles of the segment without a live token
       for (int r = run.r0; r < run.r1; ++r) {
@@ -585,7 +592,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(C::kStFull));
+        warp_arrive(bar(C::kStFull), lane);
       };
       // the state before the segment
       const float* in = p.nseg > 1 ? p.carry + (bh * p.nseg + seg) * D * D
@@ -615,7 +622,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes, base + C::kRestOff, C::kTileBytes, nullptr, tid, n, 1.f,
                                  rev ? w_tab : w_tab + kC - n);
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::kKwFull));
+        warp_arrive(bar(C::kKwFull), lane);
         ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 8));
         if (!ok) break;
         tc_fence_after();
@@ -677,7 +684,7 @@ struct SegCfg {
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kTabOff = kMiscOff + 16;                        // decay powers of k
   static constexpr uint32_t kSmemBytes = kTabOff + 4 * kRows + 1024;
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = 576;  // loads, MMA, two groups of 8 warps that scale every other step
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
@@ -698,7 +705,7 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   const long long bh = blockIdx.x / nrun;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), i == C::kScaled || i == C::kScaled + 1 ? 256 : 1);
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), i == C::kScaled || i == C::kScaled + 1 ? 8 : 1);
     misc[1] = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -720,6 +727,9 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   const uint32_t tmem = misc[0];
   const int first = run.first(), count = run.count();
   const int nt = (count + C::kRows - 1) / C::kRows;
+  // against the run's order, so that the tokens the run starts with are the
+  // ones L2 still holds
+  auto start = [&](int it) { return (p.reverse ? it : nt - 1 - it) * C::kRows; };
   auto wait = [&](int i, uint32_t parity, unsigned site) {
     return wait_bounded(bar(i), parity, abort_flag, site, p.err_word);
   };
@@ -733,8 +743,8 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx) {
           const uint32_t dst = base_u32 + s * C::kStageBytes + bx * C::kBoxBytes;
-          tma_load_4d(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + it * C::kRows, h, b);
-          tma_load_4d(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + it * C::kRows, h, b);
+          tma_load_4d(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b);
+          tma_load_4d(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b);
         }
         ++issued;
       }
@@ -767,25 +777,27 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     if (!ok && lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
     __syncwarp();
   } else {
-    const int tid = threadIdx.x - 64, hf = (warp - 2) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const int grp = (warp - 2) >> 3, tid = (threadIdx.x - 64) & 255, hf = ((warp - 2) >> 2) & 1, quad = warp & 3;
+    const int row = quad * 32 + lane;
     constexpr int kCols = D / 2;
     bool ok = true;
-    for (int it = 0; it < nt; ++it) {
-      const int s = it % C::kStages, t0 = it * C::kRows;  // from the segment's first token
+    for (int it = grp; it < nt; it += 2) {
+      const int s = it % C::kStages, t0 = start(it);  // from the segment's first token
       ok = __all_sync(0xffffffffu, wait(C::kFull + s, (it / C::kStages) & 1u, 15));
-      // the parts' tiles are free once the step before the last has been multiplied
+      // the parts' tiles are free once the group's previous step has been multiplied
       if (ok && it >= 2)
         ok = __all_sync(0xffffffffu, wait(C::kEmpty + (it - 2) % C::kStages, ((it - 2) / C::kStages) & 1u, 15));
       if (!ok) break;
       uint8_t* k = base + s * C::kStageBytes;
       const int after = count - t0 - C::kRows;  // tokens behind the step (forward); missing ones if negative
-      scale_rows<D, C::kRows, TERMS>(k, base + C::kRestOff + (it & 1) * C::kRestBytes, C::kTileBytes, k + C::kTileBytes,
-                                     tid, count - t0, ex2((float)(p.reverse ? t0 : max(after, 0)) * ld2),
+      scale_rows<D, C::kRows, TERMS>(k, base + C::kRestOff + grp * C::kRestBytes, C::kTileBytes, k + C::kTileBytes, tid,
+                                     count - t0, ex2((float)(p.reverse ? t0 : max(after, 0)) * ld2),
                                      p.reverse ? w_tab : w_tab + max(-after, 0));
       fence_proxy_async_smem();
-      mbar_arrive(bar(C::kScaled + (it & 1)));
+      warp_arrive(bar(C::kScaled + grp), lane);
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait(C::kFinal, 0, 15));
+    if (ok && grp == 0) ok = __all_sync(0xffffffffu, wait(C::kFinal, 0, 15));
+    ok = ok && grp == 0;
     ok = ok && !*abort_flag;
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();

@@ -86,7 +86,50 @@ __global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const __grid_consta
   const long long tok0 = (long long)blockIdx.x * p.tokens;
   const int ntok = (int)min((long long)p.tokens, tokens - tok0);
   const int heads = p.rows[0].heads + p.rows[1].heads;
+  const int unit = (int)threadIdx.x % p.units, group = (int)threadIdx.x / p.units;
+  const int groups = (int)blockDim.x / p.units;
   ptx::griddep_wait();
+
+  // this thread's rows: (token, head) = (k, h), stepping by `groups` heads
+  struct Item {
+    const T* in;
+    T* out;
+    int k;
+  };
+  int k_next = group / heads, h_next = group - k_next * heads;
+  auto next_row = [&]() {
+    Item r{nullptr, nullptr, k_next};
+    if (k_next < ntok) {
+      const long long tok = tok0 + k_next;
+      const long long b = p.B == 1 ? 0 : tok / p.L, t = tok - b * p.L;
+      const int w = h_next >= p.rows[0].heads;
+      const int h = w ? h_next - p.rows[0].heads : h_next;
+      const RotaryRows& x = p.rows[w];
+      r.in = static_cast<const T*>(x.in) + b * x.in_batch + t * x.in_token + (long long)h * p.D;
+      r.out = static_cast<T*>(x.out) + b * x.out_batch + t * x.out_token + (long long)h * p.D;
+      h_next += groups;
+      while (h_next >= heads) h_next -= heads, ++k_next;
+    }
+    return r;
+  };
+
+  // element offset of the unit's first vector; a kHalfVec pair unit's second
+  // vector lies `half` elements further
+  const bool pairs = M == kHalfVec && unit < half / N;
+  const int e0 = (M == kHalfVec && !pairs) ? unit * N + half : unit * N;
+  Item row[kBatch];
+  uint4 va[kBatch], vb[kBatch];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      row[u] = next_row();
+      if (M != kHalfScalar && row[u].in != nullptr) {
+        va[u] = *reinterpret_cast<const uint4*>(row[u].in + e0);
+        if (pairs) vb[u] = *reinterpret_cast<const uint4*>(row[u].in + e0 + half);
+      }
+    }
+  };
+  fetch();  // in flight while the angles are worked out
 
   // sine and cosine of every (token, pair)
   for (int i = threadIdx.x; i < ntok * half; i += blockDim.x) {
@@ -101,76 +144,40 @@ __global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const __grid_consta
   }
   __syncthreads();
 
-  const int unit = (int)threadIdx.x % p.units, group = (int)threadIdx.x / p.units;
-  const int groups = (int)blockDim.x / p.units;
-  if (group >= groups) return;
-  const int items = ntok * heads;
-  auto row_of = [&](int item, const T*& in, T*& out, int& k) {
-    k = item / heads;
-    int h = item - k * heads;
-    const long long tok = tok0 + k;
-    const long long b = tok / p.L, t = tok - b * p.L;
-    const int w = h >= p.rows[0].heads;
-    if (w) h -= p.rows[0].heads;
-    const RotaryRows& r = p.rows[w];
-    in = static_cast<const T*>(r.in) + b * r.in_batch + t * r.in_token + (long long)h * p.D;
-    out = static_cast<T*>(r.out) + b * r.out_batch + t * r.out_token + (long long)h * p.D;
-  };
-
-  if constexpr (M == kHalfScalar) {
-    for (int item = group; item < items; item += groups) {
-      const T* in;
-      T* out;
-      int k;
-      row_of(item, in, out, k);
-      if (unit < half) {
-        float a, b;
-        turn(cs[k * half + unit], V::load(in + unit), V::load(in + unit + half), a, b);
-        V::store(out + unit, a);
-        V::store(out + unit + half, b);
+  while (row[0].in != nullptr) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (row[u].in == nullptr) break;
+      const float2* c = cs + row[u].k * half;
+      if constexpr (M == kHalfScalar) {
+        const T* in = row[u].in;
+        T* out = row[u].out;
+        if (unit < half) {
+          float x, y;
+          turn(c[unit], V::load(in + unit), V::load(in + unit + half), x, y);
+          V::store(out + unit, x);
+          V::store(out + unit + half, y);
+        } else {
+          out[unit + half] = in[unit + half];
+        }
       } else {
-        out[unit + half] = in[unit + half];
+        float a[N];
+        V::unpack(va[u], a);
+        if constexpr (M == kInterleaved) {
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j)
+            if (e0 + 2 * j < p.dims) turn(c[e0 / 2 + j], a[2 * j], a[2 * j + 1], a[2 * j], a[2 * j + 1]);
+        } else if (pairs) {
+          float b[N];
+          V::unpack(vb[u], b);
+#pragma unroll
+          for (int j = 0; j < N; ++j) turn(c[e0 + j], a[j], b[j], a[j], b[j]);
+          *reinterpret_cast<uint4*>(row[u].out + e0 + half) = V::pack(b);
+        }
+        *reinterpret_cast<uint4*>(row[u].out + e0) = V::pack(a);
       }
     }
-    return;
-  }
-
-  // element offset of the unit's first vector; a kHalfVec pair unit's second
-  // vector lies `half` elements further
-  const bool pairs = M == kHalfVec && unit < half / N;
-  const int e0 = (M == kHalfVec && !pairs) ? unit * N + half : unit * N;
-  for (int item = group; item < items; item += kBatch * groups) {
-    const T* in[kBatch];
-    T* out[kBatch];
-    int k[kBatch];
-    uint4 va[kBatch], vb[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (item + u * groups < items) {
-        row_of(item + u * groups, in[u], out[u], k[u]);
-        va[u] = *reinterpret_cast<const uint4*>(in[u] + e0);
-        if (pairs) vb[u] = *reinterpret_cast<const uint4*>(in[u] + e0 + half);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (item + u * groups >= items) break;
-      float a[N];
-      V::unpack(va[u], a);
-      const float2* c = cs + k[u] * half;
-      if constexpr (M == kInterleaved) {
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j)
-          if (e0 + 2 * j < p.dims) turn(c[e0 / 2 + j], a[2 * j], a[2 * j + 1], a[2 * j], a[2 * j + 1]);
-      } else if (pairs) {
-        float b[N];
-        V::unpack(vb[u], b);
-#pragma unroll
-        for (int j = 0; j < N; ++j) turn(c[e0 + j], a[j], b[j], a[j], b[j]);
-        *reinterpret_cast<uint4*>(out[u] + e0 + half) = V::pack(b);
-      }
-      *reinterpret_cast<uint4*>(out[u] + e0) = V::pack(a);
-    }
+    fetch();
   }
 }
 
@@ -182,13 +189,16 @@ cudaError_t launch(RotaryParams& p, cudaStream_t s) {
   const int threads = p.units > kMaxThreads ? kMaxThreads : kMaxThreads / p.units * p.units;
   const int heads = p.rows[0].heads + p.rows[1].heads, groups = threads / p.units;
   const long long tokens = (long long)p.B * p.L;
-  // a block takes the tokens that give each thread about one batch of
-  // vectors, but no more than leave a block for every SM
-  long long t = ((long long)kBatch * groups + heads - 1) / heads;
-  t = t > kMaxTokens ? kMaxTokens : t;
-  const long long spread = tokens / 152;
-  t = t > spread ? spread : t;
-  p.tokens = (int)(t < 1 ? 1 : t);
+  // tokens per block: as few whole batches of rows per thread as leave the
+  // fewest idle slots in the last one, but a block for every SM before that
+  int best = 1;
+  double waste = 2.0;
+  for (int t = 1; t <= kMaxTokens && (t == 1 || tokens / t >= 2 * 152); ++t) {
+    const int slots = kBatch * groups, rows = t * heads;
+    const double w = (double)((rows + slots - 1) / slots * slots) / rows;
+    if (w < waste - 0.02) best = t, waste = w;
+  }
+  p.tokens = best;
   const long long blocks = (tokens + p.tokens - 1) / p.tokens;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
