@@ -114,8 +114,8 @@ def _check(status: int, what: str):
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the raw handle of torch.cuda.current_stream(), without building the object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -480,45 +480,74 @@ def rotary_plan(bands, layout: int = ROTARY_INTERLEAVED, base: float = 10000.0, 
     return plan
 
 
-def _on_current_device(t, name):
-    if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _refuse(t, name, dev, dtypes, shape=None):
+    """Raise what is wrong with a tensor argument that failed its check."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
-def _rotary_rows(x, out, name):
+def _device():
+    """Index of the current device (-2: there is none, so no tensor is on it)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _arg(t, shape, dtype, name, dev):
+    """Device pointer of a contiguous tensor of this shape and type on the
+    current device ``dev`` (None and raw pointers pass through)."""
+    if t is None or t.__class__ is int:
+        return t
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or \
+            not t.is_contiguous():
+        _refuse(t, name, dev, (dtype,), shape)
+    return t.data_ptr()
+
+
+def _rotary_rows(x, out, name, dev):
     """Token rows of ``x`` and ``out`` ([B, L, H, D] with contiguous heads)."""
     for t, n in ((x, name), (out, name + "_out")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise TypeError(f"{n}: expected a [B, L, H, D] torch tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{n}: must be a CUDA tensor")
-        _on_current_device(t, n)
-        if t.dtype not in _DTYPES:
-            raise ValueError(f"{n}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
-        if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
-            raise ValueError(f"{n}: a token's heads must be contiguous")
+        if t.get_device() != dev or t.dtype not in _DTYPES:
+            _refuse(t, n, dev, tuple(_DTYPES))
+    B, L, H, D = x.shape
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{name}_out: expected the shape and type of {name}")
-    B, L, H, D = x.shape
-    st = [t.stride(d) if t.shape[d] > 1 else H * D for t in (x, out) for d in (0, 1)]
+    st = []
+    for t, n in ((x, name), (out, name + "_out")):
+        sb, sl, sh, sd = t.stride()
+        if (sd != 1 and D > 1) or (sh != D and H > 1):
+            raise ValueError(f"{n}: a token's heads must be contiguous")
+        st += [sb if B > 1 else H * D, sl if L > 1 else H * D]
     return RotaryRows(x.data_ptr(), out.data_ptr(), H, *st)
 
 
 def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, stream):
-    q = _rotary_rows(Q, Q_out, "Q")
+    dev = _device()
+    q = _rotary_rows(Q, Q_out, "Q", dev)
     B, L, _, D = Q.shape
     k = None
     if K is not None:
-        k = _rotary_rows(K, K_out, "K")
-        if (K.shape[0], K.shape[1], K.shape[3]) != (B, L, D) or K.dtype != Q.dtype:
+        k = _rotary_rows(K, K_out, "K", dev)
+        if K.shape[0] != B or K.shape[1] != L or K.shape[3] != D or K.dtype != Q.dtype:
             raise ValueError("K: expected Q's batch, length, head dimension and type")
-    if positions is not None:
-        _on_current_device(positions, "positions")
-        if positions.numel() != plan.axes * B * L:
-            raise ValueError("positions: expected int64 [axes, B, L]")
-    _check(fn(ctypes.byref(plan), ctypes.byref(q), None if k is None else ctypes.byref(k),
-              _ptr(positions, torch.int64, "positions"), int(first_position), B, L, D, _DTYPES[Q.dtype],
-              _stream(stream)), what)
+    if positions is not None and positions.__class__ is not int:
+        n = plan.axes * B * L
+        shape = positions.shape if positions.numel() == n else (plan.axes, B, L)
+        positions = _arg(positions, shape, torch.int64, "positions", dev)
+    _check(fn(ctypes.byref(plan), ctypes.byref(q), None if k is None else ctypes.byref(k), positions,
+              int(first_position), B, L, D, _DTYPES[Q.dtype], _stream(stream)), what)
 
 
 def rotary(plan: RotaryPlan, Q, K, Q_out, K_out=None, positions=None, first_position: int = 0, stream=None):
@@ -548,6 +577,15 @@ def decay_attention_backward_workspace(B: int, L: int, H: int, D: int) -> int:
     return int(library().sab_decay_attention_backward_workspace(int(B), int(L), int(H), int(D)))
 
 
+def _workspace(t, dev):
+    """(pointer, bytes) of a workspace tensor on device ``dev``."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "workspace", dev, (t.dtype,))
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _scratch(nbytes, like, stream):
     """``nbytes`` of device scratch for one call on ``stream`` (None: 0 bytes)."""
     if nbytes == 0:
@@ -559,16 +597,6 @@ def _scratch(nbytes, like, stream):
     return mem
 
 
-def _shaped(t, shape, dtype, name):
-    if t is not None and not isinstance(t, int):
-        p = _ptr(t, dtype, name)
-        _on_current_device(t, name)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        return p
-    return _ptr(t, dtype, name)
-
-
 def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_out=None, seq_len=None,
                     workspace=None, stream=None):
     """sab_decay_attention: linear attention of [B, L, H, D] bf16 sequences with
@@ -577,24 +605,26 @@ def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_ou
     B, L, H, D = Q.shape
     if workspace is None:
         workspace = _scratch(decay_attention_workspace(B, L, H, D), Q, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = _device()
+    ws, ws_bytes = _workspace(workspace, dev)
     x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention(
-        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(log_decay, (H,), f4, "log_decay"),
-        _shaped(seq_len, (B,), torch.int32, "seq_len"), _shaped(state_in, st, f4, "state_in"), B, L, H, D,
-        float(scale), _shaped(O, x, bf, "O"), _shaped(state_out, st, f4, "state_out"), _ptr(workspace, None, "workspace"),
-        ws_bytes, _stream(stream)), "decay_attention")
+        _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
+        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev), _arg(state_in, st, f4, "state_in", dev), B, L, H, D,
+        float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes,
+        _stream(stream)), "decay_attention")
 
 
 def decay_attention_step(Q, K, V, log_decay, scale: float, state_in, state_out, O, active=None, stream=None):
     """sab_decay_attention_step: one token [B, H, D] of every sequence;
     ``state_out`` may be ``state_in`` (see include/sab.h)."""
     B, H, D = Q.shape
+    dev = _device()
     x, st, bf, f4 = (B, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention_step(
-        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(log_decay, (H,), f4, "log_decay"),
-        _shaped(active, (B,), torch.int32, "active"), _shaped(state_in, st, f4, "state_in"), B, H, D, float(scale),
-        _shaped(O, x, bf, "O"), _shaped(state_out, st, f4, "state_out"), _stream(stream)), "decay_attention_step")
+        _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
+        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(active, (B,), torch.int32, "active", dev), _arg(state_in, st, f4, "state_in", dev), B, H, D, float(scale),
+        _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), _stream(stream)), "decay_attention_step")
 
 
 def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, state_in=None, d_state_out=None,
@@ -604,14 +634,15 @@ def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, s
     B, L, H, D = Q.shape
     if workspace is None:
         workspace = _scratch(decay_attention_backward_workspace(B, L, H, D), Q, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = _device()
+    ws, ws_bytes = _workspace(workspace, dev)
     x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention_backward(
-        _shaped(Q, x, bf, "Q"), _shaped(K, x, bf, "K"), _shaped(V, x, bf, "V"), _shaped(dO, x, bf, "dO"),
-        _shaped(log_decay, (H,), f4, "log_decay"), _shaped(seq_len, (B,), torch.int32, "seq_len"),
-        _shaped(state_in, st, f4, "state_in"), _shaped(d_state_out, st, f4, "d_state_out"), B, L, H, D, float(scale),
-        _shaped(dQ, x, bf, "dQ"), _shaped(dK, x, bf, "dK"), _shaped(dV, x, bf, "dV"),
-        _shaped(d_state_in, st, f4, "d_state_in"), _ptr(workspace, None, "workspace"), ws_bytes, _stream(stream)),
+        _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev), _arg(dO, x, bf, "dO", dev),
+        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
+        _arg(state_in, st, f4, "state_in", dev), _arg(d_state_out, st, f4, "d_state_out", dev), B, L, H, D, float(scale),
+        _arg(dQ, x, bf, "dQ", dev), _arg(dK, x, bf, "dK", dev), _arg(dV, x, bf, "dV", dev),
+        _arg(d_state_in, st, f4, "d_state_in", dev), ws, ws_bytes, _stream(stream)),
         "decay_attention_backward")
 
 

@@ -4,11 +4,13 @@
 //
 // A block takes a few tokens.  Their sines and cosines (one per token and
 // pair, shared by every head of q and k) are worked out first into shared
-// memory; then every thread moves 16-byte vectors, at a fixed place of the
-// head, over the tokens' heads.  The angle of position p is p * f turns
-// modulo one turn.  f is a 64-bit fraction of a turn, so the product wraps by
-// itself, and its upper 32 bits, as a signed fraction, go to sincospif:
-// exact range reduction for any int64 position without fp64 arithmetic.
+// memory, while the first data loads are in flight; then a thread keeps one
+// token and one place of the head, holds that place's factors in registers
+// and walks over heads: about 30 instructions per 16-byte vector, so that the
+// stream, not the issue slots, sets the pace.  The angle of position p is
+// p * f turns modulo one turn.  f is a 64-bit fraction of a turn, so the
+// product wraps by itself, and its upper 32 bits, as a signed fraction, go to
+// sincospif: exact range reduction for any int64 position without fp64.
 #include "ptx.cuh"
 #include "sab_internal.h"
 
@@ -17,7 +19,6 @@ namespace {
 
 constexpr int kMaxThreads = 256;
 constexpr int kMaxTokens = 8;   // tokens per block
-constexpr int kBatch = 4;       // vectors in flight per thread
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -61,120 +62,148 @@ struct Vec<float> {
   static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 };
 
-__device__ __forceinline__ void turn(float2 cs, float a, float b, float& ra, float& rb) {
-  ra = a * cs.x - b * cs.y;
-  rb = a * cs.y + b * cs.x;
+// (a, b) turned by cs = (cos, sin): two packed products
+__device__ __forceinline__ void turn(float2 cs, float& a, float& b) {
+  const float2 r = __ffma2_rn(make_float2(b, a), make_float2(-cs.y, cs.y),
+                              __fmul2_rn(make_float2(a, b), make_float2(cs.x, cs.x)));
+  a = r.x;
+  b = r.y;
 }
 
 enum Mode { kInterleaved, kHalfVec, kHalfScalar };
+constexpr int kBatch = 4;  // rows in flight per thread
 
 // A head's work is cut into `units`, one per thread column:
 //   kInterleaved  the head's D / N vectors; a vector holds whole pairs
-//   kHalfVec      (dims / 2 a multiple of N) one unit per vector of first
-//                 elements together with its vector of second elements, then
-//                 one per vector behind `dims`
-//   kHalfScalar   one unit per pair, then one per element behind `dims`: the
-//                 halves do not start on a 16-byte boundary
+//   kHalfVec      (dims / 2 a multiple of N) a vector of first elements with
+//                 its vector of second elements; behind `dims`, two vectors
+//   kHalfScalar   one pair, or one element behind `dims`: the halves do not
+//                 start on a 16-byte boundary
+// A block's columns of `units` threads take one token and every p.splits-th
+// head each.
+// (Blocks per SM: four of 64 registers for one vector per row; two vectors per
+// row take 100 registers, and fewer rows in flight cost more than fewer blocks:
+// 4 x 8191 tokens of 32 heads, 89 us with 4 rows and 2 blocks, 102 us with 2
+// and 3, 138 us with 1 and 4.)
 template <typename T, Mode M>
-__global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kMaxThreads, M == kHalfVec ? 2 : 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using V = Vec<T>;
   constexpr int N = V::N;
+  constexpr int kPairs = M == kInterleaved ? N / 2 : M == kHalfVec ? N : 1;  // pairs of a unit
   __shared__ __align__(16) float2 cs[kMaxTokens * kRotaryMaxPairs];
   ptx::griddep_launch_dependents();
   const int half = p.dims >> 1;
-  const long long tokens = (long long)p.B * p.L;
-  const long long tok0 = (long long)blockIdx.x * p.tokens;
-  const int ntok = (int)min((long long)p.tokens, tokens - tok0);
+  const unsigned tokens = (unsigned)p.B * (unsigned)p.L;  // at most 2^31
+  const unsigned tok0 = blockIdx.x * (unsigned)p.tokens;
+  const int ntok = (int)min((unsigned)p.tokens, tokens - tok0);
+  const int unit = (int)threadIdx.x % p.units, column = (int)threadIdx.x / p.units;
+  const int k = column / p.splits;             // token of the block
+  const bool active = k < ntok;
   const int heads = p.rows[0].heads + p.rows[1].heads;
-  const int unit = (int)threadIdx.x % p.units, group = (int)threadIdx.x / p.units;
-  const int groups = (int)blockDim.x / p.units;
+  const T *in0 = nullptr, *in1 = nullptr;      // the token's rows of q and k
+  T *out0 = nullptr, *out1 = nullptr;
+  if (active) {
+    const unsigned tok = tok0 + (unsigned)k;
+    const long long b = tok / (unsigned)p.L, t = tok - (unsigned)b * (unsigned)p.L;
+    in0 = static_cast<const T*>(p.rows[0].in) + b * p.rows[0].in_batch + t * p.rows[0].in_token;
+    out0 = static_cast<T*>(p.rows[0].out) + b * p.rows[0].out_batch + t * p.rows[0].out_token;
+    in1 = static_cast<const T*>(p.rows[1].in) + b * p.rows[1].in_batch + t * p.rows[1].in_token;
+    out1 = static_cast<T*>(p.rows[1].out) + b * p.rows[1].out_batch + t * p.rows[1].out_token;
+  }
+  // elements e0 .. (first vector or element) and e1 .. (second, if any) of a
+  // head, and the number of the unit's pairs that turn
+  const bool rot = M == kInterleaved ? unit * N < p.dims : unit < half / (M == kHalfVec ? N : 1);
+  int e0 = unit * N, e1 = -1, turns_here = kPairs;
+  if constexpr (M == kInterleaved) {
+    turns_here = rot ? min(kPairs, half - unit * kPairs) : 0;
+  } else if constexpr (M == kHalfVec) {
+    // (neighbouring units on neighbouring vectors: whole sectors per access)
+    if (!rot) e0 += half;
+    e1 = rot ? e0 + half : e0 + (p.units - half / N) * N;
+    if (e1 >= p.D) e1 = -1;
+  } else {
+    e0 = rot ? unit : unit + half;
+    e1 = rot ? unit + half : -1;
+  }
   ptx::griddep_wait();
 
-  // this thread's rows: (token, head) = (k, h), stepping by `groups` heads
-  struct Item {
-    const T* in;
-    T* out;
-    int k;
-  };
-  int k_next = group / heads, h_next = group - k_next * heads;
-  auto next_row = [&]() {
-    Item r{nullptr, nullptr, k_next};
-    if (k_next < ntok) {
-      const long long tok = tok0 + k_next;
-      const long long b = p.B == 1 ? 0 : tok / p.L, t = tok - b * p.L;
-      const int w = h_next >= p.rows[0].heads;
-      const int h = w ? h_next - p.rows[0].heads : h_next;
-      const RotaryRows& x = p.rows[w];
-      r.in = static_cast<const T*>(x.in) + b * x.in_batch + t * x.in_token + (long long)h * p.D;
-      r.out = static_cast<T*>(x.out) + b * x.out_batch + t * x.out_token + (long long)h * p.D;
-      h_next += groups;
-      while (h_next >= heads) h_next -= heads, ++k_next;
-    }
-    return r;
-  };
-
-  // element offset of the unit's first vector; a kHalfVec pair unit's second
-  // vector lies `half` elements further
-  const bool pairs = M == kHalfVec && unit < half / N;
-  const int e0 = (M == kHalfVec && !pairs) ? unit * N + half : unit * N;
-  Item row[kBatch];
+  const T* src[kBatch];
+  T* dst[kBatch];
   uint4 va[kBatch], vb[kBatch];
+  int h = active ? column % p.splits : heads;
   auto fetch = [&]() {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      row[u] = next_row();
-      if (M != kHalfScalar && row[u].in != nullptr) {
-        va[u] = *reinterpret_cast<const uint4*>(row[u].in + e0);
-        if (pairs) vb[u] = *reinterpret_cast<const uint4*>(row[u].in + e0 + half);
+      dst[u] = nullptr;
+      if (h < heads) {
+        const bool w = h >= p.rows[0].heads;
+        const int e = (w ? h - p.rows[0].heads : h) * p.D;
+        src[u] = (w ? in1 : in0) + e;
+        dst[u] = (w ? out1 : out0) + e;
+        h += p.splits;
+        if constexpr (M != kHalfScalar) {
+          va[u] = *reinterpret_cast<const uint4*>(src[u] + e0);
+          if (M == kHalfVec && e1 >= 0) vb[u] = *reinterpret_cast<const uint4*>(src[u] + e1);
+        }
       }
     }
   };
-  fetch();  // in flight while the angles are worked out
+  fetch();
 
   // sine and cosine of every (token, pair)
-  for (int i = threadIdx.x; i < ntok * half; i += blockDim.x) {
-    const int k = i / half, j = i - k * half;
-    const long long tok = tok0 + k;
-    const long long pos = p.positions != nullptr ? __ldg(p.positions + (long long)p.axis[j] * tokens + tok)
-                                                 : p.first_position + tok % p.L;
-    const unsigned long long turns = (unsigned long long)pos * p.step[j];
-    float s, c;
-    sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
-    cs[k * half + j] = make_float2(c * p.magnitude, s * p.sine);
+  const int cols = min(half, (int)blockDim.x), lines = (int)blockDim.x / cols, line = (int)threadIdx.x / cols;
+  if (line < lines) {
+    for (int j = (int)threadIdx.x - line * cols; j < half; j += cols) {
+      const unsigned long long step = p.step[j];
+      const long long* pos_j = p.positions != nullptr ? p.positions + (long long)p.axis[j] * tokens : nullptr;
+      for (int kk = line; kk < ntok; kk += lines) {
+        const unsigned tok = tok0 + (unsigned)kk;
+        const long long pos = pos_j != nullptr ? __ldg(pos_j + tok) : p.first_position + tok % (unsigned)p.L;
+        const unsigned long long turns = (unsigned long long)pos * step;
+        float s, c;
+        sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
+        cs[kk * half + j] = make_float2(c * p.magnitude, s * p.sine);
+      }
+    }
   }
   __syncthreads();
+  if (!active) return;
+  float2 f[kPairs];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j)
+    f[j] = rot && j < turns_here ? cs[k * half + unit * kPairs + j] : make_float2(0.f, 0.f);
 
-  while (row[0].in != nullptr) {
+  while (dst[0] != nullptr) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (row[u].in == nullptr) break;
-      const float2* c = cs + row[u].k * half;
+      if (dst[u] == nullptr) break;
       if constexpr (M == kHalfScalar) {
-        const T* in = row[u].in;
-        T* out = row[u].out;
-        if (unit < half) {
-          float x, y;
-          turn(c[unit], V::load(in + unit), V::load(in + unit + half), x, y);
-          V::store(out + unit, x);
-          V::store(out + unit + half, y);
+        if (rot) {
+          float x = V::load(src[u] + e0), y = V::load(src[u] + e1);
+          turn(f[0], x, y);
+          V::store(dst[u] + e0, x);
+          V::store(dst[u] + e1, y);
         } else {
-          out[unit + half] = in[unit + half];
+          dst[u][e0] = src[u][e0];
         }
       } else {
-        float a[N];
-        V::unpack(va[u], a);
-        if constexpr (M == kInterleaved) {
+        if (rot) {
+          float x[N], y[N];
+          V::unpack(va[u], x);
+          if constexpr (M == kInterleaved) {
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j)
-            if (e0 + 2 * j < p.dims) turn(c[e0 / 2 + j], a[2 * j], a[2 * j + 1], a[2 * j], a[2 * j + 1]);
-        } else if (pairs) {
-          float b[N];
-          V::unpack(vb[u], b);
+            for (int j = 0; j < kPairs; ++j)
+              if (j < turns_here) turn(f[j], x[2 * j], x[2 * j + 1]);
+          } else {
+            V::unpack(vb[u], y);
 #pragma unroll
-          for (int j = 0; j < N; ++j) turn(c[e0 + j], a[j], b[j], a[j], b[j]);
-          *reinterpret_cast<uint4*>(row[u].out + e0 + half) = V::pack(b);
+            for (int j = 0; j < kPairs; ++j) turn(f[j], x[j], y[j]);
+            vb[u] = V::pack(y);
+          }
+          va[u] = V::pack(x);
         }
-        *reinterpret_cast<uint4*>(row[u].out + e0) = V::pack(a);
+        *reinterpret_cast<uint4*>(dst[u] + e0) = va[u];
+        if (M == kHalfVec && e1 >= 0) *reinterpret_cast<uint4*>(dst[u] + e1) = vb[u];
       }
     }
     fetch();
@@ -184,26 +213,25 @@ __global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const __grid_consta
 template <typename T, Mode M>
 cudaError_t launch(RotaryParams& p, cudaStream_t s) {
   constexpr int N = Vec<T>::N;
-  const int half = p.dims / 2;
-  p.units = M == kInterleaved ? p.D / N : M == kHalfVec ? half / N + (p.D - p.dims) / N : half + p.D - p.dims;
-  const int threads = p.units > kMaxThreads ? kMaxThreads : kMaxThreads / p.units * p.units;
-  const int heads = p.rows[0].heads + p.rows[1].heads, groups = threads / p.units;
+  const int half = p.dims / 2, rest = p.D - p.dims;
+  p.units = M == kInterleaved ? p.D / N : M == kHalfVec ? half / N + (rest / N + 1) / 2 : half + rest;
+  const int columns = kMaxThreads / p.units;
+  const int heads = p.rows[0].heads + p.rows[1].heads;
   const long long tokens = (long long)p.B * p.L;
-  // tokens per block: as few whole batches of rows per thread as leave the
-  // fewest idle slots in the last one, but a block for every SM before that
-  int best = 1;
-  double waste = 2.0;
-  for (int t = 1; t <= kMaxTokens && (t == 1 || tokens / t >= 2 * 152); ++t) {
-    const int slots = kBatch * groups, rows = t * heads;
-    const double w = (double)((rows + slots - 1) / slots * slots) / rows;
-    if (w < waste - 0.02) best = t, waste = w;
+  // tokens per block: those that leave the fewest of the threads' batch slots
+  // empty, but a block or two for every SM before that
+  double best = 0.0;
+  for (int t = 1; t <= kMaxTokens && t <= columns && (t == 1 || tokens / t >= 2 * 152); ++t) {
+    const int splits = columns / t < heads ? columns / t : heads;
+    const int rows = (heads + splits - 1) / splits;  // per thread
+    const double used = (double)t * heads / ((double)columns * ((rows + kBatch - 1) / kBatch * kBatch));
+    if (t == 1 || used > best + 0.01) best = used, p.tokens = t, p.splits = splits;
   }
-  p.tokens = best;
   const long long blocks = (tokens + p.tokens - 1) / p.tokens;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.blockDim = dim3((unsigned)(p.tokens * p.splits * p.units), 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

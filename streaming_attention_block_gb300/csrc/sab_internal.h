@@ -227,7 +227,7 @@ struct RotaryParams {
   int half_layout;
   float magnitude;        // factor of the cosines
   float sine;             // factor of the sines: +magnitude forward, -magnitude backward
-  int units, tokens;      // set by the launcher: threads per head, tokens per block
+  int units, tokens, splits;  // set by the launcher: threads per head, tokens per block, head subsets per token
   unsigned char axis[kRotaryMaxPairs];
   unsigned long long step[kRotaryMaxPairs];
 };
