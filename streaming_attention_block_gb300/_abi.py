@@ -610,8 +610,8 @@ def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_ou
     x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention(
         _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
-        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev), _arg(state_in, st, f4, "state_in", dev), B, L, H, D,
-        float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes,
+        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
+        _arg(state_in, st, f4, "state_in", dev), B, L, H, D, float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes,
         _stream(stream)), "decay_attention")
 
 
@@ -623,8 +623,8 @@ def decay_attention_step(Q, K, V, log_decay, scale: float, state_in, state_out, 
     x, st, bf, f4 = (B, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention_step(
         _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
-        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(active, (B,), torch.int32, "active", dev), _arg(state_in, st, f4, "state_in", dev), B, H, D, float(scale),
-        _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), _stream(stream)), "decay_attention_step")
+        _arg(log_decay, (H,), f4, "log_decay", dev), _arg(active, (B,), torch.int32, "active", dev),
+        _arg(state_in, st, f4, "state_in", dev), B, H, D, float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), _stream(stream)), "decay_attention_step")
 
 
 def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, state_in=None, d_state_out=None,

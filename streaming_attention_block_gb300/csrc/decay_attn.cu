@@ -235,16 +235,29 @@ __device__ __forceinline__ void scale_rows(uint8_t* k, uint8_t* rest, uint32_t r
       const float wr = f * w[row];
       const uint4 x = *reinterpret_cast<const uint4*>(k + off);
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+      if constexpr (TERMS == 2) {
+        // with w = w1 + w2 in bf16: k w1 = hi + e, both bf16 (the product has
+        // 16 bits), and the rest is e + k w2: three packed bf16 operations
+        const uint32_t w1 = pack_bf16(wr, wr), h1 = w1 & 0xFFFF0000u;
+        const float r = wr - __uint_as_float(h1);
+        const uint32_t w2 = pack_bf16(r, r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 r = __fmul2_rn(make_float2(__uint_as_float(xs[j] << 16), __uint_as_float(xs[j] & 0xFFFF0000u)),
-                              make_float2(wr, wr));
+        for (int j = 0; j < 4; ++j) {
+          part[0][j] = mul_bf16x2(xs[j], w1);
+          part[1][j] = fma_bf16x2(xs[j], w2, fma_bf16x2(xs[j], w1, part[0][j] ^ 0x80008000u));
+        }
+      } else {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-          const uint32_t q = pack_bf16(r.x, r.y);
-          part[t][j] = q;
-          if (t + 1 < TERMS)
-            r = __fadd2_rn(r, make_float2(-__uint_as_float(q << 16), -__uint_as_float(q & 0xFFFF0000u)));
+        for (int j = 0; j < 4; ++j) {
+          float2 r = __fmul2_rn(make_float2(__uint_as_float(xs[j] << 16), __uint_as_float(xs[j] & 0xFFFF0000u)),
+                                make_float2(wr, wr));
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t) {
+            const uint32_t q = pack_bf16(r.x, r.y);
+            part[t][j] = q;
+            if (t + 1 < TERMS)
+              r = __fadd2_rn(r, make_float2(-__uint_as_float(q << 16), -__uint_as_float(q & 0xFFFF0000u)));
+          }
         }
       }
     } else {
@@ -274,6 +287,16 @@ __device__ __noinline__ void zero_rows(uint8_t* v, int tid, int n) {
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+// Carried states are kept as the element threads hold them: 4 columns of a row
+// together, the rows of a column group side by side.  Index of (row, col):
+// + 1 for the next column of the four, + 4 for the next row, + 8 D for the next
+// column group of the same half.
+template <int D>
+__device__ __forceinline__ int piece_index(int row, int col) {
+  const int half = col / (D / 2), c = col % (D / 2);
+  return ((c / 4) * 2 * D + half * D + row) * 4 + c % 4;
 }
 
 constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-major
@@ -349,7 +372,10 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     tmem_relinquish();
   }
   griddep_launch_dependents();
-  griddep_wait();
+  // With segments, this kernel follows the ones that sum and chain them.  Those
+  // let it start only after their own waits, so that everything before them
+  // is complete: all but the carried states may be read, and worked on, now.
+  if (p.nseg == 1) griddep_wait();
   const Run run(p, b, seg);
   const float ln = decay_ln(p.log_decay, h), ld2 = ln * kLog2e;
   if (threadIdx.x < 256) {
@@ -505,27 +531,30 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int pass = 0; pass < 4; ++pass) {
-          const int c0 = hf * 64 + 16 * pass;
-          uint32_t pk[8];
-          if ((rev ? c0 + 15 < quad * 32 : c0 > quad * 32 + 31) || c0 >= n) {  // nothing visible
+        for (int pass = 0; pass < 2; ++pass) {
+          const int c0 = hf * 64 + 32 * pass;
+          uint32_t pk[16];
+          if ((rev ? c0 + 31 < quad * 32 : c0 > quad * 32 + 31) || c0 >= n) {  // nothing visible
 #pragma unroll
-            for (int c = 0; c < 8; ++c) pk[c] = 0u;
+            for (int c = 0; c < 16; ++c) pk[c] = 0u;
           } else {
-            uint32_t x[16];
-            tmem_ld16(lane_off + C::kS + c0, x);
-            tmem_wait_ld();
-            if (c0 + 16 > n) {
+            uint32_t x[32];
+            tmem_ld32(lane_off + C::kS + c0, x);
+            const float* t = p_tab + 127 + row - c0;
+            float w[32];
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < 32; ++c) w[c] = t[-c];
+            tmem_wait_ld();
+            if (c0 + 32 > n) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
                 if (c0 + c >= n) x[c] = 0u;
             }
-            const float* t = p_tab + 127 + row - c0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              pk[c] = pack_bf16(__uint_as_float(x[2 * c]) * t[-2 * c], __uint_as_float(x[2 * c + 1]) * t[-2 * c - 1]);
+            for (int c = 0; c < 16; ++c)
+              pk[c] = pack_bf16(__uint_as_float(x[2 * c]) * w[2 * c], __uint_as_float(x[2 * c + 1]) * w[2 * c + 1]);
           }
-          tmem_st8(lane_off + C::kS + hf * 64 + 8 * pass, pk);
+          tmem_st16(lane_off + C::kS + hf * 64 + 16 * pass, pk);
         }
         tmem_wait_st();
         if (n < kC) {  // padding of v must not meet the zeros of P
@@ -595,19 +624,32 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         warp_arrive(bar(C::kStFull), lane);
       };
       // the state before the segment
-      const float* in = p.nseg > 1 ? p.carry + (bh * p.nseg + seg) * D * D
-                                   : p.state_in != nullptr ? p.state_in + bh * D * D : nullptr;
-      const bool in_t = p.nseg > 1 ? p.carry_t : p.state_t;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) st[c] = 0.f;
-      if (in != nullptr && row < D) {
-        if (in_t) {
+      if (p.nseg > 1) {
+        griddep_wait();
+        const float* in = p.carry + (bh * p.nseg + seg) * D * D;
+        if (row < D && p.carry_t) {
+          in += piece_index<D>(hf * kCols, row);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) st[c] = in[(long long)(hf * kCols + c) * D + row];
+          for (int c = 0; c < kCols; ++c) st[c] = in[4 * c];
+        } else if (row < D) {
+          in += piece_index<D>(row, hf * kCols);
+#pragma unroll
+          for (int c = 0; c < kCols / 4; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(in + c * 8 * D);
+            st[4 * c] = x.x, st[4 * c + 1] = x.y, st[4 * c + 2] = x.z, st[4 * c + 3] = x.w;
+          }
+        }
+      } else if (p.state_in != nullptr && row < D) {
+        const float* in = p.state_in + bh * D * D;
+        if (p.state_t) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) st[c] = in[(hf * kCols + c) * D + row];
         } else {
 #pragma unroll
           for (int c = 0; c < kCols / 4; ++c) {
-            const float4 x = *reinterpret_cast<const float4*>(in + (long long)row * D + hf * kCols + 4 * c);
+            const float4 x = *reinterpret_cast<const float4*>(in + row * D + hf * kCols + 4 * c);
             st[4 * c] = x.x, st[4 * c + 1] = x.y, st[4 * c + 2] = x.z, st[4 * c + 3] = x.w;
           }
         }
@@ -714,8 +756,8 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     tmem_alloc(smem_u32(misc), 128);
     tmem_relinquish();
   }
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();  // not before: the tile kernel reads its inputs ahead of its own wait
   const Run run(p, b, seg);
   const float ld2 = decay_ln(p.log_decay, h) * kLog2e;
   float* w_tab = reinterpret_cast<float*>(base + C::kTabOff);  // factor of k row j of a full step next to the end
@@ -801,7 +843,7 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     ok = ok && !*abort_flag;
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
-      float* out = p.carry + (bh * p.nseg + seg) * D * D + (long long)row * D + hf * kCols;
+      float* out = p.carry + (bh * p.nseg + seg) * D * D + piece_index<D>(row, hf * kCols);
 #pragma unroll
       for (int c0 = 0; c0 < kCols; c0 += 32) {
         uint32_t x[32];
@@ -815,7 +857,7 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
         if (row < D) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<uint4*>(out + c0 + c) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            *reinterpret_cast<uint4*>(out + (c0 + c) * 2 * D) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
         }
       }
     }
@@ -831,46 +873,58 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
 // Chains the segments' contributions, in place, into the state before every
 // segment; the state after the last goes to state_out.  One thread per four
 // elements; the contributions are fetched kAhead segments ahead.
+constexpr int kMaxSegments = 256;
 template <int D>
 __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayTileParams p) {
-  constexpr int kAhead = 8, kBlocks = D * D / 512;
-  griddep_launch_dependents();
-  griddep_wait();
+  constexpr int kAhead = 16, kBlocks = D * D / 512;
+  __shared__ float2 decays[kMaxSegments];
   const long long bh = blockIdx.x / kBlocks;
   const int e = ((int)(blockIdx.x % kBlocks) * 128 + threadIdx.x) * 4;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
-  const float ln = decay_ln(p.log_decay, h);
   const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
   float* c = p.carry + bh * p.nseg * D * D + e;
-  // the caller's orientation: element (r, col) of a run may be held at (col, r)
-  const int step = p.state_t ? D : 1;
-  const long long io = bh * D * D + (p.state_t ? (e % D) * D + e / D : e);
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.state_in != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = p.state_in[io + i * step];
-  }
+  // its place in the caller's states, where (row, col) may be held at (col, row)
+  const int row = (e / 4) % D, col = (e / (8 * D)) * 4 + ((e / 4) % (2 * D) / D) * (D / 2);
+  const long long io = bh * D * D + (p.state_t ? col * D + row : row * D + col);
+  griddep_wait();
+  griddep_launch_dependents();
   float4 add[kAhead];
-  for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
+  auto fetch = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (s0 + i < nrun) add[i] = *reinterpret_cast<const float4*>(c + (long long)(s0 + i) * D * D);
+  };
+  fetch(0);
+  const float ln = decay_ln(p.log_decay, h);
+  for (int i = threadIdx.x; i < nrun; i += 128) {
+    const Decay d((float)Run(p, b, i).count() * ln);
+    decays[i] = make_float2(d.hi, d.lo);
+  }
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.state_in != nullptr)
+    s = p.state_t ? make_float4(p.state_in[io], p.state_in[io + D], p.state_in[io + 2 * D], p.state_in[io + 3 * D])
+                  : *reinterpret_cast<const float4*>(p.state_in + io);
+  __syncthreads();
+  for (int s0 = 0; s0 < p.nseg; s0 += kAhead) {
+    if (s0 > 0) fetch(s0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (s0 + i >= p.nseg) break;
-      *reinterpret_cast<float4*>(c + (long long)(s0 + i) * D * D) = make_float4(s[0], s[1], s[2], s[3]);
+      if (s0 + i < p.nseg) *reinterpret_cast<float4*>(c + (long long)(s0 + i) * D * D) = s;
       if (s0 + i < nrun) {
-        const Decay decay((float)Run(p, b, s0 + i).count() * ln);
-        s[0] = decay(s[0]) + add[i].x;
-        s[1] = decay(s[1]) + add[i].y;
-        s[2] = decay(s[2]) + add[i].z;
-        s[3] = decay(s[3]) + add[i].w;
+        const float2 d = decays[s0 + i];
+        s.x = fmaf(s.x, d.x, s.x * d.y) + add[i].x;
+        s.y = fmaf(s.y, d.x, s.y * d.y) + add[i].y;
+        s.z = fmaf(s.z, d.x, s.z * d.y) + add[i].z;
+        s.w = fmaf(s.w, d.x, s.w * d.y) + add[i].w;
       }
     }
   }
   if (p.state_out != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.state_out[io + i * step] = s[i];
+    float* out = p.state_out + io;
+    if (p.state_t)
+      out[0] = s.x, out[D] = s.y, out[2 * D] = s.z, out[3 * D] = s.w;
+    else
+      *reinterpret_cast<float4*>(out) = s;
   }
 }
 

@@ -182,18 +182,93 @@ def _fp64_on_gpu(q, k, v, ld, scale, S):
     return O, S, Oa, A
 
 
+def _fp64_back_on_gpu(q, k, v, do, ld, scale, S, R):
+    """Gradients by the adjoint recurrence, and their absolute sums."""
+    B, L, H, D = q.shape
+    g = torch.exp(ld.double().clamp(max=0))[:, None, None]
+    A, Ra = S.abs(), R.abs()
+    out = [torch.empty((B, L, H, D), dtype=torch.float64, device=q.device) for _ in range(6)]
+    dq, dk, dv, dqa, dka, dva = out
+    for t in range(L):
+        kv = k[:, t].double().unsqueeze(-1) * v[:, t].double().unsqueeze(-2)
+        S = g * S + kv
+        A = g * A + kv.abs()
+        d = do[:, t].double().unsqueeze(-1)
+        dq[:, t] = scale * (S @ d).squeeze(-1)
+        dqa[:, t] = scale * (A @ d.abs()).squeeze(-1)
+    for t in range(L - 1, -1, -1):
+        w = scale * q[:, t].double().unsqueeze(-1) * do[:, t].double().unsqueeze(-2)
+        R = R + w
+        Ra = Ra + w.abs()
+        kk, vv = k[:, t].double().unsqueeze(-2), v[:, t].double().unsqueeze(-1)
+        dk[:, t], dv[:, t] = (R @ vv).squeeze(-1), (kk @ R).squeeze(-2)
+        dka[:, t], dva[:, t] = (Ra @ vv.abs()).squeeze(-1), (kk.abs() @ Ra).squeeze(-2)
+        R = g * R
+        Ra = g * Ra
+    return (dq, dk, dv, R), (dqa, dka, dva, Ra)
+
+
+# few heads: the sequence is worked on in parallel pieces, chained inside a
+# cluster while they are short, by kernels of their own when they are long
 @gpu
+@pytest.mark.parametrize("L", [3000, 7000, 20011])
 @pytest.mark.parametrize("D", [64, 128])
-def test_long_sequence(D):
-    """7000 tokens of few heads: the sequence is worked on in parallel pieces."""
-    B, L, H = 1, 7000, 3
-    q, k, v = (_randn((B, L, H, D), 50 + i) for i in range(3))
+def test_long_sequence(D, L):
+    B, H = 1, 3
+    q, k, v, do = (_randn((B, L, H, D), 50 + i) for i in range(4))
     ld = torch.tensor([-1e-4, -0.01, 0.0], device="cuda")
-    S = _randn((B, H, D, D), 60, torch.float32)
-    O, So = _forward(q, k, v, ld, D ** -0.5, S)
-    o, s, oa, sa = _fp64_on_gpu(q, k, v, ld, D ** -0.5, S.double())
+    scale = D ** -0.5
+    S, dS = (_randn((B, H, D, D), 60 + i, torch.float32) for i in range(2))
+    o, s, oa, sa = _fp64_on_gpu(q, k, v, ld, scale, S.double())
+    O, So = _forward(q, k, v, ld, scale, S)
     _check(O, _n(o), _n(oa), "O")
     _check(So, _n(s), _n(sa), "state", state=True)
+    O2, S2 = _forward(q, k, v, ld, scale, S, inplace=True)
+    assert torch.equal(O2, O) and torch.equal(S2, So)
+    refs, bnds = _fp64_back_on_gpu(q, k, v, do, ld, scale, S.double(), dS.double())
+    g = [_out(q.shape) for _ in range(3)]
+    ws = _ws(sab.decay_attention_backward_workspace(B, L, H, D))
+    d_in = _out(S.shape, torch.float32)
+    d_in.copy_(dS)
+    sab.decay_attention_backward(q, k, v, do, ld, scale, *g, state_in=S, d_state_out=d_in, d_state_in=d_in, workspace=ws)
+    for n, got, ref, bnd in zip(("dQ", "dK", "dV", "d_state_in"), g + [d_in], refs, bnds):
+        _check(got, _n(ref), _n(bnd), n, state=n == "d_state_in")
+
+
+@gpu
+@pytest.mark.parametrize("case", [(8, 1024, 6, 64), (3, 2300, 4, 128), (2, 9000, 2, 128)])
+def test_ragged_segments(case):
+    """Unequal lengths cut into segments: some end in the middle of one, some
+    have none of their tokens in it."""
+    B, L, H, D = case
+    lens = torch.tensor([L * (b * 37 % 100) // 100 for b in range(B)], dtype=torch.int32, device="cuda")
+    lens[-1] = L
+    q, k, v, do = (_randn((B, L, H, D), 160 + i) for i in range(4))
+    ld = _ld(H, 1)
+    S, dS = (_randn((B, H, D, D), 170 + i, torch.float32) for i in range(2))
+    for b, n in enumerate(lens.tolist()):
+        for x in (q, k, v, do):
+            x[b, n:] = float("nan")
+    O, So = _forward(q, k, v, ld, 0.1, S, lens)
+    g = [_out(q.shape) for _ in range(3)]
+    d_in = _out(S.shape, torch.float32)
+    sab.decay_attention_backward(q, k, v, do, ld, 0.1, *g, state_in=S, d_state_out=dS, d_state_in=d_in, seq_len=lens,
+                                 workspace=_ws(sab.decay_attention_backward_workspace(B, L, H, D)))
+    for b, n in enumerate(lens.tolist()):
+        for x in [O] + g:
+            assert not bool(x[b, n:].any())
+        if n == 0:
+            assert torch.equal(So[b], S[b]) and torch.equal(d_in[b], dS[b])
+            continue
+        # each sequence by itself: the same numbers, cut otherwise
+        one = [x[b:b + 1, :n].contiguous() for x in (q, k, v, do)]
+        o, s, oa, sa = _fp64_on_gpu(one[0], one[1], one[2], ld, 0.1, S[b:b + 1].double())
+        _check(O[b:b + 1, :n], _n(o), _n(oa), f"O {b}")
+        _check(So[b:b + 1], _n(s), _n(sa), f"state {b}", state=True)
+        refs, bnds = _fp64_back_on_gpu(*one, ld, 0.1, S[b:b + 1].double(), dS[b:b + 1].double())
+        for name, got, ref, bnd in zip(("dQ", "dK", "dV"), g, refs, bnds):
+            _check(got[b:b + 1, :n], _n(ref), _n(bnd), f"{name} {b}")
+        _check(d_in[b:b + 1], _n(refs[3]), _n(bnds[3]), f"d_state_in {b}", state=True)
 
 
 @gpu
