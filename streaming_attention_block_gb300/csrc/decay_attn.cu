@@ -306,7 +306,11 @@ constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-maj
 // the state, 18 stores.  The two element groups work on the same tile at once:
 // neither needs the other within a tile, and each alone takes about half of
 // the time HBM needs for a tile.
-// A tile's output is staged over its v once the update has read it.
+// D = 128: a tile's output is staged over its v once the update has read it;
+// nothing else is free.  D = 64 has room for an output buffer of its own and
+// for two sets of k's parts (kRoomy): the next tile's scores go ahead of the
+// update, its k is scaled while the update runs, and the chain from state to
+// state is update, state, state product only.
 template <int D_, int TERMS_>
 struct TileCfg {
   static constexpr int D = D_, TERMS = TERMS_;
@@ -314,20 +318,23 @@ struct TileCfg {
   static constexpr uint32_t kBoxBytes = kC * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
   static constexpr int kQStages = D == 128 ? 1 : 2;
-  static constexpr int kVStages = D == 128 && TERMS == 3 ? 1 : 2;
   // (D = 64: the update's A operand, M = 128, takes its upper 64 rows from the
   // box behind a k tile; they land in accumulator rows that nothing reads)
-  static constexpr uint32_t kKOff = 0;                                       // [2]; scaled in place
-  static constexpr uint32_t kRestOff = kKOff + 2 * kTileBytes;               // [TERMS - 1]
-  static constexpr uint32_t kQOff = kRestOff + (TERMS - 1) * kTileBytes;
+  static constexpr uint32_t kKOff = 0;                                       // [kKStages]; scaled in place
+  static constexpr bool kRoomy = D == 64;
+  static constexpr int kKStages = kRoomy ? 3 : 2, kVStages = kRoomy ? 3 : TERMS == 3 ? 1 : 2;
+  static constexpr uint32_t kRestOff = kKOff + kKStages * kTileBytes;             // [kRoomy ? 2 : 1][TERMS - 1]
+  static constexpr uint32_t kRestBytes = (TERMS - 1) * kTileBytes;
+  static constexpr uint32_t kQOff = kRestOff + (kRoomy ? 2 : 1) * kRestBytes;
   static constexpr uint32_t kVOff = kQOff + kQStages * kTileBytes;
-  static constexpr uint32_t kStOff = kVOff + kVStages * kTileBytes;          // bf16 state [D][D]
+  static constexpr uint32_t kOutOff = kVOff + kVStages * kTileBytes;
+  static constexpr uint32_t kStOff = kOutOff + (kRoomy ? kTileBytes : 0);   // bf16 state [D][D]
   static constexpr uint32_t kStBoxBytes = D * 128u;
   static constexpr uint32_t kBarOff = kStOff + kBoxes * kStBoxBytes;
-  static constexpr int kFullQ = 0, kFullK = 2, kFullV = 4;                   // [2] each
-  static constexpr int kEmptyQ = 6, kEmptyK = 8, kEmptyV = 10, kOut = 12;    // [2] each
-  static constexpr int kSFull = 14, kPFull = 15, kKwFull = 16, kOFull = 17, kORead = 18, kUFull = 19, kStFull = 20,
-                       kDrain = 21, kNumBars = 22;
+  // barriers; those of a slot [3]
+  static constexpr int kFullQ = 0, kFullK = 3, kFullV = 6, kEmptyQ = 9, kEmptyK = 12, kEmptyV = 15, kOut = 18;
+  static constexpr int kSFull = 21, kPFull = 22, kKwFull = 23, kOFull = 24, kORead = 25, kUFull = 26, kStFull = 27,
+                       kDrain = 28, kOutFree = 29, kNumBars = 30;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;               // tmem address, abort flag
   static constexpr uint32_t kTabOff = kMiscOff + 16;                         // decay powers: of P [256], of k [128]
   static constexpr uint32_t kSmemBytes = kTabOff + 4 * (256 + 128) + 1024;
@@ -359,8 +366,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i)
-      mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kORead || i == C::kStFull || i == C::kOut ||
-                                i == C::kOut + 1
+      mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kORead || i == C::kStFull ||
+                                (i >= C::kOut && i < C::kOut + 3)
                             ? 8
                             : 1);
     misc[1] = 0;
@@ -416,7 +423,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       auto load_q = [&](int it) { return load(&p.q_map, C::kQOff, C::kFullQ, C::kEmptyQ, C::kQStages, nq, it); };
       bool ok = load_q(0);
       for (int it = 0; ok && it < nt; ++it) {
-        ok = load(&p.k_map, C::kKOff, C::kFullK, C::kEmptyK, 2, nk, it) &&
+        ok = load(&p.k_map, C::kKOff, C::kFullK, C::kEmptyK, C::kKStages, nk, it) &&
              (it == 0 || C::kVStages > 1 || load_q(it)) &&
              load(&p.v_map, C::kVOff, C::kFullV, C::kEmptyV, C::kVStages, nv, it) &&
              (it == 0 || C::kVStages == 1 || load_q(it));
@@ -425,7 +432,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         auto drain = [&](int full, int stages, int n) {
           for (int i = max(0, n - stages); i < n; ++i) wait_drain(bar(full + i % stages), (i / stages) & 1u, p.err_word);
         };
-        drain(C::kFullK, 2, nk);
+        drain(C::kFullK, C::kKStages, nk);
         drain(C::kFullQ, C::kQStages, nq);
         drain(C::kFullV, C::kVStages, nv);
       }
@@ -433,6 +440,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
+    const uint32_t lead = elect_lead();
     constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0);                 // q . k: both K-major
     constexpr uint32_t id_o = idesc_bf16_f32(128, D, 1);                   // B = v or state, MN-major
     constexpr uint32_t id_u = idesc_bf16_f32(128, D, 1) | kAMajorMN;       // A = scaled k, MN-major
@@ -447,49 +455,60 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       return r;
     };
     auto scores = [&](int it) {
-      const int s = it & 1, sq = it % C::kQStages;
-      if (!wait_all(C::kFullQ + sq, (it / C::kQStages) & 1u, 10) || !wait_all(C::kFullK + s, (it / 2) & 1u, 10))
+      const int s = it % C::kKStages, sq = it % C::kQStages;
+      if (!wait_all(C::kFullQ + sq, (it / C::kQStages) & 1u, 10) || !wait_all(C::kFullK + s, (it / C::kKStages) & 1u, 10))
         return false;
       const uint32_t q = C::kQOff + sq * C::kTileBytes, k = C::kKOff + s * C::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_e(tmem + C::kS, at(kmaj, q + k_off(kk)), at(kmaj, k + k_off(kk)), id_s, kk > 0);
-      mma_commit_e(bar(C::kSFull));
+        mma_ss_l(lead, tmem + C::kS, at(kmaj, q + k_off(kk)), at(kmaj, k + k_off(kk)), id_s, kk > 0);
+      mma_commit_l(lead, bar(C::kSFull));
       return true;
     };
     bool ok = nt > 0 && scores(0);
     for (int it = 0; ok && it < nt; ++it) {
-      const int s = it & 1, sv = it % C::kVStages, sq = it % C::kQStages;
+      const int s = it % C::kKStages, sv = it % C::kVStages, sq = it % C::kQStages;
       const uint32_t q = C::kQOff + sq * C::kTileBytes, k = C::kKOff + s * C::kTileBytes,
                      v = C::kVOff + sv * C::kTileBytes;
-      // the state before the tile is published, the previous output rows are read
-      ok = wait_all(C::kStFull, it & 1u, 11) && (it == 0 || wait_all(C::kORead, (it - 1) & 1u, 11));
-      if (!ok) break;
+      auto state_product = [&]() {
+        if (!wait_all(C::kStFull, it & 1u, 11)) return false;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_e(tmem + C::kInter, at(kmaj, q + k_off(kk)), at(mn_st, C::kStOff + kk * 2048u), id_o, kk > 0);
-      mma_commit_e(bar(C::kEmptyQ + sq));
-      ok = wait_all(C::kPFull, it & 1u, 12) && wait_all(C::kFullV + sv, (it / C::kVStages) & 1u, 10);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_l(lead, tmem + C::kInter, at(kmaj, q + k_off(kk)), at(mn_st, C::kStOff + kk * 2048u), id_o, kk > 0);
+        mma_commit_l(lead, bar(C::kEmptyQ + sq));
+        return true;
+      };
+      // the previous output rows are read
+      ok = it == 0 || wait_all(C::kORead, (it - 1) & 1u, 11);
+      if (ok && !C::kRoomy) ok = state_product();
+      ok = ok && wait_all(C::kPFull, it & 1u, 12) && wait_all(C::kFullV + sv, (it / C::kVStages) & 1u, 10);
       if (!ok) break;
 #pragma unroll
       for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ts_e(tmem + C::kIntra, tmem + C::kS + (kk >> 2) * 64 + (kk & 3) * 8, at(mn, v + kk * 2048u), id_o, kk > 0);
-      mma_commit_e(bar(C::kOFull));
+        mma_ts_l(lead, tmem + C::kIntra, tmem + C::kS + (kk >> 2) * 64 + (kk & 3) * 8, at(mn, v + kk * 2048u), id_o, kk > 0);
+      if (!C::kRoomy) mma_commit_l(lead, bar(C::kOFull));
+      if (it < n_upd && !(ok = wait_all(C::kKwFull, it & 1u, 13))) break;
+      if (C::kRoomy) {
+        if (it + 1 < nt && !(ok = scores(it + 1))) break;
+        if (!(ok = state_product())) break;
+        mma_commit_l(lead, bar(C::kOFull));
+      }
       if (it < n_upd) {
-        if (!(ok = wait_all(C::kKwFull, it & 1u, 13))) break;
+        const uint32_t rest = C::kRestOff + (C::kRoomy ? (uint32_t)(it & 1) * C::kRestBytes : 0u);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk)
-            mma_ss_e(tmem + C::kUpd, at(mn, (t == 0 ? k : C::kRestOff + (t - 1) * C::kTileBytes) + kk * 2048u),
+            mma_ss_l(lead, tmem + C::kUpd, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
                      at(mn, v + kk * 2048u), id_u, t > 0 || kk > 0);
-        mma_commit_e(bar(C::kUFull));
-        mma_commit_e(bar(C::kEmptyK + s));
+        mma_commit_l(lead, bar(C::kUFull));
+        mma_commit_l(lead, bar(C::kEmptyK + s));
+        if (C::kRoomy) mma_commit_l(lead, bar(C::kEmptyV + sv));
       }
-      if (it + 1 < nt) ok = scores(it + 1);
+      if (!C::kRoomy && it + 1 < nt) ok = scores(it + 1);
     }
     if (__any_sync(0xffffffffu, (nt > 0 && !ok) || *abort_flag)) {
-      mma_commit_e(bar(C::kDrain));
+      mma_commit_l(lead, bar(C::kDrain));
       if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
     }
     __syncwarp();
@@ -497,14 +516,14 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     // --------------------------------------------------------- output store
     if (lane == 0) {
       for (int it = 0; it < nt; ++it) {
-        const int sv = it % C::kVStages;
-        if (!wait(C::kOut + sv, (it / C::kVStages) & 1u, 14)) break;
+        const int so = C::kRoomy ? 0 : it % C::kVStages;  // staging slot
+        if (!wait(C::kOut + so, (C::kRoomy ? it : it / C::kVStages) & 1u, 14)) break;
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_store_4d(&p.o_map, base_u32 + C::kVOff + sv * C::kTileBytes + bx * C::kBoxBytes, bx * 64,
-                       run.tile(run.a + it) * kC, h, b);
+          tma_store_4d(&p.o_map, base_u32 + (C::kRoomy ? C::kOutOff : C::kVOff) + so * C::kTileBytes + bx * C::kBoxBytes,
+                       bx * 64, run.tile(run.a + it) * kC, h, b);
         tma_store_commit_and_wait_read();
-        mbar_arrive(bar(C::kEmptyV + sv));
+        mbar_arrive(bar(C::kRoomy ? C::kOutFree : C::kEmptyV + so));
       }
     }
     __syncwarp();
@@ -587,16 +606,18 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         }
         tc_fence_before();
         warp_arrive(bar(C::kORead), lane);
-        if (it < n_upd) {  // v is free once the update has read it
-          ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 15));
+        // v is free once the update has read it, the own buffer once stored
+        if (C::kRoomy ? it > 0 : it < n_upd) {
+          ok = __all_sync(0xffffffffu, C::kRoomy ? wait(C::kOutFree, (it - 1) & 1u, 15) : wait(C::kUFull, it & 1u, 15));
           if (!ok) break;
         }
+        uint8_t* ot = C::kRoomy ? base + C::kOutOff : vt;
 #pragma unroll
         for (int c = 0; c < kCols / 8; ++c)
-          *reinterpret_cast<uint4*>(vt + piece(c, C::kBoxBytes)) =
+          *reinterpret_cast<uint4*>(ot + piece(c, C::kBoxBytes)) =
               make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         fence_proxy_async_smem();
-        warp_arrive(bar(C::kOut + sv), lane);
+        warp_arrive(bar(C::kOut + (C::kRoomy ? 0 : sv)), lane);
       }
       // tiles of the segment without a live token
       for (int r = run.r0; r < run.r1; ++r) {
@@ -656,15 +677,23 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       }
       if (nt > 0) publish();
       Decay decay = decay_over(kC, ln);
-      for (int it = 0; it < n_upd; ++it) {
-        const int s = it & 1, n = run.tokens(run.a + it);
-        // the scores have read k; its scaled form replaces it
-        ok = __all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 8) && wait(C::kFullK + s, (it / 2) & 1u, 8));
-        if (!ok) break;
-        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes, base + C::kRestOff, C::kTileBytes, nullptr, tid, n, 1.f,
-                                 rev ? w_tab : w_tab + kC - n);
+      // the scores have read a tile's k; its scaled form replaces it
+      auto scale = [&](int it) {
+        const int s = it % C::kKStages, n = run.tokens(run.a + it);
+        if (!__all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 8) && wait(C::kFullK + s, (it / C::kKStages) & 1u, 8)))
+          return false;
+        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes,
+                                 base + C::kRestOff + (C::kRoomy ? (it & 1) * C::kRestBytes : 0), C::kTileBytes, nullptr, tid, n,
+                                 1.f, rev ? w_tab : w_tab + kC - n);
         fence_proxy_async_smem();
         warp_arrive(bar(C::kKwFull), lane);
+        return true;
+      };
+      for (int it = C::kRoomy ? -1 : 0; it < n_upd; ++it) {
+        const int next = C::kRoomy ? it + 1 : it;
+        if (next < n_upd && !(ok = scale(next))) break;
+        if (it < 0) continue;
+        const int n = run.tokens(run.a + it);
         ok = __all_sync(0xffffffffu, wait(C::kUFull, it & 1u, 8));
         if (!ok) break;
         tc_fence_after();
@@ -690,9 +719,14 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       // an aborted CTA stores no state; its outputs are not valid either
       if (ok && !*abort_flag && p.state_out != nullptr && row < D) {
         float* out = p.state_out + bh * D * D;
+        if (p.state_t) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          out[p.state_t ? (long long)(hf * kCols + c) * D + row : (long long)row * D + hf * kCols + c] = st[c];
+          for (int c = 0; c < kCols; ++c) out[(hf * kCols + c) * D + row] = st[c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4)
+            *reinterpret_cast<float4*>(out + row * D + hf * kCols + c) = make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
+        }
       }
     }
   }
@@ -796,6 +830,7 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     }
     __syncwarp();
   } else if (warp == 1) {
+    const uint32_t lead = elect_lead();
     constexpr uint32_t id_u = idesc_bf16_f32(128, D, 1) | kAMajorMN;
     const uint64_t mn = smem_desc_sw128(base_u32, C::kBoxBytes, 1024);
     auto at = [](uint64_t d, uint32_t off) { return make_desc((uint32_t)d + (off >> 4), (uint32_t)(d >> 32)); };
@@ -811,11 +846,11 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
       for (int t = 0; t < TERMS; ++t)
 #pragma unroll
         for (int kk = 0; kk < C::kRows / 16; ++kk)
-          mma_ss_e(tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u), at(mn, v + kk * 2048u), id_u,
+          mma_ss_l(lead, tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u), at(mn, v + kk * 2048u), id_u,
                    it > 0 || t > 0 || kk > 0);
-      mma_commit_e(bar(C::kEmpty + s));
+      mma_commit_l(lead, bar(C::kEmpty + s));
     }
-    mma_commit_e(bar(ok ? C::kFinal : C::kDrain));
+    mma_commit_l(lead, bar(ok ? C::kFinal : C::kDrain));
     if (!ok && lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
     __syncwarp();
   } else {
