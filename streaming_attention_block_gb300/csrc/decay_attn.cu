@@ -120,6 +120,100 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
   }
 }
 
+// Short runs, token by token in fp32: one CTA per (b, h) and 32 value columns,
+// the state in registers (a warp owns D / 8 key rows, a lane one column).  The
+// state passes once, a token costs 0.2 us (fp32 multiply-adds and broadcast
+// reads), and nothing of the tile kernel's set-up is paid.
+constexpr int kShortBatch = 16;  // tokens staged at a time
+template <int D>
+__global__ void __launch_bounds__(256) decay_short_kernel(const __grid_constant__ DecayTileParams p) {
+  constexpr int R = D / 8;
+  __shared__ __align__(16) float sq[kShortBatch][D], sk[kShortBatch][D], sv[kShortBatch][32];
+  __shared__ float part[8][kShortBatch][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long bh = blockIdx.x / (D / 32);
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H), col0 = (int)(blockIdx.x % (D / 32)) * 32, col = col0 + lane;
+  const int len = p.seq_len != nullptr ? min(max(__ldg(p.seq_len + b), 0), p.L) : p.L;
+  const Decay decay(decay_ln(p.log_decay, h));
+  float s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) s[r] = 0.f;
+  if (p.state_in != nullptr) {
+    const float* in = p.state_in + bh * D * D;
+    if (p.state_t) {
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(in + col * D + warp * R + r);
+        s[r] = x.x, s[r + 1] = x.y, s[r + 2] = x.z, s[r + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = in[(warp * R + r) * D + col];
+    }
+  }
+  const long long base = (long long)b * p.L;
+  for (int c0 = 0; c0 < len; c0 += kShortBatch) {
+    const int n = min(kShortBatch, len - c0);
+    auto row_of = [&](int i) { return ((base + (p.reverse ? len - 1 - (c0 + i) : c0 + i)) * p.H + h) * D; };
+    __syncthreads();
+    for (int i = tid; i < n * (D / 8); i += 256) {
+      const int t = i / (D / 8), d = i % (D / 8) * 8;
+      const long long e = row_of(t) + d;
+      const uint4 q = *reinterpret_cast<const uint4*>(p.q + e), k = *reinterpret_cast<const uint4*>(p.k + e);
+      const uint32_t qw[4] = {q.x, q.y, q.z, q.w}, kw[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sq[t][d + 2 * j] = __uint_as_float(qw[j] << 16);
+        sq[t][d + 2 * j + 1] = __uint_as_float(qw[j] & 0xFFFF0000u);
+        sk[t][d + 2 * j] = __uint_as_float(kw[j] << 16) * p.kv_mul;
+        sk[t][d + 2 * j + 1] = __uint_as_float(kw[j] & 0xFFFF0000u) * p.kv_mul;
+      }
+    }
+    for (int i = tid; i < n * 32; i += 256) sv[i >> 5][i & 31] = bf(p.v[row_of(i >> 5) + col0 + (i & 31)]);
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      const float v = sv[t][lane];
+      float o = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sk[t][warp * R + r]);
+        const float4 q4 = *reinterpret_cast<const float4*>(&sq[t][warp * R + r]);
+        const float k[4] = {k4.x, k4.y, k4.z, k4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = s[r + j];
+          if (!p.reverse) x = decay(x);
+          x = fmaf(k[j], v, x);
+          o = fmaf(q[j], x, o);
+          s[r + j] = p.reverse ? decay(x) : x;
+        }
+      }
+      part[warp][t][lane] = o;
+    }
+    __syncthreads();
+    for (int i = tid; i < n * 32; i += 256) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) o += part[w][i >> 5][i & 31];
+      p.o[row_of(i >> 5) + col0 + (i & 31)] = (uint16_t)(pack_bf16(o * p.o_mul, 0.f) & 0xFFFFu);
+    }
+  }
+  for (int t = len + warp; t < p.L; t += 8) p.o[((base + t) * p.H + h) * D + col] = 0;
+  if (p.state_out != nullptr) {
+    float* out = p.state_out + bh * D * D;
+    if (p.state_t) {
+#pragma unroll
+      for (int r = 0; r < R; r += 4)
+        *reinterpret_cast<float4*>(out + col * D + warp * R + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) out[(warp * R + r) * D + col] = s[r];
+    }
+  }
+}
+
 // ---------------------------------------------------------------- tiles
 //
 // Tokens in tiles of C = 128.  With S the state before a tile of n live
@@ -803,14 +897,16 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   const uint32_t tmem = misc[0];
   const int first = run.first(), count = run.count();
   const int nt = (count + C::kRows - 1) / C::kRows;
-  // against the run's order, so that the tokens the run starts with are the
-  // ones L2 still holds
+  // against the run's order: the tokens it starts with are read last
   auto start = [&](int it) { return (p.reverse ? it : nt - 1 - it) * C::kRows; };
   auto wait = [&](int i, uint32_t parity, unsigned site) {
     return wait_bounded(bar(i), parity, abort_flag, site, p.err_word);
   };
   if (warp == 0) {
     if (lane == 0) {
+      // (2 x 30720 tokens of 12 heads: 196 us for the whole call, 202 us with the
+      // default policy)
+      const uint64_t policy = l2_evict_first();
       int issued = 0;
       for (int it = 0; it < nt; ++it) {
         const int s = it % C::kStages;
@@ -819,8 +915,8 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx) {
           const uint32_t dst = base_u32 + s * C::kStageBytes + bx * C::kBoxBytes;
-          tma_load_4d(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b);
-          tma_load_4d(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b);
+          tma_load_4d_hint(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b, policy);
+          tma_load_4d_hint(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b, policy);
         }
         ++issued;
       }
@@ -1019,6 +1115,12 @@ cudaError_t launch_tiles(const DecayTileParams& p, cudaStream_t s) {
 cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s) {
   if (p.state_out != nullptr) return p.D == 128 ? launch_segments<128, 3>(p, s) : launch_segments<64, 3>(p, s);
   return p.D == 128 ? launch_segments<128, 2>(p, s) : launch_segments<64, 2>(p, s);
+}
+
+cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s) {
+  const unsigned grid = (unsigned)((long long)p.B * p.H * (p.D / 32));
+  return p.D == 128 ? launch(decay_short_kernel<128>, grid, 256, 0, p, s)
+                    : launch(decay_short_kernel<64>, grid, 256, 0, p, s);
 }
 
 cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s) {

@@ -238,6 +238,7 @@ struct RotaryParams {
 struct DecayTileParams {
   CUtensorMap q_map, k_map, v_map, o_map;  // dims (D, L, H, B), box (64, 128, 1, 1), SW128
   CUtensorMap k_map_h, v_map_h;            // the same with 64-row boxes (segment sums)
+  const uint16_t *q, *k, *v;  // short runs read them directly
   uint16_t* o;              // tiles without a live token are zeroed directly
   const float* log_decay;   // [H]
   const int* seq_len;       // [B] or null
@@ -277,6 +278,7 @@ cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
 // the state before every segment, into p.carry (nseg > 1); the state after the
 // last, if p.state_out is given
 cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s);
+cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
