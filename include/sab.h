@@ -616,7 +616,7 @@ sab_status sab_get_last_device_error(void* stream);
  * boundary), the scale entry of an 8-bit append, every key run of an
  * attention CTA against the rows of its source, the FP8 scale entries it
  * reads, its workspace tile and counter, and the row ranges of the backward
- * tiles.  The checks are uniform over a CTA: a CTA that fails one records
+ * tiles, and the places of the decay attention's carried states.  The checks are uniform over a CTA: a CTA that fails one records
  * SAB_ERR_BOUNDS in the device error word and leaves through the same path as
  * a CTA whose wait gave up (no copy, no store; split-merge counters still
  * return to zero).  Nothing traps.  Release builds compile the checks out.

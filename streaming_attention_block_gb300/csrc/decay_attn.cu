@@ -280,6 +280,19 @@ __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned*
   }
 }
 
+// Debug builds: the place of a segment's state lies inside the scratch, and the
+// block belongs to a sequence.  Uniform over the CTA, before any copy or store.
+__device__ __forceinline__ bool in_bounds(const DecayTileParams& p, long long bh, int seg) {
+  if constexpr (kDebugBounds) {
+    if (bh >= 0 && bh < (long long)p.B * p.H && seg >= 0 && seg < p.nseg &&
+        (p.nseg == 1 || bh * p.nseg + seg < p.carry_states))
+      return true;
+    if (threadIdx.x == 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
+    return false;
+  }
+  return true;
+}
+
 // The tiles [r0, r1) of a segment in run order, and of those the live ones
 // [a, b) (tokens inside the sequence).
 struct Run {
@@ -455,8 +468,9 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = blockIdx.x % p.nseg;
-  const long long bh = blockIdx.x / p.nseg;
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  int b = (int)(blockIdx.x / p.nseg / p.H);
+  const int h = (int)(blockIdx.x / p.nseg % p.H);
+  if (!in_bounds(p, blockIdx.x / p.nseg, seg)) return;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i)
@@ -477,6 +491,23 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   // let it start only after their own waits, so that everything before them
   // is complete: all but the carried states may be read, and worked on, now.
   if (p.nseg == 1) griddep_wait();
+  if (p.by_length) {
+    // more sequences than SMs, of unequal lengths: the longest first, so that
+    // the last to start are the shortest (8 sequences of up to 2047 tokens, 24
+    // heads of 64, eight draws: 42.3 us on average, 47.6 us in their own order)
+    int* lens = reinterpret_cast<int*>(base + C::kTabOff);  // the tables come later
+    if ((int)threadIdx.x < p.B) lens[threadIdx.x] = min(max(__ldg(p.seq_len + threadIdx.x), 0), p.L);
+    __syncthreads();
+    if ((int)threadIdx.x < p.B) {
+      int rank = 0;
+      for (int i = 0; i < p.B; ++i)
+        rank += lens[i] > lens[threadIdx.x] || (lens[i] == lens[threadIdx.x] && i < (int)threadIdx.x);
+      if (rank == b) misc[2] = threadIdx.x;
+    }
+    __syncthreads();
+    b = (int)misc[2];
+  }
+  const long long bh = (long long)b * p.H + h;
   const Run run(p, b, seg);
   const float ln = decay_ln(p.log_decay, h), ld2 = ln * kLog2e;
   if (threadIdx.x < 256) {
@@ -589,12 +620,15 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       }
       if (it < n_upd) {
         const uint32_t rest = C::kRestOff + (C::kRoomy ? (uint32_t)(it & 1) * C::kRestBytes : 0u);
+        // the small parts first: an accumulator is cut short at every addition,
+        // by up to 2^-23 of what it holds, always towards zero (24 additions at
+        // full size lost 6e-7 of the state, 8 lose 1e-7)
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
+        for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk)
             mma_ss_l(lead, tmem + C::kUpd, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
-                     at(mn, v + kk * 2048u), id_u, t > 0 || kk > 0);
+                     at(mn, v + kk * 2048u), id_u, t < TERMS - 1 || kk > 0);
         mma_commit_l(lead, bar(C::kUFull));
         mma_commit_l(lead, bar(C::kEmptyK + s));
         if (C::kRoomy) mma_commit_l(lead, bar(C::kEmptyV + sv));
@@ -835,7 +869,9 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
 // A segment's own contribution to the state after it: its tokens' updates with
 // the decays to the segment's end, accumulated in TMEM over the segment, 64
 // tokens at a time.  Nothing but the loads and the scaling of k runs per
-// step, so the loads are kept many steps ahead.
+// step, so the loads are kept many steps ahead.  A sum that the caller gets
+// (TERMS = 3) is moved to fp32 registers every 256 tokens: an accumulator loses
+// 1e-8 of itself at every addition, always towards zero.
 template <int D_, int TERMS_>
 struct SegCfg {
   static constexpr int D = D_, TERMS = TERMS_;
@@ -850,7 +886,12 @@ struct SegCfg {
   static constexpr uint32_t kPadOff = kRestOff + 2 * kRestBytes;            // D = 64: behind the last A operand
   static constexpr uint32_t kBarOff = kPadOff + (D == 64 ? kTileBytes : 0);
   static constexpr int kFull = 0, kEmpty = kStages, kScaled = 2 * kStages, kFinal = kScaled + 2, kDrain = kFinal + 1,
-                       kNumBars = kDrain + 1;
+                       kGroupFull = kDrain + 1 /* [2] */, kGroupFree = kGroupFull + 2 /* [2] */,
+                       kNumBars = kGroupFree + 2;
+  // TERMS = 3: the sum leaves TMEM for fp32 registers every kGroup steps, first
+  // parts and the others apart, two buffers of 2 D columns
+  static constexpr int kGroup = 4;
+  static constexpr uint32_t kTmemCols = TERMS == 3 ? 4 * D : 128;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kTabOff = kMiscOff + 16;                        // decay powers of k
   static constexpr uint32_t kSmemBytes = kTabOff + 4 * kRows + 1024;
@@ -874,14 +915,16 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   const int seg = blockIdx.x % nrun;
   const long long bh = blockIdx.x / nrun;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  if (!in_bounds(p, bh, seg)) return;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), i == C::kScaled || i == C::kScaled + 1 ? 8 : 1);
+    for (int i = 0; i < C::kNumBars; ++i)
+      mbar_init(bar(i), i == C::kScaled || i == C::kScaled + 1 ? 8 : i >= C::kGroupFree ? 16 : 1);
     misc[1] = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(misc), 128);
+    tmem_alloc(smem_u32(misc), C::kTmemCols);
     tmem_relinquish();
   }
   griddep_wait();
@@ -938,13 +981,32 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
       if (!ok) break;
       tc_fence_after();
       const uint32_t k = s * C::kStageBytes, v = k + C::kTileBytes, rest = C::kRestOff + (it & 1) * C::kRestBytes;
+      if constexpr (TERMS == 3) {
+        const int g = it / C::kGroup, buf = g & 1;
+        const bool fresh = it % C::kGroup == 0;
+        if (fresh && g >= 2) {
+          ok = __all_sync(0xffffffffu, wait(C::kGroupFree + buf, (g / 2 - 1) & 1u, 13));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t acc = tmem + (uint32_t)buf * 2 * D;
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t)
+        for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
-        for (int kk = 0; kk < C::kRows / 16; ++kk)
-          mma_ss_l(lead, tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u), at(mn, v + kk * 2048u), id_u,
-                   it > 0 || t > 0 || kk > 0);
-      mma_commit_l(lead, bar(C::kEmpty + s));
+          for (int kk = 0; kk < C::kRows / 16; ++kk)
+            mma_ss_l(lead, t == 0 ? acc : acc + D, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
+                     at(mn, v + kk * 2048u), id_u, !fresh || t == 1 || kk > 0);
+        mma_commit_l(lead, bar(C::kEmpty + s));
+        if (it % C::kGroup == C::kGroup - 1 || it + 1 == nt) mma_commit_l(lead, bar(C::kGroupFull + buf));
+      } else {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+          for (int kk = 0; kk < C::kRows / 16; ++kk)
+            mma_ss_l(lead, tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
+                     at(mn, v + kk * 2048u), id_u, it > 0 || t > 0 || kk > 0);
+        mma_commit_l(lead, bar(C::kEmpty + s));
+      }
     }
     mma_commit_l(lead, bar(ok ? C::kFinal : C::kDrain));
     if (!ok && lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
@@ -953,6 +1015,34 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
     const int grp = (warp - 2) >> 3, tid = (threadIdx.x - 64) & 255, hf = ((warp - 2) >> 2) & 1, quad = warp & 3;
     const int row = quad * 32 + lane;
     constexpr int kCols = D / 2;
+    // TERMS = 3: this thread's quarter of the row, summed over the groups
+    constexpr int kPart = D / 4;
+    const int part = ((warp - 2) >> 2) & 3;
+    float sum[TERMS == 3 ? kPart : 1];
+    int added = 0;  // groups
+    auto add_group = [&]() {
+      const int buf = added & 1;
+      if (!__all_sync(0xffffffffu, wait(C::kGroupFull + buf, (added / 2) & 1u, 15))) return false;
+      tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + buf * 2 * D + part * kPart;
+#pragma unroll
+      for (int c0 = 0; c0 < kPart; c0 += 16) {
+        uint32_t x[16], y[16];
+        tmem_ld16(src + c0, x);
+        tmem_ld16(src + D + c0, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) sum[c0 + c] += __uint_as_float(x[c]) + __uint_as_float(y[c]);
+      }
+      tc_fence_before();
+      warp_arrive(bar(C::kGroupFree + buf), lane);
+      ++added;
+      return true;
+    };
+    if constexpr (TERMS == 3) {
+#pragma unroll
+      for (int c = 0; c < kPart; ++c) sum[c] = 0.f;
+    }
     bool ok = true;
     for (int it = grp; it < nt; it += 2) {
       const int s = it % C::kStages, t0 = start(it);  // from the segment's first token
@@ -968,27 +1058,40 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
                                      p.reverse ? w_tab : w_tab + max(-after, 0));
       fence_proxy_async_smem();
       warp_arrive(bar(C::kScaled + grp), lane);
+      if constexpr (TERMS == 3) {  // the group before has been multiplied by now
+        if (it % C::kGroup >= 2 && it >= C::kGroup && !(ok = add_group())) break;
+      }
     }
-    if (ok && grp == 0) ok = __all_sync(0xffffffffu, wait(C::kFinal, 0, 15));
-    ok = ok && grp == 0;
-    ok = ok && !*abort_flag;
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      float* out = p.carry + (bh * p.nseg + seg) * D * D + piece_index<D>(row, hf * kCols);
+    if constexpr (TERMS == 3) {
+      while (ok && added * C::kGroup < nt) ok = add_group();
+      if (__all_sync(0xffffffffu, ok && !*abort_flag) && row < D) {
+        float* out = p.carry + (bh * p.nseg + seg) * D * D + piece_index<D>(row, part * kPart);
 #pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        uint32_t x[32];
-        if (nt > 0) {
-          tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + hf * kCols + c0, x);
-          tmem_wait_ld();
-        } else {
+        for (int c = 0; c < kPart; c += 4)
+          *reinterpret_cast<float4*>(out + c * 2 * D) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+      }
+    } else {
+      if (ok && grp == 0) ok = __all_sync(0xffffffffu, wait(C::kFinal, 0, 15));
+      ok = ok && grp == 0;
+      ok = ok && !*abort_flag;
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        float* out = p.carry + (bh * p.nseg + seg) * D * D + piece_index<D>(row, hf * kCols);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = 0u;
-        }
-        if (row < D) {
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          uint32_t x[32];
+          if (nt > 0) {
+            tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + hf * kCols + c0, x);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<uint4*>(out + (c0 + c) * 2 * D) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            for (int c = 0; c < 32; ++c) x[c] = 0u;
+          }
+          if (row < D) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<uint4*>(out + (c0 + c) * 2 * D) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+          }
         }
       }
     }
@@ -997,7 +1100,7 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -1013,6 +1116,7 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant_
   const int e = ((int)(blockIdx.x % kBlocks) * 128 + threadIdx.x) * 4;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
+  if (!in_bounds(p, bh, p.nseg - 1)) return;
   float* c = p.carry + bh * p.nseg * D * D + e;
   // its place in the caller's states, where (row, col) may be held at (col, row)
   const int row = (e / 4) % D, col = (e / (8 * D)) * 4 + ((e / 4) % (2 * D) / D) * (D / 2);

@@ -872,6 +872,8 @@ static sab_status rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, 
   const int esize = dtype == SAB_DTYPE_BF16 ? 2 : 4;
   if (!rotary_rows_ok(q, B, L, D, esize) || (k != nullptr && !rotary_rows_ok(k, B, L, D, esize)))
     return SAB_ERR_INVALID_ARG;
+  // one tensor's rows turned twice, or turned while the other is read
+  if (k != nullptr && (k->out == q->out || k->out == q->in || q->out == k->in)) return SAB_ERR_INVALID_ARG;
   RotaryParams p;
   memset(&p, 0, sizeof(p));
   for (int w = 0; w < 2; ++w) {
@@ -953,7 +955,7 @@ struct DecayRun {
   bool chain;
 };
 static sab_status decay_run(const DecayRun& r, const float* log_decay, const int* seq_len, int B, int L, int H, int D,
-                            void* workspace, void* stream) {
+                            void* workspace, size_t ws_bytes, void* stream) {
   DecayTileParams p;
   memset(&p, 0, sizeof(p));
   p.seg_tiles = decay_segment_tiles(B, L, H);
@@ -968,10 +970,12 @@ static sab_status decay_run(const DecayRun& r, const float* log_decay, const int
   p.state_out = r.out;
   p.carry = static_cast<float*>(workspace);
   p.carry_t = !r.chain;
+  p.carry_states = (long long)(ws_bytes / ((size_t)D * D * sizeof(float)));
   p.B = B;
   p.L = L;
   p.H = H;
   p.D = D;
+  p.by_length = seq_len != nullptr && p.nseg == 1 && B > 1 && B <= kMaxByLength && (long long)B * H > device_sms();
   p.reverse = r.reverse;
   p.state_t = r.state_t;
   p.kv_mul = r.kv_mul;
@@ -1005,7 +1009,7 @@ sab_status sab_decay_attention(const void* Q, const void* K, const void* V, cons
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
   return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, true}, log_decay, seq_len, B, L, H, D, workspace,
-                   stream);
+                   ws_bytes, stream);
 }
 
 sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -1066,7 +1070,7 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
                             {K, Q, dO, dV, d_state_out, cut ? d_state_in : nullptr, 1, 0, scale, 1.f, true},
                             {V, dO, Q, dK, d_state_out, cut ? nullptr : d_state_in, 1, 1, scale, 1.f, false}};
   for (const DecayRun& r : runs) {
-    const sab_status st = decay_run(r, log_decay, seq_len, B, L, H, D, workspace, stream);
+    const sab_status st = decay_run(r, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
     if (st != SAB_OK) return st;
   }
   return SAB_OK;

@@ -232,6 +232,8 @@ struct RotaryParams {
   unsigned long long step[kRotaryMaxPairs];
 };
 
+constexpr int kMaxByLength = 128;
+
 // One run of the decay recurrence over [B, L, H, D] rows (see
 // sab_decay_attention): forward, S = g S + (kv_mul k) v^T then o = o_mul q S;
 // reversed in time, S += (kv_mul k) v^T, o = o_mul q S, then S *= g.
@@ -245,9 +247,11 @@ struct DecayTileParams {
   const float* state_in;    // [B, H, D, D] or null
   float* state_out;         // or null
   float* carry;             // [B, H, nseg, D, D] scratch when nseg > 1
+  long long carry_states;   // debug-build index checks: states that scratch holds
   int carry_t;              // the carried states are [v dimension][k dimension]
   int B, L, H, D;
   int nseg, seg_tiles;      // segments per sequence, 128-token tiles per segment
+  int by_length;            // sequences are taken longest first (at most kMaxByLength of them, nseg == 1)
   int reverse;
   int state_t;              // the caller's states are [v dimension][k dimension]
   float kv_mul, o_mul;

@@ -236,10 +236,11 @@ def test_long_sequence(D, L):
 
 
 @gpu
-@pytest.mark.parametrize("case", [(8, 1024, 6, 64), (3, 2300, 4, 128), (2, 9000, 2, 128)])
+@pytest.mark.parametrize("case", [(8, 1024, 6, 64), (3, 2300, 4, 128), (2, 9000, 2, 128), (23, 400, 8, 64)])
 def test_ragged_segments(case):
     """Unequal lengths cut into segments: some end in the middle of one, some
-    have none of their tokens in it."""
+    have none of their tokens in it.  The last case has more sequences than
+    SMs, which are then taken longest first."""
     B, L, H, D = case
     lens = torch.tensor([L * (b * 37 % 100) // 100 for b in range(B)], dtype=torch.int32, device="cuda")
     lens[-1] = L

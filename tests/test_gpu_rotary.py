@@ -239,7 +239,8 @@ def test_refusals_before_any_cuda_call():
         bad = [dict(pl=None), dict(pl=sab.RotaryPlan()), dict(q=0), dict(q=_rows(inp=None)), dict(q=_rows(out=None)),
                dict(q=_rows(inp=4104)), dict(q=_rows(out=8200)), dict(q=_rows(heads=0)), dict(q=_rows(in_token=132)),
                dict(q=_rows(out_token=64)), dict(q=_rows(in_token=-128)), dict(B=2),  # batches on top of each other
-               dict(q=_rows(out=4096, out_token=256)), dict(k=_rows(heads=-1)), dict(k=_rows(inp=None)),
+               dict(q=_rows(out=4096, out_token=256)), dict(k=_rows()), dict(k=_rows(inp=8192, out=12288)),
+               dict(k=_rows(out=4096)), dict(k=_rows(heads=-1)), dict(k=_rows(inp=None)),
                dict(pl=multi), dict(pos=ctypes.c_void_p(4100)), dict(D=60), dict(D=0), dict(D=264), dict(D=32),
                dict(B=0), dict(L=0), dict(L=(1 << 30) + 1), dict(dt=2), dict(dt=-1),
                dict(pl=multi, pos=ctypes.c_void_p(4097))]
