@@ -516,7 +516,8 @@ typedef struct {
 
 /*
  * Rotate B x L tokens of q and (unless k is NULL) of k, which may have
- * another number of heads, in one launch.
+ * another number of heads, in one launch.  q and k may read the same tensor,
+ * but neither may be written where the other reads or writes.
  * positions  device int64 [axes, B, L], 8-byte aligned, any sign; or NULL for
  *            one axis: token t of every sequence is at first_position + t.
  * D          head dimension, a multiple of 8, plan->dims <= D <= 256.
@@ -561,8 +562,11 @@ sab_status sab_rotary_backward(const sab_rotary_plan* plan, const sab_rotary_row
  *             can overlap on the GPU need one each.
  * Products run on bf16 tensor cores with fp32 accumulation: q, k, v as they
  * are, the masked scores and the state's copy that multiplies q rounded to
- * bf16, the state itself held in fp32 and fed by k rounded to 16 bits of
- * mantissa.  D must be 64 or 128.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ * bf16; the state itself is held in fp32 and fed by k with 24 bits of mantissa
+ * (16 bits where no state_out is wanted).  Short runs are fp32 throughout.  A
+ * live k or v that is not finite reaches, besides the later outputs, those of
+ * up to 127 tokens before it (masked scores are zeros, and 0 * NaN is NaN).
+ * D must be 64 or 128.  Errors: INVALID_ARG, WORKSPACE, CUDA.
  */
 size_t sab_decay_attention_workspace(int B, int L, int H, int D);
 sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -615,8 +619,10 @@ sab_status sab_get_last_device_error(void* stream);
  * slot rows of an append (inside the (batch, head) block, on a slot
  * boundary), the scale entry of an 8-bit append, every key run of an
  * attention CTA against the rows of its source, the FP8 scale entries it
- * reads, its workspace tile and counter, and the row ranges of the backward
- * tiles, and the places of the decay attention's carried states.  The checks are uniform over a CTA: a CTA that fails one records
+ * reads, its workspace tile and counter, the row ranges of the backward
+ * tiles, and the places of the decay attention's carried states.  (The rotary
+ * and single-token kernels form no index but from their block and the checked
+ * shape.)  The checks are uniform over a CTA: a CTA that fails one records
  * SAB_ERR_BOUNDS in the device error word and leaves through the same path as
  * a CTA whose wait gave up (no copy, no store; split-merge counters still
  * return to zero).  Nothing traps.  Release builds compile the checks out.

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -113,9 +114,9 @@ def _check(status: int, what: str):
         raise SabError(status, what)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:  # the raw handle of torch.cuda.current_stream(), without building the object
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -514,23 +515,30 @@ def _arg(t, shape, dtype, name, dev):
     return t.data_ptr()
 
 
+_ROWS = struct.Struct("@PPiqqqq")  # the layout of RotaryRows, packed faster than the structure is built
+
+
+def _strides(t, name):
+    """(batch, token) strides of [B, L, H, D] rows whose heads are contiguous."""
+    B, L, H, D = t.shape
+    sb, sl, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return sb if B > 1 else H * D, sl if L > 1 else H * D
+
+
 def _rotary_rows(x, out, name, dev):
-    """Token rows of ``x`` and ``out`` ([B, L, H, D] with contiguous heads)."""
+    """Token rows of ``x`` and ``out``: [B, L, H, D] with contiguous heads."""
     for t, n in ((x, name), (out, name + "_out")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise TypeError(f"{n}: expected a [B, L, H, D] torch tensor")
         if t.get_device() != dev or t.dtype not in _DTYPES:
             _refuse(t, n, dev, tuple(_DTYPES))
-    B, L, H, D = x.shape
-    if out.shape != x.shape or out.dtype != x.dtype:
+    if out is not x and (out.shape != x.shape or out.dtype != x.dtype):
         raise ValueError(f"{name}_out: expected the shape and type of {name}")
-    st = []
-    for t, n in ((x, name), (out, name + "_out")):
-        sb, sl, sh, sd = t.stride()
-        if (sd != 1 and D > 1) or (sh != D and H > 1):
-            raise ValueError(f"{n}: a token's heads must be contiguous")
-        st += [sb if B > 1 else H * D, sl if L > 1 else H * D]
-    return RotaryRows(x.data_ptr(), out.data_ptr(), H, *st)
+    ib, il = _strides(x, name)
+    ob, ol = (ib, il) if out is x else _strides(out, name + "_out")
+    return _ROWS.pack(x.data_ptr(), out.data_ptr(), x.shape[2], ib, il, ob, ol)
 
 
 def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, stream):
@@ -540,14 +548,17 @@ def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, strea
     k = None
     if K is not None:
         k = _rotary_rows(K, K_out, "K", dev)
-        if K.shape[0] != B or K.shape[1] != L or K.shape[3] != D or K.dtype != Q.dtype:
+        Bk, Lk, _, Dk = K.shape
+        if Bk != B or Lk != L or Dk != D or K.dtype != Q.dtype:
             raise ValueError("K: expected Q's batch, length, head dimension and type")
     if positions is not None and positions.__class__ is not int:
         n = plan.axes * B * L
         shape = positions.shape if positions.numel() == n else (plan.axes, B, L)
         positions = _arg(positions, shape, torch.int64, "positions", dev)
-    _check(fn(ctypes.byref(plan), ctypes.byref(q), None if k is None else ctypes.byref(k), positions,
-              int(first_position), B, L, D, _DTYPES[Q.dtype], _stream(stream)), what)
+    status = fn(ctypes.byref(plan), q, k, positions, int(first_position), B, L, D, _DTYPES[Q.dtype],
+                _stream(stream, dev))
+    if status != 0:
+        raise SabError(status, what)
 
 
 def rotary(plan: RotaryPlan, Q, K, Q_out, K_out=None, positions=None, first_position: int = 0, stream=None):
@@ -611,8 +622,8 @@ def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_ou
     _check(library().sab_decay_attention(
         _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
         _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
-        _arg(state_in, st, f4, "state_in", dev), B, L, H, D, float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes,
-        _stream(stream)), "decay_attention")
+        _arg(state_in, st, f4, "state_in", dev), B, L, H, D, float(scale), _arg(O, x, bf, "O", dev),
+        _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes, _stream(stream, dev)), "decay_attention")
 
 
 def decay_attention_step(Q, K, V, log_decay, scale: float, state_in, state_out, O, active=None, stream=None):
@@ -624,7 +635,8 @@ def decay_attention_step(Q, K, V, log_decay, scale: float, state_in, state_out, 
     _check(library().sab_decay_attention_step(
         _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
         _arg(log_decay, (H,), f4, "log_decay", dev), _arg(active, (B,), torch.int32, "active", dev),
-        _arg(state_in, st, f4, "state_in", dev), B, H, D, float(scale), _arg(O, x, bf, "O", dev), _arg(state_out, st, f4, "state_out", dev), _stream(stream)), "decay_attention_step")
+        _arg(state_in, st, f4, "state_in", dev), B, H, D, float(scale), _arg(O, x, bf, "O", dev),
+        _arg(state_out, st, f4, "state_out", dev), _stream(stream, dev)), "decay_attention_step")
 
 
 def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, state_in=None, d_state_out=None,
@@ -640,9 +652,9 @@ def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, s
     _check(library().sab_decay_attention_backward(
         _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev), _arg(dO, x, bf, "dO", dev),
         _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
-        _arg(state_in, st, f4, "state_in", dev), _arg(d_state_out, st, f4, "d_state_out", dev), B, L, H, D, float(scale),
-        _arg(dQ, x, bf, "dQ", dev), _arg(dK, x, bf, "dK", dev), _arg(dV, x, bf, "dV", dev),
-        _arg(d_state_in, st, f4, "d_state_in", dev), ws, ws_bytes, _stream(stream)),
+        _arg(state_in, st, f4, "state_in", dev), _arg(d_state_out, st, f4, "d_state_out", dev), B, L, H, D,
+        float(scale), _arg(dQ, x, bf, "dQ", dev), _arg(dK, x, bf, "dK", dev), _arg(dV, x, bf, "dV", dev),
+        _arg(d_state_in, st, f4, "d_state_in", dev), ws, ws_bytes, _stream(stream, dev)),
         "decay_attention_backward")
 
 

@@ -410,9 +410,10 @@ constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-maj
 
 // The tile kernel's warps: 0 loads, 1 issues MMAs, 2-9 ("rows") turn scores
 // into P and accumulators into output rows, 10-17 ("state") scale k and carry
-// the state, 18 stores.  The two element groups work on the same tile at once:
-// neither needs the other within a tile, and each alone takes about half of
-// the time HBM needs for a tile.
+// the state, 18 stores.  The two element groups work on the same tile at once
+// and need each other only through the MMAs.  (One group doing all four steps
+// in turn: 198 us for 2 x 30720 tokens of 12 heads of 128; two: 135 us, the
+// four roles' code kept small enough for the instruction cache, 222 us before.)
 // D = 128: a tile's output is staged over its v once the update has read it;
 // nothing else is free.  D = 64 has room for an output buffer of its own and
 // for two sets of k's parts (kRoomy): the next tile's scores go ahead of the
@@ -555,7 +556,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       }
       if (*abort_flag) {
         auto drain = [&](int full, int stages, int n) {
-          for (int i = max(0, n - stages); i < n; ++i) wait_drain(bar(full + i % stages), (i / stages) & 1u, p.err_word);
+          for (int i = max(0, n - stages); i < n; ++i)
+            wait_drain(bar(full + i % stages), (i / stages) & 1u, p.err_word);
         };
         drain(C::kFullK, C::kKStages, nk);
         drain(C::kFullQ, C::kQStages, nq);
@@ -581,7 +583,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     };
     auto scores = [&](int it) {
       const int s = it % C::kKStages, sq = it % C::kQStages;
-      if (!wait_all(C::kFullQ + sq, (it / C::kQStages) & 1u, 10) || !wait_all(C::kFullK + s, (it / C::kKStages) & 1u, 10))
+      if (!wait_all(C::kFullQ + sq, (it / C::kQStages) & 1u, 10) ||
+          !wait_all(C::kFullK + s, (it / C::kKStages) & 1u, 10))
         return false;
       const uint32_t q = C::kQOff + sq * C::kTileBytes, k = C::kKOff + s * C::kTileBytes;
 #pragma unroll
@@ -610,7 +613,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
       if (!ok) break;
 #pragma unroll
       for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ts_l(lead, tmem + C::kIntra, tmem + C::kS + (kk >> 2) * 64 + (kk & 3) * 8, at(mn, v + kk * 2048u), id_o, kk > 0);
+        mma_ts_l(lead, tmem + C::kIntra, tmem + C::kS + (kk >> 2) * 64 + (kk & 3) * 8, at(mn, v + kk * 2048u), id_o,
+                 kk > 0);
       if (!C::kRoomy) mma_commit_l(lead, bar(C::kOFull));
       if (it < n_upd && !(ok = wait_all(C::kKwFull, it & 1u, 13))) break;
       if (C::kRoomy) {
@@ -648,8 +652,9 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         if (!wait(C::kOut + so, (C::kRoomy ? it : it / C::kVStages) & 1u, 14)) break;
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_store_4d(&p.o_map, base_u32 + (C::kRoomy ? C::kOutOff : C::kVOff) + so * C::kTileBytes + bx * C::kBoxBytes,
-                       bx * 64, run.tile(run.a + it) * kC, h, b);
+          tma_store_4d(&p.o_map,
+                       base_u32 + (C::kRoomy ? C::kOutOff : C::kVOff) + so * C::kTileBytes + bx * C::kBoxBytes, bx * 64,
+                       run.tile(run.a + it) * kC, h, b);
         tma_store_commit_and_wait_read();
         mbar_arrive(bar(C::kRoomy ? C::kOutFree : C::kEmptyV + so));
       }
@@ -810,9 +815,9 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         const int s = it % C::kKStages, n = run.tokens(run.a + it);
         if (!__all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 8) && wait(C::kFullK + s, (it / C::kKStages) & 1u, 8)))
           return false;
-        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes,
-                                 base + C::kRestOff + (C::kRoomy ? (it & 1) * C::kRestBytes : 0), C::kTileBytes, nullptr, tid, n,
-                                 1.f, rev ? w_tab : w_tab + kC - n);
+        uint8_t* rest = base + C::kRestOff + (C::kRoomy ? (it & 1) * C::kRestBytes : 0);
+        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes, rest, C::kTileBytes, nullptr, tid, n, 1.f,
+                                 rev ? w_tab : w_tab + kC - n);
         fence_proxy_async_smem();
         warp_arrive(bar(C::kKwFull), lane);
         return true;
@@ -853,7 +858,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         } else {
 #pragma unroll
           for (int c = 0; c < kCols; c += 4)
-            *reinterpret_cast<float4*>(out + row * D + hf * kCols + c) = make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
+            *reinterpret_cast<float4*>(out + row * D + hf * kCols + c) =
+                make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
         }
       }
     }
@@ -932,8 +938,10 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   const Run run(p, b, seg);
   const float ld2 = decay_ln(p.log_decay, h) * kLog2e;
   float* w_tab = reinterpret_cast<float*>(base + C::kTabOff);  // factor of k row j of a full step next to the end
-  if (threadIdx.x < C::kRows)
-    w_tab[threadIdx.x] = p.kv_mul * ex2((float)(p.reverse ? (int)threadIdx.x + 1 : C::kRows - 1 - (int)threadIdx.x) * ld2);
+  if (threadIdx.x < C::kRows) {
+    const int n = p.reverse ? (int)threadIdx.x + 1 : C::kRows - 1 - (int)threadIdx.x;
+    w_tab[threadIdx.x] = p.kv_mul * ex2((float)n * ld2);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -959,7 +967,8 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
         for (int bx = 0; bx < C::kBoxes; ++bx) {
           const uint32_t dst = base_u32 + s * C::kStageBytes + bx * C::kBoxBytes;
           tma_load_4d_hint(dst, &p.k_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b, policy);
-          tma_load_4d_hint(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b, policy);
+          tma_load_4d_hint(dst + C::kTileBytes, &p.v_map_h, bar(C::kFull + s), bx * 64, first + start(it), h, b,
+                           policy);
         }
         ++issued;
       }
@@ -1008,8 +1017,11 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
         mma_commit_l(lead, bar(C::kEmpty + s));
       }
     }
-    mma_commit_l(lead, bar(ok ? C::kFinal : C::kDrain));
-    if (!ok && lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
+    if (ok) mma_commit_l(lead, bar(C::kFinal));
+    if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
+      mma_commit_l(lead, bar(C::kDrain));
+      if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
+    }
     __syncwarp();
   } else {
     const int grp = (warp - 2) >> 3, tid = (threadIdx.x - 64) & 255, hf = ((warp - 2) >> 2) & 1, quad = warp & 3;
