@@ -924,24 +924,43 @@ static bool decay_short(int B, int L, int H, int D) {
   return L <= (D == 128 && (long long)B * H * (D / 32) <= device_sms() ? 40 : 16);
 }
 
-// Segments a decay attention run cuts each sequence into, so that B * H
-// sequences fill the SMs with one CTA each: tiles per segment.
-static int decay_segment_tiles(int B, int L, int H) {
+// How a call cuts its sequences.  A CTA takes a sequence's head as a whole, or,
+// when B * H of them leave SMs idle, segments of it, one CTA per SM; the states
+// before the segments then cost a pass over k and v and two launches.  Chosen
+// by the modelled times below, in us per call for T tiles in a row (whole) or
+// T tiles per segment with a share f of the SMs at work.  Measured, whole
+// against cut, without and with state_out, heads of 128: 2 sequences of 2 tiles
+// 8.2 / 11.3 and 16.0 / 11.9; 24 of 4 tiles 14.2 / 13.0 and 23.9 / 15.0; 72 of
+// 12 tiles 38.6 / 40.8 and 54.8 / 47.8; 24 of 32 tiles 95 / 37 and 127 / 43.
+// (More segments than SMs lose: 156 of 12 tiles 76.7 / 101.6.)
+struct DecayCut {
+  int nseg, seg_tiles;
+};
+static DecayCut decay_cut(int B, int L, int H, int D, bool state, bool gradients) {
   const int tiles = (L + kTileM - 1) / kTileM;
-  const long long want = device_sms() / ((long long)B * H);
-  if (want < 2) return tiles;
-  return (int)((tiles + want - 1) / want);
+  const long long bh = (long long)B * H, most = std::min<long long>(device_sms() / bh, tiles);
+  if (most < 2) return {1, tiles};
+  const int per = (int)((tiles + most - 1) / most), n = (tiles + per - 1) / per;
+  const double f = (double)(bh * n) / device_sms();
+  auto whole = [&](bool st) {
+    return D == 128 ? (st ? 8.5 + 3.8 * tiles : 3.0 + 2.9 * tiles) : (st ? 3.6 + 2.15 * tiles : 2.5 + 2.03 * tiles);
+  };
+  auto cut = [&](bool st) {
+    return D == 128 ? 7.0 + 4.3 * per + 4.5 * f + (st ? 1.0 + 0.5 * per + 2.5 * f : 0.0)
+                    : 6.2 + 2.95 * per + 1.7 * f + (st ? 0.6 + 0.3 * per + f : 0.0);
+  };
+  // gradients: three runs, of which the last finds its states worked out
+  const double a = whole(state) + (gradients ? 2 * whole(false) : 0.0);
+  const double c = cut(state) + (gradients ? cut(false) + (D == 128 ? 4.0 + 2.9 * per : 3.0 + 2.03 * per) : 0.0);
+  return n > 1 && c < a ? DecayCut{n, per} : DecayCut{1, tiles};
 }
-static int decay_segments(int B, int L, int H) {
-  const int tiles = (L + kTileM - 1) / kTileM, per = decay_segment_tiles(B, L, H);
-  return (tiles + per - 1) / per;
-}
-
-size_t sab_decay_attention_workspace(int B, int L, int H, int D) {
+static size_t decay_workspace(int B, int L, int H, int D, bool gradients) {
   if (!decay_shape_ok(B, L, H, D)) return 0;
-  const int n = decay_segments(B, L, H);
+  const int n = std::max(decay_cut(B, L, H, D, false, gradients).nseg, decay_cut(B, L, H, D, true, gradients).nseg);
   return n == 1 ? 0 : align_up((size_t)B * H * n * D * D * sizeof(float), kAlign);
 }
+
+size_t sab_decay_attention_workspace(int B, int L, int H, int D) { return decay_workspace(B, L, H, D, false); }
 
 // One run of the recurrence.  chain: work out the states before the segments
 // first; otherwise the workspace holds them from the run before, transposed.
@@ -954,12 +973,12 @@ struct DecayRun {
   float kv_mul, o_mul;
   bool chain;
 };
-static sab_status decay_run(const DecayRun& r, const float* log_decay, const int* seq_len, int B, int L, int H, int D,
-                            void* workspace, size_t ws_bytes, void* stream) {
+static sab_status decay_run(const DecayRun& r, const DecayCut& cut, const float* log_decay, const int* seq_len, int B,
+                            int L, int H, int D, void* workspace, size_t ws_bytes, void* stream) {
   DecayTileParams p;
   memset(&p, 0, sizeof(p));
-  p.seg_tiles = decay_segment_tiles(B, L, H);
-  p.nseg = decay_segments(B, L, H);
+  p.seg_tiles = cut.seg_tiles;
+  p.nseg = cut.nseg;
   p.q = static_cast<const uint16_t*>(r.q);
   p.k = static_cast<const uint16_t*>(r.k);
   p.v = static_cast<const uint16_t*>(r.v);
@@ -1008,7 +1027,8 @@ sab_status sab_decay_attention(const void* Q, const void* K, const void* V, cons
   const size_t need = sab_decay_attention_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, true}, log_decay, seq_len, B, L, H, D, workspace,
+  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, true},
+                   decay_cut(B, L, H, D, state_out != nullptr, false), log_decay, seq_len, B, L, H, D, workspace,
                    ws_bytes, stream);
 }
 
@@ -1039,9 +1059,7 @@ sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V,
   return launch_decay_step(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 
-size_t sab_decay_attention_backward_workspace(int B, int L, int H, int D) {
-  return sab_decay_attention_workspace(B, L, H, D);  // its three runs use it one after the other
-}
+size_t sab_decay_attention_backward_workspace(int B, int L, int H, int D) { return decay_workspace(B, L, H, D, true); }
 
 sab_status sab_decay_attention_backward(const void* Q, const void* K, const void* V, const void* dO,
                                         const float* log_decay, const int* seq_len, const float* state_in,
@@ -1065,12 +1083,13 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   // dV before dK: one chain of states serves both (dK's run holds them
   // transposed).  d_state_in, which may be d_state_out, is written by the last
   // run to read d_state_out: with the chain, or else by dK's run.
-  const bool cut = decay_segments(B, L, H) > 1;
+  const DecayCut how = decay_cut(B, L, H, D, d_state_in != nullptr, true);
+  const bool cut = how.nseg > 1;
   const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale, true},
                             {K, Q, dO, dV, d_state_out, cut ? d_state_in : nullptr, 1, 0, scale, 1.f, true},
                             {V, dO, Q, dK, d_state_out, cut ? nullptr : d_state_in, 1, 1, scale, 1.f, false}};
   for (const DecayRun& r : runs) {
-    const sab_status st = decay_run(r, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
+    const sab_status st = decay_run(r, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
     if (st != SAB_OK) return st;
   }
   return SAB_OK;
