@@ -329,14 +329,15 @@ __device__ __forceinline__ uint32_t piece_off(int row, int c) {
 // the first in place, the others (the rounded rest of the one before) in tiles
 // of `rest_bytes` behind `rest`.  Rows from n on become zero; so do those of
 // `v`, if given: they may hold anything, and 0 * NaN would reach every sum.
-template <int D, int ROWS, int TERMS>
+template <int D, int ROWS, int TERMS, int FROM = 0, int TO = ROWS>
 __device__ __forceinline__ void scale_rows(uint8_t* k, uint8_t* rest, uint32_t rest_bytes, uint8_t* v, int tid, int n,
                                            float f, const float* w) {
   constexpr int kPieces = D / 8;             // per row
   constexpr int kStep = 256 / kPieces;       // rows between a thread's pieces
-  uint32_t off = piece_off<ROWS>(tid / kPieces, tid % kPieces);
+  static_assert(FROM % kStep == 0 && TO % kStep == 0, "whole steps");
+  uint32_t off = piece_off<ROWS>(FROM + tid / kPieces, tid % kPieces);
 #pragma unroll 2
-  for (int row = tid / kPieces; row < ROWS; row += kStep, off += kStep * 128) {
+  for (int row = FROM + tid / kPieces; row < TO; row += kStep, off += kStep * 128) {
     uint32_t part[TERMS][4];
     if (row < n) {
       const float wr = f * w[row];
@@ -430,6 +431,7 @@ struct TileCfg {
   // box behind a k tile; they land in accumulator rows that nothing reads)
   static constexpr uint32_t kKOff = 0;                                       // [kKStages]; scaled in place
   static constexpr bool kRoomy = D == 64;
+  static constexpr int kShared = kRoomy ? kC : 80;  // k rows from here on are scaled by the rows' warps
   static constexpr int kKStages = kRoomy ? 3 : 2, kVStages = kRoomy ? 3 : TERMS == 3 ? 1 : 2;
   static constexpr uint32_t kRestOff = kKOff + kKStages * kTileBytes;             // [kRoomy ? 2 : 1][TERMS - 1]
   static constexpr uint32_t kRestBytes = (TERMS - 1) * kTileBytes;
@@ -477,7 +479,7 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
     for (int i = 0; i < C::kNumBars; ++i)
       mbar_init(bar(i), i == C::kPFull || i == C::kKwFull || i == C::kORead || i == C::kStFull ||
                                 (i >= C::kOut && i < C::kOut + 3)
-                            ? 8
+                            ? (i == C::kKwFull && C::kShared < kC ? 16 : 8)
                             : 1);
     misc[1] = 0;
     fence_mbar_init();
@@ -717,6 +719,17 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         }
         tc_fence_before();
         warp_arrive(bar(C::kPFull), lane);
+        // a share of k's rows while P V runs (96 sequences of 4096 tokens of heads
+        // of 128: 92 us, 97 us with all of them left to the state's warps)
+        if (C::kShared < kC && it < n_upd) {
+          const int s = it % C::kKStages;
+          ok = __all_sync(0xffffffffu, wait(C::kFullK + s, (it / C::kKStages) & 1u, 15));
+          if (!ok) break;
+          scale_rows<D, kC, TERMS, C::kShared, kC>(base + C::kKOff + s * C::kTileBytes, base + C::kRestOff, C::kTileBytes,
+                                                   nullptr, tid, n, 1.f, rev ? w_tab : w_tab + kC - n);
+          fence_proxy_async_smem();
+          warp_arrive(bar(C::kKwFull), lane);
+        }
         // output rows
         const float f = p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2);
         ok = __all_sync(0xffffffffu, wait(C::kOFull, it & 1u, 15));
@@ -816,8 +829,8 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
         if (!__all_sync(0xffffffffu, wait(C::kSFull, it & 1u, 8) && wait(C::kFullK + s, (it / C::kKStages) & 1u, 8)))
           return false;
         uint8_t* rest = base + C::kRestOff + (C::kRoomy ? (it & 1) * C::kRestBytes : 0);
-        scale_rows<D, kC, TERMS>(base + C::kKOff + s * C::kTileBytes, rest, C::kTileBytes, nullptr, tid, n, 1.f,
-                                 rev ? w_tab : w_tab + kC - n);
+        scale_rows<D, kC, TERMS, 0, C::kShared>(base + C::kKOff + s * C::kTileBytes, rest, C::kTileBytes, nullptr, tid, n,
+                                                1.f, rev ? w_tab : w_tab + kC - n);
         fence_proxy_async_smem();
         warp_arrive(bar(C::kKwFull), lane);
         return true;
