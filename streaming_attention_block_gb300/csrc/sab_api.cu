@@ -863,6 +863,10 @@ static sab_status rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, 
                          const long long* positions, long long first_position, int B, int L, int D, int dtype,
                          bool backward, void* stream) {
   if (plan == nullptr || plan->magic != kRotaryMagic || q == nullptr) return SAB_ERR_INVALID_ARG;
+  if (plan->axes < 1 || plan->axes > 3 || plan->dims < 2 || plan->dims > SAB_ROTARY_MAX_DIMS || plan->dims % 2 != 0)
+    return SAB_ERR_INVALID_ARG;
+  for (int j = 0; j < plan->dims / 2; ++j)
+    if (plan->axis[j] >= plan->axes) return SAB_ERR_INVALID_ARG;
   if (dtype != SAB_DTYPE_BF16 && dtype != SAB_DTYPE_FP32) return SAB_ERR_INVALID_ARG;
   if (B < 1 || L < 1 || L > (1 << 30) || (long long)B * L > (1LL << 31) || D < 8 || D % 8 != 0 ||
       D > SAB_ROTARY_MAX_DIMS || plan->dims > D)

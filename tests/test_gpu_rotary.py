@@ -246,6 +246,13 @@ def test_refusals_before_any_cuda_call():
                dict(pl=multi, pos=ctypes.c_void_p(4097))]
         for kw in bad:
             assert call(fn=fn, **kw) == 1, (fn, kw)
+    for field, value in (("axes", 0), ("axes", 4), ("dims", 0), ("dims", 63), ("dims", 258), ("magic", 1)):
+        broken = sab.rotary_plan((64,))
+        setattr(broken, field, value)
+        assert call(pl=broken) == 1, field
+    broken = sab.rotary_plan((64,))
+    broken.axis[31] = 1
+    assert call(pl=broken) == 1
     assert P.value == 4096
 
 
