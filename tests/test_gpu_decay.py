@@ -14,6 +14,9 @@ is also below 2^-8 of the output's norm: two uniform errors of 2^-8 / sqrt(3)
 each give 0.82 * 2^-8."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -230,7 +233,8 @@ def test_long_sequence(D, L):
     ws = _ws(sab.decay_attention_backward_workspace(B, L, H, D))
     d_in = _out(S.shape, torch.float32)
     d_in.copy_(dS)
-    sab.decay_attention_backward(q, k, v, do, ld, scale, *g, state_in=S, d_state_out=d_in, d_state_in=d_in, workspace=ws)
+    sab.decay_attention_backward(q, k, v, do, ld, scale, *g, state_in=S, d_state_out=d_in, d_state_in=d_in,
+                                 workspace=ws)
     for n, got, ref, bnd in zip(("dQ", "dK", "dV", "d_state_in"), g + [d_in], refs, bnds):
         _check(got, _n(ref), _n(bnd), n, state=n == "d_state_in")
 
@@ -459,6 +463,52 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         for p, q, w in zip(flat(a), flat(b), flat(want)):
             assert torch.equal(p, w) and torch.equal(q, w)
+
+
+@gpu
+def test_two_streams_at_once():
+    """Calls of two streams overlap on the GPU; each has its own workspace."""
+    ld = torch.tensor([-0.02, 0.0], device="cuda")
+    sides = []
+    for i, (B, L, H, D) in enumerate([(1, 2000, 2, 128), (2, 900, 2, 64)]):
+        x = [_randn((B, L, H, D), 180 + 10 * i + j) for j in range(4)]
+        want = [torch.empty_like(x[0]) for _ in range(4)] + [torch.empty((B, H, D, D), device="cuda")]
+        got = [torch.zeros_like(t) for t in want]
+        ws = [torch.empty(max(256, n), dtype=torch.uint8, device="cuda") for n in
+              (sab.decay_attention_workspace(B, L, H, D), sab.decay_attention_backward_workspace(B, L, H, D))]
+        sides.append((x, want, got, ws, torch.cuda.Stream()))
+
+    def run(x, out, ws, stream=None):
+        sab.decay_attention(x[0], x[1], x[2], ld, 0.1, out[0], state_out=out[4], workspace=ws[0], stream=stream)
+        sab.decay_attention_backward(*x, ld, 0.1, *out[1:4], workspace=ws[1], stream=stream)
+
+    for x, want, _, ws, _ in sides:
+        run(x, want, ws)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, _, got, ws, s in sides:
+            run(x, got, ws, s)
+    torch.cuda.synchronize()
+    for _, want, got, _, _ in sides:
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+@gpu
+@pytest.mark.skipif("SAB_LIBRARY" in os.environ, reason="the library is chosen by the caller")
+def test_debug_build_agrees():
+    """Small cases with the debug library (its index checks on) in a child process."""
+    from streaming_attention_block_gb300.build import DEBUG_LIB, build
+
+    build(debug_bounds=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", "-k",
+                        "test_forward or test_backward or test_strided_rows or 1-12 or test_special_values",
+                        os.path.join(here, "test_gpu_decay.py"), os.path.join(here, "test_gpu_rotary.py")],
+                       cwd=os.path.dirname(here), env=dict(os.environ, SAB_LIBRARY=DEBUG_LIB), capture_output=True,
+                       text=True, timeout=900)
+    tail = "\n".join((r.stdout + r.stderr).splitlines()[-15:])
+    assert r.returncode == 0 and " passed" in tail, tail
 
 
 @gpu
