@@ -390,8 +390,7 @@ __device__ __noinline__ void zero_rows(uint8_t* v, int tid, int n) {
     *reinterpret_cast<uint4*>(v + piece_off<kC>(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// One arrival per warp, after its lanes' writes (each lane fences its own): 32
-// arrivals on one word cost as much as the work they report.
+// One arrival per warp, after its lanes' writes (each lane fences its own).
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
@@ -488,8 +487,10 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   if (warp == 1) {
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
+    // not before: a dependent on this SM that took TMEM first and then waited
+    // for this grid would never give it back
+    griddep_launch_dependents();
   }
-  griddep_launch_dependents();
   // With segments, this kernel follows the ones that sum and chain them.  Those
   // let it start only after their own waits, so that everything before them
   // is complete: all but the carried states may be read, and worked on, now.
