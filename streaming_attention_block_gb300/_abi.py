@@ -597,15 +597,28 @@ def _workspace(t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _empty_on(shape, dtype, device, stream):
+    """Uninitialised memory for a call on ``stream`` (None: the current one),
+    from that stream's own pool: what the current stream has freed may still be
+    in use there, and is safe only for work queued behind it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(nbytes, like, stream):
     """``nbytes`` of device scratch for one call on ``stream`` (None: 0 bytes)."""
-    if nbytes == 0:
-        return None
-    mem = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:  # the allocator must not hand it out again before that stream is done
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        mem.record_stream(s)
-    return mem
+    return None if nbytes == 0 else _empty_on(nbytes, torch.uint8, like.device, stream)
+
+
+def _output(like, stream):
+    """An output for a call on ``stream`` that the current stream will use."""
+    out = _empty_on(like.shape, like.dtype, like.device, stream)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(like.device))
+    return out
 
 
 def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_out=None, seq_len=None,
@@ -674,13 +687,13 @@ class DecayState:
         self.state.zero_()
 
     def attention(self, Q, K, V, scale=None, O=None, seq_len=None, workspace=None, stream=None):
-        O = torch.empty_like(Q) if O is None else O
+        O = _output(Q, stream) if O is None else O
         decay_attention(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, O, self.state,
                         self.state, seq_len, workspace, stream)
         return O
 
     def step(self, Q, K, V, scale=None, O=None, active=None, stream=None):
-        O = torch.empty_like(Q) if O is None else O
+        O = _output(Q, stream) if O is None else O
         decay_attention_step(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, self.state,
                              self.state, O, active, stream)
         return O

@@ -495,6 +495,31 @@ def test_two_streams_at_once():
 
 
 @gpu
+def test_memory_for_a_side_stream_is_its_own():
+    """Scratch and outputs made for a call on another stream are not blocks that
+    the current stream freed, whose earlier work may still be writing them."""
+    from streaming_attention_block_gb300 import _abi
+
+    s, n = torch.cuda.Stream(), 5 << 20
+    like = torch.empty((1, 4096, 5, 128), dtype=torch.bfloat16, device="cuda")  # n bytes
+    for make in (lambda st: _abi._scratch(n, like, st), lambda st: _abi._output(like, st)):
+        for stream in (s, s.cuda_stream):
+            mem = torch.empty(n, dtype=torch.uint8, device="cuda")
+            freed = mem.data_ptr()
+            del mem
+            assert make(None).data_ptr() == freed  # the current stream's calls may reuse it at once
+            assert make(stream).data_ptr() != freed
+    state = sab.DecayState(torch.tensor([-0.1, -0.2], device="cuda"), 1, 128)
+    other = sab.DecayState(state.log_decay, 1, 128)
+    q, k, v = (_randn((1, 700, 2, 128), 200 + i) for i in range(3))
+    s.wait_stream(torch.cuda.current_stream())
+    a, b = state.attention(q, k, v), other.attention(q, k, v, stream=s)
+    c, d = state.step(q[:, 0], k[:, 0], v[:, 0]), other.step(q[:, 0], k[:, 0], v[:, 0], stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(c, d) and torch.equal(state.state, other.state)
+
+
+@gpu
 @pytest.mark.skipif("SAB_LIBRARY" in os.environ, reason="the library is chosen by the caller")
 def test_debug_build_agrees():
     """Small cases with the debug library (its index checks on) in a child process."""
