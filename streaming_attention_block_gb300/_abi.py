@@ -545,6 +545,8 @@ def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, strea
     dev = _device()
     q = _rotary_rows(Q, Q_out, "Q", dev)
     B, L, _, D = Q.shape
+    if B * L > 1 << 31:  # would be cut to 32 bits on the way to the library
+        raise SabError(1, what)
     k = None
     if K is not None:
         k = _rotary_rows(K, K_out, "K", dev)

@@ -263,3 +263,13 @@ def test_python_refusals():
         sab.rotary(plan, x, None, x)  # not on the GPU
     with pytest.raises(TypeError):
         sab.rotary(plan, x[0], None, x[0])
+
+
+@gpu
+def test_more_tokens_than_32_bits_are_refused():
+    plan = sab.rotary_plan((8,))
+    x = torch.ones((1, 1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(sab.SabError):  # not taken for one token
+        sab.rotary(plan, x.expand((1 << 32) + 1, 1, 1, 8), None, x.expand((1 << 32) + 1, 1, 1, 8), first_position=1)
+    torch.cuda.synchronize()
+    assert bool((x == 1).all())
