@@ -499,65 +499,73 @@ def _refuse(t, name, dev, dtypes, shape=None):
 def _device():
     """Index of the current device (-2: there is none, so no tensor is on it)."""
     try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
+        return torch._C._cuda_getDevice()  # torch.cuda.current_device() without its start-up check
+    except (RuntimeError, AttributeError):
         return -2
 
 
 def _arg(t, shape, dtype, name, dev):
     """Device pointer of a contiguous tensor of this shape and type on the
     current device ``dev`` (None and raw pointers pass through)."""
-    if t is None or t.__class__ is int:
-        return t
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or \
-            not t.is_contiguous():
-        _refuse(t, name, dev, (dtype,), shape)
-    return t.data_ptr()
+    if t is None:
+        return None
+    try:
+        if t.get_device() == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+    _refuse(t, name, dev, (dtype,), shape)
 
 
 _ROWS = struct.Struct("@PPiqqqq")  # the layout of RotaryRows, packed faster than the structure is built
 
 
-def _strides(t, name):
-    """(batch, token) strides of [B, L, H, D] rows whose heads are contiguous."""
-    B, L, H, D = t.shape
-    sb, sl, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return sb if B > 1 else H * D, sl if L > 1 else H * D
-
-
 def _rotary_rows(x, out, name, dev):
-    """Token rows of ``x`` and ``out``: [B, L, H, D] with contiguous heads."""
-    for t, n in ((x, name), (out, name + "_out")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise TypeError(f"{n}: expected a [B, L, H, D] torch tensor")
-        if t.get_device() != dev or t.dtype not in _DTYPES:
-            _refuse(t, n, dev, tuple(_DTYPES))
-    if out is not x and (out.shape != x.shape or out.dtype != x.dtype):
-        raise ValueError(f"{name}_out: expected the shape and type of {name}")
-    ib, il = _strides(x, name)
-    ob, ol = (ib, il) if out is x else _strides(out, name + "_out")
-    return _ROWS.pack(x.data_ptr(), out.data_ptr(), x.shape[2], ib, il, ob, ol)
+    """Token rows of ``x`` and ``out``, [B, L, H, D] with contiguous heads, and
+    what the call's other tensors have to agree with."""
+    if not isinstance(x, torch.Tensor) or not isinstance(out, torch.Tensor) or x.dim() != 4 or out.dim() != 4:
+        raise TypeError(f"{name}, {name}_out: expected [B, L, H, D] torch tensors")
+    dtype = x.dtype
+    if x.get_device() != dev or dtype not in _DTYPES:
+        _refuse(x, name, dev, tuple(_DTYPES))
+    B, L, H, D = shape = x.shape
+    ib, il, ih, id_ = x.stride()
+    if out is x:
+        ob, ol, oh, od = ib, il, ih, id_
+    else:
+        if out.get_device() != dev:
+            _refuse(out, name + "_out", dev, (dtype,))
+        if out.dtype != dtype or out.shape != shape:
+            raise ValueError(f"{name}_out: expected the shape and type of {name}")
+        ob, ol, oh, od = out.stride()
+    if ((id_ != 1 or od != 1) and D > 1) or ((ih != D or oh != D) and H > 1):
+        raise ValueError(f"{name}, {name}_out: a token's heads must be contiguous")
+    if B == 1:  # strides of axes of one entry say nothing
+        ib = ob = H * D
+    if L == 1:
+        il = ol = H * D
+    return _ROWS.pack(x.data_ptr(), out.data_ptr(), H, ib, il, ob, ol), B, L, D, dtype
 
 
 def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, stream):
     dev = _device()
-    q = _rotary_rows(Q, Q_out, "Q", dev)
-    B, L, _, D = Q.shape
+    q, B, L, D, dtype = _rotary_rows(Q, Q_out, "Q", dev)
     if B * L > 1 << 31:  # would be cut to 32 bits on the way to the library
         raise SabError(1, what)
     k = None
     if K is not None:
-        k = _rotary_rows(K, K_out, "K", dev)
-        Bk, Lk, _, Dk = K.shape
-        if Bk != B or Lk != L or Dk != D or K.dtype != Q.dtype:
+        k, *same = _rotary_rows(K, K_out, "K", dev)
+        if same != [B, L, D, dtype]:
             raise ValueError("K: expected Q's batch, length, head dimension and type")
     if positions is not None and positions.__class__ is not int:
-        n = plan.axes * B * L
-        shape = positions.shape if positions.numel() == n else (plan.axes, B, L)
-        positions = _arg(positions, shape, torch.int64, "positions", dev)
-    status = fn(ctypes.byref(plan), q, k, positions, int(first_position), B, L, D, _DTYPES[Q.dtype],
+        if not isinstance(positions, torch.Tensor) or positions.get_device() != dev or \
+                positions.dtype != torch.int64 or positions.numel() != plan.axes * B * L or \
+                not positions.is_contiguous():
+            sized = isinstance(positions, torch.Tensor) and positions.numel() == plan.axes * B * L
+            _refuse(positions, "positions", dev, (torch.int64,), None if sized else (plan.axes, B, L))
+        positions = positions.data_ptr()
+    status = fn(ctypes.byref(plan), q, k, positions, int(first_position), B, L, D, _DTYPES[dtype],
                 _stream(stream, dev))
     if status != 0:
         raise SabError(status, what)
