@@ -293,6 +293,17 @@ __device__ __forceinline__ bool in_bounds(const DecayTileParams& p, long long bh
   return true;
 }
 
+// This block's run, and its index among that run's blocks.
+__device__ __forceinline__ const DecayTileParams& pick(const DecayRuns& r, unsigned& block) {
+  block = blockIdx.x;
+  if (block < r.first) return r.run[0];
+  block -= r.first;
+  if (r.n == 2) return r.run[1];
+  const int i = 1 + (int)(block & 1u);
+  block >>= 1;
+  return r.run[i];
+}
+
 // The tiles [r0, r1) of a segment in run order, and of those the live ones
 // [a, b) (tokens inside the sequence).
 struct Run {
@@ -455,8 +466,13 @@ struct TileCfg {
 
 template <int D, int TERMS>
 __global__ void __launch_bounds__(TileCfg<D, TERMS>::kThreads, 1)
-decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
+decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
   using C = TileCfg<D, TERMS>;
+  // A run that writes its state (TERMS = 3) has a launch to itself; choosing
+  // would cost registers it does not have (1 us of 46 for 8 sequences of up to
+  // 2047 tokens, 24 heads of 64).
+  unsigned block = blockIdx.x;
+  const DecayTileParams& p = TERMS == 3 ? runs.run[0] : pick(runs, block);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
@@ -469,10 +485,10 @@ decay_tile_kernel(const __grid_constant__ DecayTileParams p) {
   float* w_tab = p_tab + 256;
   auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seg = blockIdx.x % p.nseg;
-  int b = (int)(blockIdx.x / p.nseg / p.H);
-  const int h = (int)(blockIdx.x / p.nseg % p.H);
-  if (!in_bounds(p, blockIdx.x / p.nseg, seg)) return;
+  const int seg = block % p.nseg;
+  int b = (int)(block / p.nseg / p.H);
+  const int h = (int)(block / p.nseg % p.H);
+  if (!in_bounds(p, block / p.nseg, seg)) return;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i)
@@ -921,8 +937,10 @@ struct SegCfg {
 
 template <int D, int TERMS>
 __global__ void __launch_bounds__(SegCfg<D, TERMS>::kThreads, 1)
-decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
+decay_segment_kernel(const __grid_constant__ DecayRuns runs) {
   using C = SegCfg<D, TERMS>;
+  unsigned block;
+  const DecayTileParams& p = pick(runs, block);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
@@ -932,8 +950,8 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
   auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;  // the last segment's is wanted by state_out only
-  const int seg = blockIdx.x % nrun;
-  const long long bh = blockIdx.x / nrun;
+  const int seg = block % nrun;
+  const long long bh = block / nrun;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   if (!in_bounds(p, bh, seg)) return;
   if (threadIdx.x == 0) {
@@ -1135,11 +1153,13 @@ decay_segment_kernel(const __grid_constant__ DecayTileParams p) {
 // elements; the contributions are fetched kAhead segments ahead.
 constexpr int kMaxSegments = 256;
 template <int D>
-__global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayTileParams p) {
+__global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant__ DecayRuns runs) {
+  unsigned block;
+  const DecayTileParams& p = pick(runs, block);
   constexpr int kAhead = 16, kBlocks = D * D / 512;
   __shared__ float2 decays[kMaxSegments];
-  const long long bh = blockIdx.x / kBlocks;
-  const int e = ((int)(blockIdx.x % kBlocks) * 128 + threadIdx.x) * 4;
+  const long long bh = block / kBlocks;
+  const int e = ((int)(block % kBlocks) * 128 + threadIdx.x) * 4;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
   if (!in_bounds(p, bh, p.nseg - 1)) return;
@@ -1216,46 +1236,60 @@ cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<unsigned long long>&
 }
 
 template <int D, int TERMS>
-cudaError_t launch_segments(const DecayTileParams& p, cudaStream_t s) {
+cudaError_t launch_segments(DecayRuns& r, cudaStream_t s) {
   using C = SegCfg<D, TERMS>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem(decay_segment_kernel<D, TERMS>, C::kSmemBytes, ready);
   if (e != cudaSuccess) return e;
-  const long long bh = (long long)p.B * p.H;
-  const int nrun = p.state_out != nullptr ? p.nseg : p.nseg - 1;
-  e = launch(decay_segment_kernel<D, TERMS>, (unsigned)(bh * nrun), C::kThreads, C::kSmemBytes, p, s);
+  const unsigned bh = (unsigned)r.run[0].B * r.run[0].H;
+  unsigned grid = 0;
+  for (int i = 0; i < r.n; ++i) {
+    grid += bh * (r.run[i].state_out != nullptr ? r.run[i].nseg : r.run[i].nseg - 1);
+    if (i == 0) r.first = grid;
+  }
+  e = launch(decay_segment_kernel<D, TERMS>, grid, C::kThreads, C::kSmemBytes, r, s);
   if (e != cudaSuccess) return e;
-  return launch(decay_carry_kernel<D>, (unsigned)(bh * (D * D / 512)), 128, 0, p, s);
+  r.first = bh * (D * D / 512);
+  return launch(decay_carry_kernel<D>, r.first * r.n, 128, 0, r, s);
 }
 
 template <int D, int TERMS>
-cudaError_t launch_tiles(const DecayTileParams& p, cudaStream_t s) {
+cudaError_t launch_tiles(DecayRuns& r, cudaStream_t s) {
   using C = TileCfg<D, TERMS>;
   static std::atomic<unsigned long long> ready{0};
   const cudaError_t e = allow_smem(decay_tile_kernel<D, TERMS>, C::kSmemBytes, ready);
   if (e != cudaSuccess) return e;
-  return launch(decay_tile_kernel<D, TERMS>, (unsigned)((long long)p.B * p.H * p.nseg), C::kThreads, C::kSmemBytes, p,
-                s);
+  r.first = (unsigned)r.run[0].B * r.run[0].H * r.run[0].nseg;
+  return launch(decay_tile_kernel<D, TERMS>, r.first * r.n, C::kThreads, C::kSmemBytes, r, s);
+}
+
+bool wants_state(const DecayRuns& r) {
+  for (int i = 0; i < r.n; ++i)
+    if (r.run[i].state_out != nullptr) return true;
+  return false;
 }
 
 }  // namespace
 
 // k enters a state that the caller gets as three bf16 parts (24 bits), a state
 // that only feeds bf16 outputs as two (16 bits).
-cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s) {
-  if (p.state_out != nullptr) return p.D == 128 ? launch_segments<128, 3>(p, s) : launch_segments<64, 3>(p, s);
-  return p.D == 128 ? launch_segments<128, 2>(p, s) : launch_segments<64, 2>(p, s);
+cudaError_t launch_decay_segments(DecayRuns& r, cudaStream_t s) {
+  if (wants_state(r)) return r.run[0].D == 128 ? launch_segments<128, 3>(r, s) : launch_segments<64, 3>(r, s);
+  return r.run[0].D == 128 ? launch_segments<128, 2>(r, s) : launch_segments<64, 2>(r, s);
+}
+
+cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s) {
+  if (wants_state(r)) {
+    if (r.n != 1) return cudaErrorInvalidValue;
+    return r.run[0].D == 128 ? launch_tiles<128, 3>(r, s) : launch_tiles<64, 3>(r, s);
+  }
+  return r.run[0].D == 128 ? launch_tiles<128, 2>(r, s) : launch_tiles<64, 2>(r, s);
 }
 
 cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s) {
   const unsigned grid = (unsigned)((long long)p.B * p.H * (p.D / 32));
   return p.D == 128 ? launch(decay_short_kernel<128>, grid, 256, 0, p, s)
                     : launch(decay_short_kernel<64>, grid, 256, 0, p, s);
-}
-
-cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s) {
-  if (p.state_out != nullptr) return p.D == 128 ? launch_tiles<128, 3>(p, s) : launch_tiles<64, 3>(p, s);
-  return p.D == 128 ? launch_tiles<128, 2>(p, s) : launch_tiles<64, 2>(p, s);
 }
 
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s) {

@@ -929,45 +929,73 @@ static bool decay_short(int B, int L, int H, int D) {
 }
 
 // How a call cuts its sequences.  A CTA takes a sequence's head as a whole, or,
-// when B * H of them leave SMs idle, segments of it, one CTA per SM; the states
-// before the segments then cost a pass over k and v and two launches.  Chosen
-// by the modelled times below, in us per call for T tiles in a row (whole) or
-// T tiles per segment with a share f of the SMs at work.  Measured, whole
-// against cut, without and with state_out, heads of 128: 2 sequences of 2 tiles
-// 8.2 / 11.3 and 16.0 / 11.9; 24 of 4 tiles 14.2 / 13.0 and 23.9 / 15.0; 72 of
-// 12 tiles 38.6 / 40.8 and 54.8 / 47.8; 24 of 32 tiles 95 / 37 and 127 / 43.
-// (More segments than SMs lose: 156 of 12 tiles 76.7 / 101.6.)
+// when B * H of them leave SMs idle, segments of it; the states before the
+// segments then cost a pass over k and v and two launches.  Chosen by modelled
+// times, in us, for T tiles in a row (whole) or `per` tiles a segment with a
+// share f of the SMs at work.
 struct DecayCut {
   int nseg, seg_tiles;
 };
-static DecayCut decay_cut(int B, int L, int H, int D, bool state, bool gradients) {
-  const int tiles = (L + kTileM - 1) / kTileM;
-  const long long bh = (long long)B * H, most = std::min<long long>(device_sms() / bh, tiles);
+
+// One run, one segment per SM.  Measured, whole against cut, without and with
+// state_out, heads of 128: 2 sequences of 2 tiles 8.2 / 11.3 and 16.0 / 11.9; 24
+// of 4 tiles 14.2 / 13.0 and 23.9 / 15.0; 72 of 12 tiles 38.6 / 40.8 and 54.8 /
+// 47.8; 24 of 32 tiles 95 / 37 and 127 / 43.  (More segments than SMs lose: 156
+// of 12 tiles 76.7 / 101.6.)
+static DecayCut decay_cut_forward(int tiles, long long bh, int D, bool state) {
+  const long long most = std::min<long long>(device_sms() / bh, tiles);
   if (most < 2) return {1, tiles};
   const int per = (int)((tiles + most - 1) / most), n = (tiles + per - 1) / per;
   const double f = (double)(bh * n) / device_sms();
-  auto whole = [&](bool st) {
-    return D == 128 ? (st ? 8.5 + 3.8 * tiles : 3.0 + 2.9 * tiles) : (st ? 3.6 + 2.15 * tiles : 2.5 + 2.03 * tiles);
-  };
-  auto cut = [&](bool st) {
-    return D == 128 ? 7.0 + 4.3 * per + 4.5 * f + (st ? 1.0 + 0.5 * per + 2.5 * f : 0.0)
-                    : 6.2 + 2.95 * per + 1.7 * f + (st ? 0.6 + 0.3 * per + f : 0.0);
-  };
-  // gradients: three runs, of which the last finds its states worked out
-  const double a = whole(state) + (gradients ? 2 * whole(false) : 0.0);
-  const double c = cut(state) + (gradients ? cut(false) + (D == 128 ? 4.0 + 2.9 * per : 3.0 + 2.03 * per) : 0.0);
-  return n > 1 && c < a ? DecayCut{n, per} : DecayCut{1, tiles};
+  const double whole =
+      D == 128 ? (state ? 8.5 + 3.8 * tiles : 3.0 + 2.9 * tiles) : (state ? 3.6 + 2.15 * tiles : 2.5 + 2.03 * tiles);
+  const double cut = D == 128 ? 7.0 + 4.3 * per + 4.5 * f + (state ? 1.0 + 0.5 * per + 2.5 * f : 0.0)
+                              : 6.2 + 2.95 * per + 1.7 * f + (state ? 0.6 + 0.3 * per + f : 0.0);
+  return n > 1 && cut < whole ? DecayCut{n, per} : DecayCut{1, tiles};
+}
+
+// Three runs that share launches: one CTA a segment and run, in waves over the
+// SMs, so fewer and longer segments than one per SM.  Fitted to 300 calls (1
+// to 96 heads, 4 to 240 tiles, 1 to 152 segments) to 3 %; the choice was never
+// 2 % slower than the best.  Heads of 128, without state, us by segments: 12
+// of 12 tiles 41 (whole), 40 (2), 30 (4), 38 (6), 44 (12); 24 of 240 tiles 664,
+// 513 (2), 464 (4), 490 (6); 48 of 32 tiles 104, 142 (2), 163 (4).
+static DecayCut decay_cut_gradients(int tiles, long long bh, int D, bool state) {
+  const long long sms = device_sms(), most = std::min<long long>(sms / bh, tiles);
+  auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+  double best = D == 128 ? (state ? waves(2 * bh) * (6.3 + 2.8 * tiles) + waves(bh) * (10.0 + 3.65 * tiles)
+                                  : waves(3 * bh) * (8.0 + 2.8 * tiles))
+                         : (state ? waves(2 * bh) * (7.0 + 2.15 * tiles) + waves(bh) * (4.3 + 2.22 * tiles)
+                                  : 4.6 + waves(3 * bh) * (3.4 + 2.15 * tiles));
+  DecayCut how{1, tiles};
+  for (int n = 2, last = tiles; n <= most; ++n) {  // the fewest segments of each length
+    const int per = (tiles + n - 1) / n;
+    if (per == last) continue;
+    last = per;
+    const double f = (double)(bh * n) / sms, sums = waves(bh * (2 * n - 2 + state)) * per, wt = waves(3 * bh * n);
+    const double t = D == 128 ? (state ? 11.3 : 10.0) + 0.05 * n + 24.0 * f + (state ? 1.5 : 0.9) * sums +
+                                    wt * (0.9 + 3.1 * per)
+                              : 9.6 + 0.05 * n + 13.0 * f + (state ? 1.4 : 0.9) * sums + wt * (0.6 + 2.1 * per);
+    if (t < best) best = t, how = {n, per};
+  }
+  return how;
+}
+
+static DecayCut decay_cut(int B, int L, int H, int D, bool state, bool gradients) {
+  const int tiles = (L + kTileM - 1) / kTileM;
+  return gradients ? decay_cut_gradients(tiles, (long long)B * H, D, state)
+                   : decay_cut_forward(tiles, (long long)B * H, D, state);
 }
 static size_t decay_workspace(int B, int L, int H, int D, bool gradients) {
   if (!decay_shape_ok(B, L, H, D)) return 0;
   const int n = std::max(decay_cut(B, L, H, D, false, gradients).nseg, decay_cut(B, L, H, D, true, gradients).nseg);
-  return n == 1 ? 0 : align_up((size_t)B * H * n * D * D * sizeof(float), kAlign);
+  return n == 1 ? 0 : (gradients ? 2 : 1) * align_up((size_t)B * H * n * D * D * sizeof(float), kAlign);
 }
 
 size_t sab_decay_attention_workspace(int B, int L, int H, int D) { return decay_workspace(B, L, H, D, false); }
 
-// One run of the recurrence.  chain: work out the states before the segments
-// first; otherwise the workspace holds them from the run before, transposed.
+// One run of the recurrence.  carry: the part of the workspace that holds the
+// states before the segments; carry_t: run 1's, transposed.
 struct DecayRun {
   const void *q, *k, *v;
   void* o;
@@ -975,46 +1003,72 @@ struct DecayRun {
   float* out;
   int reverse, state_t;
   float kv_mul, o_mul;
-  bool chain;
+  int carry, carry_t;
 };
-static sab_status decay_run(const DecayRun& r, const DecayCut& cut, const float* log_decay, const int* seq_len, int B,
-                            int L, int H, int D, void* workspace, size_t ws_bytes, void* stream) {
-  DecayTileParams p;
-  memset(&p, 0, sizeof(p));
-  p.seg_tiles = cut.seg_tiles;
-  p.nseg = cut.nseg;
-  p.q = static_cast<const uint16_t*>(r.q);
-  p.k = static_cast<const uint16_t*>(r.k);
-  p.v = static_cast<const uint16_t*>(r.v);
-  p.o = static_cast<uint16_t*>(r.o);
-  p.log_decay = log_decay;
-  p.seq_len = seq_len;
-  p.state_in = r.in;
-  p.state_out = r.out;
-  p.carry = static_cast<float*>(workspace);
-  p.carry_t = !r.chain;
-  p.carry_states = (long long)(ws_bytes / ((size_t)D * D * sizeof(float)));
-  p.B = B;
-  p.L = L;
-  p.H = H;
-  p.D = D;
-  p.by_length = seq_len != nullptr && p.nseg == 1 && B > 1 && B <= kMaxByLength && (long long)B * H > device_sms();
-  p.reverse = r.reverse;
-  p.state_t = r.state_t;
-  p.kv_mul = r.kv_mul;
-  p.o_mul = r.o_mul;
-  p.err_word = device_error_word();
+// Up to three runs, of which the third, if any, reads the second's carried
+// states.  Runs share their launches, except that whole sequences whose state
+// is wanted go by themselves: they multiply more, and may write a state that
+// another run reads.
+static sab_status decay_runs(const DecayRun* runs, int n, const DecayCut& cut, const float* log_decay,
+                             const int* seq_len, int B, int L, int H, int D, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  DecayRuns all;
+  memset(&all, 0, sizeof(all));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (decay_short(B, L, H, D)) return launch_decay_short(p, s) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
-  const bool sums = p.nseg > 1 && r.chain;
-  if (!encode_token_major(&p.q_map, r.q, B, L, H, D) || !encode_token_major(&p.k_map, r.k, B, L, H, D) ||
-      !encode_token_major(&p.v_map, r.v, B, L, H, D) || !encode_token_major(&p.o_map, r.o, B, L, H, D) ||
-      (sums && (!encode_token_major(&p.k_map_h, r.k, B, L, H, D, 64) ||
-                !encode_token_major(&p.v_map_h, r.v, B, L, H, D, 64))))
-    return SAB_ERR_CUDA;
-  if (sums && launch_decay_segments(p, s) != cudaSuccess) return SAB_ERR_CUDA;
-  if (p.nseg > 1) p.state_out = nullptr;  // written with the segments' states
-  return launch_decay_tiles(p, s) == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+  const bool is_short = decay_short(B, L, H, D), cut_up = cut.nseg > 1;
+  const size_t states = cut_up ? (size_t)B * H * cut.nseg : 0, held = ws_bytes / ((size_t)D * D * sizeof(float));
+  for (int i = 0; i < n; ++i) {
+    const DecayRun& r = runs[i];
+    DecayTileParams& p = all.run[i];
+    p.seg_tiles = cut.seg_tiles;
+    p.nseg = cut.nseg;
+    p.q = static_cast<const uint16_t*>(r.q);
+    p.k = static_cast<const uint16_t*>(r.k);
+    p.v = static_cast<const uint16_t*>(r.v);
+    p.o = static_cast<uint16_t*>(r.o);
+    p.log_decay = log_decay;
+    p.seq_len = seq_len;
+    p.state_in = r.in;
+    p.state_out = r.out;
+    p.carry = static_cast<float*>(workspace) + r.carry * states * D * D;
+    p.carry_t = r.carry_t;
+    p.carry_states = (long long)held - (long long)(r.carry * states);
+    p.B = B;
+    p.L = L;
+    p.H = H;
+    p.D = D;
+    p.by_length = seq_len != nullptr && p.nseg == 1 && B > 1 && B <= kMaxByLength && (long long)B * H > device_sms();
+    p.reverse = r.reverse;
+    p.state_t = r.state_t;
+    p.kv_mul = r.kv_mul;
+    p.o_mul = r.o_mul;
+    p.err_word = device_error_word();
+    if (is_short) {
+      if (launch_decay_short(p, s) != cudaSuccess) return SAB_ERR_CUDA;
+      continue;
+    }
+    const bool sums = cut_up && !r.carry_t;
+    if (!encode_token_major(&p.q_map, r.q, B, L, H, D) || !encode_token_major(&p.k_map, r.k, B, L, H, D) ||
+        !encode_token_major(&p.v_map, r.v, B, L, H, D) || !encode_token_major(&p.o_map, r.o, B, L, H, D) ||
+        (sums && (!encode_token_major(&p.k_map_h, r.k, B, L, H, D, 64) ||
+                  !encode_token_major(&p.v_map_h, r.v, B, L, H, D, 64))))
+      return SAB_ERR_CUDA;
+  }
+  if (is_short) return SAB_OK;
+  if (cut_up) {
+    all.n = std::min(n, 2);
+    if (launch_decay_segments(all, s) != cudaSuccess) return SAB_ERR_CUDA;
+    for (int i = 0; i < n; ++i) all.run[i].state_out = nullptr;  // written with the segments' states
+  }
+  const bool apart = n > 1 && all.run[n - 1].state_out != nullptr;
+  all.n = apart ? n - 1 : n;
+  if (launch_decay_tiles(all, s) != cudaSuccess) return SAB_ERR_CUDA;
+  if (apart) {
+    all.run[0] = all.run[n - 1];
+    all.n = 1;
+    if (launch_decay_tiles(all, s) != cudaSuccess) return SAB_ERR_CUDA;
+  }
+  return SAB_OK;
 }
 
 sab_status sab_decay_attention(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -1031,9 +1085,9 @@ sab_status sab_decay_attention(const void* Q, const void* K, const void* V, cons
   const size_t need = sab_decay_attention_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  return decay_run({Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, true},
-                   decay_cut(B, L, H, D, state_out != nullptr, false), log_decay, seq_len, B, L, H, D, workspace,
-                   ws_bytes, stream);
+  const DecayRun run = {Q, K, V, O, state_in, state_out, 0, 0, 1.f, scale, 0, 0};
+  return decay_runs(&run, 1, decay_cut(B, L, H, D, state_out != nullptr, false), log_decay, seq_len, B, L, H, D,
+                    workspace, ws_bytes, stream);
 }
 
 sab_status sab_decay_attention_step(const void* Q, const void* K, const void* V, const float* log_decay,
@@ -1084,19 +1138,15 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   const size_t need = sab_decay_attention_backward_workspace(B, L, H, D);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
     return SAB_ERR_WORKSPACE;
-  // dV before dK: one chain of states serves both (dK's run holds them
-  // transposed).  d_state_in, which may be d_state_out, is written by the last
-  // run to read d_state_out: with the chain, or else by dK's run.
+  // dV and dK share one chain of states (dK's run holds them transposed).
+  // d_state_in, which may be d_state_out, is written by the last to read
+  // d_state_out: the chain, or else dK's run.
   const DecayCut how = decay_cut(B, L, H, D, d_state_in != nullptr, true);
   const bool cut = how.nseg > 1;
-  const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale, true},
-                            {K, Q, dO, dV, d_state_out, cut ? d_state_in : nullptr, 1, 0, scale, 1.f, true},
-                            {V, dO, Q, dK, d_state_out, cut ? nullptr : d_state_in, 1, 1, scale, 1.f, false}};
-  for (const DecayRun& r : runs) {
-    const sab_status st = decay_run(r, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
-    if (st != SAB_OK) return st;
-  }
-  return SAB_OK;
+  const DecayRun runs[3] = {{dO, V, K, dQ, state_in, nullptr, 0, 1, 1.f, scale, 0, 0},
+                            {K, Q, dO, dV, d_state_out, cut ? d_state_in : nullptr, 1, 0, scale, 1.f, 1, 0},
+                            {V, dO, Q, dK, d_state_out, cut ? nullptr : d_state_in, 1, 1, scale, 1.f, 1, 1}};
+  return decay_runs(runs, 3, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
 }
 
 sab_status sab_selftest_split_abort(const sab_ring* ring, int layer, long long chunk, const void* Q,

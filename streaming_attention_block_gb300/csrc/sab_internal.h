@@ -258,6 +258,14 @@ struct DecayTileParams {
   unsigned int* err_word;   // the library's device error word
 };
 
+// Up to three runs of one shape in one launch: the blocks [0, first) are run
+// 0's, the others run 1's or, of three, run 1's and run 2's in turn.
+struct DecayRuns {
+  DecayTileParams run[3];
+  unsigned first;
+  int n;
+};
+
 // One token of every sequence.
 struct DecayStepParams {
   const uint16_t* q;        // [B, H, D]
@@ -281,10 +289,10 @@ cudaError_t launch_attention_backward(const BwdParams& p, cudaStream_t s);
 cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
 // the state before every segment, into p.carry (nseg > 1); the state after the
 // last, if p.state_out is given
-cudaError_t launch_decay_segments(const DecayTileParams& p, cudaStream_t s);
+cudaError_t launch_decay_segments(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
-cudaError_t launch_decay_tiles(const DecayTileParams& p, cudaStream_t s);
+cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
 // One query tile per CTA, key-half softmax warpgroups; unsplit KV only.

@@ -277,6 +277,43 @@ def test_ragged_segments(case):
 
 
 @gpu
+@pytest.mark.parametrize("states", [False, True], ids=["no_states", "states"])
+@pytest.mark.parametrize("case", [(2, 1300, 12, 64), (1, 4000, 24, 128), (1, 4000, 24, 64), (1, 1500, 12, 128),
+                                  (60, 200, 3, 128), (60, 200, 3, 64), (5, 700, 30, 128)])
+def test_gradients_in_several_waves(case, states):
+    """The three runs of a gradient share launches of up to four times as many
+    blocks as SMs, in segments and as whole sequences of equal or unequal
+    lengths, with and without states."""
+    B, L, H, D = case
+    q, k, v, do = (_randn((B, L, H, D), 210 + i) for i in range(4))
+    ld = _ld(H, 1)
+    S, dS = (_randn((B, H, D, D), 220 + i, torch.float32) if states else None for i in range(2))
+    lens = torch.tensor([L - 11 * b for b in range(B)], dtype=torch.int32).clamp(min=0).cuda() if B > 2 else None
+    if lens is not None:
+        for b, n in enumerate(lens.tolist()):
+            for x in (q, k, v, do):
+                x[b, n:] = float("nan")
+    g = [_out(q.shape) for _ in range(3)]
+    d_in = _out((B, H, D, D), torch.float32) if states else None
+    sab.decay_attention_backward(q, k, v, do, ld, 0.1, *g, state_in=S, d_state_out=dS, d_state_in=d_in, seq_len=lens,
+                                 workspace=_ws(sab.decay_attention_backward_workspace(B, L, H, D)))
+    zero = torch.zeros((B, H, D, D), dtype=torch.float64, device="cuda")
+    for b, n in enumerate([L] * B if lens is None else lens.tolist()):
+        for x in g:
+            assert not bool(x[b, n:].any())
+        if n == 0:
+            assert d_in is None or torch.equal(d_in[b], dS[b])
+            continue
+        one = [x[b:b + 1, :n].contiguous() for x in (q, k, v, do)]
+        s0, r0 = ((S[b:b + 1].double(), dS[b:b + 1].double()) if states else (zero[b:b + 1], zero[b:b + 1]))
+        refs, bnds = _fp64_back_on_gpu(*one, ld, 0.1, s0, r0)
+        for name, got, ref, bnd in zip(("dQ", "dK", "dV"), g, refs, bnds):
+            _check(got[b:b + 1, :n], _n(ref), _n(bnd), f"{name} {b}")
+        if states:
+            _check(d_in[b:b + 1], _n(refs[3]), _n(bnds[3]), f"d_state_in {b}", state=True)
+
+
+@gpu
 def test_pieces_and_single_tokens_equal_the_whole():
     """A stream fed as chunks and then token by token, through DecayState."""
     B, L, H, D = 2, 300, 3, 128
