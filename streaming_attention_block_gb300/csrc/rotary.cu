@@ -83,12 +83,12 @@ constexpr int kBatch = 4;  // rows in flight per thread
 //                 start on a 16-byte boundary
 // A block's columns of `units` threads take one token and every p.splits-th
 // head each.
-// (Blocks per SM: four of 64 registers for one vector per row; two vectors per
-// row take 100 registers, and fewer rows in flight cost more than fewer blocks:
-// 4 x 8191 tokens of 32 heads, 89 us with 4 rows and 2 blocks, 102 us with 2
-// and 3, 138 us with 1 and 4.)
+// (Blocks per SM: four of 64 registers for one vector per row, three of 80 for
+// two.  Fewer rows in flight cost more than fewer blocks: 4 x 8191 tokens of 32
+// heads, 89 us with 4 rows and 2 blocks, 102 us with 2 and 3, 138 us with 1 and
+// 4; 81 us with 4 and 3, see kKeep.)
 template <typename T, Mode M>
-__global__ void __launch_bounds__(kMaxThreads, M == kHalfVec ? 2 : 4)
+__global__ void __launch_bounds__(kMaxThreads, M == kHalfVec ? 3 : 4)
 rotary_kernel(const __grid_constant__ RotaryParams p) {
   using V = Vec<T>;
   constexpr int N = V::N;
@@ -130,17 +130,25 @@ rotary_kernel(const __grid_constant__ RotaryParams p) {
   }
   ptx::griddep_wait();
 
+  // A row's places: kept from the load to the store, except that kHalfVec works
+  // them out anew, which frees the registers for its third block.  (With it 4 x
+  // 8191 tokens of 32 heads go from 95 to 87 us, L2 flushed; in kInterleaved 2 x
+  // 30720 tokens of 24 heads would go from 117 to 148.)
+  constexpr bool kKeep = M != kHalfVec;
   const T* src[kBatch];
   T* dst[kBatch];
   uint4 va[kBatch], vb[kBatch];
-  int h = active ? column % p.splits : heads;
+  const int hq = p.rows[0].heads;
+  int h = active ? column % p.splits : heads;  // next head to fetch
+  int first = h;                               // this batch's first
   auto fetch = [&]() {
+    if (!kKeep) first = h;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       dst[u] = nullptr;
       if (h < heads) {
-        const bool w = h >= p.rows[0].heads;
-        const int e = (w ? h - p.rows[0].heads : h) * p.D;
+        const bool w = h >= hq;
+        const int e = (w ? h - hq : h) * p.D;
         src[u] = (w ? in1 : in0) + e;
         dst[u] = (w ? out1 : out0) + e;
         h += p.splits;
@@ -176,18 +184,23 @@ rotary_kernel(const __grid_constant__ RotaryParams p) {
   for (int j = 0; j < kPairs; ++j)
     f[j] = rot && j < turns_here ? cs[k * half + unit * kPairs + j] : make_float2(0.f, 0.f);
 
-  while (dst[0] != nullptr) {
+  while (kKeep ? dst[0] != nullptr : first < heads) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (dst[u] == nullptr) break;
+      if (kKeep ? dst[u] == nullptr : first + u * p.splits >= heads) break;
+      T* to = dst[u];
+      if (!kKeep) {
+        const int hu = first + u * p.splits;
+        to = hu < hq ? out0 + hu * p.D : out1 + (hu - hq) * p.D;
+      }
       if constexpr (M == kHalfScalar) {
         if (rot) {
           float x = V::load(src[u] + e0), y = V::load(src[u] + e1);
           turn(f[0], x, y);
-          V::store(dst[u] + e0, x);
-          V::store(dst[u] + e1, y);
+          V::store(to + e0, x);
+          V::store(to + e1, y);
         } else {
-          dst[u][e0] = src[u][e0];
+          to[e0] = src[u][e0];
         }
       } else {
         if (rot) {
@@ -205,8 +218,8 @@ rotary_kernel(const __grid_constant__ RotaryParams p) {
           }
           va[u] = V::pack(x);
         }
-        *reinterpret_cast<uint4*>(dst[u] + e0) = va[u];
-        if (M == kHalfVec && e1 >= 0) *reinterpret_cast<uint4*>(dst[u] + e1) = vb[u];
+        *reinterpret_cast<uint4*>(to + e0) = va[u];
+        if (M == kHalfVec && e1 >= 0) *reinterpret_cast<uint4*>(to + e1) = vb[u];
       }
     }
     fetch();
