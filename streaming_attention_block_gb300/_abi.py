@@ -613,8 +613,10 @@ def _empty_on(shape, dtype, device, stream):
     in use there, and is safe only for work queued behind it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(s):
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)  # 0 names the default stream, but would make ExternalStream take a new one
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -546,6 +546,12 @@ def test_memory_for_a_side_stream_is_its_own():
             del mem
             assert make(None).data_ptr() == freed  # the current stream's calls may reuse it at once
             assert make(stream).data_ptr() != freed
+    mem = torch.empty(n, dtype=torch.uint8, device="cuda")
+    freed = mem.data_ptr()
+    del mem
+    with torch.cuda.stream(s):  # handle 0 is the default stream
+        assert torch.cuda.default_stream().cuda_stream == 0 and _abi._scratch(n, like, 0).data_ptr() == freed
+        assert _abi._scratch(n, like, None).data_ptr() != freed
     state = sab.DecayState(torch.tensor([-0.1, -0.2], device="cuda"), 1, 128)
     other = sab.DecayState(state.log_decay, 1, 128)
     q, k, v = (_randn((1, 700, 2, 128), 200 + i) for i in range(3))
