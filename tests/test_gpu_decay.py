@@ -211,8 +211,8 @@ def _fp64_back_on_gpu(q, k, v, do, ld, scale, S, R):
     return (dq, dk, dv, R), (dqa, dka, dva, Ra)
 
 
-# few heads: the sequence is worked on in parallel pieces, chained inside a
-# cluster while they are short, by kernels of their own when they are long
+# few heads: the sequence is worked on in parallel segments, whose states are
+# summed and chained by kernels of their own
 @gpu
 @pytest.mark.parametrize("L", [3000, 7000, 20011])
 @pytest.mark.parametrize("D", [64, 128])
