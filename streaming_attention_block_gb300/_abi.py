@@ -559,11 +559,13 @@ def _rotary(fn, what, plan, Q, K, Q_out, K_out, positions, first_position, strea
         if same != [B, L, D, dtype]:
             raise ValueError("K: expected Q's batch, length, head dimension and type")
     if positions is not None and positions.__class__ is not int:
+        want = (plan.axes, B, L)
         if not isinstance(positions, torch.Tensor) or positions.get_device() != dev or \
-                positions.dtype != torch.int64 or positions.numel() != plan.axes * B * L or \
-                not positions.is_contiguous():
-            sized = isinstance(positions, torch.Tensor) and positions.numel() == plan.axes * B * L
-            _refuse(positions, "positions", dev, (torch.int64,), None if sized else (plan.axes, B, L))
+                positions.dtype != torch.int64 or not positions.is_contiguous():
+            _refuse(positions, "positions", dev, (torch.int64,))
+        # the order of the numbers is what counts: axes of one entry may be left out or added
+        if positions.shape != want and [n for n in positions.shape if n != 1] != [n for n in want if n != 1]:
+            raise ValueError(f"positions: expected shape {want}, got {tuple(positions.shape)}")
         positions = positions.data_ptr()
     status = fn(ctypes.byref(plan), q, k, positions, int(first_position), B, L, D, _DTYPES[dtype],
                 _stream(stream, dev))
