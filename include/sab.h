@@ -565,7 +565,8 @@ sab_status sab_rotary_backward(const sab_rotary_plan* plan, const sab_rotary_row
  * bf16; the state itself is held in fp32 and fed by k with 24 bits of mantissa
  * (16 bits where no state_out is wanted).  Short runs are fp32 throughout.  A
  * live k or v that is not finite reaches, besides the later outputs, those of
- * up to 127 tokens before it (masked scores are zeros, and 0 * NaN is NaN).
+ * up to 127 tokens before it (masked scores are zeros, and 0 * NaN is NaN).  An
+ * infinite element of state_in stays infinite while g is not 0 in fp32.
  * D must be 64 or 128.  Errors: INVALID_ARG, WORKSPACE, CUDA.
  */
 size_t sab_decay_attention_workspace(int B, int L, int H, int D);

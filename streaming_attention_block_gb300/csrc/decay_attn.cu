@@ -25,20 +25,34 @@ __device__ __forceinline__ float decay_ln(const float* log_decay, int h) {
   const float x = __ldg(log_decay + h);
   return x > 0.f ? 0.f : x < -1e4f ? -1e4f : x;
 }
+// Whether a decay of ln per token is 0 in fp32: then, and only then, may a decay
+// take an infinity with it (0 * inf is NaN).
+__device__ __forceinline__ bool decays_to_zero(float ln) { return expf(ln) == 0.f; }
+constexpr float kLeast = 0x1p-149f;  // the smallest positive fp32 number
 // exp(x) for x <= 0 as a rounded value and the rest.  Multiplying a state by
 // the rounded value alone would repeat its error of up to 2^-25 at every token
-// (10^4 tokens with a decay near 1: 3e-4).  Above 1/2 the rest is
-// (1 - hi) - (1 - exp(x)), the first difference exact; below, the state is
-// gone before the error adds up.
+// (10^4 tokens with a decay near 1: 3e-4).  Above 1/2 the value is rounded down
+// and the rest is (1 - hi) - (1 - exp(x)), the first difference exact; below,
+// the state is gone before the error adds up.  Unless the decay is 0 for good
+// (`zero`), both are positive, kLeast in place of 0: an infinite state stays
+// infinite, and no finite state is moved by more than 1e-6.
 struct Decay {
   float hi, lo;
-  __device__ __forceinline__ explicit Decay(float x) : hi(expf(x)), lo(0.f) {
-    if (hi >= 0.5f) lo = (1.f - hi) + expm1f(x);
+  __device__ __forceinline__ Decay(float x, bool zero) : hi(expf(x)), lo(0.f) {
+    if (hi >= 0.5f) {
+      const float m = expm1f(x);
+      hi = __fadd_rd(1.f, m);
+      if (hi >= 0.5f) lo = (1.f - hi) + m;
+    }
+    if (!zero) {
+      if (hi == 0.f) hi = kLeast;
+      if (!(lo > 0.f)) lo = kLeast;
+    }
   }
   __device__ __forceinline__ float operator()(float s) const { return fmaf(s, hi, s * lo); }
 };
 // over n tokens
-__device__ __noinline__ Decay decay_over(int n, float ln) { return Decay((float)n * ln); }
+__device__ __noinline__ Decay decay_over(int n, float ln) { return Decay((float)n * ln, decays_to_zero(ln)); }
 
 // One token: the state passes once through registers.  One CTA per (b, h)
 // and W value columns; W / 4 lanes hold a row's columns as 16-byte vectors, so
@@ -79,7 +93,8 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
     const uint2 vw = *reinterpret_cast<const uint2*>(p.v + bh * D + col);
     const float v[4] = {__uint_as_float(vw.x << 16), __uint_as_float(vw.x & 0xFFFF0000u), __uint_as_float(vw.y << 16),
                         __uint_as_float(vw.y & 0xFFFF0000u)};
-    const Decay decay(decay_ln(p.log_decay, h));
+    const float ln = decay_ln(p.log_decay, h);
+    const Decay decay(ln, decays_to_zero(ln));
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -126,7 +141,7 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
 // reads), and nothing of the tile kernel's set-up is paid.
 constexpr int kShortBatch = 16;  // tokens staged at a time
 template <int D>
-__global__ void __launch_bounds__(256) decay_short_kernel(const __grid_constant__ DecayTileParams p) {
+__global__ void __launch_bounds__(256, D == 128 ? 6 : 8) decay_short_kernel(const __grid_constant__ DecayTileParams p) {
   constexpr int R = D / 8;
   __shared__ __align__(16) float sq[kShortBatch][D], sk[kShortBatch][D], sv[kShortBatch][32];
   __shared__ float part[8][kShortBatch][32];
@@ -136,7 +151,8 @@ __global__ void __launch_bounds__(256) decay_short_kernel(const __grid_constant_
   const long long bh = blockIdx.x / (D / 32);
   const int b = (int)(bh / p.H), h = (int)(bh % p.H), col0 = (int)(blockIdx.x % (D / 32)) * 32, col = col0 + lane;
   const int len = p.seq_len != nullptr ? min(max(__ldg(p.seq_len + b), 0), p.L) : p.L;
-  const Decay decay(decay_ln(p.log_decay, h));
+  const float ln = decay_ln(p.log_decay, h);
+  const Decay decay(ln, decays_to_zero(ln));
   float s[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) s[r] = 0.f;
@@ -694,6 +710,8 @@ decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
     if (warp < 10) {
       // ------------------------------------------------------------- rows
       const int tid = threadIdx.x - 64;
+      // a row's factor of the state: as a Decay, 0 only where the decay is (inf * 0)
+      const float f_least = decays_to_zero(ln) ? 0.f : kLeast;
       for (int it = 0; it < nt; ++it) {
         const int n = run.tokens(run.a + it), sv = it % C::kVStages;
         uint8_t* vt = base + C::kVOff + sv * C::kTileBytes;
@@ -748,7 +766,7 @@ decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
           warp_arrive(bar(C::kKwFull), lane);
         }
         // output rows
-        const float f = p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2);
+        const float f = fmaxf(p.o_mul * ex2((float)(rev ? n - 1 - row : row + 1) * ld2), f_least);
         ok = __all_sync(0xffffffffu, wait(C::kOFull, it & 1u, 15));
         if (!ok) break;
         tc_fence_after();
@@ -1177,8 +1195,9 @@ __global__ void __launch_bounds__(128) decay_carry_kernel(const __grid_constant_
   };
   fetch(0);
   const float ln = decay_ln(p.log_decay, h);
+  const bool zero = decays_to_zero(ln);
   for (int i = threadIdx.x; i < nrun; i += 128) {
-    const Decay d((float)Run(p, b, i).count() * ln);
+    const Decay d((float)Run(p, b, i).count() * ln, zero);
     decays[i] = make_float2(d.hi, d.lo);
   }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
