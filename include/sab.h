@@ -453,11 +453,13 @@ sab_status sab_block_causal_attention(const void* Q, const void* K, const void* 
  *                    Language Models", section 3.2; the paper's temperature
  *                    is `magnitude`).
  *            NONE takes s = 1.
- * Angles are exact for positions of any size: a frequency is held in turns
- * per position as a 64-bit fraction, so position * frequency modulo one turn
- * is one wrapping integer product (its error is position * 2^-65 turns, next
- * to the 2^-53 relative error of the fp64 frequency).  Sine, cosine and
- * products are fp32; one rounding to the element type.
+ * Angles are reduced exactly for positions of any size: a frequency is held in
+ * turns per position as a 64-bit fraction, so position * frequency modulo one
+ * turn is one wrapping integer product.  The fraction is within 2^-65 turns and
+ * the fp64 frequency that it is taken from within 2^-50 of itself (RAMP: that
+ * times 1 + s * ramp_fast / (ramp_fast - ramp_slow)); an angle's error is the
+ * position times both.  Sine, cosine and products are fp32; one rounding to the
+ * element type.
  */
 typedef enum { SAB_ROTARY_INTERLEAVED = 0, SAB_ROTARY_HALF = 1 } sab_rotary_layout;
 typedef enum {

@@ -788,6 +788,16 @@ sab_status sab_memory_prefix_attention_backward(const void* Q, const void* K, co
                             dQ, dK, dV, workspace, ws_bytes, stream);
 }
 
+// x^(num/den) within 2^-51 of it.  The quotient's rounding, up to 2^-53 of it,
+// would grow by ln(x^(num/den)) (2^-50.4 for base 10^4 and 44 dimensions), so its
+// exact remainder goes into a first-order factor.
+static double power_of_quotient(double x, int num, int den) {
+  const double e = (double)num / den;
+  const double rest = fma(-e, (double)den, (double)num) / den;
+  const double f = pow(x, e);
+  return fma(f, rest * log(x), f);
+}
+
 sab_status sab_rotary_plan_init(const sab_rotary_desc* desc, sab_rotary_plan* plan) {
   if (desc == nullptr || plan == nullptr) return SAB_ERR_INVALID_ARG;
   const sab_rotary_desc& d = *desc;
@@ -818,11 +828,12 @@ sab_status sab_rotary_plan_init(const sab_rotary_desc* desc, sab_rotary_plan* pl
   memset(plan, 0, sizeof(*plan));
   int j = 0;
   for (int a = 0; a < d.axes; ++a) {
-    const double n = d.band[a];
-    const double base = d.scaling == SAB_ROTARY_SCALE_BASE ? d.base * pow(s, n / (n - 2.0)) : d.base;
-    if (!isfinite(base)) return SAB_ERR_INVALID_ARG;
-    for (int i = 0; i < d.band[a] / 2; ++i, ++j) {
-      double f = pow(base, -2.0 * i / n);
+    const int n = d.band[a];
+    if (d.scaling == SAB_ROTARY_SCALE_BASE && !isfinite(d.base * pow(s, n / (n - 2.0)))) return SAB_ERR_INVALID_ARG;
+    for (int i = 0; i < n / 2; ++i, ++j) {
+      double f = power_of_quotient(d.base, -2 * i, n);
+      // (base s^(n/(n-2)))^(-2i/n)
+      if (d.scaling == SAB_ROTARY_SCALE_BASE) f *= power_of_quotient(s, -2 * i, n - 2);
       if (d.scaling == SAB_ROTARY_SCALE_LINEAR) f /= s;
       if (d.scaling == SAB_ROTARY_SCALE_RAMP) {
         const double w = (d.original_context * f / kTwoPi - d.ramp_slow) / (d.ramp_fast - d.ramp_slow);
