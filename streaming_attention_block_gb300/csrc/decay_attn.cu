@@ -628,6 +628,8 @@ decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
       mma_commit_l(lead, bar(C::kSFull));
       return true;
     };
+    // A slot is announced free only to a load that waits for it: an arrival that
+    // nobody waits for could reach shared memory that the CTA has left.
     bool ok = nt > 0 && scores(0);
     for (int it = 0; ok && it < nt; ++it) {
       const int s = it % C::kKStages, sv = it % C::kVStages, sq = it % C::kQStages;
@@ -638,7 +640,7 @@ decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss_l(lead, tmem + C::kInter, at(kmaj, q + k_off(kk)), at(mn_st, C::kStOff + kk * 2048u), id_o, kk > 0);
-        mma_commit_l(lead, bar(C::kEmptyQ + sq));
+        if (it + C::kQStages < nt) mma_commit_l(lead, bar(C::kEmptyQ + sq));
         return true;
       };
       // the previous output rows are read
@@ -669,8 +671,8 @@ decay_tile_kernel(const __grid_constant__ DecayRuns runs) {
             mma_ss_l(lead, tmem + C::kUpd, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
                      at(mn, v + kk * 2048u), id_u, t < TERMS - 1 || kk > 0);
         mma_commit_l(lead, bar(C::kUFull));
-        mma_commit_l(lead, bar(C::kEmptyK + s));
-        if (C::kRoomy) mma_commit_l(lead, bar(C::kEmptyV + sv));
+        if (it + C::kKStages < nt) mma_commit_l(lead, bar(C::kEmptyK + s));
+        if (C::kRoomy && it + C::kVStages < nt) mma_commit_l(lead, bar(C::kEmptyV + sv));
       }
       if (!C::kRoomy && it + 1 < nt) ok = scores(it + 1);
     }
@@ -1055,7 +1057,6 @@ decay_segment_kernel(const __grid_constant__ DecayRuns runs) {
           for (int kk = 0; kk < C::kRows / 16; ++kk)
             mma_ss_l(lead, t == 0 ? acc : acc + D, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
                      at(mn, v + kk * 2048u), id_u, !fresh || t == 1 || kk > 0);
-        mma_commit_l(lead, bar(C::kEmpty + s));
         if (it % C::kGroup == C::kGroup - 1 || it + 1 == nt) mma_commit_l(lead, bar(C::kGroupFull + buf));
       } else {
 #pragma unroll
@@ -1064,10 +1065,12 @@ decay_segment_kernel(const __grid_constant__ DecayRuns runs) {
           for (int kk = 0; kk < C::kRows / 16; ++kk)
             mma_ss_l(lead, tmem, at(mn, (t == 0 ? k : rest + (t - 1) * C::kTileBytes) + kk * 2048u),
                      at(mn, v + kk * 2048u), id_u, it > 0 || t > 0 || kk > 0);
-        mma_commit_l(lead, bar(C::kEmpty + s));
       }
+      // to the group that scales step it + 2, and to the load of step it +
+      // kStages; nobody waits for the last two (see the tile kernel)
+      if (it + 2 < nt) mma_commit_l(lead, bar(C::kEmpty + s));
     }
-    if (ok) mma_commit_l(lead, bar(C::kFinal));
+    if (TERMS != 3 && ok) mma_commit_l(lead, bar(C::kFinal));
     if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
       mma_commit_l(lead, bar(C::kDrain));
       if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
