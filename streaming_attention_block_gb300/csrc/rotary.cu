@@ -227,7 +227,7 @@ rotary_kernel(const __grid_constant__ RotaryParams p) {
 }
 
 template <typename T, Mode M>
-cudaError_t launch(RotaryParams& p, cudaStream_t s) {
+cudaError_t launch(RotaryParams& p, int sms, cudaStream_t s) {
   constexpr int N = Vec<T>::N;
   const int half = p.dims / 2, rest = p.D - p.dims;
   p.units = M == kInterleaved ? p.D / N : M == kHalfVec ? half / N + (rest / N + 1) / 2 : half + rest;
@@ -237,7 +237,7 @@ cudaError_t launch(RotaryParams& p, cudaStream_t s) {
   // tokens per block: those that leave the fewest of the threads' batch slots
   // empty, but a block or two for every SM before that
   double best = 0.0;
-  for (int t = 1; t <= kMaxTokens && t <= columns && (t == 1 || tokens / t >= 2 * 152); ++t) {
+  for (int t = 1; t <= kMaxTokens && t <= columns && (t == 1 || tokens / t >= 2 * sms); ++t) {
     const int splits = columns / t < heads ? columns / t : heads;
     const int rows = (heads + splits - 1) / splits;  // per thread
     const double used = (double)t * heads / ((double)columns * ((rows + kBatch - 1) / kBatch * kBatch));
@@ -258,15 +258,15 @@ cudaError_t launch(RotaryParams& p, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_layout(RotaryParams& p, cudaStream_t s) {
-  if (!p.half_layout) return launch<T, kInterleaved>(p, s);
-  return (p.dims / 2) % Vec<T>::N == 0 ? launch<T, kHalfVec>(p, s) : launch<T, kHalfScalar>(p, s);
+cudaError_t launch_layout(RotaryParams& p, int sms, cudaStream_t s) {
+  if (!p.half_layout) return launch<T, kInterleaved>(p, sms, s);
+  return (p.dims / 2) % Vec<T>::N == 0 ? launch<T, kHalfVec>(p, sms, s) : launch<T, kHalfScalar>(p, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s) {
-  return fp32 ? launch_layout<float>(p, s) : launch_layout<uint16_t>(p, s);
+cudaError_t launch_rotary(RotaryParams& p, bool fp32, int sms, cudaStream_t s) {
+  return fp32 ? launch_layout<float>(p, sms, s) : launch_layout<uint16_t>(p, sms, s);
 }
 
 }  // namespace sab

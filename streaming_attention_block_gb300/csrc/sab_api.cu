@@ -907,8 +907,8 @@ static sab_status rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, 
   p.sine = backward ? -plan->magnitude : plan->magnitude;
   memcpy(p.axis, plan->axis, sizeof(p.axis));
   memcpy(p.step, plan->step, sizeof(p.step));
-  return launch_rotary(p, dtype == SAB_DTYPE_FP32, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
-                                                                                                   : SAB_ERR_CUDA;
+  const cudaError_t e = launch_rotary(p, dtype == SAB_DTYPE_FP32, device_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 
 sab_status sab_rotary(const sab_rotary_plan* plan, const sab_rotary_rows* q, const sab_rotary_rows* k,

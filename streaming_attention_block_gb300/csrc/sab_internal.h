@@ -286,7 +286,7 @@ cudaError_t launch_append_fp8(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_counter_add(long long* counter, long long delta, cudaStream_t s);
 cudaError_t launch_qk_rope(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_attention_backward(const BwdParams& p, cudaStream_t s);
-cudaError_t launch_rotary(RotaryParams& p, bool fp32, cudaStream_t s);
+cudaError_t launch_rotary(RotaryParams& p, bool fp32, int sms, cudaStream_t s);
 // the state before every segment, into p.carry (nseg > 1); the state after the
 // last, if p.state_out is given
 cudaError_t launch_decay_segments(DecayRuns& r, cudaStream_t s);
