@@ -480,7 +480,7 @@ typedef struct {
   double original_context;  /* RAMP: c > 0                                              */
   double ramp_fast;         /* RAMP: turns from which a pair keeps its frequency        */
   double ramp_slow;         /* RAMP: turns up to which it is stretched fully (< fast)   */
-  double magnitude;         /* factor on the rotated pairs, finite, > 0                 */
+  double magnitude;         /* factor on the rotated pairs, finite and > 0 in fp32      */
 } sab_rotary_desc;
 
 #define SAB_ROTARY_MAX_DIMS 256

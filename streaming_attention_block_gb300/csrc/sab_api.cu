@@ -809,7 +809,7 @@ sab_status sab_rotary_plan_init(const sab_rotary_desc* desc, sab_rotary_plan* pl
     dims += d.band[a];
   }
   if (dims > SAB_ROTARY_MAX_DIMS) return SAB_ERR_INVALID_ARG;
-  if (!(d.base > 1.0) || !isfinite(d.base) || !(d.magnitude > 0.0) || !isfinite((float)d.magnitude))
+  if (!(d.base > 1.0) || !isfinite(d.base) || !((float)d.magnitude > 0.f) || !isfinite((float)d.magnitude))
     return SAB_ERR_INVALID_ARG;
   double s = 1.0;
   if (d.scaling != SAB_ROTARY_SCALE_NONE) {

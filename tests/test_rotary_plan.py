@@ -52,3 +52,11 @@ def test_frequencies_to_the_documented_error(scaling, base):
     if scaling == sab.ROTARY_SCALE_RAMP:
         limit *= 1 + s * fast / (fast - slow)
     assert worst <= limit, f"2^{math.log2(worst):.2f}"
+
+
+def test_a_magnitude_that_fp32_holds_as_zero_is_refused():
+    """It would turn every pair to zero without an error."""
+    for bad in (1e-60, 7e-46):
+        with pytest.raises(sab.SabError):
+            sab.rotary_plan((64,), magnitude=bad)
+    assert sab.rotary_plan((64,), magnitude=2e-45).magnitude > 0
