@@ -641,13 +641,14 @@ def decay_attention(Q, K, V, log_decay, scale: float, O, state_in=None, state_ou
     a decay per head, from the state [B, H, D, D] fp32 ``state_in`` to
     ``state_out`` (see include/sab.h)."""
     B, L, H, D = Q.shape
+    dev = _device()
+    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
+    q = _arg(Q, x, bf, "Q", dev)  # before scratch is made on its device
     if workspace is None:
         workspace = _scratch(decay_attention_workspace(B, L, H, D), Q, stream)
-    dev = _device()
     ws, ws_bytes = _workspace(workspace, dev)
-    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention(
-        _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
+        q, _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev),
         _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
         _arg(state_in, st, f4, "state_in", dev), B, L, H, D, float(scale), _arg(O, x, bf, "O", dev),
         _arg(state_out, st, f4, "state_out", dev), ws, ws_bytes, _stream(stream, dev)), "decay_attention")
@@ -671,13 +672,14 @@ def decay_attention_backward(Q, K, V, dO, log_decay, scale: float, dQ, dK, dV, s
     """sab_decay_attention_backward: (dQ, dK, dV) and d_state_in of
     decay_attention (see include/sab.h)."""
     B, L, H, D = Q.shape
+    dev = _device()
+    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
+    q = _arg(Q, x, bf, "Q", dev)  # before scratch is made on its device
     if workspace is None:
         workspace = _scratch(decay_attention_backward_workspace(B, L, H, D), Q, stream)
-    dev = _device()
     ws, ws_bytes = _workspace(workspace, dev)
-    x, st, bf, f4 = (B, L, H, D), (B, H, D, D), torch.bfloat16, torch.float32
     _check(library().sab_decay_attention_backward(
-        _arg(Q, x, bf, "Q", dev), _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev), _arg(dO, x, bf, "dO", dev),
+        q, _arg(K, x, bf, "K", dev), _arg(V, x, bf, "V", dev), _arg(dO, x, bf, "dO", dev),
         _arg(log_decay, (H,), f4, "log_decay", dev), _arg(seq_len, (B,), torch.int32, "seq_len", dev),
         _arg(state_in, st, f4, "state_in", dev), _arg(d_state_out, st, f4, "d_state_out", dev), B, L, H, D,
         float(scale), _arg(dQ, x, bf, "dQ", dev), _arg(dK, x, bf, "dK", dev), _arg(dV, x, bf, "dV", dev),
