@@ -930,13 +930,28 @@ static bool decay_shape_ok(int B, int L, int H, int D) {
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Runs this short go token by token: 16 tokens of 12 heads of 128 take 5.2 us so
-// against 11.1 us in tiles, of 96 heads 14.4 against 11.7, of 768 heads 56
-// against 63; of 12, 192 and 768 heads of 64 3.8, 7.8 and 19 against 5.2, 11 and
-// 32.  While the CTAs (32 value columns each) fit the SMs once, the tile
-// kernel's set-up buys more tokens: 40 of 12 heads of 128 in 10 us.
-static bool decay_short(int B, int L, int H, int D) {
-  return L <= (D == 128 && (long long)B * H * (D / 32) <= device_sms() ? 40 : 16);
+// Runs of up to so many tokens go token by token in fp32, with 32 value columns a
+// CTA; longer ones in tiles.  Measured, us, token by token against tiles:
+//   forward, heads of 128, 16 tokens: 12 heads 4.7 / 5.2, with states 5.3 / 11.0;
+//     96 heads 13.6 / 5.5 and 15.9 / 12.5; 768 heads 56.6 / 30.4 and 60.5 / 66.4.
+//     40 tokens of 12 heads 10.1 / 5.4 and 10.6 / 11.1; 4 tokens of 96 heads 5.1 /
+//     5.4 and 7.7 / 12.3.  Heads of 64, 16 tokens: 12, 192 and 768 heads 3.5 / 4.4,
+//     7.3 / 8.6 and 18.7 / 24.6, with states 3.8 / 5.7, 7.7 / 11.1 and 21.0 / 34.1.
+//   gradients (three launches token by token, shared ones in tiles), heads of 128:
+//     12 tokens of 12 heads 11.5 / 5.3, with states 13.4 / 14.3; of 48 heads 34.4 /
+//     5.5 and 43.4 / 16.2; 4 tokens of 192 heads 18.1 / 20.3 and 31.3 / 36.9.  Heads
+//     of 64: 8 tokens of 12 heads 8.1 / 4.5 and 8.8 / 9.8; 12 tokens of 304 heads
+//     18.6 / 26.6 and 23.3 / 31.5.
+// So: longer runs while the CTAs fit the SMs once, shorter ones beside tiles that
+// need one wave, longer ones beside tiles that write states or need several waves.
+static int decay_short_tokens(long long bh, int D, bool state, bool gradients) {
+  const long long sms = device_sms();
+  const bool once = bh * (D / 32) <= sms;
+  if (!gradients) return D == 64 ? 16 : once ? (state ? 40 : 16) : (state ? 12 : 4);
+  const long long waves = (3 * bh + sms - 1) / sms;  // of the tiles
+  if (waves >= 3) return D == 128 ? 4 : 12;
+  if (D == 128) return once && state ? 12 : 0;
+  return waves == 2 ? 2 : state ? 8 : 0;
 }
 
 // How a call cuts its sequences.  A CTA takes a sequence's head as a whole, or,
@@ -1026,7 +1041,9 @@ static sab_status decay_runs(const DecayRun* runs, int n, const DecayCut& cut, c
   DecayRuns all;
   memset(&all, 0, sizeof(all));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool is_short = decay_short(B, L, H, D), cut_up = cut.nseg > 1;
+  bool state = false;
+  for (int i = 0; i < n; ++i) state = state || runs[i].out != nullptr;
+  const bool is_short = L <= decay_short_tokens((long long)B * H, D, state, n > 1), cut_up = cut.nseg > 1;
   const size_t states = cut_up ? (size_t)B * H * cut.nseg : 0, held = ws_bytes / ((size_t)D * D * sizeof(float));
   for (int i = 0; i < n; ++i) {
     const DecayRun& r = runs[i];
