@@ -441,6 +441,8 @@ constexpr uint32_t kAMajorMN = 1u << 15;  // instruction descriptor: A is MN-maj
 // and need each other only through the MMAs.  (One group doing all four steps
 // in turn: 198 us for 2 x 30720 tokens of 12 heads of 128; two: 135 us, the
 // four roles' code kept small enough for the instruction cache, 222 us before.)
+// 608 threads leave 96 registers each; heads of 128 spill 44 bytes of a thread
+// (68 and 144 bytes reloaded with two and three parts), heads of 64 up to 8.
 // D = 128: a tile's output is staged over its v once the update has read it;
 // nothing else is free.  D = 64 has room for an output buffer of its own and
 // for two sets of k's parts (kRoomy): the next tile's scores go ahead of the
