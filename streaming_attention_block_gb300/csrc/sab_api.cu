@@ -864,6 +864,13 @@ static bool rotary_rows_ok(const sab_rotary_rows* r, int B, int L, int D, int es
   if (r->in == r->out && (r->in_batch != r->out_batch || r->in_token != r->out_token) && (long long)B * L > 1)
     return false;
   const long long row = (long long)r->heads * D;
+  // whole extents within 2^47 elements, more than a device can address: what is
+  // formed from the strides below and in the kernel stays within 64 bits
+  constexpr long long kMost = 1LL << 47;
+  for (int i = 0; i < 4; i += 2) {
+    if (B > 1 && st[i] > kMost / (B - 1)) return false;
+    if (L > 1 && st[i + 1] > kMost / (L - 1)) return false;
+  }
   const bool token_apart = L == 1 || r->out_token >= row, batch_apart = B == 1 || r->out_batch >= row;
   const bool token_inner = B == 1 || r->out_batch >= (L - 1) * r->out_token + row;
   const bool batch_inner = L == 1 || r->out_token >= (B - 1) * r->out_batch + row;
