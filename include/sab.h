@@ -607,6 +607,53 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
                                         void* stream);
 
 /*
+ * Layer norm over the channels of each row, and its gradients.  The method
+ * normalises queries and keys only (sab_qk_norm_rope); a video transformer's
+ * block also has a layer norm with weights before its cross attention, and
+ * ones whose scale and shift come from the noise level, which in a streamed
+ * video is a chunk's own.  So `group_rows` consecutive rows share one row of
+ * weight and bias (group_rows >= rows: one row for all):
+ *   y = xhat * (weight_offset + weight_g) + bias_g,  xhat = (x - mean) * rstd,
+ *   mean = sum(x) / C,  rstd = 1 / sqrt(sum((x - mean)^2) / C + eps),
+ * g = row / group_rows.  weight_offset is 1 where a scale around 0 is given, 0
+ * for weights around 1.  weight NULL: factor 1; bias NULL: 0.
+ * X, Y        device rows of C channels of type `dtype`, row r at element
+ *             r * stride (strides in elements, rows of Y apart); element-
+ *             aligned.  16-byte aligned rows take 16-byte accesses.  Y may be X
+ *             with the same stride.
+ * weight, bias  device fp32 [ceil(rows / group_rows), C].
+ * mean, rstd  device fp32 [rows] or NULL (not wanted): what the backward reads.
+ * Computed in fp32, rounded once.  C <= SAB_NORM_MAX_CHANNELS.
+ *
+ * Backward, for dY with respect to Y, with t = dY * (weight_offset + weight_g):
+ *   dX = rstd * (t - mean(t) - xhat * mean(t * xhat)),
+ *   dweight_g = sum over the group's rows of dY * xhat,  dbias_g = sum of dY
+ * (fp32 [groups, C], or NULL: not wanted).  dX may be dY or X with the same
+ * stride.  workspace: device scratch of sab_layer_norm_backward_workspace bytes
+ * (0: may be NULL), 256-byte aligned, no zero-fill needed; calls that can
+ * overlap on the GPU need one each.  The sums' order is fixed by the shape:
+ * equal calls give equal bits.
+ * Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+#define SAB_NORM_MAX_CHANNELS 8192
+typedef struct {
+  long long rows;        /* 1 .. 2^31 - 1                              */
+  int channels;          /* C                                          */
+  long long group_rows;  /* rows that share a row of weight and bias   */
+  float weight_offset;
+  float eps;             /* > 0                                        */
+  int dtype;             /* sab_dtype of X, Y, dX, dY                  */
+} sab_norm_desc;
+
+sab_status sab_layer_norm(const sab_norm_desc* desc, const void* X, long long x_stride, const float* weight,
+                          const float* bias, void* Y, long long y_stride, float* mean, float* rstd, void* stream);
+size_t sab_layer_norm_backward_workspace(long long rows, int channels, long long group_rows);
+sab_status sab_layer_norm_backward(const sab_norm_desc* desc, const void* X, long long x_stride, const void* dY,
+                                   long long dy_stride, const float* weight, const float* mean, const float* rstd,
+                                   void* dX, long long dx_stride, float* dweight, float* dbias, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then report and clear the device error word that
  * bounded pipeline waits set when they give up (SAB_ERR_TIMEOUT) and that the
  * index checks of a debug build set (SAB_ERR_BOUNDS, reported first when both

@@ -98,6 +98,9 @@ def library() -> ctypes.CDLL:
         "sab_decay_attention_step": (I, [P, P, P, P, P, P, I, I, I, F, P, P, P]),
         "sab_decay_attention_backward_workspace": (SZ, [I, I, I, I]),
         "sab_decay_attention_backward": (I, [P] * 8 + [I, I, I, I, F] + [P] * 5 + [SZ, P]),
+        "sab_layer_norm": (I, [P, P, LL, P, P, P, LL, P, P, P]),
+        "sab_layer_norm_backward_workspace": (SZ, [LL, I, LL]),
+        "sab_layer_norm_backward": (I, [P, P, LL, P, LL, P, P, P, P, LL, P, P, P, SZ, P]),
         "sab_status_string": (ctypes.c_char_p, [I]),
         "sab_version": (ctypes.c_char_p, []),
     }
@@ -713,6 +716,105 @@ class DecayState:
         decay_attention_step(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, self.state,
                              self.state, O, active, stream)
         return O
+
+
+# ------------------------------------------------------------- layer norm
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("channels", ctypes.c_int), ("group_rows", ctypes.c_longlong),
+                ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+_NORM = struct.Struct("@qiqffi4x")  # the layout of NormDesc, packed faster than the structure is built
+
+
+def _norm_rows(t, like, name, dev):
+    """Device pointer and row stride of ``t``, rows of channels in its last
+    axis: all leading axes as one, with one stride between rows."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in _DTYPES:
+        _refuse(t, name, dev, tuple(_DTYPES))
+    if t.dim() == 0 or t.numel() == 0:
+        raise ValueError(f"{name}: expected [..., channels] with at least one row and channel")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name}: expected the shape and type of X, {tuple(like.shape)} {like.dtype}, got "
+                         f"{tuple(t.shape)} {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: a row's channels must be contiguous")
+    step = span = None  # stride of the innermost leading axis, and what the next one has to have
+    for n, st in reversed(tuple(zip(t.shape[:-1], t.stride()[:-1]))):
+        if n == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != span:
+            raise ValueError(f"{name}: rows must be one stride apart")
+        span = st * n
+    return t.data_ptr(), t.shape[-1] if step is None else step
+
+
+def _norm_desc(X, group_rows, weight_offset, eps):
+    C = X.shape[-1]
+    rows = X.numel() // C
+    group_rows = rows if group_rows is None else int(group_rows)
+    if group_rows < 1:
+        raise SabError(1, "layer_norm: group_rows")
+    groups = -(-rows // group_rows)
+    return _NORM.pack(rows, C, group_rows, float(weight_offset), float(eps), _DTYPES[X.dtype]), rows, C, groups
+
+
+def _norm_param(t, groups, C, name, dev):
+    """Device pointer of a [groups, C] fp32 tensor ([C] for one group), or None."""
+    if t is None:
+        return None
+    return _arg(t, (C,) if groups == 1 and isinstance(t, torch.Tensor) and t.dim() == 1 else (groups, C),
+                torch.float32, name, dev)
+
+
+def layer_norm(X, weight, bias, eps: float, Y, mean=None, rstd=None, group_rows=None, weight_offset: float = 0.0,
+               stream=None):
+    """sab_layer_norm: normalise the rows of ``X`` [..., C] (bf16 or fp32, rows
+    one stride apart) into ``Y`` (may be X).  ``weight``, ``bias``: fp32 [C], or
+    [groups, C] with ``group_rows`` rows to a group, or None.  ``mean``,
+    ``rstd``: fp32 [rows], kept for the gradients (see include/sab.h)."""
+    dev = _device()
+    x, xs = _norm_rows(X, None, "X", dev)
+    y, ys = (x, xs) if Y is X else _norm_rows(Y, X, "Y", dev)
+    desc, rows, C, groups = _norm_desc(X, group_rows, weight_offset, eps)
+    status = library().sab_layer_norm(
+        desc, x, xs, _norm_param(weight, groups, C, "weight", dev), _norm_param(bias, groups, C, "bias", dev), y, ys,
+        _arg(mean, (rows,), torch.float32, "mean", dev), _arg(rstd, (rows,), torch.float32, "rstd", dev),
+        _stream(stream, dev))
+    if status != 0:
+        raise SabError(status, "layer_norm")
+
+
+def layer_norm_backward_workspace(rows: int, channels: int, group_rows: int) -> int:
+    return int(library().sab_layer_norm_backward_workspace(int(rows), int(channels), int(group_rows)))
+
+
+def layer_norm_backward(X, dY, weight, mean, rstd, dX, dweight=None, dbias=None, group_rows=None,
+                        weight_offset: float = 0.0, workspace=None, stream=None):
+    """sab_layer_norm_backward: dX (may be dY or X) and the sums ``dweight``,
+    ``dbias`` (shaped as weight and bias, or None) from layer_norm's input and
+    its ``mean`` and ``rstd`` (see include/sab.h)."""
+    dev = _device()
+    x, xs = _norm_rows(X, None, "X", dev)
+    dy, dys = _norm_rows(dY, X, "dY", dev)
+    dx, dxs = _norm_rows(dX, X, "dX", dev)
+    desc, rows, C, groups = _norm_desc(X, group_rows, weight_offset, 1.0)  # eps is in rstd
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = _scratch(layer_norm_backward_workspace(rows, C, rows if group_rows is None else group_rows), X,
+                             stream)
+    ws, ws_bytes = _workspace(workspace, dev)
+    status = library().sab_layer_norm_backward(
+        desc, x, xs, dy, dys, _norm_param(weight, groups, C, "weight", dev),
+        _arg(mean, (rows,), torch.float32, "mean", dev), _arg(rstd, (rows,), torch.float32, "rstd", dev), dx, dxs,
+        _norm_param(dweight, groups, C, "dweight", dev), _norm_param(dbias, groups, C, "dbias", dev), ws, ws_bytes,
+        _stream(stream, dev))
+    if status != 0:
+        raise SabError(status, "layer_norm_backward")
 
 
 class KVRing:

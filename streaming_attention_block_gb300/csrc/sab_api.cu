@@ -1184,6 +1184,128 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   return decay_runs(runs, 3, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
 }
 
+// Row ranges of a group whose sums a layer norm's gradients keep apart: about
+// four blocks for every SM over all groups, none of fewer than 16 rows.
+struct NormCut {
+  long long groups, split_rows;
+  int splits;
+};
+static NormCut norm_cut(long long rows, long long group_rows) {
+  NormCut n;
+  if (group_rows > rows) group_rows = rows;
+  n.groups = (rows + group_rows - 1) / group_rows;
+  long long splits = 4LL * device_sms() / n.groups;
+  splits = std::max(1LL, std::min(splits, group_rows / 16));
+  n.split_rows = (group_rows + splits - 1) / splits;
+  n.splits = (int)((group_rows + n.split_rows - 1) / n.split_rows);
+  return n;
+}
+static bool norm_shape_ok(long long rows, int channels, long long group_rows) {
+  return rows >= 1 && rows <= 0x7fffffffLL && channels >= 1 && channels <= SAB_NORM_MAX_CHANNELS && group_rows >= 1;
+}
+static bool norm_stride_ok(long long stride, long long rows, int channels, bool out) {
+  if (stride < 0 || (rows > 1 && stride > (1LL << 47) / rows)) return false;
+  return !out || rows == 1 || stride >= channels;
+}
+
+// What the two directions share; `io` are the tensors of the rows' type.
+static sab_status norm_common(const sab_norm_desc* d, const void* const* io, const long long* strides, int n,
+                              const void* const* f32, int nf, NormParams& p, bool& vec) {
+  if (d == nullptr || !norm_shape_ok(d->rows, d->channels, d->group_rows)) return SAB_ERR_INVALID_ARG;
+  if (d->dtype != SAB_DTYPE_BF16 && d->dtype != SAB_DTYPE_FP32) return SAB_ERR_INVALID_ARG;
+  if (!(d->eps > 0.f) || !isfinite(d->eps) || !isfinite(d->weight_offset)) return SAB_ERR_INVALID_ARG;
+  const uintptr_t es = d->dtype == SAB_DTYPE_BF16 ? 2 : 4;
+  vec = (d->channels * es) % 16 == 0;
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(io[i]);
+    if (a == 0 || a % es != 0 || !norm_stride_ok(strides[i], d->rows, d->channels, i == n - 1))
+      return SAB_ERR_INVALID_ARG;
+    vec = vec && a % 16 == 0 && (strides[i] * es) % 16 == 0;
+  }
+  for (int i = 0; i + 1 < n; ++i)  // in place: the same rows
+    if (io[i] == io[n - 1] && strides[i] != strides[n - 1] && d->rows > 1) return SAB_ERR_INVALID_ARG;
+  for (int i = 0; i < nf; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(f32[i]);
+    if (a % 4 != 0) return SAB_ERR_INVALID_ARG;
+    vec = vec && a % 16 == 0;
+  }
+  memset(&p, 0, sizeof(p));
+  const NormCut cut = norm_cut(d->rows, d->group_rows);
+  p.rows = d->rows;
+  p.group_rows = std::min(d->group_rows, d->rows);
+  p.groups = cut.groups;
+  p.splits = cut.splits;
+  p.split_rows = cut.split_rows;
+  p.C = d->channels;
+  p.inv_c = 1.f / (float)d->channels;
+  p.eps = d->eps;
+  p.offset = d->weight_offset;
+  return SAB_OK;
+}
+
+sab_status sab_layer_norm(const sab_norm_desc* desc, const void* X, long long x_stride, const float* weight,
+                          const float* bias, void* Y, long long y_stride, float* mean, float* rstd, void* stream) {
+  const void* io[] = {X, Y};
+  const long long strides[] = {x_stride, y_stride};
+  const void* f32[] = {weight, bias};
+  NormParams p;
+  bool vec = false;
+  const sab_status st = norm_common(desc, io, strides, 2, f32, 2, p, vec);
+  if (st != SAB_OK) return st;
+  if (!aligned4(mean) || !aligned4(rstd)) return SAB_ERR_INVALID_ARG;
+  p.x = X;
+  p.x_row = x_stride;
+  p.y = Y;
+  p.y_row = y_stride;
+  p.weight = weight;
+  p.bias = bias;
+  p.mean = mean;
+  p.rstd = rstd;
+  const cudaError_t e =
+      launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, vec, false, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+}
+
+size_t sab_layer_norm_backward_workspace(long long rows, int channels, long long group_rows) {
+  if (!norm_shape_ok(rows, channels, group_rows)) return 0;
+  const NormCut n = norm_cut(rows, group_rows);
+  return n.splits == 1 ? 0 : align_up((size_t)n.groups * n.splits * 2 * channels * sizeof(float), kAlign);
+}
+
+sab_status sab_layer_norm_backward(const sab_norm_desc* desc, const void* X, long long x_stride, const void* dY,
+                                   long long dy_stride, const float* weight, const float* mean, const float* rstd,
+                                   void* dX, long long dx_stride, float* dweight, float* dbias, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  const void* io[] = {X, dY, dX};
+  const long long strides[] = {x_stride, dy_stride, dx_stride};
+  const void* f32[] = {weight, dweight, dbias};
+  NormParams p;
+  bool vec = false;
+  const sab_status st = norm_common(desc, io, strides, 3, f32, 3, p, vec);
+  if (st != SAB_OK) return st;
+  if (mean == nullptr || rstd == nullptr || !aligned4(mean) || !aligned4(rstd)) return SAB_ERR_INVALID_ARG;
+  if (dweight != nullptr && dweight == dbias) return SAB_ERR_INVALID_ARG;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  const size_t need = sums ? sab_layer_norm_backward_workspace(desc->rows, desc->channels, desc->group_rows) : 0;
+  if (need > 0 && (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0))
+    return SAB_ERR_WORKSPACE;
+  p.x = X;
+  p.x_row = x_stride;
+  p.dy = dY;
+  p.dy_row = dy_stride;
+  p.y = dX;
+  p.y_row = dx_stride;
+  p.weight = weight;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.part = static_cast<float*>(workspace);
+  const cudaError_t e =
+      launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, vec, true, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
+}
+
 sab_status sab_selftest_split_abort(const sab_ring* ring, int layer, long long chunk, const void* Q,
                                     const void* K_cur, const void* V_cur, int window, int use_sink, int num_splits,
                                     float softmax_scale, void* O, float* LSE, void* workspace, size_t ws_bytes,

@@ -280,6 +280,26 @@ struct DecayStepParams {
   float scale;
 };
 
+// Layer norm of rows of C channels, forward and backward (see sab_layer_norm).
+struct NormParams {
+  const void* x;
+  const void* dy;           // backward
+  void* y;                  // Y, or dX
+  long long x_row, dy_row, y_row;  // row strides in elements
+  const float* weight;      // [groups, C] or null
+  const float* bias;
+  float* mean;              // [rows] (forward: written, may be null)
+  float* rstd;
+  float* dweight;           // [groups, C] or null
+  float* dbias;
+  float* part;              // [groups][splits][2][C] partial sums (splits > 1)
+  long long rows, group_rows, groups, split_rows;
+  int splits;               // row ranges of a group (backward)
+  int C;
+  int lanes, warps;         // threads of a row, set by the launcher
+  float inv_c, eps, offset;
+};
+
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_append_bf16(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_append_fp8(const AppendParams& p, cudaStream_t s);
@@ -294,6 +314,8 @@ cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
+// vec: channels, strides and pointers allow 16-byte accesses
+cudaError_t launch_layer_norm(NormParams& p, bool fp32, bool vec, bool back, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
 // One query tile per CTA, key-half softmax warpgroups; unsplit KV only.
 cudaError_t launch_chunk_attention_kh(const AttnParams& p, cudaStream_t s);
