@@ -13,6 +13,9 @@
 // one read to its write, so the variance is taken about the mean (a second pass
 // over registers, not E[x^2] - mean^2, which loses all digits of rows far off
 // centre).  Sums, moments and the weight's gradients are fp32.
+#include <algorithm>
+#include <atomic>
+
 #include "ptx.cuh"
 #include "sab_internal.h"
 
@@ -21,286 +24,419 @@ namespace {
 
 using namespace ptx;
 
-// N elements of a row, as one access.  Rows whose channels and strides are
-// multiples of 16 bytes go in 16-byte vectors, all others element by element.
-template <typename T, bool V>
+// Values in registers: pairs in packed fp32 arithmetic, or single ones where an
+// access holds one element.
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float both(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float both(float a) { return a; }
+template <typename E>
+__device__ __forceinline__ E splat(float x);
+template <>
+__device__ __forceinline__ float2 splat<float2>(float x) {
+  return make_float2(x, x);
+}
+template <>
+__device__ __forceinline__ float splat<float>(float x) {
+  return x;
+}
+
+// N elements of a row, as one access of A bytes: 16 where rows, strides and
+// weights allow it, else 4, else (bf16 with an odd stride) one element.  M
+// values of type E.
+__device__ __forceinline__ float2 wide(uint32_t w) {  // two bf16
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <typename T, int A>
 struct Pack;
 template <>
-struct Pack<uint16_t, true> {
-  static constexpr int N = 8;
+struct Pack<uint16_t, 16> {
+  static constexpr int N = 8, M = 4;
   typedef uint4 Raw;
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  typedef float2 E;
+  static __device__ __forceinline__ void unpack(const Raw& r, E (&f)[M]) {
+    f[0] = wide(r.x), f[1] = wide(r.y), f[2] = wide(r.z), f[3] = wide(r.w);
   }
-  static __device__ __forceinline__ Raw pack(const float (&f)[N]) {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  static __device__ __forceinline__ Raw pack(const E (&f)[M]) {
+    return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                      pack_bf16(f[3].x, f[3].y));
   }
   static __device__ __forceinline__ Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
 };
 template <>
-struct Pack<float, true> {
-  static constexpr int N = 4;
+struct Pack<float, 16> {
+  static constexpr int N = 4, M = 2;
   typedef float4 Raw;
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
-    f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w;
+  typedef float2 E;
+  static __device__ __forceinline__ void unpack(const Raw& r, E (&f)[M]) {
+    f[0] = make_float2(r.x, r.y), f[1] = make_float2(r.z, r.w);
   }
-  static __device__ __forceinline__ Raw pack(const float (&f)[N]) { return make_float4(f[0], f[1], f[2], f[3]); }
+  static __device__ __forceinline__ Raw pack(const E (&f)[M]) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
   static __device__ __forceinline__ Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 template <>
-struct Pack<uint16_t, false> {
-  static constexpr int N = 1;
+struct Pack<uint16_t, 4> {
+  static constexpr int N = 2, M = 1;
+  typedef uint32_t Raw;
+  typedef float2 E;
+  static __device__ __forceinline__ void unpack(const Raw& r, E (&f)[M]) { f[0] = wide(r); }
+  static __device__ __forceinline__ Raw pack(const E (&f)[M]) { return pack_bf16(f[0].x, f[0].y); }
+  static __device__ __forceinline__ Raw zero() { return 0u; }
+};
+template <>
+struct Pack<uint16_t, 2> {
+  static constexpr int N = 1, M = 1;
   typedef uint16_t Raw;
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
-    f[0] = __uint_as_float((uint32_t)r << 16);
-  }
-  static __device__ __forceinline__ Raw pack(const float (&f)[N]) { return (uint16_t)pack_bf16(f[0], 0.f); }
+  typedef float E;
+  static __device__ __forceinline__ void unpack(const Raw& r, E (&f)[M]) { f[0] = __uint_as_float((uint32_t)r << 16); }
+  static __device__ __forceinline__ Raw pack(const E (&f)[M]) { return (uint16_t)pack_bf16(f[0], 0.f); }
   static __device__ __forceinline__ Raw zero() { return 0; }
 };
 template <>
-struct Pack<float, false> {
-  static constexpr int N = 1;
+struct Pack<float, 4> {
+  static constexpr int N = 1, M = 1;
   typedef float Raw;
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) { f[0] = r; }
-  static __device__ __forceinline__ Raw pack(const float (&f)[N]) { return f[0]; }
+  typedef float E;
+  static __device__ __forceinline__ void unpack(const Raw& r, E (&f)[M]) { f[0] = r; }
+  static __device__ __forceinline__ Raw pack(const E (&f)[M]) { return f[0]; }
   static __device__ __forceinline__ Raw zero() { return 0.f; }
 };
 
-// N consecutive fp32 values of a weight row
-template <int N>
-__device__ __forceinline__ void load_f32(const float* p, float (&f)[N]) {
-  if constexpr (N == 1) {
-    f[0] = __ldg(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
-    }
-  }
+// Hides where a raw access came from: what is unpacked after this is unpacked
+// anew, instead of held in twice the registers across a barrier.
+__device__ __forceinline__ void forget(uint4& r) { asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)); }
+__device__ __forceinline__ void forget(float4& r) { asm volatile("" : "+f"(r.x), "+f"(r.y), "+f"(r.z), "+f"(r.w)); }
+__device__ __forceinline__ void forget(uint32_t& r) { asm volatile("" : "+r"(r)); }
+__device__ __forceinline__ void forget(uint16_t& r) { asm volatile("" : "+h"(r)); }
+__device__ __forceinline__ void forget(float& r) { asm volatile("" : "+f"(r)); }
+
+// the values of a weight row that belong to an access
+__device__ __forceinline__ void load_f32(const float* p, float2 (&f)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
-template <int N>
-__device__ __forceinline__ void store_f32(float* p, const float (&f)[N]) {
-  if constexpr (N == 1) {
-    *p = f[0];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-  }
+__device__ __forceinline__ void load_f32(const float* p, float2 (&f)[2]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
 }
+__device__ __forceinline__ void load_f32(const float* p, float2 (&f)[1]) { f[0] = make_float2(__ldg(p), __ldg(p + 1)); }
+__device__ __forceinline__ void load_f32(const float* p, float (&f)[1]) { f[0] = __ldg(p); }
+__device__ __forceinline__ void store_f32(float* p, const float2 (&f)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+}
+__device__ __forceinline__ void store_f32(float* p, const float2 (&f)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+}
+__device__ __forceinline__ void store_f32(float* p, const float2 (&f)[1]) { p[0] = f[0].x, p[1] = f[0].y; }
+__device__ __forceinline__ void store_f32(float* p, const float (&f)[1]) { *p = f[0]; }
 
 // A row is shared by `lanes` (a power of two) lanes of a warp, or by all 32 of
-// p.warps warps.  Sum of K values over the row's threads; `buf` holds two sets
+// `warps` warps.  Sum of K values over the row's threads; `buf` holds two sets
 // of 32 x K floats, taken in turn so that one barrier a sum suffices.
 template <int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], int lanes, int warps, float* buf, int& turn) {
-  for (int o = lanes >> 1; o > 0; o >>= 1)
+  if (warps == 1) {
+    for (int o = lanes >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (warps == 1) return;
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    return;
+  }
+  // each step halves the lanes of a value or, while there are several, the
+  // values of a lane: K + 3 exchanges instead of 5 K (K = 8: 9 for 40)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int idx = 0;
+  float t[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) t[k] = v[k];
+  int left = K, low = 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (left > 1) {
+      left >>= 1;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int k = 0; k < K / 2; ++k)
+        if (k < left) {
+          const float give = up ? t[k] : t[k + left];
+          t[k] = (up ? t[k + left] : t[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      idx += up ? left : 0;
+      low = o - 1;
+    } else {
+      t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+    }
+  }
   float* b = buf + turn * 32 * K;
   turn ^= 1;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) b[warp * K + k] = v[k];
-  }
+  if ((lane & low) == 0) b[warp * K + idx] = t[0];
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = 0; w < warps; ++w)
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
+    if constexpr (K % 4 == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += b[w * K + k];
-}
-
-// One row per group of row threads; NV accesses a thread.
-template <typename T, bool V, int NV>
-__global__ void __launch_bounds__(V ? 512 : 1024) norm_kernel(const __grid_constant__ NormParams p) {
-  using P = Pack<T, V>;
-  constexpr int N = P::N;
-  __shared__ float buf[2 * 32];
-  const int per_row = p.lanes * p.warps;  // threads of a row
-  const int slot = threadIdx.x / per_row, me = threadIdx.x - slot * per_row;
-  const long long row = (long long)blockIdx.x * (blockDim.x / per_row) + slot;
-  const bool live = row < p.rows;
-  const int packs = p.C / N;
-  int turn = 0;
-  griddep_launch_dependents();
-  griddep_wait();
-  const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.x_row;
-  typename P::Raw raw[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = me + i * per_row;
-    raw[i] = live && j < packs ? reinterpret_cast<const typename P::Raw*>(x)[j] : P::zero();
-  }
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float f[N];
-    P::unpack(raw[i], f);
-#pragma unroll
-    for (int c = 0; c < N; ++c) s[0] += f[c];
-  }
-  row_sum<1>(s, p.lanes, p.warps, buf, turn);
-  const float mean = s[0] * p.inv_c;
-  s[0] = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float f[N];
-    P::unpack(raw[i], f);
-    const bool in = me + i * per_row < packs;
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const float d = in ? f[c] - mean : 0.f;
-      s[0] = fmaf(d, d, s[0]);
-    }
-  }
-  row_sum<1>(s, p.lanes, p.warps, buf, turn);
-  const float rstd = 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps));
-  if (!live) return;
-  if (me == 0) {
-    if (p.mean != nullptr) p.mean[row] = mean;
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
-  }
-  const long long group = p.group_rows >= p.rows ? 0 : row / p.group_rows;
-  const float* w = p.weight != nullptr ? p.weight + group * p.C : nullptr;
-  const float* b = p.bias != nullptr ? p.bias + group * p.C : nullptr;
-  T* y = static_cast<T*>(p.y) + row * p.y_row;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = me + i * per_row;
-    if (j >= packs) break;
-    float f[N], wf[N], bf[N];
-    P::unpack(raw[i], f);
-    if (w != nullptr) load_f32<N>(w + j * N, wf);
-    if (b != nullptr) load_f32<N>(b + j * N, bf);
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const float u = (f[c] - mean) * rstd;
-      f[c] = fmaf(u, w != nullptr ? p.offset + wf[c] : 1.f, b != nullptr ? bf[c] : 0.f);
-    }
-    reinterpret_cast<typename P::Raw*>(y)[j] = P::pack(f);
-  }
-}
-
-// A block takes a range of one group's rows, kRows at a time per group of row
-// threads, and keeps its channels' sums of dy * xhat and dy in registers over
-// the whole range.  Ranges of a group that several blocks share leave partial
-// sums for norm_sums_kernel: no atomics, so the results do not change from
-// call to call.
-constexpr int kRows = 4;
-
-template <typename T, bool V, int NV>
-__global__ void __launch_bounds__(V ? 512 : 1024) norm_back_kernel(const __grid_constant__ NormParams p) {
-  using P = Pack<T, V>;
-  constexpr int N = P::N;
-  extern __shared__ float sm[];  // row sums, or the blocks' channel sums of several row slots
-  const int per_row = p.lanes * p.warps;
-  const int slots = blockDim.x / per_row;
-  const int slot = threadIdx.x / per_row, me = threadIdx.x - slot * per_row;
-  const long long group = blockIdx.x / p.splits;
-  const int split = (int)(blockIdx.x - group * p.splits);
-  const long long g0 = group * p.group_rows;
-  const long long g1 = g0 + p.group_rows < p.rows ? g0 + p.group_rows : p.rows;
-  const long long r0 = g0 + split * p.split_rows;
-  const long long r1 = r0 + p.split_rows < g1 ? r0 + p.split_rows : g1;
-  const int packs = p.C / N;
-  int turn = 0;
-  griddep_launch_dependents();
-  griddep_wait();
-  float w[NV][N], dw[NV][N], db[NV][N];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = me + i * per_row;
-    if (p.weight != nullptr && j < packs) load_f32<N>(p.weight + group * p.C + j * N, w[i]);
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      w[i][c] = p.weight != nullptr && j < packs ? w[i][c] + p.offset : 1.f;
-      dw[i][c] = db[i][c] = 0.f;
-    }
-  }
-  const T* x = static_cast<const T*>(p.x);
-  const T* dy = static_cast<const T*>(p.dy);
-  for (long long base = r0; base < r1; base += (long long)slots * kRows) {
-    typename P::Raw xr[kRows][NV], yr[kRows][NV];
-    float mean[kRows], rstd[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const long long r = base + slot + (long long)k * slots;
-      const bool in = r < r1;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int j = me + i * per_row;
-        const bool on = in && j < packs;
-        xr[k][i] = on ? reinterpret_cast<const typename P::Raw*>(x + r * p.x_row)[j] : P::zero();
-        yr[k][i] = on ? reinterpret_cast<const typename P::Raw*>(dy + r * p.dy_row)[j] : P::zero();
+      for (int k = 0; k < K; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(b + w * K + k);
+        v[k] += x.x, v[k + 1] += x.y, v[k + 2] += x.z, v[k + 3] += x.w;
       }
-      mean[k] = in ? __ldg(p.mean + r) : 0.f;
-      rstd[k] = in ? __ldg(p.rstd + r) : 0.f;
-    }
-    float s[2 * kRows];
+    } else {
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      s[2 * k] = s[2 * k + 1] = 0.f;
+      for (int k = 0; k < K; ++k) v[k] += b[w * K + k];
+    }
+  }
+}
+
+// Where a block works: the rows [r0, r1) of one group, `slots` groups of row
+// threads side by side, each K rows at a time.
+struct Place {
+  int per_row, slots, slot, me, packs;
+  long long group, r0, r1;
+};
+__device__ __forceinline__ Place place(const NormParams& p, int n) {
+  Place a;
+  a.per_row = p.lanes * p.warps;
+  a.slots = blockDim.x / a.per_row;
+  a.slot = threadIdx.x / a.per_row;
+  a.me = threadIdx.x - a.slot * a.per_row;
+  a.packs = p.C / n;
+  a.group = blockIdx.x / p.splits;
+  const int split = (int)(blockIdx.x - a.group * p.splits);
+  const long long g0 = a.group * p.group_rows;
+  const long long g1 = min(g0 + p.group_rows, p.rows);
+  a.r0 = g0 + split * p.split_rows;
+  a.r1 = min(a.r0 + p.split_rows, g1);
+  return a;
+}
+
+// K rows' accesses of this thread, 0 where there is no row or channel
+template <typename P, typename T, int NV, int K>
+__device__ __forceinline__ void load_rows(typename P::Raw (&raw)[K][NV], const T* x, long long stride,
+                                          const Place& a, long long base) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const long long r = base + a.slot + (long long)k * a.slots;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = a.me + i * a.per_row;
+      raw[k][i] = r < a.r1 && j < a.packs ? reinterpret_cast<const typename P::Raw*>(x + r * stride)[j] : P::zero();
+    }
+  }
+}
+
+// A thread keeps its channels' weights in registers over all rows of its
+// block, and has the next K rows in flight while it works on K.
+template <typename T, int A, int NV, int K, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_kernel(const __grid_constant__ NormParams p) {
+  using P = Pack<T, A>;
+  using E = typename P::E;
+  constexpr int N = P::N, M = P::M;
+  __shared__ __align__(16) float buf[2 * 32 * K];
+  const Place a = place(p, N);
+  int turn = 0;
+  griddep_launch_dependents();
+  griddep_wait();
+  const T* x = static_cast<const T*>(p.x);
+  typename P::Raw nxt[K][NV];
+  load_rows<P>(nxt, x, p.x_row, a, a.r0);
+  E w[NV][M], b[NV][M];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = a.me + i * a.per_row;
+    const bool in = j < a.packs;
+    if (p.weight != nullptr && in) load_f32(p.weight + a.group * p.C + j * N, w[i]);
+    if (p.bias != nullptr && in) load_f32(p.bias + a.group * p.C + j * N, b[i]);
+#pragma unroll
+    for (int c = 0; c < M; ++c) {
+      w[i][c] = p.weight != nullptr && in ? vadd(w[i][c], splat<E>(p.offset)) : splat<E>(1.f);
+      b[i][c] = p.bias != nullptr && in ? b[i][c] : splat<E>(0.f);
+    }
+  }
+  const long long step = (long long)a.slots * K;
+  for (long long base = a.r0; base < a.r1; base += step) {
+    typename P::Raw raw[K][NV];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) raw[k][i] = nxt[k][i];
+    if (base + step < a.r1) load_rows<P>(nxt, x, p.x_row, a, base + step);
+    float s[K], mean[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      E t = splat<E>(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const bool in = me + i * per_row < packs;  // a missing channel holds 0, not the mean
-        float f[N], g[N];
-        P::unpack(xr[k][i], f);
-        P::unpack(yr[k][i], g);
+        E f[M];
+        P::unpack(raw[k][i], f);
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const float u = in ? (f[c] - mean[k]) * rstd[k] : 0.f;
-          const float t = g[c] * w[i][c];
-          s[2 * k] += t;
-          s[2 * k + 1] = fmaf(t, u, s[2 * k + 1]);
-          dw[i][c] = fmaf(g[c], u, dw[i][c]);
-          db[i][c] += g[c];
+        for (int c = 0; c < M; ++c) t = vadd(t, f[c]);
+      }
+      s[k] = both(t);
+    }
+    row_sum<K>(s, p.lanes, p.warps, buf, turn);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      mean[k] = s[k] * p.inv_c;
+      E t = splat<E>(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        E f[M];
+        forget(raw[k][i]);
+        P::unpack(raw[k][i], f);
+        if (a.me + i * a.per_row < a.packs) {
+#pragma unroll
+          for (int c = 0; c < M; ++c) {
+            const E d = vadd(f[c], splat<E>(-mean[k]));
+            t = vfma(d, d, t);
+          }
         }
       }
+      s[k] = both(t);
     }
-    row_sum<2 * kRows>(s, p.lanes, p.warps, sm, turn);
+    row_sum<K>(s, p.lanes, p.warps, buf, turn);
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const long long r = base + slot + (long long)k * slots;
-      if (r >= r1) break;
-      const float mt = s[2 * k] * p.inv_c, mu = s[2 * k + 1] * p.inv_c;
+    for (int k = 0; k < K; ++k) {
+      const long long r = base + a.slot + (long long)k * a.slots;
+      if (r >= a.r1) break;
+      const float rstd = 1.f / sqrtf(fmaf(s[k], p.inv_c, p.eps));
+      if (a.me == 0) {
+        if (p.mean != nullptr) p.mean[r] = mean[k];
+        if (p.rstd != nullptr) p.rstd[r] = rstd;
+      }
+      T* y = static_cast<T*>(p.y) + r * p.y_row;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = a.me + i * a.per_row;
+        if (j >= a.packs) break;
+        E f[M];
+        forget(raw[k][i]);
+        P::unpack(raw[k][i], f);
+#pragma unroll
+        for (int c = 0; c < M; ++c)
+          f[c] = vfma(vmul(vadd(f[c], splat<E>(-mean[k])), splat<E>(rstd)), w[i][c], b[i][c]);
+        reinterpret_cast<typename P::Raw*>(y)[j] = P::pack(f);
+      }
+    }
+  }
+}
+
+// The same for the gradients, with the sums of dy * xhat and dy of a thread's
+// channels in registers over all rows of its block.  Blocks that share a group
+// leave partial sums for norm_sums_kernel: no atomics, so the results do not
+// change from call to call.
+template <typename T, int A, int NV, int K, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_back_kernel(const __grid_constant__ NormParams p) {
+  using P = Pack<T, A>;
+  using E = typename P::E;
+  constexpr int N = P::N, M = P::M;
+  extern __shared__ __align__(16) float sm[];  // row sums, or the channel sums of several row slots
+  const Place a = place(p, N);
+  int turn = 0;
+  griddep_launch_dependents();
+  griddep_wait();
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  typename P::Raw nx[K][NV], ny[K][NV];
+  float nm[K], nr[K];
+  auto fetch = [&](long long base) {
+    load_rows<P>(nx, x, p.x_row, a, base);
+    load_rows<P>(ny, dy, p.dy_row, a, base);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long long r = base + a.slot + (long long)k * a.slots;
+      nm[k] = r < a.r1 ? __ldg(p.mean + r) : 0.f;
+      nr[k] = r < a.r1 ? __ldg(p.rstd + r) : 0.f;
+    }
+  };
+  fetch(a.r0);
+  E w[NV][M], dw[NV][M], db[NV][M];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = a.me + i * a.per_row;
+    const bool in = j < a.packs;
+    if (p.weight != nullptr && in) load_f32(p.weight + a.group * p.C + j * N, w[i]);
+#pragma unroll
+    for (int c = 0; c < M; ++c) {
+      w[i][c] = p.weight != nullptr && in ? vadd(w[i][c], splat<E>(p.offset)) : splat<E>(1.f);
+      dw[i][c] = db[i][c] = splat<E>(0.f);
+    }
+  }
+  const long long step = (long long)a.slots * K;
+  for (long long base = a.r0; base < a.r1; base += step) {
+    typename P::Raw xr[K][NV], yr[K][NV];
+    float mean[K], rstd[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      mean[k] = nm[k];
+      rstd[k] = nr[k];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) xr[k][i] = nx[k][i], yr[k][i] = ny[k][i];
+    }
+    if (base + step < a.r1) fetch(base + step);
+    float s[2 * K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      E s0 = splat<E>(0.f), s1 = s0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        E f[M], g[M];
+        P::unpack(xr[k][i], f);
+        P::unpack(yr[k][i], g);  // 0 where there is no channel: nothing is added there
+#pragma unroll
+        for (int c = 0; c < M; ++c) {
+          const E u = vmul(vadd(f[c], splat<E>(-mean[k])), splat<E>(rstd[k]));
+          const E t = vmul(g[c], w[i][c]);
+          s0 = vadd(s0, t);
+          s1 = vfma(t, u, s1);
+          dw[i][c] = vfma(g[c], u, dw[i][c]);
+          db[i][c] = vadd(db[i][c], g[c]);
+        }
+      }
+      s[2 * k] = both(s0);
+      s[2 * k + 1] = both(s1);
+    }
+    row_sum<2 * K>(s, p.lanes, p.warps, sm, turn);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long long r = base + a.slot + (long long)k * a.slots;
+      if (r >= a.r1) break;
+      const E mt = splat<E>(-s[2 * k] * p.inv_c), mu = splat<E>(-s[2 * k + 1] * p.inv_c);
       T* dx = static_cast<T*>(p.y) + r * p.y_row;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int j = me + i * per_row;
-        if (j >= packs) break;
-        float f[N], g[N];
+        const int j = a.me + i * a.per_row;
+        if (j >= a.packs) break;
+        E f[M], g[M];
+        forget(xr[k][i]);
+        forget(yr[k][i]);
         P::unpack(xr[k][i], f);
         P::unpack(yr[k][i], g);
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const float u = (f[c] - mean[k]) * rstd[k];
-          f[c] = rstd[k] * (fmaf(g[c], w[i][c], -mt) - u * mu);
+        for (int c = 0; c < M; ++c) {
+          const E u = vmul(vadd(f[c], splat<E>(-mean[k])), splat<E>(rstd[k]));
+          f[c] = vmul(splat<E>(rstd[k]), vfma(u, mu, vfma(g[c], w[i][c], mt)));
         }
         reinterpret_cast<typename P::Raw*>(dx)[j] = P::pack(f);
       }
     }
   }
   if (p.dweight == nullptr && p.dbias == nullptr) return;
-  // one range a group: the gradients themselves; several: this range's part
-  float* to_w = p.splits == 1 ? (p.dweight != nullptr ? p.dweight + group * p.C : nullptr)
+  // one block a group: the gradients themselves; several: this block's part
+  float* to_w = p.splits == 1 ? (p.dweight != nullptr ? p.dweight + a.group * p.C : nullptr)
                               : p.part + (long long)blockIdx.x * 2 * p.C;
-  float* to_b = p.splits == 1 ? (p.dbias != nullptr ? p.dbias + group * p.C : nullptr) : to_w + p.C;
-  if (slots == 1) {
+  float* to_b = p.splits == 1 ? (p.dbias != nullptr ? p.dbias + a.group * p.C : nullptr) : to_w + p.C;
+  if (a.slots == 1) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = me + i * per_row;
-      if (j >= packs) break;
-      if (to_w != nullptr) store_f32<N>(to_w + j * N, dw[i]);
-      if (to_b != nullptr) store_f32<N>(to_b + j * N, db[i]);
+      const int j = a.me + i * a.per_row;
+      if (j >= a.packs) break;
+      if (to_w != nullptr) store_f32(to_w + j * N, dw[i]);
+      if (to_b != nullptr) store_f32(to_b + j * N, db[i]);
     }
     return;
   }
@@ -310,19 +446,20 @@ __global__ void __launch_bounds__(V ? 512 : 1024) norm_back_kernel(const __grid_
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = me + i * per_row;
-      if (j < packs) {
+      const int j = a.me + i * a.per_row;
+      if (j < a.packs) {
+        float* to = sm + a.slot * p.C + j * N;
 #pragma unroll
-        for (int c = 0; c < N; ++c) sm[slot * p.C + j * N + c] = t == 0 ? dw[i][c] : db[i][c];
+        for (int c = 0; c < M; ++c) *reinterpret_cast<E*>(to + c * (N / M)) = t == 0 ? dw[i][c] : db[i][c];
       }
     }
     __syncthreads();
     float* to = t == 0 ? to_w : to_b;
     if (to != nullptr)
       for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-        float a = 0.f;
-        for (int k = 0; k < slots; ++k) a += sm[k * p.C + c];
-        to[c] = a;
+        float v = 0.f;
+        for (int k = 0; k < a.slots; ++k) v += sm[k * p.C + c];
+        to[c] = v;
       }
   }
 }
@@ -371,69 +508,106 @@ cudaError_t launch(K kernel, long long blocks, int threads, size_t smem, const N
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Threads of a row: lanes of one warp while `most` accesses a lane hold the
-// row, whole warps from there; returns the accesses a thread.
-int row_threads(int packs, int most, NormParams& p) {
+// Cuts every group's rows so that all groups together make one wave of
+// `resident` blocks an SM, in ranges of whole steps of `step` rows; at most
+// `most` ranges a group.
+void cut(NormParams& p, long long step, int resident, int sms, long long most) {
+  const long long steps = (p.group_rows + step - 1) / step;
+  const long long splits = std::max(1LL, std::min({steps, most, (long long)sms * resident / p.groups}));
+  p.split_rows = (steps + splits - 1) / splits * step;
+  p.splits = (int)((p.group_rows + p.split_rows - 1) / p.split_rows);
+}
+template <typename K>
+int resident_blocks(K kernel, int threads, size_t smem) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) n = 1;
+  return std::max(1, n);
+}
+
+// Threads of a row and of a block for NV accesses a thread; `threads` is 256
+// where a warp or less holds a row, but no more row slots than a group has
+// rows for.
+int block_threads(NormParams& p, int packs, int nv, int k) {
   p.lanes = 32;
-  p.warps = (packs + 32 * most - 1) / (32 * most);
-  if (p.warps == 1)
-    while (packs * 2 <= p.lanes) p.lanes /= 2;
-  return (packs + p.lanes * p.warps - 1) / (p.lanes * p.warps);
+  p.warps = (packs + 32 * nv - 1) / (32 * nv);
+  while (p.warps == 1 && packs * 2 <= p.lanes) p.lanes /= 2;
+  if (p.warps > 1) return 32 * p.warps;
+  int threads = 256;
+  while (threads > 32 && (long long)(threads / 2 / p.lanes) * k >= p.group_rows) threads /= 2;
+  return threads;
 }
 
-template <typename T, bool V>
-cudaError_t forward(NormParams& p, cudaStream_t s) {
-  const int packs = p.C / Pack<T, V>::N;
-  const int nv = row_threads(packs, packs > 6 * 1024 ? 8 : 6, p);
-  const int threads = p.warps == 1 ? 256 : 32 * p.warps;
-  const int slots = threads / (p.lanes * p.warps);
-  const long long blocks = (p.rows + slots - 1) / slots;
-  switch (nv) {
-    case 1: return launch(norm_kernel<T, V, 1>, blocks, threads, 0, p, s);
-    case 2: return launch(norm_kernel<T, V, 2>, blocks, threads, 0, p, s);
-    case 3: return launch(norm_kernel<T, V, 3>, blocks, threads, 0, p, s);
-    case 4: return launch(norm_kernel<T, V, 4>, blocks, threads, 0, p, s);
-    case 5: return launch(norm_kernel<T, V, 5>, blocks, threads, 0, p, s);
-    case 6: return launch(norm_kernel<T, V, 6>, blocks, threads, 0, p, s);
-    case 7:
-    case 8:
-      if constexpr (!V) return launch(norm_kernel<T, V, 8>, blocks, threads, 0, p, s);
-  }
-  return cudaErrorInvalidValue;
+// One instance each: NV accesses a thread, K rows at a time, blocks of at most
+// MAXT threads.
+template <typename T, int A, int NV, int K, int MAXT>
+cudaError_t forward(NormParams& p, int sms, cudaStream_t s) {
+  const int threads = block_threads(p, p.C / Pack<T, A>::N, NV, K);
+  if (threads > MAXT) return cudaErrorInvalidValue;
+  static std::atomic<int> held[33];  // blocks an SM holds, by warps a block
+  std::atomic<int>& h = held[threads / 32];
+  if (h.load() == 0) h.store(resident_blocks(norm_kernel<T, A, NV, K, MAXT>, threads, 0));
+  cut(p, (long long)(threads / (p.lanes * p.warps)) * K, h.load(), sms, p.rows);
+  return launch(norm_kernel<T, A, NV, K, MAXT>, p.groups * p.splits, threads, 0, p, s);
 }
-
-template <typename T, bool V>
-cudaError_t backward(NormParams& p, cudaStream_t s) {
-  const int packs = p.C / Pack<T, V>::N;
-  const int nv = row_threads(packs, V ? 16 / Pack<T, V>::N : 8, p);
-  const int threads = p.warps == 1 ? 256 : 32 * p.warps;
+template <typename T, int A, int NV, int K, int MAXT, int MINB = 0>
+cudaError_t backward(NormParams& p, int sms, cudaStream_t s) {
+  const auto kernel = norm_back_kernel<T, A, NV, K, MAXT, MINB>;
+  const int threads = block_threads(p, p.C / Pack<T, A>::N, NV, K);
+  if (threads > MAXT) return cudaErrorInvalidValue;
   const int slots = threads / (p.lanes * p.warps);
-  const size_t smem = sizeof(float) * (slots > 1 ? (size_t)slots * p.C : 2 * 32 * 2 * kRows);
-  const long long blocks = p.groups * p.splits;
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (nv) {
-    case 1: e = launch(norm_back_kernel<T, V, 1>, blocks, threads, smem, p, s); break;
-    case 2: e = launch(norm_back_kernel<T, V, 2>, blocks, threads, smem, p, s); break;
-    case 3:
-    case 4:
-      if constexpr (Pack<T, V>::N <= 4) e = launch(norm_back_kernel<T, V, 4>, blocks, threads, smem, p, s);
-      break;
-    default:
-      if constexpr (!V) e = launch(norm_back_kernel<T, V, 8>, blocks, threads, smem, p, s);
-  }
+  const size_t smem = sizeof(float) * (slots > 1 ? (size_t)slots * p.C : 2 * 32 * 2 * K);
+  static std::atomic<int> held[33];
+  std::atomic<int>& h = held[threads / 32];
+  if (h.load() == 0) h.store(resident_blocks(kernel, threads, 16384));
+  cut(p, (long long)slots * K, h.load(), sms, p.splits);
+  const cudaError_t e = launch(kernel, p.groups * p.splits, threads, smem, p, s);
   if (e != cudaSuccess || p.splits == 1 || (p.dweight == nullptr && p.dbias == nullptr)) return e;
   return launch(norm_sums_kernel, p.groups * 2 * ((p.C + 31) / 32), 256, 0, p, s);
 }
 
+// Which instance: what counts is bytes in flight an SM against the cost of a
+// barrier, which a thread's work has to cover.  61440 x 1536 bf16, forward, by
+// accesses a thread x rows: 1 x 4 77 us, 2 x 4 64, 3 x 2 63, 4 x 2 75, 6 x 1
+// 89; backward 1 x 4 111, 2 x 2 105, 3 x 1 112, 6 x 1 156.  61440 x 1024 fp32
+// (half the arithmetic a byte): forward 1 x 4 81, 3 x 2 82; backward 1 x 4 119,
+// 2 x 2 122.  Wider rows take more accesses a thread, so that 16 warps hold them.
+template <typename T, int A>
+cudaError_t pick(NormParams& p, bool back, int sms, cudaStream_t s) {
+  const int packs = p.C / Pack<T, A>::N;
+  constexpr bool kHalf = sizeof(T) == 2;
+  if constexpr (A == 16) {
+    if (packs <= 32 || (!kHalf && packs <= 256))
+      return back ? backward<T, A, 1, 4, 256>(p, sms, s) : forward<T, A, 1, 4, 256>(p, sms, s);
+    if (back) {
+      if (packs <= 512) return backward<T, A, 2, 2, 256>(p, sms, s);
+      if (packs <= 640) return backward<T, A, 2, 1, 320, 2>(p, sms, s);
+      if constexpr (kHalf)
+        return backward<T, A, 2, 1, 512>(p, sms, s);
+      else
+        return backward<T, A, 4, 1, 512>(p, sms, s);
+    }
+    if (packs <= 512 && !kHalf) return forward<T, A, 2, 2, 256>(p, sms, s);
+    if (kHalf && packs <= 512) {  // the fewest empty places, 3 accesses a thread where as few
+      const int w2 = (packs + 63) / 64 * 64, w3 = (packs + 95) / 96 * 96;
+      return w3 <= w2 ? forward<T, A, 3, 2, 256>(p, sms, s) : forward<T, A, 2, 2, 256>(p, sms, s);
+    }
+    return forward<T, A, 4, 1, 512>(p, sms, s);
+  } else {
+    if (packs <= 32) return back ? backward<T, A, 1, 4, 256>(p, sms, s) : forward<T, A, 1, 4, 256>(p, sms, s);
+    if (packs <= 1024) return back ? backward<T, A, 4, 4, 256>(p, sms, s) : forward<T, A, 4, 4, 256>(p, sms, s);
+    if (packs <= 4096) return back ? backward<T, A, 8, 1, 512>(p, sms, s) : forward<T, A, 8, 2, 512>(p, sms, s);
+    if constexpr (Pack<T, A>::N == 1)
+      return back ? backward<T, A, 16, 1, 512>(p, sms, s) : forward<T, A, 16, 1, 512>(p, sms, s);
+    return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_layer_norm(NormParams& p, bool fp32, bool vec, bool back, cudaStream_t s) {
-  if (fp32) {
-    if (back) return vec ? backward<float, true>(p, s) : backward<float, false>(p, s);
-    return vec ? forward<float, true>(p, s) : forward<float, false>(p, s);
-  }
-  if (back) return vec ? backward<uint16_t, true>(p, s) : backward<uint16_t, false>(p, s);
-  return vec ? forward<uint16_t, true>(p, s) : forward<uint16_t, false>(p, s);
+cudaError_t launch_layer_norm(NormParams& p, bool fp32, int access, bool back, int sms, cudaStream_t s) {
+  if (fp32) return access == 16 ? pick<float, 16>(p, back, sms, s) : pick<float, 4>(p, back, sms, s);
+  if (access == 16) return pick<uint16_t, 16>(p, back, sms, s);
+  return access == 4 ? pick<uint16_t, 4>(p, back, sms, s) : pick<uint16_t, 2>(p, back, sms, s);
 }
 
 }  // namespace sab

@@ -1184,20 +1184,18 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   return decay_runs(runs, 3, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
 }
 
-// Row ranges of a group whose sums a layer norm's gradients keep apart: about
-// four blocks for every SM over all groups, none of fewer than 16 rows.
+// The most row ranges of a group whose sums a layer norm's gradients may keep
+// apart (the launcher takes one wave of blocks or fewer): about ten blocks for
+// every SM over all groups, none of fewer than 8 rows.
 struct NormCut {
-  long long groups, split_rows;
+  long long groups;
   int splits;
 };
 static NormCut norm_cut(long long rows, long long group_rows) {
   NormCut n;
   if (group_rows > rows) group_rows = rows;
   n.groups = (rows + group_rows - 1) / group_rows;
-  long long splits = 4LL * device_sms() / n.groups;
-  splits = std::max(1LL, std::min(splits, group_rows / 16));
-  n.split_rows = (group_rows + splits - 1) / splits;
-  n.splits = (int)((group_rows + n.split_rows - 1) / n.split_rows);
+  n.splits = (int)std::max(1LL, std::min(10LL * device_sms() / n.groups, group_rows / 8));
   return n;
 }
 static bool norm_shape_ok(long long rows, int channels, long long group_rows) {
@@ -1210,32 +1208,32 @@ static bool norm_stride_ok(long long stride, long long rows, int channels, bool 
 
 // What the two directions share; `io` are the tensors of the rows' type.
 static sab_status norm_common(const sab_norm_desc* d, const void* const* io, const long long* strides, int n,
-                              const void* const* f32, int nf, NormParams& p, bool& vec) {
+                              const void* const* f32, int nf, NormParams& p, int& access) {
   if (d == nullptr || !norm_shape_ok(d->rows, d->channels, d->group_rows)) return SAB_ERR_INVALID_ARG;
   if (d->dtype != SAB_DTYPE_BF16 && d->dtype != SAB_DTYPE_FP32) return SAB_ERR_INVALID_ARG;
   if (!(d->eps > 0.f) || !isfinite(d->eps) || !isfinite(d->weight_offset)) return SAB_ERR_INVALID_ARG;
   const uintptr_t es = d->dtype == SAB_DTYPE_BF16 ? 2 : 4;
-  vec = (d->channels * es) % 16 == 0;
+  uintptr_t low = d->channels * es;  // its lowest bits, or-ed together: what all divide
   for (int i = 0; i < n; ++i) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(io[i]);
     if (a == 0 || a % es != 0 || !norm_stride_ok(strides[i], d->rows, d->channels, i == n - 1))
       return SAB_ERR_INVALID_ARG;
-    vec = vec && a % 16 == 0 && (strides[i] * es) % 16 == 0;
+    low |= a | (uintptr_t)strides[i] * es;
   }
   for (int i = 0; i + 1 < n; ++i)  // in place: the same rows
     if (io[i] == io[n - 1] && strides[i] != strides[n - 1] && d->rows > 1) return SAB_ERR_INVALID_ARG;
   for (int i = 0; i < nf; ++i) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(f32[i]);
     if (a % 4 != 0) return SAB_ERR_INVALID_ARG;
-    vec = vec && a % 16 == 0;
+    low |= a;
   }
+  access = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 2;
   memset(&p, 0, sizeof(p));
   const NormCut cut = norm_cut(d->rows, d->group_rows);
   p.rows = d->rows;
   p.group_rows = std::min(d->group_rows, d->rows);
   p.groups = cut.groups;
   p.splits = cut.splits;
-  p.split_rows = cut.split_rows;
   p.C = d->channels;
   p.inv_c = 1.f / (float)d->channels;
   p.eps = d->eps;
@@ -1249,8 +1247,8 @@ sab_status sab_layer_norm(const sab_norm_desc* desc, const void* X, long long x_
   const long long strides[] = {x_stride, y_stride};
   const void* f32[] = {weight, bias};
   NormParams p;
-  bool vec = false;
-  const sab_status st = norm_common(desc, io, strides, 2, f32, 2, p, vec);
+  int access = 0;
+  const sab_status st = norm_common(desc, io, strides, 2, f32, 2, p, access);
   if (st != SAB_OK) return st;
   if (!aligned4(mean) || !aligned4(rstd)) return SAB_ERR_INVALID_ARG;
   p.x = X;
@@ -1261,8 +1259,8 @@ sab_status sab_layer_norm(const sab_norm_desc* desc, const void* X, long long x_
   p.bias = bias;
   p.mean = mean;
   p.rstd = rstd;
-  const cudaError_t e =
-      launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, vec, false, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, access, false, device_sms(),
+                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 
@@ -1280,8 +1278,8 @@ sab_status sab_layer_norm_backward(const sab_norm_desc* desc, const void* X, lon
   const long long strides[] = {x_stride, dy_stride, dx_stride};
   const void* f32[] = {weight, dweight, dbias};
   NormParams p;
-  bool vec = false;
-  const sab_status st = norm_common(desc, io, strides, 3, f32, 3, p, vec);
+  int access = 0;
+  const sab_status st = norm_common(desc, io, strides, 3, f32, 3, p, access);
   if (st != SAB_OK) return st;
   if (mean == nullptr || rstd == nullptr || !aligned4(mean) || !aligned4(rstd)) return SAB_ERR_INVALID_ARG;
   if (dweight != nullptr && dweight == dbias) return SAB_ERR_INVALID_ARG;
@@ -1301,8 +1299,8 @@ sab_status sab_layer_norm_backward(const sab_norm_desc* desc, const void* X, lon
   p.dweight = dweight;
   p.dbias = dbias;
   p.part = static_cast<float*>(workspace);
-  const cudaError_t e =
-      launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, vec, true, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_layer_norm(p, desc->dtype == SAB_DTYPE_FP32, access, true, device_sms(),
+                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SAB_OK : SAB_ERR_CUDA;
 }
 

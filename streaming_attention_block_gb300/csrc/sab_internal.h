@@ -314,8 +314,8 @@ cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
-// vec: channels, strides and pointers allow 16-byte accesses
-cudaError_t launch_layer_norm(NormParams& p, bool fp32, bool vec, bool back, cudaStream_t s);
+// access: bytes of an access (16, 4, 2) that channels, strides and pointers allow
+cudaError_t launch_layer_norm(NormParams& p, bool fp32, int access, bool back, int sms, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
 // One query tile per CTA, key-half softmax warpgroups; unsplit KV only.
 cudaError_t launch_chunk_attention_kh(const AttnParams& p, cudaStream_t s);
