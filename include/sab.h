@@ -607,6 +607,57 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
                                         void* stream);
 
 /*
+ * Cross attention: queries of one sequence over the keys and values of another
+ * of its own length, the states of an encoder (a prompt, a reference image),
+ * which every block of a video diffusion transformer attends to besides its
+ * own sequence.  The states are computed once per prompt and serve every chunk
+ * and denoising step.  For query i of head h and keys j < kv_len[b] of head
+ * h / (heads / kv_heads):
+ *   s_ij = softmax_scale * <q_i, k_j>,  O_i = sum_j softmax_j(s_ij) v_j,
+ *   LSE_i = ln sum_j exp(s_ij).
+ * Q, O      [batch, q_tokens, heads, head_dim] bf16 rows.
+ * K, V      [kv_batch, kv_tokens, kv_heads, head_dim] bf16 rows.  kv_batch is
+ *           batch, or 1: all sequences attend to the same states.
+ * q_len     device int32 [batch] or NULL (all q_tokens), kv_len: device int32
+ *           [kv_batch] or NULL (all kv_tokens); clamped on the device.  Tokens
+ *           past them are padding: never used, whatever they hold.  Padded
+ *           queries, and all queries of a sequence without keys, get O = 0 and
+ *           LSE = -inf.
+ * LSE       device fp32 [batch, heads, q_tokens] or NULL.
+ * O overlaps no input.  heads is a multiple of kv_heads, at most 128 times it;
+ * head_dim 64 or 128; softmax_scale > 0.  One token per sequence (q_tokens 1)
+ * is the form for decoding; there is no workspace: where a call has fewer query
+ * tiles than the GPU has SMs, the keys of a tile are cut among the blocks of a
+ * thread-block cluster, which join their parts through shared memory.
+ * Scores and sums are fp32; P is rounded to bf16 for its product.
+ * Errors: INVALID_ARG, CUDA.
+ */
+typedef struct {
+  int batch;      /* sequences of queries                        */
+  int q_tokens;
+  int kv_batch;   /* sequences of keys: batch, or 1 for all      */
+  int kv_tokens;
+  int heads;
+  int kv_heads;
+  int head_dim;   /* 64 or 128                                   */
+} sab_cross_desc;
+
+/*
+ * Token rows of one tensor: token (b, t) holds heads * head_dim contiguous
+ * elements at data + b * batch + t * token (strides in elements, multiples of
+ * 8, at least a token's extent), so that a slice of a fused projection needs no
+ * copy.  data is 16-byte aligned.  Strides of axes of one entry are not read.
+ */
+typedef struct {
+  void* data;
+  long long batch, token;
+} sab_token_rows;
+
+sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
+                               const sab_token_rows* V, const int* q_len, const int* kv_len, float softmax_scale,
+                               const sab_token_rows* O, float* LSE, void* stream);
+
+/*
  * Layer norm over the channels of each row, and its gradients.  The method
  * normalises queries and keys only (sab_qk_norm_rope); a video transformer's
  * block also has a layer norm with weights before its cross attention, and

@@ -98,6 +98,7 @@ def library() -> ctypes.CDLL:
         "sab_decay_attention_step": (I, [P, P, P, P, P, P, I, I, I, F, P, P, P]),
         "sab_decay_attention_backward_workspace": (SZ, [I, I, I, I]),
         "sab_decay_attention_backward": (I, [P] * 8 + [I, I, I, I, F] + [P] * 5 + [SZ, P]),
+        "sab_cross_attention": (I, [P] * 6 + [F, P, P, P]),
         "sab_layer_norm": (I, [P, P, LL, P, P, P, LL, P, P, P]),
         "sab_layer_norm_backward_workspace": (SZ, [LL, I, LL]),
         "sab_layer_norm_backward": (I, [P, P, LL, P, LL, P, P, P, P, LL, P, P, P, SZ, P]),
@@ -716,6 +717,63 @@ class DecayState:
         decay_attention_step(Q, K, V, self.log_decay, Q.shape[-1] ** -0.5 if scale is None else scale, self.state,
                              self.state, O, active, stream)
         return O
+
+
+# --------------------------------------------------------- cross attention
+
+class CrossDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "q_tokens", "kv_batch", "kv_tokens", "heads", "kv_heads",
+                                            "head_dim")]
+
+
+class TokenRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+
+
+_CROSS = struct.Struct("@7i")       # the layouts of CrossDesc and TokenRows, packed faster than the structures
+_TOKENS = struct.Struct("@Pqq")     # are built
+
+
+def _token_rows(t, shape, name, dev):
+    """Token rows of a bf16 [B, L, H, D] tensor with contiguous heads."""
+    try:
+        if t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != shape:
+            _refuse(t, name, dev, (torch.bfloat16,), shape)
+    except AttributeError:
+        _refuse(t, name, dev, (torch.bfloat16,), shape)
+    b, l, h, d = t.stride()
+    if (d != 1 and shape[3] > 1) or (h != shape[3] and shape[2] > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return _TOKENS.pack(t.data_ptr(), b, l)
+
+
+def _cross_shapes(Q, K):
+    """(query shape, key shape, description) of a call."""
+    for t, name in ((Q, "Q"), (K, "K")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise TypeError(f"{name}: expected a [B, L, H, D] torch tensor")
+    x, y = Q.shape, K.shape
+    if max(*x, *y) > 0x7FFFFFFF:  # would be cut to 32 bits on the way to the library
+        raise SabError(1, "cross_attention")
+    if y[3] != x[3]:
+        raise ValueError(f"K: expected a head dimension of {x[3]}, got {y[3]}")
+    return x, y, _CROSS.pack(x[0], x[1], y[0], y[1], x[2], y[2], x[3])
+
+
+def cross_attention(Q, K, V, softmax_scale: float, O, LSE=None, q_len=None, kv_len=None, stream=None):
+    """sab_cross_attention: queries ``Q`` [B, Lq, H, D] over an encoder's ``K``,
+    ``V`` [B or 1, Lk, Hk, D] (bf16, batch and token strides free), of which the
+    first ``q_len`` and ``kv_len`` tokens (int32 per sequence) are real (see
+    include/sab.h)."""
+    dev = _device()
+    x, y, desc = _cross_shapes(Q, K)
+    i32, f4 = torch.int32, torch.float32
+    status = library().sab_cross_attention(
+        desc, _token_rows(Q, x, "Q", dev), _token_rows(K, y, "K", dev), _token_rows(V, y, "V", dev),
+        _arg(q_len, x[:1], i32, "q_len", dev), _arg(kv_len, y[:1], i32, "kv_len", dev), float(softmax_scale),
+        _token_rows(O, x, "O", dev), _arg(LSE, (x[0], x[2], x[1]), f4, "LSE", dev), _stream(stream, dev))
+    if status != 0:
+        raise SabError(status, "cross_attention")
 
 
 # ------------------------------------------------------------- layer norm

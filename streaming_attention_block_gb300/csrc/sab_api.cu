@@ -1184,6 +1184,122 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
   return decay_runs(runs, 3, how, log_decay, seq_len, B, L, H, D, workspace, ws_bytes, stream);
 }
 
+// ------------------------------------------------------------ cross attention
+
+static bool cross_shape_ok(const sab_cross_desc* d) {
+  if (d == nullptr || d->batch < 1 || d->q_tokens < 1 || d->kv_tokens < 1 || d->heads < 1 || d->kv_heads < 1)
+    return false;
+  if (d->head_dim != 64 && d->head_dim != 128) return false;
+  if (d->heads % d->kv_heads != 0 || d->heads / d->kv_heads > kTileM) return false;
+  if (d->kv_batch != 1 && d->kv_batch != d->batch) return false;
+  if (d->q_tokens > (1 << 30) || d->kv_tokens > (1 << 30) || d->heads > (1 << 20)) return false;
+  return (long long)d->batch * d->heads * ((d->q_tokens + 31) / 32) <= (1LL << 30) &&
+         (long long)d->kv_batch * d->kv_heads * ((d->kv_tokens + 31) / 32) <= (1LL << 30);
+}
+// Rows of one [B, L, heads, D] tensor: pointer and strides that a tensor map
+// takes; tokens of a written tensor apart from one another.
+static bool token_rows_ok(const sab_token_rows* r, int B, int L, long long row, bool out) {
+  if (r == nullptr || r->data == nullptr || !aligned16(r->data)) return false;
+  constexpr long long kMost = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
+  if (L > 1 && (r->token < row || r->token > kMost || r->token % 8 != 0)) return false;
+  if (B > 1 && (r->batch < row || r->batch > kMost || r->batch % 8 != 0)) return false;
+  if (!out || B == 1 || L == 1) return true;
+  return r->batch >= (L - 1) * r->token + row || r->token >= (B - 1) * r->batch + row;
+}
+// strides of axes of one entry say nothing
+static long long batch_of(const sab_token_rows* r, int B, long long row) { return B > 1 ? r->batch : row; }
+static long long token_of(const sab_token_rows* r, int L, long long row) { return L > 1 ? r->token : row; }
+
+// Query rows: a map of tiles of `pack` heads x `tokens` tokens.
+static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D, int pack,
+                              int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const long long row = (long long)H * D;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)token_of(r, L, row) * 2,
+                                 (cuuint64_t)batch_of(r, B, row) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)pack, (cuuint32_t)tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D) {
+  const long long row = (long long)H * D;
+  return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
+                    (size_t)batch_of(r, B, row) * 2);
+}
+
+// Heads of one tile of `rows` query rows: the number, among those that divide
+// the heads of a key head, with the fewest tiles; of equals the largest, whose
+// tiles share their keys.
+static int cross_pack(int q_tokens, int group, int rows) {
+  int best = 1;
+  long long least = 0;
+  for (int k = 1; k <= group && k <= rows; ++k) {
+    if (group % k != 0) continue;
+    const int tokens = rows / k;
+    const long long tiles = (long long)((q_tokens + tokens - 1) / tokens) * (group / k);
+    if (k == 1 || tiles <= least) best = k, least = tiles;
+  }
+  return best;
+}
+
+// Blocks among which the keys of a query tile are cut: as many (a power of two,
+// at most 8) as the SMs that the query tiles leave idle, each with a key tile.
+static int cross_splits(unsigned items, int key_tiles) {
+  int n = 1;
+  while (n < 8 && 2LL * n * items <= device_sms() && 2 * n <= key_tiles) n *= 2;
+  return n;
+}
+
+sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
+                               const sab_token_rows* V, const int* q_len, const int* kv_len, float softmax_scale,
+                               const sab_token_rows* O, float* LSE, void* stream) {
+  if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
+  const sab_cross_desc& d = *desc;
+  const long long qrow = (long long)d.heads * d.head_dim, krow = (long long)d.kv_heads * d.head_dim;
+  if (!token_rows_ok(Q, d.batch, d.q_tokens, qrow, false) || !token_rows_ok(K, d.kv_batch, d.kv_tokens, krow, false) ||
+      !token_rows_ok(V, d.kv_batch, d.kv_tokens, krow, false) || !token_rows_ok(O, d.batch, d.q_tokens, qrow, true))
+    return SAB_ERR_INVALID_ARG;
+  if (O->data == Q->data || O->data == K->data || O->data == V->data || !aligned4(q_len) || !aligned4(kv_len) ||
+      !aligned16(LSE))
+    return SAB_ERR_INVALID_ARG;
+  CrossParams p;
+  memset(&p, 0, sizeof(p));
+  p.q_len = q_len;
+  p.kv_len = kv_len;
+  p.O = static_cast<uint16_t*>(O->data);
+  p.o_batch = batch_of(O, d.batch, qrow);
+  p.o_token = token_of(O, d.q_tokens, qrow);
+  p.LSE = LSE;
+  p.B = d.batch;
+  p.Bk = d.kv_batch;
+  p.Lq = d.q_tokens;
+  p.Lk = d.kv_tokens;
+  p.H = d.heads;
+  p.D = d.head_dim;
+  p.group = d.heads / d.kv_heads;
+  p.pack = cross_pack(d.q_tokens, p.group, kTileM);
+  p.tile_tokens = kTileM / p.pack;
+  p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
+  p.head_blocks = d.heads / p.pack;
+  p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
+  p.splits = cross_splits(p.items, (d.kv_tokens + kTileN - 1) / kTileN);
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.err_word = device_error_word();
+  if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.o_map, O, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim))
+    return SAB_ERR_CUDA;
+  return launch_cross_forward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
+                                                                                              : SAB_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ layer norm
+
 // The most row ranges of a group whose sums a layer norm's gradients may keep
 // apart (the launcher takes one wave of blocks or fewer): about ten blocks for
 // every SM over all groups, none of fewer than 8 rows.

@@ -300,6 +300,25 @@ struct NormParams {
   float inv_c, eps, offset;
 };
 
+// Cross attention forward (see sab_cross_attention).
+struct CrossParams {
+  CUtensorMap q_map, o_map;  // dims (D, H, Lq, B), box (64, pack, tile_tokens, 1), SW128
+  CUtensorMap k_map, v_map;  // dims (D, Lk, Hk, Bk), box (64, 128, 1, 1), SW128
+  const int* q_len;          // [B] or null
+  const int* kv_len;         // [Bk] or null
+  uint16_t* O;
+  long long o_batch, o_token;
+  float* LSE;                // [B, H, Lq] or null
+  int B, Bk, Lq, Lk, H, D;
+  int group;                 // heads that share a key head
+  int pack, tile_tokens;     // heads and tokens of a tile of 128 rows
+  int n_qtiles, head_blocks; // tiles along the tokens, and along the heads
+  unsigned items;            // query tiles
+  int splits;                // blocks of a cluster among which a tile's keys are cut
+  float scale_log2;
+  unsigned int* err_word;
+};
+
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_append_bf16(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_append_fp8(const AppendParams& p, cudaStream_t s);
@@ -314,6 +333,7 @@ cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
+cudaError_t launch_cross_forward(const CrossParams& p, int sms, cudaStream_t s);
 // access: bytes of an access (16, 4, 2) that channels, strides and pointers allow
 cudaError_t launch_layer_norm(NormParams& p, bool fp32, int access, bool back, int sms, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(unsigned long long timeout_ns, cudaStream_t s);
