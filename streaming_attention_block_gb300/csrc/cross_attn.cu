@@ -32,11 +32,14 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // P = 2^(s - m) in bf16 has fp32's exponents and is summed in fp32, so the
-// reference m need not be the row's maximum: any m within 2^40 of it gives the
-// same digits.  Rows start with m = 0 and move it only when a score leaves this
-// range, which scores of normalised or random queries never do: no tile then
-// waits for its maximum, and O is never rescaled.
-constexpr float kRange = 40.0f;
+// reference m need not be the row's maximum: any m that keeps the sum l within
+// 2^80 of 1 gives the same digits (nothing overflows, and what ftz drops is
+// below 2^-46 of the sum).  Rows take m = 0, without looking for a maximum, which
+// scores below 55 in size never need; a tile with a row whose l leaves the range,
+// or whose O is not finite, is done again with its running maxima.
+constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p80f;
+constexpr float kRescale = 8.0f;  // running maxima: O is rescaled when one grows by more than 2^8
+constexpr int kRedoList = 64;     // query tiles a block remembers
 
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
@@ -84,26 +87,37 @@ struct Ring {
   }
 };
 
+// The number of a query tile, counted one by one, from its item and stream.
+__device__ __forceinline__ uint32_t tile_of(const CrossParams& p, unsigned item, int st, int pair) {
+  const unsigned n = (unsigned)(p.n_qtiles + pair - 1) / (unsigned)pair;
+  const unsigned r = item / n;
+  return r * (unsigned)p.n_qtiles + (item - r * n) * (unsigned)pair + (unsigned)st;
+}
+
 // ------------------------------------------------------------------ forward
 
-// One tile of queries: `pack` heads from head hb * pack on, tile_tokens tokens
-// from t0 on, and the key tiles [first, first + nt) of its sequence.
-struct Work {
-  int b, hb, t0;
-  int live;         // tokens of the tile inside q_len
-  int first, nt;
-  int keys;         // keys of the range
-};
 __device__ __forceinline__ int length_of(const int* lens, int b, int most) {
   return lens == nullptr ? most : min(max(__ldg(lens + b), 0), most);
 }
-__device__ __forceinline__ Work work_at(const CrossParams& p, unsigned item, int split) {
+
+// One or two query tiles (`streams`) of `pack` heads from head hb * pack on,
+// tile_tokens tokens each from t0 on, and the key tiles [first, first + nt).
+struct Work {
+  int b, hb, t0;
+  int live;         // tokens from t0 on that are inside q_len
+  int streams;
+  int first, nt;
+  int keys;         // keys of the range
+};
+__device__ __forceinline__ Work work_at(const CrossParams& p, unsigned item, int split, int pair) {
   Work w;
-  const unsigned r = item / (unsigned)p.n_qtiles;
-  w.t0 = (int)(item - r * (unsigned)p.n_qtiles) * p.tile_tokens;
+  const unsigned n = (unsigned)(p.n_qtiles + pair - 1) / (unsigned)pair;
+  const unsigned r = item / n;
+  w.t0 = (int)(item - r * n) * pair * p.tile_tokens;
   w.b = (int)(r / (unsigned)p.head_blocks);
   w.hb = (int)(r - (unsigned)w.b * (unsigned)p.head_blocks);
-  w.live = min(p.tile_tokens, length_of(p.q_len, w.b, p.Lq) - w.t0);
+  w.live = length_of(p.q_len, w.b, p.Lq) - w.t0;
+  w.streams = pair == 2 && w.live > p.tile_tokens ? 2 : 1;
   const int kl = w.live > 0 ? length_of(p.kv_len, p.Bk == 1 ? 0 : w.b, p.Lk) : 0;
   const int total = (kl + kTileN - 1) / kTileN;
   w.first = (int)((long long)total * split / p.splits);
@@ -118,21 +132,30 @@ __device__ __forceinline__ Work work_at(const CrossParams& p, unsigned item, int
   }
   return w;
 }
-// The blocks' tiles in order, tile by tile of keys.
+
+// What a block works through.  Pass 0: every step-th item.  Pass 1: the query
+// tiles of the list, one by one.  Pass 2: the items of pass 0 from the one on at
+// which the list was full.
+struct Pass {
+  unsigned first, step, end;  // items, or places of the list
+  const uint32_t* list;       // or null
+  int pair, split;
+};
+// Steps of a pass in order: each key tile of an item, for each of its streams.
 struct Cursor {
-  unsigned item;
+  unsigned at, item;
   Work w;
-  int j;
+  int j, st;
   bool more;
-  // first item of this block that has keys
-  __device__ __forceinline__ void start(const CrossParams& p, unsigned first, unsigned step, int split) {
-    item = first;
-    seek(p, step, split);
+  __device__ __forceinline__ void start(const CrossParams& p, const Pass& a) {
+    at = a.first;
+    seek(p, a);
   }
-  __device__ __forceinline__ void seek(const CrossParams& p, unsigned step, int split) {
-    j = 0;
-    for (; item < p.items; item += step) {
-      w = work_at(p, item, split);
+  __device__ __forceinline__ void seek(const CrossParams& p, const Pass& a) {
+    j = st = 0;
+    for (; at < a.end; at += a.step) {
+      item = a.list != nullptr ? a.list[at] : at;
+      w = work_at(p, item, a.split, a.pair);
       if (w.nt > 0) {
         more = true;
         return;
@@ -140,58 +163,78 @@ struct Cursor {
     }
     more = false;
   }
-  __device__ __forceinline__ void next(const CrossParams& p, unsigned step, int split) {
-    if (++j < w.nt) return;
-    item += step;
-    seek(p, step, split);
+  __device__ __forceinline__ void skip(const CrossParams& p, const Pass& a) {
+    at += a.step;
+    seek(p, a);
+  }
+  __device__ __forceinline__ bool last() const { return j + 1 == w.nt; }
+  // the next step; true where it has another key tile
+  __device__ __forceinline__ bool next(const CrossParams& p, const Pass& a) {
+    if (++st < w.streams) return false;
+    st = 0;
+    if (++j == w.nt) skip(p, a);
+    return true;
   }
 };
 
-template <int D_>
+template <int D_, bool PAIR>
 struct FwdCfg {
   static constexpr int D = D_;
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = 128u * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
-  static constexpr int kSlots = D == 128 ? 5 : 10;          // K and V tiles in the order of their use
-  static constexpr uint32_t kQOff = 0;                      // two tiles: Q, then its O on the way out
-  static constexpr uint32_t kRingOff = 2 * kTileBytes;
+  static constexpr int kStreams = PAIR ? 2 : 1;
+  static constexpr int kSlots = D == 128 ? (PAIR ? 4 : 5) : 10;  // K and V tiles in turn
+  static constexpr uint32_t kOOff = 0;                           // O on its way out
+  static constexpr uint32_t kQOff = kTileBytes;                  // a query tile of each stream
+  static constexpr uint32_t kRingOff = (1 + kStreams) * kTileBytes;
   static constexpr uint32_t kBarOff = kRingOff + kSlots * kTileBytes;
-  static constexpr int kQFull = 0;                          // [2]
-  static constexpr int kQFree = 2;                          // [2] O has left the tile
+  static constexpr int kQFull = 0;                          // [2 streams]
+  static constexpr int kQFree = 2;                          // [2] the tile's last scores are done
   static constexpr int kFull = 4;                           // [kSlots]
   static constexpr int kEmpty = kFull + kSlots;             // [kSlots]
   static constexpr int kSFull = kEmpty + kSlots;            // [2 buffers]
   static constexpr int kPFull = kSFull + 2;                 // [2 buffers][2 halves]
   static constexpr int kPVDone = kPFull + 4;
-  static constexpr int kODone = kPVDone + 1;                // a query tile's last product
-  static constexpr int kOReady = kODone + 1;                // O staged for its store
-  static constexpr int kDrain = kOReady + 1;
+  static constexpr int kODone = kPVDone + 1;                // [2 streams] a query tile's last product
+  static constexpr int kOReady = kODone + 2;                // O staged for its store
+  static constexpr int kOFree = kOReady + 1;                // and read by it
+  static constexpr int kMeet = kOFree + 1;                  // the softmax warps, at a query tile's end
+  static constexpr int kPairMeet = kMeet + 1;               // [4 quadrants] two warps, running maxima
+  static constexpr int kDrain = kPairMeet + 4;
   static constexpr int kNumBars = kDrain + 1;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kSmemBytes = kMiscOff + 16 + 1024;
-  // producer, products, 8 softmax warps, the store of O
-  static constexpr int kThreads = 32 * 11;
+  static constexpr uint32_t kListOff = kMiscOff + 32;
+  static constexpr uint32_t kMaxOff = (kListOff + kRedoList * 4 + 15u) & ~15u;  // [2 halves][128] row maxima
+  static constexpr uint32_t kSmemBytes = kMaxOff + 1024 + 1024;
+  // K and V, products, 8 softmax warps, the store of O, Q
+  static constexpr int kThreads = 32 * 12;
   static constexpr uint32_t kTmemO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// One block per SM walks its query tiles (SPLIT: one tile, its keys cut among
-// the blocks of a cluster, see the end).  Scores of a key tile are in one of
-// two TMEM buffers; the keys [0, 64) and [64, 128) of every tile are two halves
-// with four softmax warps, a reference m, a sum l and an accumulator O each, so
-// that they meet only when a query tile is done.  The products are issued in
-// the order PV(g), S(g + 2) over all tiles of the block, also from one query
-// tile to the next.
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const __grid_constant__ CrossParams p) {
-  using C = FwdCfg<D>;
+// One block per SM walks its items: one query tile, or two that share their
+// key tiles (PAIR), which halves the traffic of K and V from L2.  SPLIT: one
+// item a block, its keys cut among the blocks of a cluster (see the end).
+// Scores of a step (a key tile and a stream) are in one of two TMEM buffers; the
+// keys [0, 64) and [64, 128) of a tile are two halves with four softmax warps
+// and a sum l each, and one accumulator O per stream.  Products are issued in the
+// order PV(g), S(g + 2) over all steps of the block, also from one query tile to
+// the next; a query tile's end (its O leaves) is put off until P of the next
+// one's first keys is there, so that its last products run meanwhile.
+template <int D, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(FwdCfg<D, PAIR>::kThreads, 1)
+cross_fwd_kernel(const __grid_constant__ CrossParams p) {
+  using C = FwdCfg<D, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u32 - raw_u32);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(base + C::kMiscOff);  // [0] tmem, [1] abort
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  // [0] tmem, [1] abort, [2] tiles to be done again, [3] item at which the list
+  // was full, [4] the end of a query tile that was last put on it
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kMiscOff + 4);
+  uint32_t* list = reinterpret_cast<uint32_t*>(base + C::kListOff);
   auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
   auto wait = [&](int i, uint32_t parity, unsigned site) -> bool {
     return wait_bounded(bar(i), parity, abort_flag, site, p.err_word);
@@ -201,8 +244,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
   };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = SPLIT ? (int)(blockIdx.x % (unsigned)p.splits) : 0;
-  const unsigned first_item = SPLIT ? blockIdx.x / (unsigned)p.splits : blockIdx.x;
-  const unsigned step = SPLIT ? p.items : gridDim.x;  // SPLIT: one item a block
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -211,21 +252,25 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
       mbar_init(bar(C::kSFull + i), 1);
       mbar_init(bar(C::kPFull + 2 * i), 128);
       mbar_init(bar(C::kPFull + 2 * i + 1), 128);
+      mbar_init(bar(C::kODone + i), 1);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(bar(C::kFull + s), 1);
       mbar_init(bar(C::kEmpty + s), 1);
     }
     mbar_init(bar(C::kPVDone), 1);
-    mbar_init(bar(C::kODone), 1);
     mbar_init(bar(C::kOReady), 256);
+    mbar_init(bar(C::kOFree), 1);
+    mbar_init(bar(C::kMeet), 256);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(C::kPairMeet + i), 64);
     mbar_init(bar(C::kDrain), 1);
-    misc[1] = 0;
+    misc[1] = misc[2] = misc[4] = 0;
+    misc[3] = 0xffffffffu;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(misc), 512);
+    tmem_alloc(base_u32 + C::kMiscOff, 512);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -241,55 +286,74 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
   griddep_launch_dependents();
   griddep_wait();
 
+  Pass pass;
+  pass.first = SPLIT ? blockIdx.x / (unsigned)p.splits : blockIdx.x;
+  pass.step = SPLIT ? p.items : gridDim.x;
+  pass.end = p.items;
+  pass.list = nullptr;
+  pass.pair = PAIR ? 2 : 1;
+  pass.split = split;
+  // To the next pass, after all roles are through with this one; false: done.
+  auto next_pass = [&](int& number) -> bool {
+    if (SPLIT) return false;  // running maxima from the start
+    __syncwarp();
+    named_bar_sync(2, C::kThreads);
+    if (*abort_flag) return false;
+    const uint32_t n = min(misc[2], (uint32_t)kRedoList), over = misc[3];
+    if (number == 0 && n > 0) {
+      number = 1;
+      pass.first = 0;
+      pass.step = 1;
+      pass.end = n;
+      pass.list = list;
+      pass.pair = 1;
+      return true;
+    }
+    if (number < 2 && over != 0xffffffffu) {
+      number = 2;
+      pass.first = over;
+      pass.step = gridDim.x;
+      pass.end = p.items;
+      pass.list = nullptr;
+      pass.pair = PAIR ? 2 : 1;
+      return true;
+    }
+    return false;
+  };
+  int number = 0;
+
   if (warp == 0) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint32_t q_bytes = (uint32_t)(C::kBoxes * p.pack * p.tile_tokens) * 128u;
-      Ring<C::kSlots> r;
-      int loads = 0, tiles = 0;  // K and V tiles, query tiles requested
-      bool ok = true;
-      // one K or V tile into the next slot
-      auto load = [&](const CUtensorMap* m, int row, int head, int b) -> bool {
-        if (loads >= C::kSlots && !wait(C::kEmpty + r.slot, r.parity ^ 1u, 0)) return false;
-        const uint32_t full = bar(C::kFull + r.slot);
-        mbar_arrive_expect_tx(full, C::kTileBytes);
-#pragma unroll
-        for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_4d(base_u32 + C::kRingOff + r.slot * C::kTileBytes + bx * C::kBoxBytes, m, full, bx * 64, row, head,
-                      b);
-        r.next();
-        ++loads;
-        return true;
-      };
-      Cursor c;
-      c.start(p, first_item, step, split);
-      int v_row = -1, v_head = 0, v_b = 0;  // the V tile that is still to be requested
-      while (c.more) {
-        const int head = c.w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : c.w.b;
-        const int row = (c.w.first + c.j) * kTileN;
-        if (c.j == 0) {
-          const int qb = tiles & 1;
-          if (tiles >= 2 && !(ok = wait(C::kQFree + qb, (uint32_t)(tiles / 2 - 1) & 1u, 1))) break;
-          mbar_arrive_expect_tx(bar(C::kQFull + qb), q_bytes);
+    // -------------------------------------------------------------- K and V
+    Ring<C::kSlots> r;
+    int loads = 0;
+    do {
+      if (lane == 0) {
+        // one tile into the next slot
+        auto load = [&](const CUtensorMap* m, int row, int head, int b) -> bool {
+          if (loads >= C::kSlots && !wait(C::kEmpty + r.slot, r.parity ^ 1u, 0)) return false;
+          const uint32_t full = bar(C::kFull + r.slot);
+          mbar_arrive_expect_tx(full, C::kTileBytes);
 #pragma unroll
           for (int bx = 0; bx < C::kBoxes; ++bx)
-            tma_load_4d(base_u32 + C::kQOff + qb * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + qb),
-                        bx * 64, c.w.hb * p.pack, c.w.t0, c.w.b);
-          ++tiles;
+            tma_load_4d(base_u32 + C::kRingOff + r.slot * C::kTileBytes + bx * C::kBoxBytes, m, full, bx * 64, row,
+                        head, b);
+          r.next();
+          ++loads;
+          return true;
+        };
+        Cursor c;
+        for (c.start(p, pass); c.more;) {
+          const int head = c.w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : c.w.b;
+          const int row = (c.w.first + c.j) * kTileN;
+          if (!load(&p.k_map, row, head, kb) || !load(&p.v_map, row, head, kb)) break;
+          while (!c.next(p, pass)) {
+          }
         }
-        if (!(ok = load(&p.k_map, row, head, kb))) break;
-        if (v_row >= 0 && !(ok = load(&p.v_map, v_row, v_head, v_b))) break;
-        v_row = row, v_head = head, v_b = kb;
-        c.next(p, step, split);
       }
-      if (ok && v_row >= 0) load(&p.v_map, v_row, v_head, v_b);
-      if (*abort_flag) {  // nothing of this block's copies may land after it
-        for (int k = max(0, tiles - 2); k < tiles; ++k)
-          wait_drain(bar(C::kQFull + (k & 1)), (uint32_t)(k / 2) & 1u, p.err_word);
-        for (int k = max(0, loads - C::kSlots); k < loads; ++k)
-          wait_drain(bar(C::kFull + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
-      }
-    }
+    } while (next_pass(number));
+    if (lane == 0 && *abort_flag)  // nothing of this block's copies may land after it
+      for (int k = max(0, loads - C::kSlots); k < loads; ++k)
+        wait_drain(bar(C::kFull + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
@@ -301,239 +365,190 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
     const uint32_t kq_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
     constexpr uint32_t kStep = C::kTileBytes >> 4;
     const uint32_t lead = elect_lead();
-    Ring<C::kSlots> r;
+    Ring<C::kSlots> rk, rv;  // the places of the two cursors' tiles
+    rv.next();
+    int gs = 0, gv = 0;
+    uint32_t q_parity[2] = {0u, 0u};
     bool ok = true;
-    Cursor cs, cv;  // the tile whose scores, and whose values, come next
-    cs.start(p, first_item, step, split);
-    cv = cs;
-    int gs = 0, gv = 0, tiles = 0;
-    auto issue_s = [&]() -> bool {  // S(gs) = Q K^T
-      if (cs.j == 0) {
-        if (!wait_warp(C::kQFull + (tiles & 1), (uint32_t)(tiles >> 1) & 1u, 2)) return false;
-        ++tiles;
-      }
-      if (!wait_warp(C::kFull + r.slot, r.parity, 3)) return false;
-      tc_fence_after();
-      const uint32_t a0 = (uint32_t)dq + (uint32_t)((tiles - 1) & 1) * kStep, b0 = (uint32_t)dk + r.slot * kStep;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-        mma_ss_l(lead, tmem + (uint32_t)(gs & 1) * 128u, make_desc(a0 + off, kq_hi), make_desc(b0 + off, kq_hi),
-                 idesc_qk, kk > 0 ? 1u : 0u);
-      }
-      mma_commit_l(lead, bar(C::kSFull + (gs & 1)));
-      mma_commit_l(lead, bar(C::kEmpty + r.slot));
-      r.next();
-      ++gs;
-      cs.next(p, step, split);
-      return true;
-    };
-    auto issue_pv = [&]() -> bool {  // O_half += P_half V_half
-      if (!wait_warp(C::kFull + r.slot, r.parity, 3)) return false;
-      const int valid = min(kTileN, cv.w.keys - cv.j * kTileN);
-      const int steps = (valid + 15) >> 4;  // 16 keys each
-      if (valid & 15) {
-        // keys past the sequence's end may hold anything, and 0 * NaN is NaN:
-        // the values of the last step's are zeroed (later steps are left out)
-        uint8_t* v = base + C::kRingOff + r.slot * C::kTileBytes;
-        const int n = (16 * steps - valid) * 8;  // 16-byte pieces a box
-        for (int i = lane; i < n * C::kBoxes; i += 32) {
-          const int bx = i >= n ? 1 : 0, k = i - bx * n;
-          *reinterpret_cast<uint4*>(v + bx * C::kBoxBytes + (valid + (k >> 3)) * 128 + (k & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+    do {
+      Cursor cs, cv;  // the step whose scores, and whose values, come next
+      cs.start(p, pass);
+      cv = cs;
+      auto issue_s = [&]() -> bool {  // S(gs) = Q K^T
+        const int st = PAIR ? cs.st : 0;
+        if (cs.j == 0) {
+          if (!wait_warp(C::kQFull + st, st ? q_parity[1] : q_parity[0], 2)) return false;
+          if (st) q_parity[1] ^= 1u;
+          else q_parity[0] ^= 1u;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const uint32_t b0 = (uint32_t)dv + r.slot * kStep;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (!wait_warp(C::kPFull + 2 * (gv & 1) + hf, (uint32_t)(gv >> 1) & 1u, 4 + hf)) return false;
+        if (!wait_warp(C::kFull + rk.slot, rk.parity, 3)) return false;
         tc_fence_after();
+        const uint32_t a0 = (uint32_t)dq + (uint32_t)st * kStep, b0 = (uint32_t)dk + rk.slot * kStep;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (hf * 4 + kk < steps)
-            mma_ts_l(lead, tmem + C::kTmemO + hf * D, tmem + (uint32_t)(gv & 1) * 128u + hf * 64u + kk * 8,
-                     make_desc(b0 + (((hf * 4 + kk) * 16 * 128) >> 4), v_hi), idesc_pv,
-                     kk > 0 || cv.j > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss_l(lead, tmem + (uint32_t)(gs & 1) * 128u, make_desc(a0 + off, kq_hi), make_desc(b0 + off, kq_hi),
+                   idesc_qk, kk > 0 ? 1u : 0u);
         }
+        mma_commit_l(lead, bar(C::kSFull + (gs & 1)));
+        if (cs.last()) mma_commit_l(lead, bar(C::kQFree + st));
+        const int slot = rk.slot;
+        ++gs;
+        if (cs.next(p, pass)) {
+          mma_commit_l(lead, bar(C::kEmpty + slot));
+          rk.next();
+          rk.next();
+        }
+        return true;
+      };
+      auto issue_pv = [&]() -> bool {  // O += P V
+        const int st = PAIR ? cv.st : 0;
+        if (!wait_warp(C::kFull + rv.slot, rv.parity, 3)) return false;
+        const int valid = min(kTileN, cv.w.keys - cv.j * kTileN);
+        const int steps = (valid + 15) >> 4;  // 16 keys each
+        if ((valid & 15) && st == 0) {
+          // keys past the sequence's end may hold anything, and 0 * NaN is NaN:
+          // the values of the last step's are zeroed (later steps are left out)
+          uint8_t* v = base + C::kRingOff + rv.slot * C::kTileBytes;
+          const int n = (16 * steps - valid) * 8;  // 16-byte pieces a box
+          for (int i = lane; i < n * C::kBoxes; i += 32) {
+            const int bx = i >= n ? 1 : 0, k = i - bx * n;
+            *reinterpret_cast<uint4*>(v + bx * C::kBoxBytes + (valid + (k >> 3)) * 128 + (k & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint32_t b0 = (uint32_t)dv + rv.slot * kStep, d0 = tmem + C::kTmemO + (uint32_t)st * D;
+        const uint32_t a0 = tmem + (uint32_t)(gv & 1) * 128u;
+        // the first product of a query tile overwrites O, whose columns each half
+        // of the warps has read a part of
+        if (cv.j == 0 && !wait_warp(C::kPFull + 2 * (gv & 1) + 1, (uint32_t)(gv >> 1) & 1u, 5)) return false;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!wait_warp(C::kPFull + 2 * (gv & 1) + hf, (uint32_t)(gv >> 1) & 1u, 4 + hf)) return false;
+          tc_fence_after();
+          if (steps == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_l(lead, d0, a0 + hf * 64u + kk * 8, make_desc(b0 + (((hf * 4 + kk) * 16 * 128) >> 4), v_hi),
+                       idesc_pv, hf + kk > 0 || cv.j > 0 ? 1u : 0u);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < 4 && hf * 4 + kk < steps; ++kk)
+              mma_ts_l(lead, d0, a0 + hf * 64u + kk * 8, make_desc(b0 + (((hf * 4 + kk) * 16 * 128) >> 4), v_hi),
+                       idesc_pv, hf + kk > 0 || cv.j > 0 ? 1u : 0u);
+          }
+        }
+        mma_commit_l(lead, bar(C::kPVDone));
+        if (cv.last()) mma_commit_l(lead, bar(C::kODone + st));
+        const int slot = rv.slot;
+        ++gv;
+        if (cv.next(p, pass)) {
+          mma_commit_l(lead, bar(C::kEmpty + slot));
+          rv.next();
+          rv.next();
+        }
+        return true;
+      };
+      while (ok && cv.more) {
+        while (ok && cs.more && gs < gv + 2) {
+          // a query tile that is not there yet does not hold up the products
+          // of the one before
+          if (cs.j == 0 && gs > gv &&
+              !__all_sync(0xffffffffu, mbar_test_wait(bar(C::kQFull + (PAIR ? cs.st : 0)),
+                                                      PAIR && cs.st ? q_parity[1] : q_parity[0])))
+            break;
+          ok = issue_s();
+        }
+        ok = ok && issue_pv();
       }
-      mma_commit_l(lead, bar(C::kPVDone));
-      if (cv.j + 1 == cv.w.nt) mma_commit_l(lead, bar(C::kODone));
-      mma_commit_l(lead, bar(C::kEmpty + r.slot));
-      r.next();
-      ++gv;
-      cv.next(p, step, split);
-      return true;
-    };
-    if (cs.more) ok = issue_s();
-    if (ok && cs.more) ok = issue_s();
-    while (ok && cv.more) {
-      ok = issue_pv();
-      if (ok && cs.more) ok = issue_s();
-    }
+    } while (next_pass(number) && ok);
     if (!ok) {
       mma_commit_l(lead, bar(C::kDrain));
       if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
     }
     __syncwarp();
   } else if (warp < 10) {
-    // ---------------------------------------------------- softmax, epilogue
+    // ------------------------------------------------ softmax, ends of tiles
     const int hf = (warp - 2) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tSh = tmem + lane_off + (uint32_t)hf * 64u;  // + buffer * 128
-    const uint32_t tO = tmem + lane_off + C::kTmemO + (uint32_t)hf * D;
+    const uint32_t tOh = tmem + lane_off + C::kTmemO + (uint32_t)(hf * (D / 2));  // this half's columns of O
     const int row_t = row / p.pack, row_g = row - row_t * p.pack;
     const int warp_t = (quad * 32) / p.pack;  // first token of the warp's rows
     const float sl = p.scale_log2;
-    int g = 0, tiles = 0;
+    constexpr int kCols = D / 2;
+    int g = 0, ended = 0, ended_by[2] = {0, 0};
     bool ok = true;
-    for (unsigned item = first_item; ok && item < p.items; item += step) {
-      const Work w = work_at(p, item, split);
-      const int t = w.t0 + row_t;
+
+    // zeros and -inf for a query tile without a query or without a key
+    auto clear = [&](const Work& w, int t0) {
+      const int t = t0 + row_t, head = w.hb * p.pack + row_g;
+      if (row_t < p.tile_tokens && t < p.Lq) {
+        uint16_t* o = p.O + w.b * p.o_batch + t * p.o_token + head * D + hf * kCols;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (hf == 0 && p.LSE != nullptr) p.LSE[((long long)w.b * p.H + head) * p.Lq + t] = -INFINITY;
+      }
+    };
+    // The end of a query tile: the halves' sums meet and O leaves.
+    auto finish = [&](unsigned item, int st, float m, float l_own) -> bool {
+      asm volatile("" : "+r"(item));  // worked out anew: it would take registers that the scores need
+      const Work w = work_at(p, item, split, pass.pair);
+      const int t = w.t0 + st * p.tile_tokens + row_t;
       const bool stored = row_t < p.tile_tokens && t < p.Lq;  // this row has an O and an LSE
-      const bool live = row_t < w.live;
+      const bool live = row_t < p.tile_tokens && st * p.tile_tokens + row_t < w.live;
       const long long lse_at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + t;
-      if (!SPLIT && w.nt == 0) {  // no query or no key: zeros, and -inf
-        if (stored) {
-          uint16_t* o = p.O + w.b * p.o_batch + t * p.o_token + (w.hb * p.pack + row_g) * D + hf * (D / 2);
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (hf == 0 && p.LSE != nullptr) p.LSE[lse_at] = -INFINITY;
-        }
-        continue;
-      }
-      const bool busy = warp_t < w.live;  // some row of the warp is live
-      float m_run = 0.f, l_run = 0.f;
-      for (int j = 0; j < w.nt; ++j, ++g) {
-        if (!(ok = wait_warp(C::kSFull + (g & 1), (uint32_t)(g >> 1) & 1u, 6 + hf))) break;
-        const int hi = w.keys - j * kTileN - hf * 64;  // visible columns of this half
-        if (busy && hi > 0) {
-          tc_fence_after();
-          const uint32_t tS = tSh + (uint32_t)(g & 1) * 128u;
-          uint32_t s0[32], s1[32], pk[32];
-          tmem_ld32(tS, s0);
-          tmem_ld32(tS + 32, s1);
-          auto mask = [&](uint32_t (&sv)[32], int cb) {
-            if (hi < 64) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) sv[c] = cb + c < hi ? sv[c] : 0xff800000u;
-            }
-          };
-          auto max32 = [&](const uint32_t (&sv)[32]) -> float {
-            float pm[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float m = fmax3(__uint_as_float(sv[k]), __uint_as_float(sv[k + 4]), __uint_as_float(sv[k + 8]));
-              m = fmax3(m, __uint_as_float(sv[k + 12]), __uint_as_float(sv[k + 16]));
-              m = fmax3(m, __uint_as_float(sv[k + 20]), __uint_as_float(sv[k + 24]));
-              pm[k] = fmaxf(m, __uint_as_float(sv[k + 28]));
-            }
-            return fmax3(fmaxf(pm[0], pm[1]), pm[2], pm[3]);
-          };
-          const float2 sl2 = make_float2(sl, sl);
-          auto exps32 = [&](const uint32_t (&sv)[32], float m, uint32_t* pko, float2& ps) {
-            const float2 m2 = make_float2(-m, -m);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float2 x =
-                  __ffma2_rn(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sl2, m2);
-              const float e0 = ex2(x.x), e1 = ex2(x.y);
-              ps = __fadd2_rn(ps, make_float2(e0, e1));
-              pko[c] = pack_bf16(e0, e1);
-            }
-          };
-          float2 psa = make_float2(0.f, 0.f), psb = make_float2(0.f, 0.f);
-          tmem_wait_ld();
-          mask(s0, 0);
-          float mx = max32(s0);
-          exps32(s0, m_run, pk, psa);
-          mask(s1, 32);
-          mx = fmaxf(mx, max32(s1)) * sl;
-          exps32(s1, m_run, pk + 16, psb);
-          // above the range at any time; below it on the first tile, where a
-          // low maximum may be the row's
-          const bool need = mx > m_run + kRange || (j == 0 && mx < -kRange && mx > -INFINITY);
-          if (__any_sync(0xffffffffu, need)) {
-            float alpha = 1.f;
-            if (need) {
-              if (j > 0) alpha = ex2(m_run - mx);
-              l_run *= alpha;
-              m_run = mx;
-            }
-            if (j > 0) {
-              // S(g) is there, so PV(g - 2) is done: PV(g - 1) is this phase or the last
-              if (!(ok = wait_warp(C::kPVDone, (uint32_t)(g - 1) & 1u, 8))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int cc = 0; cc < D; cc += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + cc, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                tmem_st32(tO + cc, o);
-              }
-            }
-            psa = psb = make_float2(0.f, 0.f);
-            exps32(s0, m_run, pk, psa);
-            exps32(s1, m_run, pk + 16, psb);
-          }
-          tmem_st32(tS, pk);
-          l_run += (psa.x + psa.y) + (psb.x + psb.y);
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        mbar_arrive(bar(C::kPFull + 2 * (g & 1) + hf));
-      }
-      if (!ok) break;
-      // ---------------------------------------------------------- epilogue
-      // the halves meet: (m, l) through the query tile, which is read no more
-      // (the other half may be a tile behind, so a barrier of query tiles, whose
-      // every phase is waited for, says when: not that of key tiles)
-      if (w.nt > 0 && !(ok = wait_warp(C::kODone, (uint32_t)tiles & 1u, 9))) break;
+      // the other half may be a step behind, so barriers of query tiles, whose
+      // every phase is waited for, say when: not that of steps
+      if (!SPLIT && ended > 0 && !wait_warp(C::kOFree, (uint32_t)(ended - 1) & 1u, 11)) return false;
+      if (w.nt > 0 && !wait_warp(C::kODone + st, (uint32_t)(st ? ended_by[1] : ended_by[0]) & 1u, 9)) return false;
+      ++ended;
+      if (st) ++ended_by[1];
+      else ++ended_by[0];
       tc_fence_after();
-      uint8_t* stage = base + C::kQOff + (tiles & 1) * C::kTileBytes;
-      float2* xch = reinterpret_cast<float2*>(stage);
-      xch[hf * 128 + row] = make_float2(m_run, l_run);
-      named_bar_sync(1, 256);
-      const float2 other = xch[(1 - hf) * 128 + row];
-      const float m0 = hf == 0 ? m_run : other.x, l0 = hf == 0 ? l_run : other.y;
-      const float m1 = hf == 0 ? other.x : m_run, l1 = hf == 0 ? other.y : l_run;
-      // a sum of 0 has no say; NaN has
-      const bool on0 = live && l0 != 0.f, on1 = live && l1 != 0.f;
-      const float M = fmaxf(on0 ? m0 : -INFINITY, on1 ? m1 : -INFINITY);
-      const float e0 = on0 ? ex2(m0 - M) : 0.f, e1 = on1 ? ex2(m1 - M) : 0.f;
-      const float L = (on0 ? l0 * e0 : 0.f) + (on1 ? l1 * e1 : 0.f);
-      constexpr int kCols = D / 2;
-      const uint32_t tO0 = tmem + lane_off + C::kTmemO + (uint32_t)(hf * kCols);
-      // columns cc .. cc + 31 of this half's share of O, weighted; what a half
-      // without keys left in TMEM is no number to count on
-      auto join32 = [&](int cc, float f0, float f1, float (&v)[32]) {
-        uint32_t oa[32], ob[32];
-        if (w.nt > 0) {
-          tmem_ld32(tO0 + cc, oa);
-          tmem_ld32(tO0 + D + cc, ob);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          v[c] = (on0 ? __uint_as_float(oa[c]) * f0 : 0.f) + (on1 ? __uint_as_float(ob[c]) * f1 : 0.f);
-      };
+      // the sums meet in score columns that P leaves free (no score is written
+      // to this buffer before its P has arrived)
+      const uint32_t tX = tmem + lane_off + (uint32_t)(g & 1) * 128u + 32u + (uint32_t)st;
+      tmem_st1(tX + (uint32_t)hf * 64u, __float_as_uint(l_own));
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::kMeet));
+      if (!wait_warp(C::kMeet, (uint32_t)(ended - 1) & 1u, 12)) return false;
+      tc_fence_after();
+      const float l = l_own + __uint_as_float(tmem_ld1(tX + (uint32_t)(1 - hf) * 64u));
+      uint8_t* stage = base + C::kOOff;
+      const bool on = live && l != 0.f;  // a sum of 0 has no say; NaN has
+      const uint32_t tO = tOh + (uint32_t)(st * D);
       if constexpr (!SPLIT) {
-        const float inv = on0 || on1 ? 1.f / L : 0.f;
-        const float f0 = e0 * inv, f1 = e1 * inv;
+        const float inv = on ? 1.f / l : 0.f;
         uint32_t o[kCols / 2];
+        float2 sound = make_float2(0.f, 0.f);  // stays 0 unless some value is not finite
 #pragma unroll
         for (int cc = 0; cc < kCols; cc += 32) {
-          float v[32];
-          join32(cc, f0, f1, v);
+          uint32_t v[32];
+          tmem_ld32(tO + cc, v);
+          tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[cc / 2 + c] = pack_bf16(v[2 * c], v[2 * c + 1]);
+          for (int c = 0; c < 16; ++c) {
+            const float2 x = on ? __fmul2_rn(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
+                                             make_float2(inv, inv))
+                                : make_float2(0.f, 0.f);
+            sound = __ffma2_rn(x, make_float2(0.f, 0.f), sound);
+            o[cc / 2 + c] = pack_bf16(x.x, x.y);
+            asm volatile("" : "+r"(o[cc / 2 + c]));  // packed before the next columns are loaded
+          }
+        }
+        const bool again =
+            number == 0 && live && !(l >= kLeastSum && l <= kMostSum && sound.x == 0.f && sound.y == 0.f);
+        if (again && atomicMax(&misc[4], (uint32_t)ended) < (uint32_t)ended) {  // the tile's first such row
+          const uint32_t n = atomicAdd(&misc[2], 1u);
+          if (n < kRedoList) list[n] = tile_of(p, item, st, pass.pair);
+          else atomicMin(&misc[3], item);
         }
         tc_fence_before();
-        named_bar_sync(1, 256);  // O and the exchange are read: both may be written again
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
           const int k = hf * (kCols / 8) + i;
@@ -542,20 +557,19 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(C::kOReady));
-        if (hf == 0 && stored && p.LSE != nullptr)
-          p.LSE[lse_at] = on0 || on1 ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        if (hf == 0 && stored && p.LSE != nullptr) p.LSE[lse_at] = on ? (m + __log2f(l)) * kLn2 : -INFINITY;
       } else {
         // ------------------------- the cluster's blocks join their key ranges
-        // This block's (M, L) of every row where its cluster reads them; then
+        // This block's (m, l) of every row where its cluster reads them; then
         // O, weighted, to the block that sums its columns (D / splits each).
-        constexpr uint32_t kStat = 4096;  // past the exchange
+        constexpr uint32_t kStat = 4096;  // past the sums
         if (hf == 0)
           *reinterpret_cast<float2*>(stage + kStat + row * 8) =
-              make_float2(on0 || on1 ? M : -INFINITY, *abort_flag ? -1.f : L);
+              make_float2(on ? m : -INFINITY, *abort_flag ? -1.f : l);
         cluster_sync_all();
         float top = -INFINITY;
         bool bad = false;
-        const uint32_t stat = base_u32 + C::kQOff + kStat + (uint32_t)row * 8u;
+        const uint32_t stat = base_u32 + C::kOOff + kStat + (uint32_t)row * 8u;
         float2 part[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -571,21 +585,27 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
         for (int c = 0; c < 8; ++c)
           if (c < p.splits && part[c].x > -INFINITY) total += part[c].y * ex2(part[c].x - top);
         const bool any = top > -INFINITY;
-        const float inv = any ? 1.f / total : 0.f;
-        const float f0 = on0 ? ex2(m0 - top) * inv : 0.f, f1 = on1 ? ex2(m1 - top) * inv : 0.f;
+        const float f = on ? ex2(m - top) / total : 0.f;
         const int per = D / p.splits;  // columns of a block's sum
 #pragma unroll 1
-        for (int cc = 0; cc < kCols; cc += 32) {
-          float v[32];
-          join32(cc, f0, f1, v);
-          if (!stored) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int col = hf * kCols + cc + 4 * i, to = col / per;
-            st_dsmem_v4(mapa(base_u32 + C::kRingOff + (uint32_t)((split * 128 + row) * per + col - to * per) * 4u,
-                             (uint32_t)to),
-                        v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int cc = 0; cc < kCols; cc += 16) {
+          uint32_t v[16];
+          if (w.nt > 0) {
+            tmem_ld16(tO + cc, v);
+            tmem_wait_ld();
           }
+          if (stored) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = hf * kCols + cc + 4 * i, to = col / per;
+              // what a block without keys left in TMEM is no number to count on
+              st_dsmem_v4(mapa(base_u32 + C::kRingOff + (uint32_t)((split * 128 + row) * per + col - to * per) * 4u,
+                               (uint32_t)to),
+                          on ? __uint_as_float(v[4 * i]) * f : 0.f, on ? __uint_as_float(v[4 * i + 1]) * f : 0.f,
+                          on ? __uint_as_float(v[4 * i + 2]) * f : 0.f, on ? __uint_as_float(v[4 * i + 3]) * f : 0.f);
+            }
+          }
+          __syncwarp();
         }
         cluster_sync_all();
         if (stored && !bad) {
@@ -599,34 +619,209 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
             }
             *reinterpret_cast<uint2*>(o + cc) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
           }
-          if (split == 0 && hf == 0 && p.LSE != nullptr) p.LSE[lse_at] = any ? (top + __log2f(total)) * kLn2 : -INFINITY;
+          if (split == 0 && hf == 0 && p.LSE != nullptr)
+            p.LSE[lse_at] = any ? (top + __log2f(total)) * kLn2 : -INFINITY;
         }
       }
-      if (w.nt > 0) ++tiles;
-    }
-    if (SPLIT && !ok) {  // the cluster still meets twice
-      if (hf == 0) *reinterpret_cast<float2*>(base + C::kQOff + 4096 + row * 8) = make_float2(-INFINITY, -1.f);
-      cluster_sync_all();
-      cluster_sync_all();
-    }
-  } else if (!SPLIT) {
-    // ------------------------------------------------------- the store of O
-    if (lane == 0) {
-      int tiles = 0;
-      Cursor c;
-      for (c.start(p, first_item, step, split); c.more; ++tiles) {
-        const int qb = tiles & 1;
-        if (!wait(C::kOReady, (uint32_t)tiles & 1u, 10) || *abort_flag) break;
+      return true;
+    };
+    auto mask = [&](uint32_t (&sv)[32], int hi) {  // columns from hi on do not exist
+      if (hi < 32) {
 #pragma unroll
-        for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_store_4d(&p.o_map, base_u32 + C::kQOff + qb * C::kTileBytes + bx * C::kBoxBytes, bx * 64,
-                       c.w.hb * p.pack, c.w.t0, c.w.b);
-        tma_store_commit_and_wait_read();
-        mbar_arrive(bar(C::kQFree + qb));
-        c.item += step;
-        c.seek(p, step, split);
+        for (int c = 0; c < 32; ++c) sv[c] = c < hi ? sv[c] : 0xff800000u;
       }
+    };
+    auto exps = [&](const uint32_t (&sv)[32], float m, uint32_t* pk, float2& ps) {
+      const float2 sl2 = make_float2(sl, sl), m2 = make_float2(-m, -m);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sl2, m2);
+        const float e0 = ex2(x.x), e1 = ex2(x.y);
+        ps = __fadd2_rn(ps, make_float2(e0, e1));
+        pk[c] = pack_bf16(e0, e1);
+      }
+    };
+    uint32_t pair_parity = 0;
+    auto meet_pair = [&]() -> bool {  // the two warps of a quadrant
+      mbar_arrive(bar(C::kPairMeet + quad));
+      pair_parity ^= 1u;
+      return wait_warp(C::kPairMeet + quad, pair_parity ^ 1u, 13);
+    };
+    do {
+      const bool slow = SPLIT || number > 0;
+      Cursor c;
+      unsigned prev = 0;  // the item before this one: its tiles' (m, l) until they end
+      int prev_streams = 0;
+      float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, pm0 = 0.f, pm1 = 0.f, pl0 = 0.f, pl1 = 0.f;
+      // the next item with keys; tiles without are cleared on the way
+      auto seek = [&]() {
+        c.j = c.st = 0;
+        for (; c.at < pass.end; c.at += pass.step) {
+          c.item = pass.list != nullptr ? pass.list[c.at] : c.at;
+          c.w = work_at(p, c.item, split, pass.pair);
+          if (!SPLIT) {
+            if (c.w.nt == 0) clear(c.w, c.w.t0);
+            if (pass.pair == 2 && (c.w.nt == 0 || c.w.streams == 1) && c.w.t0 + p.tile_tokens < p.Lq)
+              clear(c.w, c.w.t0 + p.tile_tokens);
+          }
+          if (SPLIT || c.w.nt > 0) return true;
+        }
+        return false;
+      };
+      c.at = pass.first;
+      c.more = seek();
+      for (;;) {
+        const int st = PAIR ? c.st : 0;
+        if (c.more && c.w.nt > 0) {
+          if (!(ok = wait_warp(C::kSFull + (g & 1), (uint32_t)(g >> 1) & 1u, 6 + hf))) break;
+          const int hi = c.w.keys - c.j * kTileN - hf * 64;  // visible columns of this half
+          const bool busy = st * p.tile_tokens + warp_t < c.w.live;  // some row of the warp is live
+          const uint32_t tS = tSh + (uint32_t)(g & 1) * 128u;
+          if (!slow) {
+            if (busy && hi > 0) {
+              tc_fence_after();
+              uint32_t s0[32], s1[32], pk[32];
+              tmem_ld32(tS, s0);
+              tmem_ld32(tS + 32, s1);
+              float2 psa = make_float2(0.f, 0.f), psb = make_float2(0.f, 0.f);
+              tmem_wait_ld();
+              if (hi < 64) {
+                mask(s0, hi);
+                mask(s1, hi - 32);
+              }
+              exps(s0, 0.f, pk, psa);
+              exps(s1, 0.f, pk + 16, psb);
+              tmem_st32(tS, pk);
+              const float ps = (psa.x + psa.y) + (psb.x + psb.y);
+              if (st) l1 += ps;
+              else l0 += ps;
+              tmem_wait_st();
+              tc_fence_before();
+            }
+          } else {
+            // running maxima, the same for the row's two halves: they meet
+            // through shared memory at every step
+            float* mx = reinterpret_cast<float*>(base + C::kMaxOff);
+            uint32_t s0[32], s1[32];
+            float own = -INFINITY;
+            tc_fence_after();
+            tmem_ld32(tS, s0);
+            tmem_ld32(tS + 32, s1);
+            tmem_wait_ld();
+            mask(s0, hi);
+            mask(s1, hi - 32);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              own = fmax3(own, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
+            mx[hf * 128 + row] = own;
+            if (!(ok = meet_pair())) break;
+            const float top = fmaxf(own, mx[(1 - hf) * 128 + row]) * sl;
+            const float m_old = st ? m1 : m0;
+            float m_new = m_old, alpha = 1.f;
+            if (c.j == 0) m_new = top > -INFINITY ? top : 0.f;
+            else if (top > m_old + kRescale) m_new = top, alpha = ex2(m_old - top);
+            if (c.j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // S(g) is there, so PV(g - 2) is done; with one stream the last
+              // product into this O is PV(g - 1): this phase or the last
+              if (c.w.streams == 1 && !(ok = wait_warp(C::kPVDone, (uint32_t)(g - 1) & 1u, 8))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < kCols; cc += 32) {
+                uint32_t o[32];
+                const uint32_t tO = tOh + (uint32_t)(st * D + cc);
+                tmem_ld32(tO, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st32(tO, o);
+              }
+            }
+            uint32_t pk[32];
+            float2 ps = make_float2(0.f, 0.f);
+            exps(s0, m_new, pk, ps);
+            exps(s1, m_new, pk + 16, ps);
+            tmem_st32(tS, pk);
+            if (st) l1 = l1 * alpha + (ps.x + ps.y), m1 = m_new;
+            else l0 = l0 * alpha + (ps.x + ps.y), m0 = m_new;
+            tmem_wait_st();
+            tc_fence_before();
+            if (!(ok = meet_pair())) break;  // both halves of O are rescaled, the maxima read
+          }
+        }
+        // query tiles that end here: P of the next one's first keys is ready,
+        // and only now may PV overwrite their O
+        int e0 = 0, e1 = 0;
+        if (!c.more) e1 = prev_streams;
+        else if (c.j == 0 && c.st == 0) e1 = c.w.streams == 1 ? prev_streams : min(prev_streams, 1);
+        else if (c.j == 0) e0 = 1, e1 = prev_streams;
+#pragma unroll 1
+        for (int e = e0; ok && e < e1; ++e) ok = finish(prev, e, e ? pm1 : pm0, e ? pl1 : pl0);
+        if (!ok || !c.more) break;
+        if (c.w.nt > 0) mbar_arrive(bar(C::kPFull + 2 * (g & 1) + hf));
+        ++g;
+        if (++c.st < c.w.streams) continue;
+        c.st = 0;
+        if (++c.j < c.w.nt) continue;
+        prev = c.item, prev_streams = c.w.streams;
+        pm0 = m0, pm1 = m1, pl0 = l0, pl1 = l1;
+        m0 = m1 = l0 = l1 = 0.f;
+        c.at += pass.step;
+        c.more = seek();
+      }
+    } while (next_pass(number) && ok);
+    if (SPLIT && !ok) {  // the cluster still meets twice
+      if (hf == 0) *reinterpret_cast<float2*>(base + C::kOOff + 4096 + row * 8) = make_float2(-INFINITY, -1.f);
+      cluster_sync_all();
+      cluster_sync_all();
     }
+  } else if (warp == 10) {
+    // ------------------------------------------------------- the store of O
+    int tile = 0;
+    do {
+      if (lane == 0 && !SPLIT) {
+        Cursor c;
+        bool ok = true;
+        for (c.start(p, pass); ok && c.more; c.skip(p, pass)) {
+          for (int st = 0; st < c.w.streams; ++st, ++tile) {
+            if (!(ok = wait(C::kOReady, (uint32_t)tile & 1u, 10) && !*abort_flag)) break;
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_store_4d(&p.o_map, base_u32 + C::kOOff + bx * C::kBoxBytes, bx * 64, c.w.hb * p.pack,
+                           c.w.t0 + st * p.tile_tokens, c.w.b);
+            tma_store_commit_and_wait_read();
+            mbar_arrive(bar(C::kOFree));
+          }
+        }
+        tma_store_wait_all();  // a later pass may write the same rows
+      }
+    } while (next_pass(number));
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------------- Q
+    int asked[2] = {0, 0};
+    do {
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(C::kBoxes * p.pack * p.tile_tokens) * 128u;
+        Cursor c;
+        bool ok = true;
+        for (c.start(p, pass); ok && c.more; c.skip(p, pass)) {
+#pragma unroll
+          for (int st = 0; st < C::kStreams; ++st) {
+            if (st >= c.w.streams) break;
+            if (asked[st] > 0 && !(ok = wait(C::kQFree + st, (uint32_t)(asked[st] - 1) & 1u, 1))) break;
+            ++asked[st];
+            mbar_arrive_expect_tx(bar(C::kQFull + st), bytes);
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_4d(base_u32 + C::kQOff + st * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + st),
+                          bx * 64, c.w.hb * p.pack, c.w.t0 + st * p.tile_tokens, c.w.b);
+          }
+        }
+      }
+    } while (next_pass(number));
+    if (lane == 0 && *abort_flag)
+      for (int st = 0; st < C::kStreams; ++st)
+        if (asked[st] > 0) wait_drain(bar(C::kQFull + st), (uint32_t)(asked[st] - 1) & 1u, p.err_word);
     __syncwarp();
   }
   if (SPLIT && (warp < 2 || warp >= 10)) {
@@ -641,15 +836,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1) cross_fwd_kernel(const
   }
 }
 
-template <int D, bool SPLIT>
+template <int D, bool PAIR, bool SPLIT>
 cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, PAIR>;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)C::kSmemBytes);
-    if (e == cudaSuccess && SPLIT)
-      e = cudaFuncSetAttribute(cross_fwd_kernel<D, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
@@ -666,14 +859,15 @@ cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, PAIR, SPLIT>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_forward(const CrossParams& p, int sms, cudaStream_t s) {
-  if (p.D == 128) return p.splits > 1 ? launch_fwd<128, true>(p, sms, s) : launch_fwd<128, false>(p, sms, s);
-  return p.splits > 1 ? launch_fwd<64, true>(p, sms, s) : launch_fwd<64, false>(p, sms, s);
+  if (p.splits > 1) return p.D == 128 ? launch_fwd<128, false, true>(p, sms, s) : launch_fwd<64, false, true>(p, sms, s);
+  if (p.pair == 2) return p.D == 128 ? launch_fwd<128, true, false>(p, sms, s) : launch_fwd<64, true, false>(p, sms, s);
+  return p.D == 128 ? launch_fwd<128, false, false>(p, sms, s) : launch_fwd<64, false, false>(p, sms, s);
 }
 
 }  // namespace sab

@@ -1285,8 +1285,13 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.tile_tokens = kTileM / p.pack;
   p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.head_blocks = d.heads / p.pack;
-  p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
-  p.splits = cross_splits(p.items, (d.kv_tokens + kTileN - 1) / kTileN);
+  // two query tiles an item where that leaves no SM without work
+  const long long columns = (long long)d.batch * p.head_blocks, sms = device_sms();
+  const long long waves1 = (columns * p.n_qtiles + sms - 1) / sms;
+  const long long waves2 = 2 * ((columns * ((p.n_qtiles + 1) / 2) + sms - 1) / sms);
+  p.pair = waves2 * 100 <= waves1 * 108 ? 2 : 1;
+  p.items = (unsigned)(columns * ((p.n_qtiles + p.pair - 1) / p.pair));
+  p.splits = p.pair == 2 ? 1 : cross_splits(p.items, (d.kv_tokens + kTileN - 1) / kTileN);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.err_word = device_error_word();
   if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||

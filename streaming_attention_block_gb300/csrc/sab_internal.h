@@ -313,7 +313,8 @@ struct CrossParams {
   int group;                 // heads that share a key head
   int pack, tile_tokens;     // heads and tokens of a tile of 128 rows
   int n_qtiles, head_blocks; // tiles along the tokens, and along the heads
-  unsigned items;            // query tiles
+  int pair;                  // query tiles of an item, which share their key tiles: 1 or 2
+  unsigned items;
   int splits;                // blocks of a cluster among which a tile's keys are cut
   float scale_log2;
   unsigned int* err_word;

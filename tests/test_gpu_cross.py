@@ -158,6 +158,21 @@ def test_scores_far_from_the_reference(q_scale, Lq, Lk):
 
 
 @gpu
+def test_scores_out_of_range_in_more_tiles_than_a_block_remembers():
+    """Every third stretch of queries has scores in the hundreds: 0, 1 or all
+    tiles of many blocks are done again."""
+    H, D, Lk = 1, 64, 40
+    Lq = 152 * 2 * 128 * 75 + 77
+    q, k, v, _ = _case(1, Lq, Lk, H, H, D)
+    for first, last in ((0, Lq // 3), (Lq // 2, Lq // 2 + 1)):
+        q[:, first:last] *= 100.0
+    o, lse = _forward(q, k, v, 0.5)
+    for at in (0, 128 * 64, Lq // 3 - 300, Lq // 2 - 64, Lq - 300):
+        part = slice(at, at + 300)
+        _check_forward(q[:, part], k, v, 0.5, o[:, part], lse[:, :, part].contiguous(), None, None, f"rows {at}")
+
+
+@gpu
 def test_strides_slices_and_rows_in_between():
     B, Lq, Lk, H, Hk, D = 2, 200, 150, 4, 2, 128
     q, k, v, _ = _case(B, Lq, Lk, H, Hk, D)
