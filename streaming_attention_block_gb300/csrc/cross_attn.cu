@@ -20,6 +20,8 @@
 // copies and products, frees TMEM and returns.
 #include <math.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "sab_internal.h"
 
@@ -30,7 +32,6 @@ using namespace ptx;
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
 // P = 2^(s - m) in bf16 has fp32's exponents and is summed in fp32, so the
 // reference m need not be the row's maximum: any m that keeps the sum l within
 // 2^80 of 1 gives the same digits (nothing overflows, and what ftz drops is
@@ -64,7 +65,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 }
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
                                              unsigned* err_word) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, site, err_word);
+  return __builtin_expect(mbar_try_wait(bar, parity), 1) || wait_slow(bar, parity, abort_flag, site, err_word);
 }
 __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned* err_word) {
   const uint64_t t0 = global_ns();
@@ -75,6 +76,19 @@ __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned*
       return;
     }
   }
+}
+
+// Zero the rows [from, to) of a tile in shared memory (whole warp).
+template <int BOXES>
+__device__ __noinline__ void zero_rows(uint8_t* tile, int from, int to) {
+  const int lane = threadIdx.x & 31, n = (to - from) * 8;  // 16-byte pieces a box of 64 columns
+  for (int i = lane; i < n * BOXES; i += 32) {
+    const int bx = i >= n ? 1 : 0, k = i - bx * n;
+    *reinterpret_cast<uint4*>(tile + bx * 128 * 128 + (from + (k >> 3)) * 128 + (k & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // A place in a ring of N slots: the slot and the parity of its current round.
@@ -150,40 +164,45 @@ struct Pass {
   const uint32_t* list;       // or null
   int pair, split;
 };
-// Steps of a pass in order: each key tile of an item, for each of its streams.
-template <bool kUniform>
-struct Cursor {
-  unsigned at, item;
-  Work w;
-  int j, st;
-  bool more;
+// The items of a pass that have keys, for the roles that take every step of
+// them: the search is a call, whose code would otherwise lie in the way of every
+// step's.
+struct Found {
+  unsigned at;
+  int nt, streams, keys, live;
+};
+__device__ __noinline__ Found find_item(const CrossParams& p, unsigned at, unsigned step, unsigned end,
+                                        const uint32_t* list, int pair, int split) {
+  Found f = {at, 0, 1, 0, 0};
+  for (; f.at < end; f.at += step) {
+    const Work w = work_at<true>(p, list != nullptr ? list[f.at] : f.at, split, pair);
+    if (w.nt == 0) continue;
+    f.nt = w.nt;
+    f.streams = w.streams;
+    f.keys = w.keys;
+    f.live = w.live;
+    break;
+  }
+  return f;
+}
+struct Items {
+  unsigned at;
+  int nt, streams, keys, live;  // nt 0: none is left
+  __device__ __forceinline__ void seek(const CrossParams& p, const Pass& a) {
+    const Found f = find_item(p, at, a.step, a.end, a.list, a.pair, a.split);
+    at = (unsigned)uniform<true>((int)f.at);
+    nt = uniform<true>(f.nt);
+    streams = uniform<true>(f.streams);
+    keys = uniform<true>(f.keys);
+    live = uniform<true>(f.live);
+  }
   __device__ __forceinline__ void start(const CrossParams& p, const Pass& a) {
     at = a.first;
     seek(p, a);
   }
-  __device__ __forceinline__ void seek(const CrossParams& p, const Pass& a) {
-    j = st = 0;
-    for (; at < a.end; at += a.step) {
-      item = a.list != nullptr ? (unsigned)uniform<kUniform>((int)a.list[at]) : at;
-      w = work_at<kUniform>(p, item, a.split, a.pair);
-      if (w.nt > 0) {
-        more = true;
-        return;
-      }
-    }
-    more = false;
-  }
-  __device__ __forceinline__ void skip(const CrossParams& p, const Pass& a) {
+  __device__ __forceinline__ void next(const CrossParams& p, const Pass& a) {
     at += a.step;
     seek(p, a);
-  }
-  __device__ __forceinline__ bool last() const { return j + 1 == w.nt; }
-  // the next step; true where it has another key tile
-  __device__ __forceinline__ bool next(const CrossParams& p, const Pass& a) {
-    if (++st < w.streams) return false;
-    st = 0;
-    if (++j == w.nt) skip(p, a);
-    return true;
   }
 };
 
@@ -193,46 +212,48 @@ struct FwdCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = 128u * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
-  static constexpr int kStreams = PAIR ? 2 : 1;
+  static constexpr int kQTiles = PAIR ? 2 : 1;
   static constexpr int kSlots = D == 128 ? (PAIR ? 4 : 5) : 10;  // K and V tiles in turn
   static constexpr uint32_t kOOff = 0;                           // O on its way out
-  static constexpr uint32_t kQOff = kTileBytes;                  // a query tile of each stream
-  static constexpr uint32_t kRingOff = (1 + kStreams) * kTileBytes;
-  static constexpr uint32_t kSumOff = kRingOff + kSlots * kTileBytes;  // [2 accumulators][2][128]
+  static constexpr uint32_t kQOff = kTileBytes;
+  static constexpr uint32_t kRingOff = (1 + kQTiles) * kTileBytes;
+  static constexpr uint32_t kSumOff = kRingOff + kSlots * kTileBytes;  // [2 streams][2][128]
   static constexpr uint32_t kBarOff = kSumOff + 2048;
-  static constexpr int kQFull = 0;                          // [2 streams]
+  static constexpr int kQFull = 0;                          // [2 query tiles]
   static constexpr int kQFree = 2;                          // [2] the tile's last scores are done
   static constexpr int kFull = 4;                           // [kSlots]
   static constexpr int kEmpty = kFull + kSlots;             // [kSlots]
-  static constexpr int kSFull = kEmpty + kSlots;            // [2 buffers]
-  static constexpr int kPFull = kSFull + 2;                 // [2 buffers]
-  static constexpr int kODone = kPFull + 2;                 // [2 accumulators] a query tile's last product
+  static constexpr int kSFull = kEmpty + kSlots;            // [2 streams]
+  static constexpr int kPFull = kSFull + 2;                 // [2]
+  static constexpr int kODone = kPFull + 2;                 // [2] a query tile's last product
   static constexpr int kLReady = kODone + 2;                // [2] its sums
   static constexpr int kORead = kLReady + 2;                // [2] both are read
-  static constexpr int kPVDone = kORead + 2;                // running maxima only
-  static constexpr int kPairMeet = kPVDone + 1;             // [4 quadrants] running maxima only
+  static constexpr int kPairMeet = kORead + 2;              // [4 quadrants] running maxima only
   static constexpr int kOReady = kPairMeet + 4;             // O staged for its store
   static constexpr int kOFree = kOReady + 1;                // and read by it
-  static constexpr int kDrain = kOFree + 1;
-  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kDrain = kOFree + 1;                 // [2 streams]
+  static constexpr int kNumBars = kDrain + 2;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kListOff = kMiscOff + 32;
   static constexpr uint32_t kSmemBytes = kListOff + kRedoList * 4;
-  // K and V, products, the store of O, Q; 8 softmax warps; 4 that end tiles
+  // K, V and Q; products of stream 0; the store of O; products of stream 1;
+  // 8 softmax warps; 4 that end tiles
   static constexpr int kThreads = 32 * 16;
   static constexpr uint32_t kTmemO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// One block per SM walks its items: one query tile, or two that share their
-// key tiles (PAIR), which halves the traffic of K and V from L2.  SPLIT: one
-// item a block, its keys cut among the blocks of a cluster (see the end).
-// Scores of a step (a key tile and a stream) are in one of two TMEM buffers; the
-// keys [0, 64) and [64, 128) of a tile are two halves with four softmax warps
-// and a sum l each.  Products are issued in the order PV(g), S(g + 2) over all
-// steps of the block, also from one query tile to the next, and there are two
-// accumulators O (of the two streams, or of every other query tile): four warps
-// of their own take a finished one out while the next tile's steps go on.
+// One block per SM walks its items.  An item's work is two streams of steps
+// that take turns: two query tiles over the same key tiles (PAIR, which halves
+// the traffic of K and V from L2), or one query tile over every other key tile
+// each.  A stream has its own scores S (P goes over them), its own accumulator O
+// and its own warp that issues the products, in the order S, PV, S, PV ...: with
+// one warp for both, which has to ask some four barriers a step, the tensor cores
+// waited for that warp (1800 cycles a step for 1024 of products; 1400 with two).
+// Softmax: the keys [0, 64) and [64, 128) of a tile are two halves with four
+// warps and a sum l each.  Four more warps take a finished O out while the next
+// tile's steps go on.  SPLIT: one item a block, its keys cut among the blocks of
+// a cluster (see the end).
 template <int D, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(FwdCfg<D, PAIR>::kThreads, 1)
 cross_fwd_kernel(const __grid_constant__ CrossParams p) {
@@ -261,22 +282,21 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kQFull + i), 1);
-      mbar_init(bar(C::kQFree + i), 1);
+      mbar_init(bar(C::kQFree + i), PAIR ? 1 : 2);
       mbar_init(bar(C::kSFull + i), 1);
       mbar_init(bar(C::kPFull + i), 8);
       mbar_init(bar(C::kODone + i), 1);
       mbar_init(bar(C::kLReady + i), 8);
       mbar_init(bar(C::kORead + i), 4);
+      mbar_init(bar(C::kDrain + i), 1);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(bar(C::kFull + s), 1);
-      mbar_init(bar(C::kEmpty + s), 1);
+      mbar_init(bar(C::kEmpty + s), 2);
     }
-    mbar_init(bar(C::kPVDone), 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar(C::kPairMeet + i), 2);
     mbar_init(bar(C::kOReady), 4);
     mbar_init(bar(C::kOFree), 1);
-    mbar_init(bar(C::kDrain), 1);
     misc[1] = (base_u32 & 1023u) != 0;  // the tiles' swizzle counts on it
     if (misc[1] != 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
     misc[2] = misc[4] = 0;
@@ -337,23 +357,18 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     return false;
   };
   int number = 0;
-  // The accumulator of a query tile, and how often each has been used: of the
-  // tile's stream in PAIR, else in turn.
-  int used[2] = {0, 0}, tiles = 0;
-  auto accumulator = [&](int st) -> int { return PAIR ? st : tiles & 1; };
-  auto uses = [&](int o) -> int { return o ? used[1] : used[0]; };
-  auto use = [&](int o) {
-    ++tiles;
-    if (o) ++used[1];
-    else ++used[0];
-  };
+  int steps_before = 0;  // of the block's items so far: in turn, steps go to stream 0 and 1 (not PAIR)
+  // whether a stream has steps in an item of nt key tiles, and (not PAIR) the first
+  auto first_tile = [&](int s) -> int { return (s ^ steps_before) & 1; };
+  auto has_steps = [&](int s, int nt, int streams) -> bool { return PAIR ? s < streams : first_tile(s) < nt; };
 
   if (warp == 0) {
-    // -------------------------------------------------------------- K and V
+    // ----------------------------------------------------------- K, V and Q
     Ring<C::kSlots> r;
-    int loads = 0;
+    int loads = 0, asked[2] = {0, 0};
     do {
       if (lane == 0) {
+        const uint32_t q_bytes = (uint32_t)(C::kBoxes * p.pack * p.tile_tokens) * 128u;
         // one tile into the next slot
         auto load = [&](const CUtensorMap* m, int row, int head, int b) -> bool {
           if (loads >= C::kSlots && !wait(C::kEmpty + r.slot, r.parity ^ 1u, 0)) return false;
@@ -367,145 +382,148 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           ++loads;
           return true;
         };
-        Cursor<false> c;
-        for (c.start(p, pass); c.more;) {
-          const int head = c.w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : c.w.b;
-          const int row = (c.w.first + c.j) * kTileN;
-          if (!load(&p.k_map, row, head, kb) || !load(&p.v_map, row, head, kb)) break;
-          while (!c.next(p, pass)) {
+        bool ok = true;
+        for (unsigned at = pass.first; ok && at < pass.end; at += pass.step) {
+          const Work w = work_at<false>(p, pass.list != nullptr ? pass.list[at] : at, split, pass.pair);
+          if (w.nt == 0) continue;
+#pragma unroll
+          for (int t = 0; t < C::kQTiles; ++t) {
+            if (t >= w.streams) break;
+            if (asked[t] > 0 && !(ok = wait(C::kQFree + t, (uint32_t)(asked[t] - 1) & 1u, 1))) break;
+            ++asked[t];
+            mbar_arrive_expect_tx(bar(C::kQFull + t), q_bytes);
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_4d(base_u32 + C::kQOff + t * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + t),
+                          bx * 64, w.hb * p.pack, w.t0 + t * p.tile_tokens, w.b);
           }
+          const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
+          for (int j = 0; ok && j < w.nt; ++j)
+            ok = load(&p.k_map, (w.first + j) * kTileN, head, kb) && load(&p.v_map, (w.first + j) * kTileN, head, kb);
         }
       }
     } while (next_pass(number));
-    if (lane == 0 && *abort_flag)  // nothing of this block's copies may land after it
+    if (lane == 0 && *abort_flag) {  // nothing of this block's copies may land after it
       for (int k = max(0, loads - C::kSlots); k < loads; ++k)
         wait_drain(bar(C::kFull + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
+#pragma unroll
+      for (int t = 0; t < C::kQTiles; ++t)
+        if (asked[t] > 0) wait_drain(bar(C::kQFull + t), (uint32_t)(asked[t] - 1) & 1u, p.err_word);
+    }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------- products
-    // Shared memory feeds the products at its full rate, so a barrier's answer
-    // takes this warp some 200 cycles: the next one is asked in the middle of
-    // the products before it.
+    const int s = warp == 3 ? 1 : 0;  // the stream
+    const int qt = PAIR ? s : 0;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTileN, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
-    const uint64_t dq = smem_desc_sw128(base_u32 + C::kQOff, 16, 1024);
+    constexpr uint32_t kStep = C::kTileBytes >> 4;
+    const uint64_t dq = smem_desc_sw128(base_u32 + C::kQOff + qt * C::kTileBytes, 16, 1024);
     const uint64_t dk = smem_desc_sw128(base_u32 + C::kRingOff, 16, 1024);
     const uint64_t dv = smem_desc_sw128(base_u32 + C::kRingOff, C::kBoxBytes, 1024);
+    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
     const uint32_t kq_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32);
-    constexpr uint32_t kStep = C::kTileBytes >> 4;
+    const uint32_t tS = tmem + (uint32_t)s * 128u, tO = tmem + C::kTmemO + (uint32_t)s * D;
     const uint32_t lead = elect_lead();
-    Ring<C::kSlots> rk, rv;  // the places of the two cursors' tiles
-    rv.next();
-    int gs = 0, gv = 0;
-    uint32_t q_parity[2] = {0u, 0u};
-    bool ok = true, p_there = false, k_there = false;  // asked ahead
-    auto ask = [&](int i, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity));
+    Ring<C::kSlots> r;  // place of the key tile; its values are one on
+    uint32_t q_parity = 0, p_parity = 0;
+    int used = 0;  // query tiles in this accumulator so far
+    bool ok = true;
+    auto scores = [&]() -> bool {  // S = Q K^T
+      if (!wait_warp(C::kFull + r.slot, r.parity, 3)) return false;
+      tc_fence_after();
+      const uint32_t b0 = k_lo + r.slot * kStep;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+        mma_ss_l(lead, tS, make_desc(q_lo + off, kq_hi), make_desc(b0 + off, kq_hi), idesc_qk, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_l(lead, bar(C::kSFull + s));
+      mma_commit_l(lead, bar(C::kEmpty + r.slot));
+      return true;
+    };
+    // Past a key tile that only the other stream works on.  Its slots are waited
+    // for and freed all the same: a parity tells two rounds of a slot apart, so
+    // no warp may be a round behind another.
+    auto pass_by = [&]() -> bool {
+      for (int i = 0; i < 2; ++i) {
+        if (!wait_warp(C::kFull + r.slot, r.parity, 3)) return false;
+        arrive_warp(C::kEmpty + r.slot);
+        r.next();
+      }
+      return true;
     };
     do {
-      Cursor<true> cs, cv;  // the step whose scores, and whose values, come next
-      cs.start(p, pass);
-      cv = cs;
-      auto issue_s = [&]() -> bool {  // S(gs) = Q K^T
-        const int st = PAIR ? cs.st : 0;
-        if (cs.j == 0) {
-          if (!wait_warp(C::kQFull + st, st ? q_parity[1] : q_parity[0], 2)) return false;
-          if (st) q_parity[1] ^= 1u;
-          else q_parity[0] ^= 1u;
-        }
-        if (st == 0 && !k_there && !wait_warp(C::kFull + rk.slot, rk.parity, 3)) return false;
-        k_there = false;
-        tc_fence_after();
-        const uint32_t a0 = (uint32_t)dq + (uint32_t)st * kStep, b0 = (uint32_t)dk + rk.slot * kStep;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-          mma_ss_l(lead, tmem + (uint32_t)(gs & 1) * 128u, make_desc(a0 + off, kq_hi), make_desc(b0 + off, kq_hi),
-                   idesc_qk, kk > 0 ? 1u : 0u);
-          if (kk == D / 32) p_there = ask(C::kPFull + (gv & 1), (uint32_t)(gv >> 1) & 1u);
-        }
-        mma_commit_l(lead, bar(C::kSFull + (gs & 1)));
-        if (cs.last()) mma_commit_l(lead, bar(C::kQFree + st));
-        const int slot = rk.slot;
-        ++gs;
-        if (cs.next(p, pass)) {
-          mma_commit_l(lead, bar(C::kEmpty + slot));
-          rk.next();
-          rk.next();
-        }
-        return true;
-      };
-      auto issue_pv = [&]() -> bool {  // O += P V
-        const int st = PAIR ? cv.st : 0, o = accumulator(st);
-        const int valid = min(kTileN, cv.w.keys - cv.j * kTileN);
-        const int steps = (valid + 15) >> 4;  // 16 keys each
-        if (st == 0) {
-          if (!wait_warp(C::kFull + rv.slot, rv.parity, 3)) return false;
-          if (valid & 15) {
-            // keys past the sequence's end may hold anything, and 0 * NaN is
-            // NaN: the values of the last step's are zeroed (later steps are
-            // left out)
-            uint8_t* v = base + C::kRingOff + rv.slot * C::kTileBytes;
-            const int n = (16 * steps - valid) * 8;  // 16-byte pieces a box
-            for (int i = lane; i < n * C::kBoxes; i += 32) {
-              const int bx = i >= n ? 1 : 0, k = i - bx * n;
-              *reinterpret_cast<uint4*>(v + bx * C::kBoxBytes + (valid + (k >> 3)) * 128 + (k & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+      Items c;
+      for (c.start(p, pass); c.nt > 0; c.next(p, pass)) {
+        if (!has_steps(s, c.nt, c.streams)) {
+          if (!PAIR) {
+            if (!(ok = wait_warp(C::kQFull, q_parity, 2))) break;
+            q_parity ^= 1u;
+            arrive_warp(C::kQFree);
           }
+          for (int j = 0; ok && j < c.nt; ++j) ok = pass_by();
+          if (!ok) break;
+          steps_before += c.nt;
+          continue;
         }
-        // the first product of a query tile overwrites what the accumulator held
-        if (cv.j == 0 && uses(o) > 0 && !wait_warp(C::kORead + o, (uint32_t)(uses(o) - 1) & 1u, 4)) return false;
-        if (!p_there && !wait_warp(C::kPFull + (gv & 1), (uint32_t)(gv >> 1) & 1u, 5)) return false;
-        p_there = false;
-        tc_fence_after();
-        const uint32_t b0 = (uint32_t)dv + rv.slot * kStep, d0 = tmem + C::kTmemO + (uint32_t)o * D;
-        const uint32_t a0 = tmem + (uint32_t)(gv & 1) * 128u;
-        // P of keys 64 .. 127 starts 64 columns after that of the first 64
-        auto product = [&](int kk) {
-          mma_ts_l(lead, d0, a0 + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u,
-                   make_desc(b0 + ((uint32_t)(kk * 16 * 128) >> 4), v_hi), idesc_pv, kk > 0 || cv.j > 0 ? 1u : 0u);
-        };
-        if (steps == 8) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            product(kk);
-            if (kk == 4 && cs.more && cs.st == 0) k_there = ask(C::kFull + rk.slot, rk.parity);
-          }
-        } else {
-#pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk) product(kk);
-        }
-        if (SPLIT || number > 0) mma_commit_l(lead, bar(C::kPVDone));
-        if (cv.last()) {
-          mma_commit_l(lead, bar(C::kODone + o));
-          use(o);
-        }
-        const int slot = rv.slot;
-        ++gv;
-        if (cv.next(p, pass)) {
-          mma_commit_l(lead, bar(C::kEmpty + slot));
-          rv.next();
-          rv.next();
-        }
-        return true;
-      };
-      while (ok && cv.more) {
-        while (ok && cs.more && gs < gv + 2) {
-          // a query tile that is not there yet does not hold up the products
-          // of the one before
-          if (cs.j == 0 && gs > gv && !ask(C::kQFull + (PAIR ? cs.st : 0), PAIR && cs.st ? q_parity[1] : q_parity[0]))
+        if (!(ok = wait_warp(C::kQFull + qt, q_parity, 2))) break;
+        q_parity ^= 1u;
+        constexpr int kBy = PAIR ? 1 : 2;  // key tiles from step to step
+        int j = PAIR ? 0 : first_tile(s);
+        if (j > 0 && !(ok = pass_by())) break;
+        if (!(ok = scores())) break;
+        bool begun = false;
+        for (;;) {
+          const bool more = j + kBy < c.nt;
+          if (!more) mma_commit_l(lead, bar(C::kQFree + qt));
+          // O += P V
+          const int keys = c.keys - j * kTileN, steps = min(8, (keys + 15) >> 4);  // 16 keys each
+          Ring<C::kSlots> v = r;
+          v.next();
+          if (!(ok = wait_warp(C::kFull + v.slot, v.parity, 3))) break;
+          // keys past the sequence's end may hold anything, and 0 * NaN is NaN:
+          // the values of the last step's are zeroed (later steps are left out)
+          if (__builtin_expect(steps * 16 > keys, 0))
+            zero_rows<C::kBoxes>(base + C::kRingOff + v.slot * C::kTileBytes, keys, steps * 16);
+          // the first product of a query tile overwrites what the accumulator held
+          if (__builtin_expect(!begun && used > 0, 0) &&
+              !(ok = wait_warp(C::kORead + s, (uint32_t)(used - 1) & 1u, 4)))
             break;
-          ok = issue_s();
+          if (!(ok = wait_warp(C::kPFull + s, p_parity, 5))) break;
+          p_parity ^= 1u;
+          tc_fence_after();
+          const uint32_t b0 = v_lo + v.slot * kStep;
+          // P of keys 64 .. 127 starts 64 columns after that of the first 64
+          auto product = [&](int kk) {
+            mma_ts_l(lead, tO, tS + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u,
+                     make_desc(b0 + ((uint32_t)(kk * 16 * 128) >> 4), v_hi), idesc_pv, kk > 0 || begun ? 1u : 0u);
+          };
+          if (__builtin_expect(steps == 8, 1)) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) product(kk);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < steps; ++kk) product(kk);
+          }
+          begun = true;
+          mma_commit_l(lead, bar(C::kEmpty + v.slot));
+          r.next();
+          r.next();
+          if (!PAIR && j + 1 < c.nt && !(ok = pass_by())) break;
+          if (!more) break;
+          j += kBy;
+          if (!(ok = scores())) break;
         }
-        ok = ok && issue_pv();
+        if (!ok) break;
+        mma_commit_l(lead, bar(C::kODone + s));
+        ++used;
+        steps_before += c.nt;
       }
     } while (next_pass(number) && ok);
     if (!ok) {
-      mma_commit_l(lead, bar(C::kDrain));
-      if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
+      mma_commit_l(lead, bar(C::kDrain + s));
+      if (lane == 0) wait_drain(bar(C::kDrain + s), 0, p.err_word);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -513,15 +531,16 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     int tile = 0;
     do {
       if (lane == 0 && !SPLIT) {
-        Cursor<false> c;
         bool ok = true;
-        for (c.start(p, pass); ok && c.more; c.skip(p, pass)) {
-          for (int st = 0; st < c.w.streams; ++st, ++tile) {
+        for (unsigned at = pass.first; ok && at < pass.end; at += pass.step) {
+          const Work w = work_at<false>(p, pass.list != nullptr ? pass.list[at] : at, split, pass.pair);
+          if (w.nt == 0) continue;
+          for (int t = 0; t < w.streams; ++t, ++tile) {
             if (!(ok = wait(C::kOReady, (uint32_t)tile & 1u, 10) && !*abort_flag)) break;
 #pragma unroll
             for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_store_4d(&p.o_map, base_u32 + C::kOOff + bx * C::kBoxBytes, bx * 64, c.w.hb * p.pack,
-                           c.w.t0 + st * p.tile_tokens, c.w.b);
+              tma_store_4d(&p.o_map, base_u32 + C::kOOff + bx * C::kBoxBytes, bx * 64, w.hb * p.pack,
+                           w.t0 + t * p.tile_tokens, w.b);
             tma_store_commit_and_wait_read();
             mbar_arrive(bar(C::kOFree));
           }
@@ -530,45 +549,19 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       }
     } while (next_pass(number));
     __syncwarp();
-  } else if (warp == 3) {
-    // -------------------------------------------------------------------- Q
-    int asked[2] = {0, 0};
-    do {
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)(C::kBoxes * p.pack * p.tile_tokens) * 128u;
-        Cursor<false> c;
-        bool ok = true;
-        for (c.start(p, pass); ok && c.more; c.skip(p, pass)) {
-#pragma unroll
-          for (int st = 0; st < C::kStreams; ++st) {
-            if (st >= c.w.streams) break;
-            if (asked[st] > 0 && !(ok = wait(C::kQFree + st, (uint32_t)(asked[st] - 1) & 1u, 1))) break;
-            ++asked[st];
-            mbar_arrive_expect_tx(bar(C::kQFull + st), bytes);
-#pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_4d(base_u32 + C::kQOff + st * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + st),
-                          bx * 64, c.w.hb * p.pack, c.w.t0 + st * p.tile_tokens, c.w.b);
-          }
-        }
-      }
-    } while (next_pass(number));
-    if (lane == 0 && *abort_flag)
-      for (int st = 0; st < C::kStreams; ++st)
-        if (asked[st] > 0) wait_drain(bar(C::kQFull + st), (uint32_t)(asked[st] - 1) & 1u, p.err_word);
-    __syncwarp();
   } else if (warp < 12) {
     // -------------------------------------------------------------- softmax
     const int hf = (warp - 4) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tSh = tmem + lane_off + (uint32_t)hf * 64u;  // + buffer * 128
+    const uint32_t tSh = tmem + lane_off + (uint32_t)hf * 64u;  // + stream * 128
     const int warp_t = (quad * 32) / p.pack;  // first token of the warp's rows
     const float sl = p.scale_log2;
-    int g = 0;
+    int used[2] = {0, 0};
+    uint32_t s_parity[2] = {0u, 0u};
     bool ok = true;
     auto mask = [&](uint32_t (&sv)[32], int hi) {  // columns from hi on do not exist
-      if (hi < 32) {
+      if (__builtin_expect(hi < 32, 0)) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) sv[c] = c < hi ? sv[c] : 0xff800000u;
       }
@@ -585,110 +578,125 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       }
       tmem_st16(to, pk);
     };
-    int done_before = -1;  // steps of the first pass, whose products PVDone does not count
     uint32_t pair_parity = 0;
     auto meet_pair = [&]() -> bool {  // the two warps of a quadrant
       arrive_warp(C::kPairMeet + quad);
       pair_parity ^= 1u;
       return wait_warp(C::kPairMeet + quad, pair_parity ^ 1u, 13);
     };
-    do {
-      const bool slow = SPLIT || number > 0;
-      if (slow && done_before < 0) done_before = g;
-      float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
-      Cursor<true> c;
-      for (c.start(p, pass); c.more; c.next(p, pass), ++g) {
-        const int st = PAIR ? c.st : 0, o = accumulator(st);
-        if (!(ok = wait_warp(C::kSFull + (g & 1), (uint32_t)(g >> 1) & 1u, 6 + hf))) break;
-        const int hi = c.w.keys - c.j * kTileN - hf * 64;          // visible columns of this half
-        const bool busy = st * p.tile_tokens + warp_t < c.w.live;  // some row of the warp is live
-        const uint32_t tS = tSh + (uint32_t)(g & 1) * 128u;
-        float m_last = 0.f;
-        if (!slow) {
-          if (busy && hi > 0) {
-            tc_fence_after();
-            uint32_t s0[32], s1[32];
-            tmem_ld32(tS, s0);
-            tmem_wait_ld();
-            tmem_ld32(tS + 32, s1);  // on its way while the first 32 are worked on
-            float2 ps = make_float2(0.f, 0.f);
-            mask(s0, hi);
-            exps(s0, 0.f, ps, tS);
-            tmem_wait_ld();
-            mask(s1, hi - 32);
-            exps(s1, 0.f, ps, tS + 16);
-            if (st) l1 += ps.x + ps.y;
-            else l0 += ps.x + ps.y;
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        } else {
-          // running maxima, the same for the row's two halves: they meet at
-          // every step, in columns of the scores that P leaves free
-          const uint32_t tX = tmem + lane_off + (uint32_t)(g & 1) * 128u + 32u;
+    // one step of stream S of an item
+    float m_s[2] = {0.f, 0.f}, l_s[2] = {0.f, 0.f};
+    auto step = [&](auto stream, bool slow, const Items& c, int tile, bool first, bool last) -> bool {
+      constexpr int S = decltype(stream)::value;
+      if (!wait_warp(C::kSFull + S, s_parity[S], 6 + hf)) return false;
+      s_parity[S] ^= 1u;
+      const int hi = c.keys - tile * kTileN - hf * 64;                       // visible columns of this half
+      const bool busy = (PAIR ? S * p.tile_tokens : 0) + warp_t < c.live;  // some row of the warp is live
+      const uint32_t tS = tSh + (uint32_t)S * 128u;
+      float& l = l_s[S];
+      float& m = m_s[S];
+      if (__builtin_expect(!slow, 1)) {
+        if (__builtin_expect(busy && hi > 0, 1)) {
+          tc_fence_after();
           uint32_t s0[32], s1[32];
-          float own = -INFINITY;
-          tc_fence_after();
           tmem_ld32(tS, s0);
-          tmem_ld32(tS + 32, s1);
           tmem_wait_ld();
-          mask(s0, hi);
-          mask(s1, hi - 32);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) own = fmax3(own, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
-          tmem_st1(tX + (uint32_t)hf * 64u, __float_as_uint(own));
-          tmem_wait_st();
-          tc_fence_before();
-          if (!(ok = meet_pair())) break;
-          tc_fence_after();
-          const float top = fmaxf(own, __uint_as_float(tmem_ld1(tX + (uint32_t)(1 - hf) * 64u))) * sl;
-          const float m_old = st ? m1 : m0;
-          float m_new = m_old, alpha = 1.f;
-          if (c.j == 0) m_new = top > -INFINITY ? top : 0.f;
-          else if (top > m_old + kRescale) m_new = top, alpha = ex2(m_old - top);
-          if (c.j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // S(g) is there, so PV(g - 2) is done; with one stream the last
-            // product into this O is PV(g - 1): this phase or the last
-            if (c.w.streams == 1 && !(ok = wait_warp(C::kPVDone, (uint32_t)(g - 1 - done_before) & 1u, 8))) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = 0; cc < D / 2; cc += 16) {  // half of the columns each
-              uint32_t v[16];
-              const uint32_t tO = tmem + lane_off + C::kTmemO + (uint32_t)(o * D + hf * (D / 2) + cc);
-              tmem_ld16(tO, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_st16(tO, v);
-            }
-          }
+          tmem_ld32(tS + 32, s1);  // on its way while the first 32 are worked on
           float2 ps = make_float2(0.f, 0.f);
-          exps(s0, m_new, ps, tS);
-          exps(s1, m_new, ps, tS + 16);
-          float& l = st ? l1 : l0;
-          l = l * alpha + (ps.x + ps.y);
-          if (st) m1 = m_new;
-          else m0 = m_new;
-          m_last = m_new;
-          if (c.last()) tmem_st1(tX + (uint32_t)hf * 64u + 1u, __float_as_uint(l));
+          mask(s0, hi);
+          exps(s0, 0.f, ps, tS);
+          tmem_wait_ld();
+          mask(s1, hi - 32);
+          exps(s1, 0.f, ps, tS + 16);
+          l += ps.x + ps.y;
           tmem_wait_st();
           tc_fence_before();
-          if (!(ok = meet_pair())) break;  // both halves of O are rescaled, the maxima read
-          if (c.last()) {                  // half 0 takes the sum, half 1 the maximum
-            tc_fence_after();
-            l = hf == 0 ? l + __uint_as_float(tmem_ld1(tX + 64u + 1u)) : m_last;
-            tc_fence_before();
+        }
+      } else {
+        // running maxima, the same for the row's two halves: they meet at every
+        // step, in columns of the scores that P leaves free
+        const uint32_t tX = tmem + lane_off + (uint32_t)S * 128u + 32u;
+        uint32_t s0[32], s1[32];
+        float own = -INFINITY;
+        tc_fence_after();
+        tmem_ld32(tS, s0);
+        tmem_ld32(tS + 32, s1);
+        tmem_wait_ld();
+        mask(s0, hi);
+        mask(s1, hi - 32);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) own = fmax3(own, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
+        tmem_st1(tX + (uint32_t)hf * 64u, __float_as_uint(own));
+        tmem_wait_st();
+        tc_fence_before();
+        if (!meet_pair()) return false;
+        tc_fence_after();
+        const float top = fmaxf(own, __uint_as_float(tmem_ld1(tX + (uint32_t)(1 - hf) * 64u))) * sl;
+        float alpha = 1.f;
+        if (first) {
+          m = top > -INFINITY ? top : 0.f;
+          l = 0.f;
+        } else if (top > m + kRescale) {
+          alpha = ex2(m - top);
+          m = top;
+        }
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // S is there, so the stream's products before it are done
+#pragma unroll 1
+          for (int cc = 0; cc < D / 2; cc += 16) {  // half of the columns each
+            uint32_t v[16];
+            const uint32_t tO = tmem + lane_off + C::kTmemO + (uint32_t)(S * D + hf * (D / 2) + cc);
+            tmem_ld16(tO, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st16(tO, v);
           }
         }
-        arrive_warp(C::kPFull + (g & 1));
-        if (c.last()) {
-          // the sums of a query tile: two halves, or (running maxima) sum and maximum
-          if (uses(o) > 0 && !(ok = wait_warp(C::kORead + o, (uint32_t)(uses(o) - 1) & 1u, 9))) break;
-          reinterpret_cast<float*>(base + C::kSumOff)[(o * 2 + hf) * 128 + row] = st ? l1 : l0;
-          arrive_warp(C::kLReady + o);
-          use(o);
-          if (st) l1 = 0.f;
-          else l0 = 0.f;
+        float2 ps = make_float2(0.f, 0.f);
+        exps(s0, m, ps, tS);
+        exps(s1, m, ps, tS + 16);
+        l = l * alpha + (ps.x + ps.y);
+        if (last) tmem_st1(tX + (uint32_t)hf * 64u + 1u, __float_as_uint(l));
+        tmem_wait_st();
+        tc_fence_before();
+        if (!meet_pair()) return false;  // both halves of O are rescaled, the maxima read
+        if (last) {                      // half 0 takes the sum, half 1 the maximum
+          tc_fence_after();
+          l = hf == 0 ? l + __uint_as_float(tmem_ld1(tX + 64u + 1u)) : m;
+          tc_fence_before();
+        }
+      }
+      arrive_warp(C::kPFull + S);
+      if (__builtin_expect(last, 0)) {
+        // the sums of a query tile: two halves, or (running maxima) sum and maximum
+        if (used[S] > 0 && !wait_warp(C::kORead + S, (uint32_t)(used[S] - 1) & 1u, 9)) return false;
+        reinterpret_cast<float*>(base + C::kSumOff)[(S * 2 + hf) * 128 + row] = l;
+        arrive_warp(C::kLReady + S);
+        ++used[S];
+        l = 0.f;
+      }
+      return true;
+    };
+    const std::integral_constant<int, 0> zero;
+    const std::integral_constant<int, 1> one;
+    do {
+      const bool slow = SPLIT || number > 0;
+      Items c;
+      for (c.start(p, pass); ok && c.nt > 0; c.next(p, pass)) {
+        if (PAIR) {
+          for (int j = 0; ok && j < c.nt; ++j) {
+            ok = step(zero, slow, c, j, j == 0, j + 1 == c.nt);
+            if (ok && c.streams == 2) ok = step(one, slow, c, j, j == 0, j + 1 == c.nt);
+          }
+        } else {
+          int j = 0;
+          if (steps_before & 1) ok = step(one, slow, c, j, true, j + 2 >= c.nt), ++j;
+          for (; ok && j < c.nt; ++j) {
+            ok = step(zero, slow, c, j, j < 2, j + 2 >= c.nt);
+            if (ok && ++j < c.nt) ok = step(one, slow, c, j, j < 2, j + 2 >= c.nt);
+          }
+          steps_before += c.nt;
         }
       }
     } while (next_pass(number) && ok);
@@ -710,44 +718,70 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         if (p.LSE != nullptr) p.LSE[((long long)w.b * p.H + head) * p.Lq + t] = -INFINITY;
       }
     };
+    int used[2] = {0, 0}, tiles = 0;
     auto finish = [&](const Work& w, unsigned item, int st) -> bool {
-      const int o = accumulator(st);
       const int t = w.t0 + st * p.tile_tokens + row_t;
       const bool stored = row_t < p.tile_tokens && t < p.Lq;  // this row has an O and an LSE
       const bool live = row_t < p.tile_tokens && st * p.tile_tokens + row_t < w.live;
       const long long lse_at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + t;
-      const uint32_t tO = tmem + lane_off + C::kTmemO + (uint32_t)(o * D);
-      if constexpr (!SPLIT) {
-        if (!wait_warp(C::kLReady + o, (uint32_t)uses(o) & 1u, 12)) return false;
-        const float a = sums[(o * 2) * 128 + row], b = sums[(o * 2 + 1) * 128 + row];
-        const float m = number > 0 ? b : 0.f, l = number > 0 ? a : a + b;
-        const bool on = live && l != 0.f;  // a sum of 0 has no say; NaN has
-        const float inv = on ? 1.f / l : 0.f;
-        if (!wait_warp(C::kODone + o, (uint32_t)uses(o) & 1u, 9)) return false;
-        tc_fence_after();
-        if (tiles > 0 && !wait_warp(C::kOFree, (uint32_t)(tiles - 1) & 1u, 11)) return false;
-        use(o);
-        float2 sound = make_float2(0.f, 0.f);  // stays 0 unless some value is not finite
+      // the streams' sums and products
+      bool on[2] = {false, false}, has[2];
+      float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
+      for (int o = 0; o < 2; ++o) {
+        has[o] = PAIR ? o == st : has_steps(o, w.nt, 1);
+        if (!has[o]) continue;
+        if (!wait_warp(C::kLReady + o, (uint32_t)used[o] & 1u, 12)) return false;
+        const float x = sums[(o * 2) * 128 + row], y = sums[(o * 2 + 1) * 128 + row];
+        l[o] = SPLIT || number > 0 ? x : x + y;
+        m[o] = SPLIT || number > 0 ? y : 0.f;
+        on[o] = live && l[o] != 0.f;  // a sum of 0 has no say; NaN has
+        if (!wait_warp(C::kODone + o, (uint32_t)used[o] & 1u, 9)) return false;
+        ++used[o];
+      }
+      tc_fence_after();
+      const float top_own = fmaxf(on[0] ? m[0] : -INFINITY, on[1] ? m[1] : -INFINITY);
+      const float sum = (on[0] ? l[0] * ex2(m[0] - top_own) : 0.f) + (on[1] ? l[1] * ex2(m[1] - top_own) : 0.f);
+      const bool any_own = on[0] || on[1];
+      const uint32_t tO = tmem + lane_off + C::kTmemO;
+      // columns cc .. cc + 31 of O: the streams' weighted (what a stream without
+      // keys left in TMEM is no number to count on)
+      auto take = [&](int cc, const float (&f)[2], float2 (&x)[16]) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) x[c] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          if (!has[o]) continue;
           uint32_t v[32];
-          tmem_ld32(tO + cc, v);
+          tmem_ld32(tO + (uint32_t)(o * D + cc), v);
           tmem_wait_ld();
           if (cc + 32 == D) {
             tc_fence_before();
             arrive_warp(C::kORead + o);
           }
+          const float2 g = make_float2(f[o], f[o]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (on[o]) x[c] = __ffma2_rn(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), g, x[c]);
+        }
+      };
+      if constexpr (!SPLIT) {
+        const float inv = any_own ? 1.f / sum : 0.f;
+        const float f[2] = {on[0] ? ex2(m[0] - top_own) * inv : 0.f, on[1] ? ex2(m[1] - top_own) * inv : 0.f};
+        if (tiles > 0 && !wait_warp(C::kOFree, (uint32_t)(tiles - 1) & 1u, 11)) return false;
+        ++tiles;
+        float2 sound = make_float2(0.f, 0.f);  // stays 0 unless some value is not finite
+#pragma unroll
+        for (int cc = 0; cc < D; cc += 32) {
+          float2 x[16];
+          take(cc, f, x);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w4[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int k = 8 * i + 2 * c;
-              const float2 x = on ? __fmul2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                                               make_float2(inv, inv))
-                                  : make_float2(0.f, 0.f);
-              sound = __ffma2_rn(x, make_float2(0.f, 0.f), sound);
-              w4[c] = pack_bf16(x.x, x.y);
+              sound = __ffma2_rn(x[4 * i + c], make_float2(0.f, 0.f), sound);
+              w4[c] = pack_bf16(x[4 * i + c].x, x[4 * i + c].y);
             }
             const int k = cc / 8 + i;
             *reinterpret_cast<uint4*>(stage + (k >> 3) * C::kBoxBytes + row * 128 + (((k & 7) ^ (row & 7)) << 4)) =
@@ -755,7 +789,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           }
         }
         const bool again =
-            number == 0 && live && !(l >= kLeastSum && l <= kMostSum && sound.x == 0.f && sound.y == 0.f);
+            number == 0 && live && !(sum >= kLeastSum && sum <= kMostSum && sound.x == 0.f && sound.y == 0.f);
         if (again && atomicMax(&misc[4], (uint32_t)tiles) < (uint32_t)tiles) {  // the tile's first such row
           const uint32_t n = atomicAdd(&misc[2], 1u);
           if (n < kRedoList) list[n] = tile_of(p, item, st, pass.pair);
@@ -763,20 +797,13 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         }
         fence_proxy_async_smem();
         arrive_warp(C::kOReady);
-        if (stored && p.LSE != nullptr) p.LSE[lse_at] = on ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        if (stored && p.LSE != nullptr) p.LSE[lse_at] = any_own ? (top_own + __log2f(sum)) * kLn2 : -INFINITY;
       } else {
         // ------------------------- the cluster's blocks join their key ranges
-        // This block's (m, l) of every row where its cluster reads them; then
-        // O, weighted, to the block that sums its columns (D / splits each).
-        float m = -INFINITY, l = 0.f;
-        if (w.nt > 0) {
-          if (!wait_warp(C::kLReady, 0u, 12) || !wait_warp(C::kODone, 0u, 9)) return false;
-          tc_fence_after();
-          l = sums[row];
-          m = sums[128 + row];
-        }
-        const bool on = live && l != 0.f;
-        *reinterpret_cast<float2*>(stage + row * 8) = make_float2(on ? m : -INFINITY, *abort_flag ? -1.f : l);
+        // This block's maximum and sum of every row where its cluster reads them;
+        // then O, weighted, to the block that sums its columns (D / splits each).
+        *reinterpret_cast<float2*>(stage + row * 8) =
+            make_float2(any_own ? top_own : -INFINITY, *abort_flag ? -1.f : sum);
         cluster_sync_all();
         float top = -INFINITY;
         bool bad = false;
@@ -796,36 +823,31 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         for (int c = 0; c < 8; ++c)
           if (c < p.splits && part[c].x > -INFINITY) total += part[c].y * ex2(part[c].x - top);
         const bool any = top > -INFINITY;
-        const float f = on ? ex2(m - top) / total : 0.f;
+        const float f[2] = {on[0] ? ex2(m[0] - top) / total : 0.f, on[1] ? ex2(m[1] - top) / total : 0.f};
         const int per = D / p.splits;  // columns of a block's sum
-#pragma unroll 1
-        for (int cc = 0; cc < D; cc += 16) {
-          uint32_t v[16];
-          if (w.nt > 0) {
-            tmem_ld16(tO + cc, v);
-            tmem_wait_ld();
-          }
+#pragma unroll
+        for (int cc = 0; cc < D; cc += 32) {
+          float2 x[16];
+          take(cc, f, x);
           if (stored) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const int col = cc + 4 * i, to = col / per;
-              // what a block without keys left in TMEM is no number to count on
               st_dsmem_v4(mapa(base_u32 + C::kRingOff + (uint32_t)((split * 128 + row) * per + col - to * per) * 4u,
                                (uint32_t)to),
-                          on ? __uint_as_float(v[4 * i]) * f : 0.f, on ? __uint_as_float(v[4 * i + 1]) * f : 0.f,
-                          on ? __uint_as_float(v[4 * i + 2]) * f : 0.f, on ? __uint_as_float(v[4 * i + 3]) * f : 0.f);
+                          x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
             }
           }
           __syncwarp();
         }
         cluster_sync_all();
         if (stored && !bad) {
-          const float* sum = reinterpret_cast<const float*>(base + C::kRingOff) + row * per;
+          const float* all = reinterpret_cast<const float*>(base + C::kRingOff) + row * per;
           uint16_t* out = p.O + w.b * p.o_batch + t * p.o_token + (w.hb * p.pack + row_g) * D + split * per;
           for (int cc = 0; cc < per; cc += 4) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = 0; c < p.splits; ++c) {
-              const float4 x = *reinterpret_cast<const float4*>(sum + c * 128 * per + cc);
+              const float4 x = *reinterpret_cast<const float4*>(all + c * 128 * per + cc);
               a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
             }
             *reinterpret_cast<uint2*>(out + cc) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
@@ -847,6 +869,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         }
 #pragma unroll 1
         for (int st = 0; ok && st < w.streams; ++st) ok = finish(w, item, st);
+        steps_before += w.nt;
       }
     } while (next_pass(number) && ok);
     if (SPLIT && !ok) {  // the cluster still meets twice

@@ -135,6 +135,19 @@ def test_lengths_and_what_lies_past_them(Lq, Lk, H, Hk, D, q_len, kv_len, junk):
 
 
 @gpu
+@pytest.mark.parametrize("Lq, H, Hk, D", [(1, 24, 8, 128), (1, 6, 6, 64), (5, 16, 16, 128), (129, 4, 4, 64)])
+def test_many_sequences_of_unequal_lengths(Lq, H, Hk, D):
+    """Several query tiles a block, of odd and even numbers of key tiles, and none."""
+    B, Lk = 64, 900
+    lens = [(97 * b) % (Lk + 1) for b in range(B)]
+    lens[5] = lens[40] = 0
+    lens[7], lens[8], lens[9] = 128, 129, 1
+    q, k, v, _ = _case(B, Lq, Lk, H, Hk, D)
+    o, lse = _forward(q, k, v, D ** -0.5, None, lens)
+    _check_forward(q, k, v, D ** -0.5, o, lse, None, lens, "many")
+
+
+@gpu
 def test_one_length_for_states_that_all_share():
     q, k, v, _ = _case(4, 70, 200, 4, 2, 128, 1)
     o, lse = _forward(q, k, v, 0.1, [70, 3, 0, 50], [150])
