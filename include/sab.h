@@ -658,6 +658,30 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
                                const sab_token_rows* O, float* LSE, void* stream);
 
 /*
+ * Gradients of sab_cross_attention for a loss with gradient dO with respect to
+ * O, from the forward's O and LSE (both needed).  With P recomputed from LSE and
+ * delta_i = sum_d dO_id O_id:
+ *   dV = P^T dO,  dS = P * (dO V^T - delta),
+ *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
+ * dK and dV summed over the query heads of a key head and, where kv_batch is 1,
+ * over the sequences.  Padded queries and keys get zero gradients and, whatever
+ * they hold, give none.
+ * dQ as Q, dK and dV as K: bf16 rows that overlap no input and not one another.
+ * workspace  device scratch of sab_cross_attention_backward_workspace bytes,
+ *            256-byte aligned, no zero-fill needed; calls that can overlap on the
+ *            GPU need one each.
+ * P and dS are rounded to bf16 for their products, sums are fp32 and in an order
+ * that the shape fixes: equal calls give equal bits.
+ * Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+size_t sab_cross_attention_backward_workspace(const sab_cross_desc* desc);
+sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
+                                        const sab_token_rows* V, const sab_token_rows* O, const sab_token_rows* dO,
+                                        const float* LSE, const int* q_len, const int* kv_len, float softmax_scale,
+                                        const sab_token_rows* dQ, const sab_token_rows* dK, const sab_token_rows* dV,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Layer norm over the channels of each row, and its gradients.  The method
  * normalises queries and keys only (sab_qk_norm_rope); a video transformer's
  * block also has a layer norm with weights before its cross attention, and

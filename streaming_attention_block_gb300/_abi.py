@@ -99,6 +99,8 @@ def library() -> ctypes.CDLL:
         "sab_decay_attention_backward_workspace": (SZ, [I, I, I, I]),
         "sab_decay_attention_backward": (I, [P] * 8 + [I, I, I, I, F] + [P] * 5 + [SZ, P]),
         "sab_cross_attention": (I, [P] * 6 + [F, P, P, P]),
+        "sab_cross_attention_backward_workspace": (SZ, [P]),
+        "sab_cross_attention_backward": (I, [P] * 9 + [F] + [P] * 4 + [SZ, P]),
         "sab_layer_norm": (I, [P, P, LL, P, P, P, LL, P, P, P]),
         "sab_layer_norm_backward_workspace": (SZ, [LL, I, LL]),
         "sab_layer_norm_backward": (I, [P, P, LL, P, LL, P, P, P, P, LL, P, P, P, SZ, P]),
@@ -774,6 +776,33 @@ def cross_attention(Q, K, V, softmax_scale: float, O, LSE=None, q_len=None, kv_l
         _token_rows(O, x, "O", dev), _arg(LSE, (x[0], x[2], x[1]), f4, "LSE", dev), _stream(stream, dev))
     if status != 0:
         raise SabError(status, "cross_attention")
+
+
+def cross_attention_backward_workspace(B: int, Lq: int, Lk: int, H: int, Hk: int, D: int, kv_batch=None) -> int:
+    """Bytes of workspace of ``cross_attention_backward``; ``kv_batch`` defaults to B."""
+    desc = _CROSS.pack(int(B), int(Lq), int(B if kv_batch is None else kv_batch), int(Lk), int(H), int(Hk), int(D))
+    return int(library().sab_cross_attention_backward_workspace(desc))
+
+
+def cross_attention_backward(Q, K, V, O, dO, LSE, softmax_scale: float, dQ, dK, dV, q_len=None, kv_len=None,
+                             workspace=None, stream=None):
+    """sab_cross_attention_backward: (dQ, dK, dV) of cross_attention from its
+    ``O`` and ``LSE`` (see include/sab.h)."""
+    dev = _device()
+    x, y, desc = _cross_shapes(Q, K)
+    i32, f4 = torch.int32, torch.float32
+    q = _token_rows(Q, x, "Q", dev)  # before scratch is made on its device
+    if workspace is None:
+        workspace = _scratch(int(library().sab_cross_attention_backward_workspace(desc)), Q, stream)
+    ws, ws_bytes = _workspace(workspace, dev)
+    status = library().sab_cross_attention_backward(
+        desc, q, _token_rows(K, y, "K", dev), _token_rows(V, y, "V", dev), _token_rows(O, x, "O", dev),
+        _token_rows(dO, x, "dO", dev), _arg(LSE, (x[0], x[2], x[1]), f4, "LSE", dev),
+        _arg(q_len, x[:1], i32, "q_len", dev), _arg(kv_len, y[:1], i32, "kv_len", dev), float(softmax_scale),
+        _token_rows(dQ, x, "dQ", dev), _token_rows(dK, y, "dK", dev), _token_rows(dV, y, "dV", dev), ws, ws_bytes,
+        _stream(stream, dev))
+    if status != 0:
+        raise SabError(status, "cross_attention_backward")
 
 
 # ------------------------------------------------------------- layer norm

@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsab.so")
 DEBUG_LIB = os.path.join(HERE, "libsab_debug.so")
 SOURCES = ["sab_api.cu", "chunk_attn.cu", "kv_append.cu", "qk_rope.cu", "rotary.cu", "decay_attn.cu",
-           "layer_norm.cu", "cross_attn.cu"]
+           "layer_norm.cu", "cross_attn.cu", "cross_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

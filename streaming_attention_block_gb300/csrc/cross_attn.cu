@@ -22,15 +22,11 @@
 
 #include <type_traits>
 
-#include "ptx.cuh"
-#include "sab_internal.h"
+#include "cross_common.cuh"
 
 namespace sab {
 namespace {
 
-using namespace ptx;
-
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 // P = 2^(s - m) in bf16 has fp32's exponents and is summed in fp32, so the
 // reference m need not be the row's maximum: any m that keeps the sum l within
@@ -42,65 +38,6 @@ constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p80f;
 constexpr float kRescale = 8.0f;  // running maxima: O is rescaled when one grows by more than 2^8
 constexpr int kRedoList = 64;     // query tiles a block remembers
 
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
-                                       unsigned* err_word) {
-  const uint64_t t0 = global_ns();
-#pragma unroll 1
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0) {
-      if (*abort_flag) return false;
-      if (global_ns() - t0 > kTimeoutNs) {
-        if (err_word != nullptr) atomicOr(err_word, 1u << site);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
-                                             unsigned* err_word) {
-  return __builtin_expect(mbar_try_wait(bar, parity), 1) || wait_slow(bar, parity, abort_flag, site, err_word);
-}
-__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned* err_word) {
-  const uint64_t t0 = global_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (global_ns() - t0 > kTimeoutNs) {
-      if (err_word != nullptr) atomicOr(err_word, 1u << 31);
-      return;
-    }
-  }
-}
-
-// Zero the rows [from, to) of a tile in shared memory (whole warp).
-template <int BOXES>
-__device__ __noinline__ void zero_rows(uint8_t* tile, int from, int to) {
-  const int lane = threadIdx.x & 31, n = (to - from) * 8;  // 16-byte pieces a box of 64 columns
-  for (int i = lane; i < n * BOXES; i += 32) {
-    const int bx = i >= n ? 1 : 0, k = i - bx * n;
-    *reinterpret_cast<uint4*>(tile + bx * 128 * 128 + (from + (k >> 3)) * 128 + (k & 7) * 16) =
-        make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-}
-
-// A place in a ring of N slots: the slot and the parity of its current round.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) slot = 0, parity ^= 1u;
-  }
-};
-
 // The number of a query tile, counted one by one, from its item and stream.
 __device__ __forceinline__ uint32_t tile_of(const CrossParams& p, unsigned item, int st, int pair) {
   const unsigned n = (unsigned)(p.n_qtiles + pair - 1) / (unsigned)pair;
@@ -110,101 +47,119 @@ __device__ __forceinline__ uint32_t tile_of(const CrossParams& p, unsigned item,
 
 // ------------------------------------------------------------------ forward
 
-// kUniform: the whole warp asks, and the answer is told the compiler to be one
-// value for all lanes (the operands of the products live in uniform registers;
-// what it does not know to be uniform it moves there lane by lane, every time).
-template <bool kUniform>
-__device__ __forceinline__ int uniform(int x) {
-  return kUniform ? __shfl_sync(0xffffffffu, x, 0) : x;
+// Scores of columns from hi on do not exist.
+__device__ __forceinline__ void mask_from(uint32_t (&s)[32], int hi) {
+  if (__builtin_expect(hi < 32, 0)) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = c < hi ? s[c] : 0xff800000u;
+  }
 }
-template <bool kUniform>
-__device__ __forceinline__ int length_of(const int* lens, int b, int most) {
-  return lens == nullptr ? most : uniform<kUniform>(min(max(__ldg(lens + b), 0), most));
+// P = 2^(s * sl - m) of 32 scores, as 16 columns of bf16 pairs to TMEM; sums by
+// pairs into ps.
+__device__ __forceinline__ void exps32(const uint32_t (&s)[32], float sl, float m, float2& ps, uint32_t to) {
+  const float2 sl2 = make_float2(sl, sl), m2 = make_float2(-m, -m);
+  uint32_t pk[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, m2);
+    const float e0 = ex2(x.x), e1 = ex2(x.y);
+    ps = __fadd2_rn(ps, make_float2(e0, e1));
+    pk[c] = pack_bf16(e0, e1);
+  }
+  tmem_st16(to, pk);
 }
 
-// One or two query tiles (`streams`) of `pack` heads from head hb * pack on,
-// tile_tokens tokens each from t0 on, and the key tiles [first, first + nt).
-struct Work {
-  int b, hb, t0;
-  int live;         // tokens from t0 on that are inside q_len
-  int streams;
-  int first, nt;
-  int keys;         // keys of the range
+// One step with the running maximum, the same for the row's two halves: their
+// warps meet twice, and exchange through columns of the scores that P leaves
+// free.  tS: the step's scores of these lanes; tO: this half's columns of O.  At
+// the last step half 0 returns the row's sum, half 1 its maximum, as l.  A call:
+// its code would lie in the way of the fast steps'.
+struct SlowSum {
+  float m, l;
+  bool ok;
 };
-template <bool kUniform>
-__device__ __forceinline__ Work work_at(const CrossParams& p, unsigned item, int split, int pair) {
-  Work w;
-  const unsigned n = (unsigned)(p.n_qtiles + pair - 1) / (unsigned)pair;
-  const unsigned r = item / n;
-  w.t0 = (int)(item - r * n) * pair * p.tile_tokens;
-  w.b = (int)(r / (unsigned)p.head_blocks);
-  w.hb = (int)(r - (unsigned)w.b * (unsigned)p.head_blocks);
-  w.live = length_of<kUniform>(p.q_len, w.b, p.Lq) - w.t0;
-  w.streams = pair == 2 && w.live > p.tile_tokens ? 2 : 1;
-  const int kl = w.live > 0 ? length_of<kUniform>(p.kv_len, p.Bk == 1 ? 0 : w.b, p.Lk) : 0;
-  const int total = (kl + kTileN - 1) / kTileN;
-  w.first = (int)((long long)total * split / p.splits);
-  const int last = (int)((long long)total * (split + 1) / p.splits);
-  w.nt = last - w.first;
-  w.keys = min(kl, last * kTileN) - w.first * kTileN;
-  if constexpr (kDebugBounds) {
-    if (w.b >= p.B || w.hb >= p.head_blocks || w.t0 >= p.Lq || w.first < 0 || last * kTileN - kTileN >= p.Lk) {
-      if (p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
-      w.nt = w.live = 0;
+__device__ __noinline__ SlowSum slow_step(const CrossParams& p, uint32_t meet, volatile int* abort_flag,
+                                          uint32_t parity, uint32_t tS, uint32_t tO, int cols, int hf, int hi,
+                                          bool first, bool last, float m, float l) {
+  const int lane = threadIdx.x & 31;
+  auto meet_pair = [&](uint32_t par) -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    return __all_sync(0xffffffffu, wait_bounded(meet, par, abort_flag, 13, p.err_word));
+  };
+  const uint32_t tX = tS + 32u;
+  tS += (uint32_t)hf * 64u;
+  uint32_t s0[32], s1[32];
+  float own = -INFINITY;
+  tc_fence_after();
+  tmem_ld32(tS, s0);
+  tmem_ld32(tS + 32, s1);
+  tmem_wait_ld();
+  mask_from(s0, hi);
+  mask_from(s1, hi - 32);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) own = fmax3(own, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
+  tmem_st1(tX + (uint32_t)hf * 64u, __float_as_uint(own));
+  tmem_wait_st();
+  tc_fence_before();
+  if (!meet_pair(parity)) return SlowSum{m, l, false};
+  tc_fence_after();
+  const float top = fmaxf(own, __uint_as_float(tmem_ld1(tX + (uint32_t)(1 - hf) * 64u))) * p.scale_log2;
+  float alpha = 1.f;
+  if (first) {
+    m = top > -INFINITY ? top : 0.f;
+    l = 0.f;
+  } else if (top > m + kRescale) {
+    alpha = ex2(m - top);
+    m = top;
+  }
+  if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+    // the scores are there, so the stream's products before them are done
+#pragma unroll 1
+    for (int cc = 0; cc < cols; cc += 16) {
+      uint32_t v[16];
+      tmem_ld16(tO + (uint32_t)cc, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+      tmem_st16(tO + (uint32_t)cc, v);
     }
   }
-  return w;
+  float2 ps = make_float2(0.f, 0.f);
+  exps32(s0, p.scale_log2, m, ps, tS);
+  exps32(s1, p.scale_log2, m, ps, tS + 16);
+  l = l * alpha + (ps.x + ps.y);
+  if (last) tmem_st1(tX + (uint32_t)hf * 64u + 1u, __float_as_uint(l));
+  tmem_wait_st();
+  tc_fence_before();
+  if (!meet_pair(parity ^ 1u)) return SlowSum{m, l, false};  // both halves of O are rescaled, the maxima read
+  if (last) {
+    tc_fence_after();
+    l = hf == 0 ? l + __uint_as_float(tmem_ld1(tX + 64u + 1u)) : m;
+    tc_fence_before();
+  }
+  return SlowSum{m, l, true};
 }
 
-// What a block works through.  Pass 0: every step-th item.  Pass 1: the query
-// tiles of the list, one by one.  Pass 2: the items of pass 0 from the one on at
-// which the list was full.
-struct Pass {
-  unsigned first, step, end;  // items, or places of the list
-  const uint32_t* list;       // or null
-  int pair, split;
-};
-// The items of a pass that have keys, for the roles that take every step of
-// them: the search is a call, whose code would otherwise lie in the way of every
-// step's.
-struct Found {
-  unsigned at;
-  int nt, streams, keys, live;
-};
-__device__ __noinline__ Found find_item(const CrossParams& p, unsigned at, unsigned step, unsigned end,
-                                        const uint32_t* list, int pair, int split) {
-  Found f = {at, 0, 1, 0, 0};
-  for (; f.at < end; f.at += step) {
-    const Work w = work_at<true>(p, list != nullptr ? list[f.at] : f.at, split, pair);
-    if (w.nt == 0) continue;
-    f.nt = w.nt;
-    f.streams = w.streams;
-    f.keys = w.keys;
-    f.live = w.live;
-    break;
-  }
-  return f;
+// Zeros and -inf for the tokens from t0 on of a query tile without a query or
+// without a key; a row for each thread.
+__device__ __noinline__ void clear_tile(const CrossParams& p, int b, int hb, int t0, int row) {
+  const int row_t = row / p.pack, head = hb * p.pack + row - row_t * p.pack, t = t0 + row_t;
+  if (row_t >= p.tile_tokens || t >= p.Lq) return;
+  uint4* o = reinterpret_cast<uint4*>(p.O + b * p.o_batch + t * p.o_token + head * p.D);
+#pragma unroll 1
+  for (int i = 0; i < p.D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (p.LSE != nullptr) p.LSE[((long long)b * p.H + head) * p.Lq + t] = -INFINITY;
 }
-struct Items {
-  unsigned at;
-  int nt, streams, keys, live;  // nt 0: none is left
-  __device__ __forceinline__ void seek(const CrossParams& p, const Pass& a) {
-    const Found f = find_item(p, at, a.step, a.end, a.list, a.pair, a.split);
-    at = (unsigned)uniform<true>((int)f.at);
-    nt = uniform<true>(f.nt);
-    streams = uniform<true>(f.streams);
-    keys = uniform<true>(f.keys);
-    live = uniform<true>(f.live);
-  }
-  __device__ __forceinline__ void start(const CrossParams& p, const Pass& a) {
-    at = a.first;
-    seek(p, a);
-  }
-  __device__ __forceinline__ void next(const CrossParams& p, const Pass& a) {
-    at += a.step;
-    seek(p, a);
-  }
-};
+// Puts a query tile on the list of those to be done again; called by each of its
+// rows that wants it (see the kernel for misc).
+__device__ __noinline__ void again_later(const CrossParams& p, uint32_t* misc, uint32_t* list, unsigned end,
+                                         unsigned item, int st, int pair) {
+  if (atomicMax(&misc[4], end) >= end) return;  // another row has
+  const uint32_t n = atomicAdd(&misc[2], 1u);
+  if (n < kRedoList) list[n] = tile_of(p, item, st, pair);
+  else atomicMin(&misc[3], item);
+}
 
 template <int D_, bool PAIR>
 struct FwdCfg {
@@ -328,6 +283,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   pass.list = nullptr;
   pass.pair = PAIR ? 2 : 1;
   pass.split = split;
+  pass.by = SPLIT ? Spot{0, 0, 0} : spot_of(p, gridDim.x, pass.pair);
   // To the next pass, after all roles are through with this one; false: done.
   auto next_pass = [&](int& number) -> bool {
     if (SPLIT) return false;  // running maxima from the start
@@ -383,23 +339,30 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           return true;
         };
         bool ok = true;
-        for (unsigned at = pass.first; ok && at < pass.end; at += pass.step) {
-          const Work w = work_at<false>(p, pass.list != nullptr ? pass.list[at] : at, split, pass.pair);
+        Walk<false> c;
+        for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
+          const Work& w = c.w;
           if (w.nt == 0) continue;
-#pragma unroll
-          for (int t = 0; t < C::kQTiles; ++t) {
-            if (t >= w.streams) break;
-            if (asked[t] > 0 && !(ok = wait(C::kQFree + t, (uint32_t)(asked[t] - 1) & 1u, 1))) break;
-            ++asked[t];
-            mbar_arrive_expect_tx(bar(C::kQFull + t), q_bytes);
-#pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_4d(base_u32 + C::kQOff + t * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + t),
-                          bx * 64, w.hb * p.pack, w.t0 + t * p.tile_tokens, w.b);
-          }
           const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
-          for (int j = 0; ok && j < w.nt; ++j)
-            ok = load(&p.k_map, (w.first + j) * kTileN, head, kb) && load(&p.v_map, (w.first + j) * kTileN, head, kb);
+          for (int j = 0; ok && j < w.nt; ++j) {
+            if (!(ok = load(&p.k_map, (w.first + j) * kTileN, head, kb))) break;
+            // there is room for the first keys before there is for the queries,
+            // which the item before reads to its end
+            if (j == 0) {
+#pragma unroll
+              for (int t = 0; t < C::kQTiles; ++t) {
+                if (t >= w.streams) break;
+                if (asked[t] > 0 && !(ok = wait(C::kQFree + t, (uint32_t)(asked[t] - 1) & 1u, 1))) break;
+                ++asked[t];
+                mbar_arrive_expect_tx(bar(C::kQFull + t), q_bytes);
+#pragma unroll
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                  tma_load_4d(base_u32 + C::kQOff + t * C::kTileBytes + bx * C::kBoxBytes, &p.q_map, bar(C::kQFull + t),
+                              bx * 64, query_c1(p, w, t), query_c2(p, w, t), w.b);
+              }
+            }
+            ok = ok && load(&p.v_map, (w.first + j) * kTileN, head, kb);
+          }
         }
       }
     } while (next_pass(number));
@@ -454,9 +417,16 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      Items c;
-      for (c.start(p, pass); c.nt > 0; c.next(p, pass)) {
+      Walk<true> ahead;  // the next item is looked up while the softmax works on this one
+      ahead.start(p, pass);
+      ahead.seek(p, pass);
+      while (ahead.more(pass)) {
+        const struct {
+          int nt, streams, keys;
+        } c = {ahead.w.nt, ahead.w.streams, ahead.w.keys};
         if (!has_steps(s, c.nt, c.streams)) {
+          ahead.next(p, pass);
+          ahead.seek(p, pass);
           if (!PAIR) {
             if (!(ok = wait_warp(C::kQFull, q_parity, 2))) break;
             q_parity ^= 1u;
@@ -473,6 +443,8 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         int j = PAIR ? 0 : first_tile(s);
         if (j > 0 && !(ok = pass_by())) break;
         if (!(ok = scores())) break;
+        ahead.next(p, pass);
+        ahead.seek(p, pass);
         bool begun = false;
         for (;;) {
           const bool more = j + kBy < c.nt;
@@ -532,15 +504,16 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     do {
       if (lane == 0 && !SPLIT) {
         bool ok = true;
-        for (unsigned at = pass.first; ok && at < pass.end; at += pass.step) {
-          const Work w = work_at<false>(p, pass.list != nullptr ? pass.list[at] : at, split, pass.pair);
+        Walk<false> c;
+        for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
+          const Work& w = c.w;
           if (w.nt == 0) continue;
           for (int t = 0; t < w.streams; ++t, ++tile) {
             if (!(ok = wait(C::kOReady, (uint32_t)tile & 1u, 10) && !*abort_flag)) break;
 #pragma unroll
             for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_store_4d(&p.o_map, base_u32 + C::kOOff + bx * C::kBoxBytes, bx * 64, w.hb * p.pack,
-                           w.t0 + t * p.tile_tokens, w.b);
+              tma_store_4d(&p.o_map, base_u32 + C::kOOff + bx * C::kBoxBytes, bx * 64, query_c1(p, w, t),
+                           query_c2(p, w, t), w.b);
             tma_store_commit_and_wait_read();
             mbar_arrive(bar(C::kOFree));
           }
@@ -556,42 +529,18 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tSh = tmem + lane_off + (uint32_t)hf * 64u;  // + stream * 128
     const int warp_t = (quad * 32) / p.pack;  // first token of the warp's rows
-    const float sl = p.scale_log2;
     int used[2] = {0, 0};
     uint32_t s_parity[2] = {0u, 0u};
     bool ok = true;
-    auto mask = [&](uint32_t (&sv)[32], int hi) {  // columns from hi on do not exist
-      if (__builtin_expect(hi < 32, 0)) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) sv[c] = c < hi ? sv[c] : 0xff800000u;
-      }
-    };
-    auto exps = [&](const uint32_t (&sv)[32], float m, float2& ps, uint32_t to) {
-      const float2 sl2 = make_float2(sl, sl), m2 = make_float2(-m, -m);
-      uint32_t pk[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sl2, m2);
-        const float e0 = ex2(x.x), e1 = ex2(x.y);
-        ps = __fadd2_rn(ps, make_float2(e0, e1));
-        pk[c] = pack_bf16(e0, e1);
-      }
-      tmem_st16(to, pk);
-    };
-    uint32_t pair_parity = 0;
-    auto meet_pair = [&]() -> bool {  // the two warps of a quadrant
-      arrive_warp(C::kPairMeet + quad);
-      pair_parity ^= 1u;
-      return wait_warp(C::kPairMeet + quad, pair_parity ^ 1u, 13);
-    };
     // one step of stream S of an item
     float m_s[2] = {0.f, 0.f}, l_s[2] = {0.f, 0.f};
-    auto step = [&](auto stream, bool slow, const Items& c, int tile, bool first, bool last) -> bool {
+    uint32_t pair_parity = 0;  // of the two warps' meetings: two a step, so it stays 0 between steps
+    auto step = [&](auto stream, bool slow, int keys, int rows_live, int tile, bool first, bool last) -> bool {
       constexpr int S = decltype(stream)::value;
       if (!wait_warp(C::kSFull + S, s_parity[S], 6 + hf)) return false;
       s_parity[S] ^= 1u;
-      const int hi = c.keys - tile * kTileN - hf * 64;                       // visible columns of this half
-      const bool busy = (PAIR ? S * p.tile_tokens : 0) + warp_t < c.live;  // some row of the warp is live
+      const int hi = keys - tile * kTileN - hf * 64;                            // visible columns of this half
+      const bool busy = (PAIR ? S * p.tile_tokens : 0) + warp_t < rows_live;  // some row of the warp is live
       const uint32_t tS = tSh + (uint32_t)S * 128u;
       float& l = l_s[S];
       float& m = m_s[S];
@@ -600,72 +549,25 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           tc_fence_after();
           uint32_t s0[32], s1[32];
           tmem_ld32(tS, s0);
+          tmem_ld32(tS + 32, s1);
           tmem_wait_ld();
-          tmem_ld32(tS + 32, s1);  // on its way while the first 32 are worked on
           float2 ps = make_float2(0.f, 0.f);
-          mask(s0, hi);
-          exps(s0, 0.f, ps, tS);
+          mask_from(s0, hi);
+          exps32(s0, p.scale_log2, 0.f, ps, tS);
           tmem_wait_ld();
-          mask(s1, hi - 32);
-          exps(s1, 0.f, ps, tS + 16);
+          mask_from(s1, hi - 32);
+          exps32(s1, p.scale_log2, 0.f, ps, tS + 16);
           l += ps.x + ps.y;
           tmem_wait_st();
           tc_fence_before();
         }
       } else {
-        // running maxima, the same for the row's two halves: they meet at every
-        // step, in columns of the scores that P leaves free
-        const uint32_t tX = tmem + lane_off + (uint32_t)S * 128u + 32u;
-        uint32_t s0[32], s1[32];
-        float own = -INFINITY;
-        tc_fence_after();
-        tmem_ld32(tS, s0);
-        tmem_ld32(tS + 32, s1);
-        tmem_wait_ld();
-        mask(s0, hi);
-        mask(s1, hi - 32);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) own = fmax3(own, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
-        tmem_st1(tX + (uint32_t)hf * 64u, __float_as_uint(own));
-        tmem_wait_st();
-        tc_fence_before();
-        if (!meet_pair()) return false;
-        tc_fence_after();
-        const float top = fmaxf(own, __uint_as_float(tmem_ld1(tX + (uint32_t)(1 - hf) * 64u))) * sl;
-        float alpha = 1.f;
-        if (first) {
-          m = top > -INFINITY ? top : 0.f;
-          l = 0.f;
-        } else if (top > m + kRescale) {
-          alpha = ex2(m - top);
-          m = top;
-        }
-        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // S is there, so the stream's products before it are done
-#pragma unroll 1
-          for (int cc = 0; cc < D / 2; cc += 16) {  // half of the columns each
-            uint32_t v[16];
-            const uint32_t tO = tmem + lane_off + C::kTmemO + (uint32_t)(S * D + hf * (D / 2) + cc);
-            tmem_ld16(tO, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-            tmem_st16(tO, v);
-          }
-        }
-        float2 ps = make_float2(0.f, 0.f);
-        exps(s0, m, ps, tS);
-        exps(s1, m, ps, tS + 16);
-        l = l * alpha + (ps.x + ps.y);
-        if (last) tmem_st1(tX + (uint32_t)hf * 64u + 1u, __float_as_uint(l));
-        tmem_wait_st();
-        tc_fence_before();
-        if (!meet_pair()) return false;  // both halves of O are rescaled, the maxima read
-        if (last) {                      // half 0 takes the sum, half 1 the maximum
-          tc_fence_after();
-          l = hf == 0 ? l + __uint_as_float(tmem_ld1(tX + 64u + 1u)) : m;
-          tc_fence_before();
-        }
+        const SlowSum x = slow_step(p, bar(C::kPairMeet + quad), abort_flag, pair_parity, tmem + lane_off + (uint32_t)S * 128u,
+                                    tmem + lane_off + C::kTmemO + (uint32_t)(S * D + hf * (D / 2)), D / 2, hf, hi,
+                                    first, last, m, l);
+        if (!x.ok) return false;
+        m = x.m;
+        l = x.l;
       }
       arrive_warp(C::kPFull + S);
       if (__builtin_expect(last, 0)) {
@@ -682,22 +584,25 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     const std::integral_constant<int, 1> one;
     do {
       const bool slow = SPLIT || number > 0;
-      Items c;
-      for (c.start(p, pass); ok && c.nt > 0; c.next(p, pass)) {
+      Walk<true> c;
+      c.start(p, pass);
+      c.seek(p, pass);
+      while (ok && c.more(pass)) {
+        const int nt = c.w.nt, streams = c.w.streams, keys = c.w.keys, live = c.w.live;
         if (PAIR) {
-          for (int j = 0; ok && j < c.nt; ++j) {
-            ok = step(zero, slow, c, j, j == 0, j + 1 == c.nt);
-            if (ok && c.streams == 2) ok = step(one, slow, c, j, j == 0, j + 1 == c.nt);
+          for (int j = 0; ok && j < nt; ++j) {
+            ok = step(zero, slow, keys, live, j, j == 0, j + 1 == nt);
+            if (ok && streams == 2) ok = step(one, slow, keys, live, j, j == 0, j + 1 == nt);
           }
         } else {
-          int j = 0;
-          if (steps_before & 1) ok = step(one, slow, c, j, true, j + 2 >= c.nt), ++j;
-          for (; ok && j < c.nt; ++j) {
-            ok = step(zero, slow, c, j, j < 2, j + 2 >= c.nt);
-            if (ok && ++j < c.nt) ok = step(one, slow, c, j, j < 2, j + 2 >= c.nt);
+          for (int j = -(steps_before & 1); ok && j < nt; j += 2) {
+            if (j >= 0) ok = step(zero, slow, keys, live, j, j < 2, j + 2 >= nt);
+            if (ok && j + 1 < nt) ok = step(one, slow, keys, live, j + 1, j < 1, j + 3 >= nt);
           }
-          steps_before += c.nt;
+          steps_before += nt;
         }
+        c.next(p, pass);
+        c.seek(p, pass);
       }
     } while (next_pass(number) && ok);
   } else {
@@ -708,16 +613,6 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     const float* sums = reinterpret_cast<const float*>(base + C::kSumOff);
     uint8_t* stage = base + C::kOOff;
     bool ok = pass.end > 0;
-    // zeros and -inf for a query tile without a query or without a key
-    auto clear = [&](const Work& w, int t0) {
-      const int t = t0 + row_t, head = w.hb * p.pack + row_g;
-      if (row_t < p.tile_tokens && t < p.Lq) {
-        uint16_t* o = p.O + w.b * p.o_batch + t * p.o_token + head * D;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.LSE != nullptr) p.LSE[((long long)w.b * p.H + head) * p.Lq + t] = -INFINITY;
-      }
-    };
     int used[2] = {0, 0}, tiles = 0;
     auto finish = [&](const Work& w, unsigned item, int st) -> bool {
       const int t = w.t0 + st * p.tile_tokens + row_t;
@@ -750,8 +645,9 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) x[c] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          if (!has[o]) continue;
+        for (int i = 0; i < (PAIR ? 1 : 2); ++i) {
+          const int o = PAIR ? st : i;
+          if (!PAIR && !has[i]) continue;
           uint32_t v[32];
           tmem_ld32(tO + (uint32_t)(o * D + cc), v);
           tmem_wait_ld();
@@ -759,10 +655,13 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
             tc_fence_before();
             arrive_warp(C::kORead + o);
           }
-          const float2 g = make_float2(f[o], f[o]);
+          const float w = o ? f[1] : f[0];
+          const float2 g = make_float2(w, w);
+          if (o ? on[1] : on[0]) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (on[o]) x[c] = __ffma2_rn(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), g, x[c]);
+            for (int c = 0; c < 16; ++c)
+              x[c] = __ffma2_rn(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), g, x[c]);
+          }
         }
       };
       if constexpr (!SPLIT) {
@@ -771,7 +670,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         if (tiles > 0 && !wait_warp(C::kOFree, (uint32_t)(tiles - 1) & 1u, 11)) return false;
         ++tiles;
         float2 sound = make_float2(0.f, 0.f);  // stays 0 unless some value is not finite
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
           float2 x[16];
           take(cc, f, x);
@@ -790,11 +689,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         }
         const bool again =
             number == 0 && live && !(sum >= kLeastSum && sum <= kMostSum && sound.x == 0.f && sound.y == 0.f);
-        if (again && atomicMax(&misc[4], (uint32_t)tiles) < (uint32_t)tiles) {  // the tile's first such row
-          const uint32_t n = atomicAdd(&misc[2], 1u);
-          if (n < kRedoList) list[n] = tile_of(p, item, st, pass.pair);
-          else atomicMin(&misc[3], item);
-        }
+        if (__builtin_expect(again, 0)) again_later(p, misc, list, (unsigned)tiles, item, st, pass.pair);
         fence_proxy_async_smem();
         arrive_warp(C::kOReady);
         if (stored && p.LSE != nullptr) p.LSE[lse_at] = any_own ? (top_own + __log2f(sum)) * kLn2 : -INFINITY;
@@ -825,7 +720,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         const bool any = top > -INFINITY;
         const float f[2] = {on[0] ? ex2(m[0] - top) / total : 0.f, on[1] ? ex2(m[1] - top) / total : 0.f};
         const int per = D / p.splits;  // columns of a block's sum
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
           float2 x[16];
           take(cc, f, x);
@@ -858,17 +753,17 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      for (unsigned at = pass.first; ok && at < pass.end; at += pass.step) {
-        const unsigned item = pass.list != nullptr ? (unsigned)uniform<true>((int)pass.list[at]) : at;
-        const Work w = work_at<true>(p, item, split, pass.pair);
+      Walk<true> c;
+      for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
+        const Work& w = c.w;
         if (!SPLIT) {
-          if (w.nt == 0) clear(w, w.t0);
+          if (w.nt == 0) clear_tile(p, w.b, w.hb, w.t0, row);
           if (pass.pair == 2 && (w.nt == 0 || w.streams == 1) && w.t0 + p.tile_tokens < p.Lq)
-            clear(w, w.t0 + p.tile_tokens);
+            clear_tile(p, w.b, w.hb, w.t0 + p.tile_tokens, row);
           if (w.nt == 0) continue;
         }
 #pragma unroll 1
-        for (int st = 0; ok && st < w.streams; ++st) ok = finish(w, item, st);
+        for (int st = 0; ok && st < w.streams; ++st) ok = finish(w, c.item(pass), st);
         steps_before += w.nt;
       }
     } while (next_pass(number) && ok);

@@ -1,0 +1,873 @@
+// Gradients of cross attention for sm_103a.  With P recomputed from the
+// forward's LSE and delta_i = sum_d dO_id O_id:
+//   dV = P^T dO,  dP = dO V^T,  dS = P * (dP - delta),
+//   dQ = scale * dS K,  dK = scale * dS^T Q.
+// Two kernels.  cross_dq_kernel walks query tiles (persistent, as the forward:
+// a query tile meets few key tiles) and works out delta on the way;
+// cross_dkv_kernel keeps a key tile and streams all queries that read it: of
+// every head of its group and, where the states are shared, of every sequence,
+// so that these sums are formed in the accumulators.  Key tiles are few, so the
+// queries of one are cut among several blocks, whose parts cross_sum_kernel adds
+// in order: no atomics, equal calls give equal bits.  S and dP are formed in both
+// kernels (14 D products a pair for the 10 D of one), which costs less than
+// sending dQ's parts, one for each key tile, through memory.
+#include <math.h>
+
+#include "cross_common.cuh"
+
+namespace sab {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------- dQ, delta
+
+template <int D_>
+struct DqCfg {
+  static constexpr int D = D_;
+  static constexpr int kBoxes = D / 64;
+  static constexpr uint32_t kBoxBytes = 128u * 128u;
+  static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
+  static constexpr int kSlots = D == 128 ? 4 : 8;  // K and V tiles in turn
+  static constexpr uint32_t kQOff = 0, kGOff = kTileBytes, kOOff = 2 * kTileBytes;  // Q, dO, O of an item
+  static constexpr uint32_t kRingOff = 3 * kTileBytes;
+  static constexpr uint32_t kStatOff = kRingOff + kSlots * kTileBytes;  // [128] {-LSE log2 e, -delta}
+  static constexpr uint32_t kBarOff = kStatOff + 1024;
+  static constexpr int kQFull = 0;
+  static constexpr int kQFree = 1;                 // scores done (2 warps), delta done (4 warps)
+  static constexpr int kFull = 2;                  // [kSlots]
+  static constexpr int kEmpty = kFull + kSlots;    // [kSlots]
+  static constexpr int kSFull = kEmpty + kSlots;   // [2 halves]
+  static constexpr int kPFull = kSFull + 2;        // [2]
+  static constexpr int kDone = kPFull + 2;         // [2] an item's last product
+  static constexpr int kRead = kDone + 2;          // [2] dQ is taken out
+  static constexpr int kStat = kRead + 2;          // LSE and delta are there
+  static constexpr int kSeen = kStat + 1;          // all warps for dS have them
+  static constexpr int kDrain = kSeen + 1;         // [2]
+  static constexpr int kNumBars = kDrain + 2;
+  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = kMiscOff + 16;
+  // loads; products of keys [0, 64) and [64, 128); a spare; 8 warps for dS; 4
+  // for delta and dQ
+  static constexpr int kThreads = 32 * 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+// S and dP of a key tile (128 columns each) and dQ do not fit in TMEM twice, so
+// the two halves of every key tile are the streams that take turns on the tensor
+// cores: each with its scores, its dP (dS goes over the scores), its part of dQ
+// and a warp that issues its products, in the order S, dP, dQ, S, dP ...
+template <int D>
+__global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const __grid_constant__ CrossBwdParams p) {
+  using C = DqCfg<D>;
+  extern __shared__ __align__(1024) uint8_t base[];
+  const uint32_t base_u32 = smem_u32(base);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + C::kMiscOff);  // [0] tmem, [1] abort
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kMiscOff + 4);
+  auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
+  auto wait = [&](int i, uint32_t parity, unsigned site) -> bool {
+    return wait_bounded(bar(i), parity, abort_flag, site, p.err_word);
+  };
+  auto wait_warp = [&](int i, uint32_t parity, unsigned site) -> bool {
+    return __all_sync(0xffffffffu, wait(i, parity, site));
+  };
+  const int warp = uniform<true>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  auto arrive_warp = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(i));
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::kQFull), 1);
+    mbar_init(bar(C::kQFree), 6);
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(bar(C::kFull + s), 1);
+      mbar_init(bar(C::kEmpty + s), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kSFull + i), 1);
+      mbar_init(bar(C::kPFull + i), 4);
+      mbar_init(bar(C::kDone + i), 1);
+      mbar_init(bar(C::kRead + i), 4);
+      mbar_init(bar(C::kDrain + i), 1);
+    }
+    mbar_init(bar(C::kStat), 4);
+    mbar_init(bar(C::kSeen), 8);
+    misc[1] = (base_u32 & 1023u) != 0;  // the tiles' swizzle counts on it
+    if (misc[1] != 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(base_u32 + C::kMiscOff, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform<true>((int)misc[0]);
+  griddep_launch_dependents();
+  griddep_wait();
+
+  Pass pass;
+  pass.first = blockIdx.x;
+  pass.step = gridDim.x;
+  pass.end = uniform<true>(*abort_flag) ? 0u : p.items;
+  pass.list = nullptr;
+  pass.pair = 1;
+  pass.split = 0;
+  pass.by = spot_of(p, gridDim.x, 1);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(3 * C::kBoxes * p.pack * p.tile_tokens) * 128u;
+      Ring<C::kSlots> r;
+      int loads = 0, asked = 0;
+      auto load = [&](const CUtensorMap* m, int row, int head, int b) -> bool {
+        if (loads >= C::kSlots && !wait(C::kEmpty + r.slot, r.parity ^ 1u, 0)) return false;
+        const uint32_t full = bar(C::kFull + r.slot);
+        mbar_arrive_expect_tx(full, C::kTileBytes);
+#pragma unroll
+        for (int bx = 0; bx < C::kBoxes; ++bx)
+          tma_load_4d(base_u32 + C::kRingOff + r.slot * C::kTileBytes + bx * C::kBoxBytes, m, full, bx * 64, row, head,
+                      b);
+        r.next();
+        ++loads;
+        return true;
+      };
+      bool ok = true;
+      Walk<false> c;
+      for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
+        const Work& w = c.w;
+        if (w.nt == 0) continue;
+        const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
+        for (int j = 0; ok && j < w.nt; ++j) {
+          if (!(ok = load(&p.k_map, j * kTileN, head, kb))) break;
+          if (j == 0) {
+            if (asked > 0 && !(ok = wait(C::kQFree, (uint32_t)(asked - 1) & 1u, 1))) break;
+            ++asked;
+            mbar_arrive_expect_tx(bar(C::kQFull), q_bytes);
+            const int c1 = query_c1(p, w, 0), c2 = query_c2(p, w, 0);
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx) {
+              const uint32_t to = base_u32 + bx * C::kBoxBytes;
+              tma_load_4d(to + C::kQOff, &p.q_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
+              tma_load_4d(to + C::kGOff, &p.do_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
+              tma_load_4d(to + C::kOOff, &p.o_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
+            }
+          }
+          ok = load(&p.v_map, j * kTileN, head, kb);
+        }
+      }
+      if (*abort_flag) {  // nothing of this block's copies may land after it
+        for (int k = max(0, loads - C::kSlots); k < loads; ++k)
+          wait_drain(bar(C::kFull + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
+        if (asked > 0) wait_drain(bar(C::kQFull), (uint32_t)(asked - 1) & 1u, p.err_word);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 3) {
+    // ------------------------------------------------------------- products
+    const int h = warp - 1;  // keys [64 h, 64 h + 64) of every tile
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, 0);
+    constexpr uint32_t idesc_q = idesc_bf16_f32(128, D, 1);
+    constexpr uint32_t kStep = C::kTileBytes >> 4;
+    constexpr uint32_t kHalf = (64u * 128u) >> 4;  // 64 rows on
+    const uint64_t dq = smem_desc_sw128(base_u32 + C::kQOff, 16, 1024);
+    const uint64_t dg = smem_desc_sw128(base_u32 + C::kGOff, 16, 1024);
+    const uint64_t dk = smem_desc_sw128(base_u32 + C::kRingOff, 16, 1024);
+    const uint64_t dm = smem_desc_sw128(base_u32 + C::kRingOff, C::kBoxBytes, 1024);  // as the MN-major operand
+    const uint32_t hi_k = (uint32_t)(dq >> 32), hi_mn = (uint32_t)(dm >> 32);
+    const uint32_t tS = tmem + (uint32_t)h * 128u, tQ = tmem + 256u + (uint32_t)h * D;
+    const uint32_t lead = elect_lead();
+    Ring<C::kSlots> r;
+    uint32_t q_parity = 0, p_parity = 0;
+    int used = 0;
+    bool ok = true;
+    auto scores = [&](uint32_t to, uint32_t a_lo, uint32_t b_lo) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+        mma_ss_l(lead, to, make_desc(a_lo + off, hi_k), make_desc(b_lo + off, hi_k), idesc_s, kk > 0 ? 1u : 0u);
+      }
+    };
+    Walk<true> c;
+    c.start(p, pass);
+    c.seek(p, pass);
+    while (ok && c.more(pass)) {
+      const int nt = c.w.nt, keys = c.w.keys;
+      if (!(ok = wait_warp(C::kQFull, q_parity, 2))) break;
+      q_parity ^= 1u;
+      bool begun = false;
+      for (int j = 0; ok && j < nt; ++j) {
+        const int live = keys - j * kTileN - 64 * h;  // keys of this half
+        Ring<C::kSlots> v = r;
+        v.next();
+        if (!(ok = wait_warp(C::kFull + r.slot, r.parity, 3) && wait_warp(C::kFull + v.slot, v.parity, 3))) break;
+        if (live > 0) {
+          tc_fence_after();
+          const uint32_t k0 = (uint32_t)dk + r.slot * kStep + h * kHalf, v0 = (uint32_t)dk + v.slot * kStep + h * kHalf;
+          scores(tS, (uint32_t)dq, k0);        // S = Q K^T
+          scores(tS + 64u, (uint32_t)dg, v0);  // dP = dO V^T
+          mma_commit_l(lead, bar(C::kSFull + h));
+          mma_commit_l(lead, bar(C::kEmpty + v.slot));
+          if (j + 1 == nt) mma_commit_l(lead, bar(C::kQFree));
+          const int steps = min(4, (live + 15) >> 4);  // 16 keys each
+          // keys past the sequence's end may hold anything, and 0 * NaN is NaN
+          if (__builtin_expect(steps * 16 > live, 0))
+            zero_rows<C::kBoxes>(base + C::kRingOff + r.slot * C::kTileBytes, 64 * h + live, 64 * h + steps * 16);
+          // the item before has its dQ taken out before this one's goes over it
+          if (__builtin_expect(!begun && used > 0, 0) &&
+              !(ok = wait_warp(C::kRead + h, (uint32_t)(used - 1) & 1u, 4)))
+            break;
+          if (!(ok = wait_warp(C::kPFull + h, p_parity, 5))) break;
+          p_parity ^= 1u;
+          tc_fence_after();
+          const uint32_t m0 = (uint32_t)dm + r.slot * kStep + h * kHalf;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // dQ += dS K
+            if (kk < steps)
+              mma_ts_l(lead, tQ, tS + kk * 8, make_desc(m0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_q,
+                       kk > 0 || begun ? 1u : 0u);
+          begun = true;
+          mma_commit_l(lead, bar(C::kEmpty + r.slot));
+        } else {  // the tile ends before this half
+          arrive_warp(C::kEmpty + r.slot);
+          arrive_warp(C::kEmpty + v.slot);
+          if (j + 1 == nt) arrive_warp(C::kQFree);
+        }
+        r.next();
+        r.next();
+      }
+      if (!ok) break;
+      if (begun) {
+        mma_commit_l(lead, bar(C::kDone + h));
+        ++used;
+      }
+      c.next(p, pass);
+      c.seek(p, pass);
+    }
+    if (!ok) {
+      mma_commit_l(lead, bar(C::kDrain + h));
+      if (lane == 0) wait_drain(bar(C::kDrain + h), 0, p.err_word);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------------- dS
+    const int hf = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)hf * 128u;
+    const float2* stat = reinterpret_cast<const float2*>(base + C::kStatOff);
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t s_parity = 0;
+    int item = 0;
+    bool ok = true;
+    Walk<true> c;
+    c.start(p, pass);
+    c.seek(p, pass);
+    while (ok && c.more(pass)) {
+      const int nt = c.w.nt, keys = c.w.keys;
+      if (!(ok = wait_warp(C::kStat, (uint32_t)item & 1u, 6))) break;
+      const float2 st = stat[row];
+      arrive_warp(C::kSeen);
+      const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
+      for (int j = 0; ok && j < nt; ++j) {
+        const int hi = keys - j * kTileN - hf * 64;
+        if (hi <= 0) break;  // only an item's last tile ends before a half
+        if (!(ok = wait_warp(C::kSFull + hf, s_parity, 7))) break;
+        s_parity ^= 1u;
+        tc_fence_after();
+#pragma unroll
+        for (int ps = 0; ps < 2; ++ps) {  // 32 columns at a time; dS goes over scores already read
+          uint32_t s[32], g[32], o[16];
+          tmem_ld32(tS + 32 * ps, s);
+          tmem_ld32(tS + 64 + 32 * ps, g);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2, nl);
+            const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+            const float2 ds =
+                __fmul2_rn(pr, __fadd2_rn(make_float2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1])), nd));
+            o[k] = pack_bf16(ds.x, ds.y);
+          }
+          if (__builtin_expect(hi < 64, 0)) {  // keys past the end
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int col = 32 * ps + 2 * k;
+              o[k] = col + 1 < hi ? o[k] : col < hi ? o[k] & 0xFFFFu : 0u;
+            }
+          }
+          tmem_st16(tS + 16 * ps, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(C::kPFull + hf);
+      }
+      ++item;
+      c.next(p, pass);
+      c.seek(p, pass);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ delta, dQ
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t tQ = tmem + ((uint32_t)(quad * 32) << 16) + 256u;
+    const int row_t = row / p.pack, row_g = row - row_t * p.pack;
+    float2* stat = reinterpret_cast<float2*>(base + C::kStatOff);
+    uint32_t q_parity = 0;
+    int item = 0, used[2] = {0, 0};
+    bool ok = true;
+    Walk<true> c;
+    for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
+      const Work& w = c.w;
+      const int t = w.t0 + row_t, head = w.hb * p.pack + row_g;
+      const bool stored = row_t < p.tile_tokens && t < p.Lq, live = row_t < w.live && row_t < p.tile_tokens;
+      uint4* out = reinterpret_cast<uint4*>(p.dQ + w.b * p.dq_batch + t * p.dq_token + head * D);
+      if (w.nt == 0) {  // no query or no key
+        if (stored)
+#pragma unroll 1
+          for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const long long at = ((long long)w.b * p.H + head) * p.Lq + t;
+      const float lse = live ? __ldg(p.LSE + at) : INFINITY;
+      if (!(ok = wait_warp(C::kQFull, q_parity, 8))) break;
+      q_parity ^= 1u;
+      float2 acc = make_float2(0.f, 0.f);
+      const uint8_t* mine = base + row * 128;
+#pragma unroll 4
+      for (int k = 0; k < D / 8; ++k) {
+        const uint32_t off = (k >> 3) * C::kBoxBytes + (((k & 7) ^ (row & 7)) << 4);
+        const uint4 a = *reinterpret_cast<const uint4*>(mine + C::kOOff + off);
+        const uint4 b = *reinterpret_cast<const uint4*>(mine + C::kGOff + off);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc = __ffma2_rn(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u)),
+                           make_float2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xFFFF0000u)), acc);
+      }
+      const float delta = acc.x + acc.y;
+      // the item before has been seen by every warp, also by those that had no step in it
+      if (item > 0 && !(ok = wait_warp(C::kSeen, (uint32_t)(item - 1) & 1u, 10))) break;
+      stat[row] = make_float2(live ? -lse * kLog2e : -INFINITY, live ? -delta : 0.f);
+      if (live) p.delta[at] = delta;
+      arrive_warp(C::kStat);
+      arrive_warp(C::kQFree);
+      // dQ: the halves' parts
+      const bool two = w.keys > 64;
+      if (!(ok = wait_warp(C::kDone, (uint32_t)used[0] & 1u, 9))) break;
+      ++used[0];
+      if (two) {
+        if (!(ok = wait_warp(C::kDone + 1, (uint32_t)used[1] & 1u, 9))) break;
+        ++used[1];
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t a[32], b[32];
+        tmem_ld32(tQ + cc, a);
+        if (two) tmem_ld32(tQ + D + cc, b);
+        tmem_wait_ld();
+        if (cc + 32 == D) {
+          tc_fence_before();
+          arrive_warp(C::kRead);
+          if (two) arrive_warp(C::kRead + 1);
+        }
+        if (stored) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 8 * i + 2 * k;
+              float2 x = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+              if (two) x = __fadd2_rn(x, make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])));
+              x = __fmul2_rn(x, make_float2(p.scale, p.scale));
+              o[k] = live ? pack_bf16(x.x, x.y) : 0u;
+            }
+            out[cc / 8 + i] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        __syncwarp();
+      }
+      ++item;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------- dK, dV
+
+template <int D_>
+struct DkvCfg {
+  static constexpr int D = D_;
+  static constexpr int kBoxes = D / 64;
+  static constexpr uint32_t kBoxBytes = 128u * 128u;
+  static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kKOff = 0, kVOff = kTileBytes;  // resident
+  static constexpr uint32_t kStageOff = 2 * kTileBytes;
+  // a stage: Q, dO, then 128 of -LSE log2 e and 128 of -delta
+  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 1024;
+  static constexpr uint32_t kBarOff = kStageOff + kStages * kStageBytes;
+  static constexpr int kRes = 0;
+  static constexpr int kFull = 1;                       // [kStages][2 halves]
+  static constexpr int kEmpty = kFull + 2 * kStages;    // [kStages][2]
+  static constexpr int kSFull = kEmpty + 2 * kStages;   // [2 halves]
+  static constexpr int kPFull = kSFull + 2;             // [2]
+  static constexpr int kTaken = kPFull + 2;             // [2] P and dS are read
+  static constexpr int kDone = kTaken + 2;
+  static constexpr int kDrain = kDone + 1;              // [2]
+  static constexpr int kNumBars = kDrain + 2;
+  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = kMiscOff + 16;
+  // loads; scores; accumulations; a spare; 8 warps for P and dS, and the end
+  static constexpr int kThreads = 32 * 12;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+// The query tiles of a block, in two halves of h_tokens tokens x h_pack heads
+// (at most 64 rows): of the block's share of the sequences, head blocks and
+// tiles that read its keys.
+struct Stream {
+  int i, end;      // tiles
+  int iq, hb, b;   // this one's place: tile, head block of the group, sequence
+  int live;        // its tokens inside q_len
+};
+
+template <int D>
+__global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const __grid_constant__ CrossBwdParams p) {
+  using C = DkvCfg<D>;
+  extern __shared__ __align__(1024) uint8_t base[];
+  const uint32_t base_u32 = smem_u32(base);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(base + C::kMiscOff);  // [0] tmem, [1] abort
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kMiscOff + 4);
+  auto bar = [&](int i) -> uint32_t { return base_u32 + C::kBarOff + 8u * (uint32_t)i; };
+  auto wait_warp = [&](int i, uint32_t parity, unsigned site) -> bool {
+    return __all_sync(0xffffffffu, wait_bounded(bar(i), parity, abort_flag, site, p.err_word));
+  };
+  const int warp = uniform<true>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  auto arrive_warp = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(i));
+  };
+  // key tile, key head, sequence of keys, and share of the queries
+  const int key_tiles = (p.Lk + kTileN - 1) / kTileN;
+  unsigned u = blockIdx.x;
+  const int k0 = (int)(u % (unsigned)key_tiles) * kTileN;
+  u /= (unsigned)key_tiles;
+  const int hk = (int)(u % (unsigned)p.Hk);
+  u /= (unsigned)p.Hk;
+  const int kb = (int)(u % (unsigned)p.Bk), share = (int)(u / (unsigned)p.Bk);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::kRes), 1);
+    for (int i = 0; i < 2 * C::kStages; ++i) {
+      mbar_init(bar(C::kFull + i), 2);  // copies, LSE and delta
+      mbar_init(bar(C::kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kSFull + i), 1);
+      mbar_init(bar(C::kPFull + i), 4);
+      mbar_init(bar(C::kTaken + i), 1);
+      mbar_init(bar(C::kDrain + i), 1);
+    }
+    mbar_init(bar(C::kDone), 1);
+    misc[1] = (base_u32 & 1023u) != 0;
+    if (misc[1] != 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
+    fence_mbar_init();
+  }
+  // rows of a half that no copy fills (3 heads x 21 tokens leave one) are zeros
+  if (p.h_pack * p.h_tokens < 64) {
+    const int first = p.h_pack * p.h_tokens, n = (64 - first) * 8;
+    for (int i = threadIdx.x; i < C::kStages * 2 * C::kBoxes * 2 * n; i += blockDim.x) {
+      const int blk = i / n, k = i - blk * n;  // box, half
+      const int st = blk / (4 * C::kBoxes), rest = blk - st * 4 * C::kBoxes;
+      uint8_t* to = base + C::kStageOff + st * C::kStageBytes + (rest >> 1) * C::kBoxBytes + (rest & 1) * (C::kBoxBytes / 2);
+      *reinterpret_cast<uint4*>(to + (first + (k >> 3)) * 128 + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc(base_u32 + C::kMiscOff, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform<true>((int)misc[0]);
+  griddep_launch_dependents();
+  griddep_wait();
+  const int keys = length_of<true>(p.kv_len, kb, p.Lk) - k0;  // of this tile, from 128 on whole
+  const bool dead = keys <= 0 || uniform<true>(*abort_flag) != 0;
+
+  const int blocks = p.group / p.h_pack, seqs = p.Bk == 1 ? p.B : 1;
+  const long long all = (long long)seqs * blocks * p.h_qtiles;
+  Stream first;
+  first.i = (int)(all * share / p.shares);
+  first.end = dead ? first.i : (int)(all * (share + 1) / p.shares);
+  {
+    const int r = first.i / p.h_qtiles;
+    first.iq = first.i - r * p.h_qtiles;
+    first.b = (p.Bk == 1 ? 0 : kb) + r / blocks;
+    first.hb = r % blocks;
+  }
+  // the next tile with a live query, from this one on
+  auto seek = [&](Stream& s) {
+    for (; s.i < s.end; ++s.i) {
+      s.live = min(2 * p.h_tokens, length_of<true>(p.q_len, s.b, p.Lq) - s.iq * 2 * p.h_tokens);
+      if (s.live > 0) return;
+      if (++s.iq == p.h_qtiles) {
+        s.iq = 0;
+        if (++s.hb == blocks) s.hb = 0, ++s.b;
+      }
+    }
+  };
+  auto next = [&](Stream& s) {
+    ++s.i;
+    if (++s.iq == p.h_qtiles) {
+      s.iq = 0;
+      if (++s.hb == blocks) s.hb = 0, ++s.b;
+    }
+    seek(s);
+  };
+  // rows of half h that hold live queries
+  auto rows_of = [&](const Stream& s, int h) { return min(max(s.live - h * p.h_tokens, 0), p.h_tokens) * p.h_pack; };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    const bool any = first.i < first.end;
+    if (lane == 0 && any) {
+      mbar_arrive_expect_tx(bar(C::kRes), 2 * C::kTileBytes);
+#pragma unroll
+      for (int bx = 0; bx < C::kBoxes; ++bx) {
+        tma_load_4d(base_u32 + C::kKOff + bx * C::kBoxBytes, &p.k_map, bar(C::kRes), bx * 64, k0, hk, kb);
+        tma_load_4d(base_u32 + C::kVOff + bx * C::kBoxBytes, &p.v_map, bar(C::kRes), bx * 64, k0, hk, kb);
+      }
+    }
+    const uint32_t half_bytes = (uint32_t)(2 * C::kBoxes * p.h_pack * p.h_tokens) * 128u;
+    // two rows of each half a lane: place within the tile's heads and tokens
+    int tok[2], hd[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane + 32 * i;
+      tok[i] = r / p.h_pack;
+      hd[i] = r - tok[i] * p.h_pack;
+    }
+    Stream s = first;
+    seek(s);
+    float ls[4], dl[4];  // of the tile to be loaded next, requested one tile ahead
+    auto fetch = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = i >> 1, r = lane + 32 * (i & 1);
+        const bool in = r < rows_of(s, h);
+        const int t = s.iq * 2 * p.h_tokens + h * p.h_tokens + tok[i & 1];
+        const int head = hk * p.group + s.hb * p.h_pack + hd[i & 1];
+        const long long at = ((long long)s.b * p.H + head) * p.Lq + t;
+        ls[i] = in ? -__ldg(p.LSE + at) * kLog2e : -INFINITY;
+        dl[i] = in ? -__ldg(p.delta + at) : 0.f;
+      }
+    };
+    if (s.i < s.end) fetch();
+    int n = 0, halves = 0;
+    bool ok = true;
+    while (ok && s.i < s.end) {
+      const int st = n % C::kStages;
+      const uint32_t so = C::kStageOff + st * C::kStageBytes;
+      const int head = hk * p.group + s.hb * p.h_pack, t0 = s.iq * 2 * p.h_tokens;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (n >= C::kStages &&
+            !(ok = wait_warp(C::kEmpty + 2 * st + h, (uint32_t)(n / C::kStages - 1) & 1u, 0)))
+          break;
+        const uint32_t full = bar(C::kFull + 2 * st + h);
+        if (lane == 0) {
+          const int t = t0 + h * p.h_tokens;
+          const int c1 = p.h_pack == 1 ? t : head, c2 = p.h_pack == 1 ? head : t;
+          mbar_arrive_expect_tx(full, half_bytes);
+#pragma unroll
+          for (int bx = 0; bx < C::kBoxes; ++bx) {
+            const uint32_t to = base_u32 + so + bx * C::kBoxBytes + h * (C::kBoxBytes / 2);
+            tma_load_4d(to, &p.q_map_h, full, bx * 64, c1, c2, s.b);
+            tma_load_4d(to + C::kTileBytes, &p.do_map_h, full, bx * 64, c1, c2, s.b);
+          }
+        }
+        float* stat = reinterpret_cast<float*>(base + so + 2 * C::kTileBytes) + 64 * h;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          stat[lane + 32 * i] = ls[2 * h + i];
+          stat[128 + lane + 32 * i] = dl[2 * h + i];
+        }
+        arrive_warp(C::kFull + 2 * st + h);
+        ++halves;
+      }
+      if (!ok) break;
+      ++n;
+      next(s);
+      if (s.i < s.end) fetch();
+    }
+    if (lane == 0 && *abort_flag) {
+      if (any) wait_drain(bar(C::kRes), 0, p.err_word);
+      for (int k = max(0, halves - 2 * C::kStages); k < halves; ++k)
+        wait_drain(bar(C::kFull + 2 * ((k >> 1) % C::kStages) + (k & 1)), (uint32_t)((k >> 1) / C::kStages) & 1u,
+                   p.err_word);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------- S^T = K Q^T, dP^T = V dO^T
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, 0);
+    constexpr uint32_t kStep = C::kStageBytes >> 4;
+    constexpr uint32_t kHalf = (64u * 128u) >> 4;
+    const uint64_t dk = smem_desc_sw128(base_u32 + C::kKOff, 16, 1024);
+    const uint64_t dv = smem_desc_sw128(base_u32 + C::kVOff, 16, 1024);
+    const uint64_t ds = smem_desc_sw128(base_u32 + C::kStageOff, 16, 1024);
+    const uint32_t hi_k = (uint32_t)(dk >> 32);
+    const uint32_t lead = elect_lead();
+    auto scores = [&](uint32_t to, uint32_t a_lo, uint32_t b_lo) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+        mma_ss_l(lead, to, make_desc(a_lo + off, hi_k), make_desc(b_lo + off, hi_k), idesc_s, kk > 0 ? 1u : 0u);
+      }
+    };
+    Stream s = first;
+    seek(s);
+    bool ok = first.i >= first.end || wait_warp(C::kRes, 0, 1);  // also where no query turns out live
+    for (int n = 0; ok && s.i < s.end; ++n, next(s)) {
+      const int st = n % C::kStages;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = wait_warp(C::kFull + 2 * st + h, (uint32_t)(n / C::kStages) & 1u, 2))) break;
+        const int rows = rows_of(s, h);
+        if (__builtin_expect(p.q_len != nullptr && rows < p.h_pack * p.h_tokens, 0)) {
+          // queries past the sequence's end may hold anything, and 0 * NaN is NaN
+          uint8_t* q = base + C::kStageOff + st * C::kStageBytes + h * (C::kBoxBytes / 2);
+          zero_rows<C::kBoxes>(q, rows, 64);
+          zero_rows<C::kBoxes>(q + C::kTileBytes, rows, 64);
+        }
+        if (n > 0 && !(ok = wait_warp(C::kTaken + h, (uint32_t)(n - 1) & 1u, 3))) break;
+        tc_fence_after();
+        const uint32_t q0 = (uint32_t)ds + st * kStep + h * kHalf;
+        scores(tmem + 128u * h, (uint32_t)dk, q0);
+        scores(tmem + 128u * h + 64u, (uint32_t)dv, q0 + (C::kTileBytes >> 4));
+        mma_commit_l(lead, bar(C::kSFull + h));
+      }
+    }
+    if (!ok) {
+      mma_commit_l(lead, bar(C::kDrain));
+      if (lane == 0) wait_drain(bar(C::kDrain), 0, p.err_word);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // --------------------------------------- dV += P^T dO, dK += dS^T Q
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1);
+    constexpr uint32_t kStep = C::kStageBytes >> 4;
+    const uint64_t dm = smem_desc_sw128(base_u32 + C::kStageOff, C::kBoxBytes, 1024);
+    const uint32_t hi_mn = (uint32_t)(dm >> 32);
+    const uint32_t lead = elect_lead();
+    Stream s = first;
+    seek(s);
+    bool ok = true, any = false;
+    for (int n = 0; ok && s.i < s.end; ++n, next(s)) {
+      const int st = n % C::kStages;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = wait_warp(C::kPFull + h, (uint32_t)n & 1u, 4))) break;
+        tc_fence_after();
+        const uint32_t q0 = (uint32_t)dm + st * kStep + ((uint32_t)(h * 64 * 128) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_l(lead, tmem + 256, tmem + 128u * h + kk * 8,
+                   make_desc(q0 + ((C::kTileBytes + kk * 16 * 128) >> 4), hi_mn), idesc_acc,
+                   n + h + kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_l(lead, tmem + 256 + D, tmem + 128u * h + 64u + kk * 8,
+                   make_desc(q0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_acc, n + h + kk > 0 ? 1u : 0u);
+        mma_commit_l(lead, bar(C::kTaken + h));
+        mma_commit_l(lead, bar(C::kEmpty + 2 * st + h));
+        any = true;
+      }
+    }
+    if (ok && any) mma_commit_l(lead, bar(C::kDone));
+    if (!ok) {
+      mma_commit_l(lead, bar(C::kDrain + 1));
+      if (lane == 0) wait_drain(bar(C::kDrain + 1), 0, p.err_word);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------- P^T, dS^T; the end
+    const int hf = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + (uint32_t)hf * 128u, tG = tS + 64;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    Stream s = first;
+    seek(s);
+    bool ok = true;
+    int n = 0;
+    for (; s.i < s.end; ++n, next(s)) {
+      if (!(ok = wait_warp(C::kSFull + hf, (uint32_t)n & 1u, 5))) break;
+      tc_fence_after();
+      const float* ls = reinterpret_cast<const float*>(base + C::kStageOff + (n % C::kStages) * C::kStageBytes +
+                                                       2 * C::kTileBytes) + hf * 64;
+#pragma unroll
+      for (int ps = 0; ps < 2; ++ps) {  // 32 queries at a time; results go over columns already read
+        uint32_t sv[32], gv[32], po[16], so[16];
+        tmem_ld32(tS + 32 * ps, sv);
+        tmem_ld32(tG + 32 * ps, gv);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 nl = *reinterpret_cast<const float4*>(ls + 32 * ps + 4 * c4);
+          const float4 nd = *reinterpret_cast<const float4*>(ls + 128 + 32 * ps + 4 * c4);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * c4 + e;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), sc2,
+                                        e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
+            const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+            const float2 g = __fadd2_rn(make_float2(__uint_as_float(gv[2 * k]), __uint_as_float(gv[2 * k + 1])),
+                                        e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
+            const float2 d = __fmul2_rn(pr, g);
+            po[k] = pack_bf16(pr.x, pr.y);
+            so[k] = pack_bf16(d.x, d.y);
+          }
+        }
+        tmem_st16(tS + 16 * ps, po);
+        tmem_st16(tG + 16 * ps, so);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      arrive_warp(C::kPFull + hf);
+    }
+    if (ok && n > 0) ok = wait_warp(C::kDone, 0, 6);
+    ok = ok && !uniform<true>(*abort_flag);
+    const int key = k0 + row;
+    if (ok && key - row < p.Lk) {  // half 0 has dV, half 1 dK
+      tc_fence_after();
+      const bool live = row < keys && n > 0;
+      const float mul = hf == 0 ? 1.f : p.scale;
+      const uint32_t from = tmem + lane_off + 256u + (uint32_t)hf * D;
+      // one share: the gradients; several: this share's part
+      uint16_t* out = hf == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * D
+                              : p.dK + kb * p.dk_batch + key * p.dk_token + hk * D;
+      float* part = p.part + ((long long)blockIdx.x * 2 + hf) * (kTileN * D) + (long long)row * 4;
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t v[32];
+        if (n > 0) {
+          tmem_ld32(from + cc, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = live ? __float_as_uint(__uint_as_float(v[k]) * mul) : 0u;
+        if (p.shares == 1) {
+          if (key < p.Lk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(out + cc)[i] = make_uint4(
+                  pack_bf16(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
+                  pack_bf16(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
+                  pack_bf16(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
+                  pack_bf16(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+        } else {  // [D / 4][128 keys] of four columns: a warp's rows are 512 contiguous bytes
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(part + (long long)(cc / 4 + i) * (kTileN * 4)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The shares' parts of a key tile's dV (even blocks) or dK, added in their order.
+template <int D>
+__global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ CrossBwdParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int key_tiles = (p.Lk + kTileN - 1) / kTileN;
+  const unsigned units = (unsigned)key_tiles * (unsigned)p.Hk * (unsigned)p.Bk;
+  constexpr unsigned kPieces = D / 4 * kTileN / 256;  // 256 places of four columns a block
+  const unsigned blk = blockIdx.x / kPieces, piece = blockIdx.x % kPieces;
+  const unsigned unit = blk >> 1;
+  const int which = (int)(blk & 1u);
+  unsigned u = unit;
+  const int k0 = (int)(u % (unsigned)key_tiles) * kTileN;
+  u /= (unsigned)key_tiles;
+  const int hk = (int)(u % (unsigned)p.Hk), kb = (int)(u / (unsigned)p.Hk);
+  const int at = (int)piece * 256 + (int)threadIdx.x, row = at & (kTileN - 1), c4 = at / kTileN;
+  const int key = k0 + row;
+  if (key >= p.Lk) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (key < length_of<false>(p.kv_len, kb, p.Lk)) {
+    const float4* from = reinterpret_cast<const float4*>(p.part) + ((long long)unit * 2 + which) * (kTileN * D / 4) + at;
+#pragma unroll 4
+    for (int s = 0; s < p.shares; ++s) {
+      const float4 x = __ldcg(from + (long long)s * units * 2 * (kTileN * D / 4));
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+  }
+  uint16_t* out = which == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * D
+                             : p.dK + kb * p.dk_batch + key * p.dk_token + hk * D;
+  *reinterpret_cast<uint2*>(out + 4 * c4) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+}
+
+template <typename K>
+cudaError_t launch(K kernel, unsigned blocks, int threads, size_t smem, const CrossBwdParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
+  static bool set = false;
+  if (!set) {
+    cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)DqCfg<D>::kSmemBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)DkvCfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  cudaError_t e = launch(cross_dq_kernel<D>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
+                         DqCfg<D>::kSmemBytes, p, s);
+  if (e != cudaSuccess) return e;
+  const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;
+  e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, p, s);
+  if (e != cudaSuccess || p.shares == 1) return e;
+  return launch(cross_sum_kernel<D>, units * 2 * (D / 4 * kTileN / 256), 256, 0, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
+  return p.D == 128 ? backward<128>(p, sms, s) : backward<64>(p, sms, s);
+}
+
+}  // namespace sab

@@ -1216,6 +1216,9 @@ static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, in
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const long long row = (long long)H * D;
+  if (pack == 1)  // tokens before heads
+    return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
+                      (size_t)batch_of(r, B, row) * 2, tokens);
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)token_of(r, L, row) * 2,
                                  (cuuint64_t)batch_of(r, B, row) * 2};
@@ -1301,6 +1304,125 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
     return SAB_ERR_CUDA;
   return launch_cross_forward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
                                                                                               : SAB_ERR_CUDA;
+}
+
+// Blocks among which the queries of a key tile are cut: those that take the
+// fewest waves of blocks times tiles, where a block begins and ends in about the
+// time of 3 tiles and parts that have to be added cost 4 more.
+static int cross_shares(long long units, long long tiles) {
+  const long long sms = device_sms();
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= 64 && n <= tiles; ++n) {
+    const double cost =
+        (double)((units * n + sms - 1) / sms) * (double)((tiles + n - 1) / n + 3) + (n > 1 ? 4.0 + 0.05 * n : 0.0);
+    if (n == 1 || cost < least) best = n, least = cost;
+  }
+  return best;
+}
+struct CrossBackPlan {
+  int h_pack, h_tokens, h_qtiles, shares;
+  long long units;
+  size_t delta_bytes, part_bytes;
+};
+static CrossBackPlan cross_back_plan(const sab_cross_desc& d) {
+  CrossBackPlan b;
+  const int group = d.heads / d.kv_heads;
+  b.h_pack = cross_pack(d.q_tokens, group, 64);
+  b.h_tokens = 64 / b.h_pack;
+  b.h_qtiles = (d.q_tokens + 2 * b.h_tokens - 1) / (2 * b.h_tokens);
+  b.units = (long long)((d.kv_tokens + kTileN - 1) / kTileN) * d.kv_heads * d.kv_batch;
+  const long long tiles = (long long)(d.batch / d.kv_batch) * (group / b.h_pack) * b.h_qtiles;
+  b.shares = cross_shares(b.units, tiles);
+  b.delta_bytes = align_up((size_t)d.batch * d.heads * d.q_tokens * sizeof(float), kAlign);
+  b.part_bytes =
+      b.shares == 1 ? 0 : align_up((size_t)b.shares * b.units * 2 * kTileN * d.head_dim * sizeof(float), kAlign);
+  return b;
+}
+
+size_t sab_cross_attention_backward_workspace(const sab_cross_desc* desc) {
+  if (!cross_shape_ok(desc)) return 0;
+  const CrossBackPlan b = cross_back_plan(*desc);
+  return b.delta_bytes + b.part_bytes;
+}
+
+sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
+                                        const sab_token_rows* V, const sab_token_rows* O, const sab_token_rows* dO,
+                                        const float* LSE, const int* q_len, const int* kv_len, float softmax_scale,
+                                        const sab_token_rows* dQ, const sab_token_rows* dK, const sab_token_rows* dV,
+                                        void* workspace, size_t ws_bytes, void* stream) {
+  if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
+  const sab_cross_desc& d = *desc;
+  const long long qrow = (long long)d.heads * d.head_dim, krow = (long long)d.kv_heads * d.head_dim;
+  const sab_token_rows* in[] = {Q, O, dO, K, V};
+  const sab_token_rows* out[] = {dQ, dK, dV};
+  for (int i = 0; i < 5; ++i)
+    if (!(i < 3 ? token_rows_ok(in[i], d.batch, d.q_tokens, qrow, false)
+                : token_rows_ok(in[i], d.kv_batch, d.kv_tokens, krow, false)))
+      return SAB_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (!(i < 1 ? token_rows_ok(out[i], d.batch, d.q_tokens, qrow, true)
+                : token_rows_ok(out[i], d.kv_batch, d.kv_tokens, krow, true)))
+      return SAB_ERR_INVALID_ARG;
+    for (const sab_token_rows* x : in)
+      if (x->data == out[i]->data) return SAB_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (out[k]->data == out[i]->data) return SAB_ERR_INVALID_ARG;
+  }
+  if (LSE == nullptr || !aligned16(LSE) || !aligned4(q_len) || !aligned4(kv_len)) return SAB_ERR_INVALID_ARG;
+  const CrossBackPlan b = cross_back_plan(d);
+  if (workspace == nullptr || ws_bytes < b.delta_bytes + b.part_bytes ||
+      (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
+    return SAB_ERR_WORKSPACE;
+  CrossBwdParams p;
+  memset(&p, 0, sizeof(p));
+  p.q_len = q_len;
+  p.kv_len = kv_len;
+  p.LSE = const_cast<float*>(LSE);
+  p.B = d.batch;
+  p.Bk = d.kv_batch;
+  p.Lq = d.q_tokens;
+  p.Lk = d.kv_tokens;
+  p.H = d.heads;
+  p.Hk = d.kv_heads;
+  p.D = d.head_dim;
+  p.group = d.heads / d.kv_heads;
+  p.pack = cross_pack(d.q_tokens, p.group, kTileM);
+  p.tile_tokens = kTileM / p.pack;
+  p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
+  p.head_blocks = d.heads / p.pack;
+  p.pair = 1;
+  p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
+  p.splits = 1;
+  p.h_pack = b.h_pack;
+  p.h_tokens = b.h_tokens;
+  p.h_qtiles = b.h_qtiles;
+  p.shares = b.shares;
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.delta = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.delta_bytes);
+  p.dQ = static_cast<uint16_t*>(dQ->data);
+  p.dK = static_cast<uint16_t*>(dK->data);
+  p.dV = static_cast<uint16_t*>(dV->data);
+  p.dq_batch = batch_of(dQ, d.batch, qrow);
+  p.dq_token = token_of(dQ, d.q_tokens, qrow);
+  p.dk_batch = batch_of(dK, d.kv_batch, krow);
+  p.dk_token = token_of(dK, d.kv_tokens, krow);
+  p.dv_batch = batch_of(dV, d.kv_batch, krow);
+  p.dv_token = token_of(dV, d.kv_tokens, krow);
+  p.err_word = device_error_word();
+  const int B = d.batch, L = d.q_tokens, H = d.heads, D = d.head_dim;
+  if (!encode_query_rows(&p.q_map, Q, B, L, H, D, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.o_map, O, B, L, H, D, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.do_map, dO, B, L, H, D, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.q_map_h, Q, B, L, H, D, p.h_pack, p.h_tokens) ||
+      !encode_query_rows(&p.do_map_h, dO, B, L, H, D, p.h_pack, p.h_tokens) ||
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, D) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, D))
+    return SAB_ERR_CUDA;
+  return launch_cross_backward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
+                                                                                               : SAB_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ layer norm

@@ -302,7 +302,7 @@ struct NormParams {
 
 // Cross attention forward (see sab_cross_attention).
 struct CrossParams {
-  CUtensorMap q_map, o_map;  // dims (D, H, Lq, B), box (64, pack, tile_tokens, 1), SW128
+  CUtensorMap q_map, o_map;  // dims (D, H, Lq, B), box (64, pack, tile_tokens, 1), SW128; of one head: (D, Lq, H, B)
   CUtensorMap k_map, v_map;  // dims (D, Lk, Hk, Bk), box (64, 128, 1, 1), SW128
   const int* q_len;          // [B] or null
   const int* kv_len;         // [Bk] or null
@@ -320,6 +320,22 @@ struct CrossParams {
   unsigned int* err_word;
 };
 
+// Its gradients (see sab_cross_attention_backward).  Query tiles of dQ as in the
+// forward (pair 1); those that dK and dV stream have halves of h_pack heads x
+// h_tokens tokens, at most 64 rows.
+struct CrossBwdParams : CrossParams {
+  CUtensorMap do_map;             // as q_map
+  CUtensorMap q_map_h, do_map_h;  // halves
+  int Hk;
+  int h_pack, h_tokens, h_qtiles;
+  int shares;                     // blocks among which the queries of a key tile are cut
+  float scale;
+  float* delta;                   // [B, H, Lq]
+  float* part;                    // [shares][Bk][Hk][key tiles][dV, dK][D / 4][128][4] (several shares)
+  uint16_t *dQ, *dK, *dV;
+  long long dq_batch, dq_token, dk_batch, dk_token, dv_batch, dv_token;
+};
+
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_append_bf16(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_append_fp8(const AppendParams& p, cudaStream_t s);
@@ -334,6 +350,7 @@ cudaError_t launch_decay_short(const DecayTileParams& p, cudaStream_t s);
 // the outputs; the state after the run if p.state_out is given (nseg == 1)
 cudaError_t launch_decay_tiles(DecayRuns& r, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayStepParams& p, cudaStream_t s);
+cudaError_t launch_cross_backward(const CrossBwdParams& p, int sms, cudaStream_t s);
 cudaError_t launch_cross_forward(const CrossParams& p, int sms, cudaStream_t s);
 // access: bytes of an access (16, 4, 2) that channels, strides and pointers allow
 cudaError_t launch_layer_norm(NormParams& p, bool fp32, int access, bool back, int sms, cudaStream_t s);
