@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kSFull + i), 1);
-      mbar_init(bar(C::kPFull + i), 4);
+      mbar_init(bar(C::kPFull + i), 8);
       mbar_init(bar(C::kDone + i), 1);
       mbar_init(bar(C::kRead + i), 4);
       mbar_init(bar(C::kDrain + i), 1);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // dQ += dS K
             if (kk < steps)
-              mma_ts_l(lead, tQ, tS + kk * 8, make_desc(m0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_q,
+              mma_ts_l(lead, tQ, tS + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u, make_desc(m0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_q,
                        kk > 0 || begun ? 1u : 0u);
           begun = true;
           mma_commit_l(lead, bar(C::kEmpty + r.slot));
@@ -255,12 +255,14 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------- dS
-    const int hf = (warp - 4) >> 2, quad = warp & 3;
+    // Eight warps to a step, 32 columns each: half the time of four from scores
+    // to dS, which is what a stream waits for.
+    const int cg = (warp - 4) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)hf * 128u;
+    const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)cg * 32u;
     const float2* stat = reinterpret_cast<const float2*>(base + C::kStatOff);
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t s_parity = 0;
+    uint32_t parity[2] = {0u, 0u};
     int item = 0;
     bool ok = true;
     Walk<true> c;
@@ -273,16 +275,16 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       arrive_warp(C::kSeen);
       const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
       for (int j = 0; ok && j < nt; ++j) {
-        const int hi = keys - j * kTileN - hf * 64;
-        if (hi <= 0) break;  // only an item's last tile ends before a half
-        if (!(ok = wait_warp(C::kSFull + hf, s_parity, 7))) break;
-        s_parity ^= 1u;
-        tc_fence_after();
 #pragma unroll
-        for (int ps = 0; ps < 2; ++ps) {  // 32 columns at a time; dS goes over scores already read
+        for (int h = 0; h < 2; ++h) {
+          const int live = keys - j * kTileN - h * 64;
+          if (live <= 0) break;  // only an item's last tile ends before a half
+          if (!(ok = wait_warp(C::kSFull + h, parity[h], 7))) break;
+          parity[h] ^= 1u;
+          tc_fence_after();
           uint32_t s[32], g[32], o[16];
-          tmem_ld32(tS + 32 * ps, s);
-          tmem_ld32(tS + 64 + 32 * ps, g);
+          tmem_ld32(tS + 128 * h, s);
+          tmem_ld32(tS + 128 * h + 64, g);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -292,18 +294,16 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
                 __fmul2_rn(pr, __fadd2_rn(make_float2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1])), nd));
             o[k] = pack_bf16(ds.x, ds.y);
           }
-          if (__builtin_expect(hi < 64, 0)) {  // keys past the end
+          const int hi = live - cg * 32;
+          if (__builtin_expect(hi < 32, 0)) {  // keys past the end
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int col = 32 * ps + 2 * k;
-              o[k] = col + 1 < hi ? o[k] : col < hi ? o[k] & 0xFFFFu : 0u;
-            }
+            for (int k = 0; k < 16; ++k) o[k] = 2 * k + 1 < hi ? o[k] : 2 * k < hi ? o[k] & 0xFFFFu : 0u;
           }
-          tmem_st16(tS + 16 * ps, o);
+          tmem_st16(tS + 128 * h, o);  // over the first half of the scores read
+          tmem_wait_st();
+          tc_fence_before();
+          arrive_warp(C::kPFull + h);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(C::kPFull + hf);
       }
       ++item;
       c.next(p, pass);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kSFull + i), 1);
-      mbar_init(bar(C::kPFull + i), 4);
+      mbar_init(bar(C::kPFull + i), 8);
       mbar_init(bar(C::kTaken + i), 1);
       mbar_init(bar(C::kDrain + i), 1);
     }
@@ -684,12 +684,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
         const uint32_t q0 = (uint32_t)dm + st * kStep + ((uint32_t)(h * 64 * 128) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_l(lead, tmem + 256, tmem + 128u * h + kk * 8,
+          mma_ts_l(lead, tmem + 256, tmem + 128u * h + (kk >> 1) * 32 + (kk & 1) * 8,
                    make_desc(q0 + ((C::kTileBytes + kk * 16 * 128) >> 4), hi_mn), idesc_acc,
                    n + h + kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_l(lead, tmem + 256 + D, tmem + 128u * h + 64u + kk * 8,
+          mma_ts_l(lead, tmem + 256 + D, tmem + 128u * h + 64u + (kk >> 1) * 32 + (kk & 1) * 8,
                    make_desc(q0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_acc, n + h + kk > 0 ? 1u : 0u);
         mma_commit_l(lead, bar(C::kTaken + h));
         mma_commit_l(lead, bar(C::kEmpty + 2 * st + h));
@@ -707,27 +707,27 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     const int hf = (warp - 4) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + (uint32_t)hf * 128u, tG = tS + 64;
+    const uint32_t tS = tmem + lane_off + (uint32_t)hf * 32u;  // eight warps to a half's step, 32 queries each
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     Stream s = first;
     seek(s);
     bool ok = true;
     int n = 0;
-    for (; s.i < s.end; ++n, next(s)) {
-      if (!(ok = wait_warp(C::kSFull + hf, (uint32_t)n & 1u, 5))) break;
-      tc_fence_after();
-      const float* ls = reinterpret_cast<const float*>(base + C::kStageOff + (n % C::kStages) * C::kStageBytes +
-                                                       2 * C::kTileBytes) + hf * 64;
+    for (; ok && s.i < s.end; ++n, next(s)) {
+      const float* stat = reinterpret_cast<const float*>(base + C::kStageOff + (n % C::kStages) * C::kStageBytes +
+                                                         2 * C::kTileBytes) + hf * 32;
 #pragma unroll
-      for (int ps = 0; ps < 2; ++ps) {  // 32 queries at a time; results go over columns already read
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = wait_warp(C::kSFull + h, (uint32_t)n & 1u, 5))) break;
+        tc_fence_after();
         uint32_t sv[32], gv[32], po[16], so[16];
-        tmem_ld32(tS + 32 * ps, sv);
-        tmem_ld32(tG + 32 * ps, gv);
+        tmem_ld32(tS + 128 * h, sv);
+        tmem_ld32(tS + 128 * h + 64, gv);
         tmem_wait_ld();
 #pragma unroll
         for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 nl = *reinterpret_cast<const float4*>(ls + 32 * ps + 4 * c4);
-          const float4 nd = *reinterpret_cast<const float4*>(ls + 128 + 32 * ps + 4 * c4);
+          const float4 nl = *reinterpret_cast<const float4*>(stat + 64 * h + 4 * c4);
+          const float4 nd = *reinterpret_cast<const float4*>(stat + 128 + 64 * h + 4 * c4);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int k = 2 * c4 + e;
@@ -741,12 +741,13 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
             so[k] = pack_bf16(d.x, d.y);
           }
         }
-        tmem_st16(tS + 16 * ps, po);
-        tmem_st16(tG + 16 * ps, so);
+        tmem_st16(tS + 128 * h, po);  // over the first half of what this warp has read
+        tmem_st16(tS + 128 * h + 64, so);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(C::kPFull + h);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      arrive_warp(C::kPFull + hf);
+      if (!ok) break;
     }
     if (ok && n > 0) ok = wait_warp(C::kDone, 0, 6);
     ok = ok && !uniform<true>(*abort_flag);
