@@ -28,26 +28,27 @@ struct DqCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = 128u * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
-  static constexpr int kSlots = D == 128 ? 4 : 8;  // K and V tiles in turn
-  static constexpr uint32_t kQOff = 0, kGOff = kTileBytes, kOOff = 2 * kTileBytes;  // Q, dO, O of an item
-  static constexpr uint32_t kRingOff = 3 * kTileBytes;
-  static constexpr uint32_t kStatOff = kRingOff + kSlots * kTileBytes;  // [128] {-LSE log2 e, -delta}
-  static constexpr uint32_t kBarOff = kStatOff + 1024;
-  static constexpr int kQFull = 0;
-  static constexpr int kQFree = 1;                 // scores done (2 warps), delta done (4 warps)
-  static constexpr int kFull = 2;                  // [kSlots]
-  static constexpr int kEmpty = kFull + kSlots;    // [kSlots]
-  static constexpr int kSFull = kEmpty + kSlots;   // [2 halves]
-  static constexpr int kPFull = kSFull + 2;        // [2]
-  static constexpr int kDone = kPFull + 2;         // [2] an item's last product
-  static constexpr int kRead = kDone + 2;          // [2] dQ is taken out
-  static constexpr int kStat = kRead + 2;          // LSE and delta are there
-  static constexpr int kSeen = kStat + 1;          // all warps for dS have them
-  static constexpr int kDrain = kSeen + 1;         // [2]
+  static constexpr uint32_t kHalfBox = kBoxBytes / 2, kHalfBytes = kTileBytes / 2;
+  static constexpr int kSlots = D == 128 ? 3 : 8;  // of a stream: halves of V and K tiles in turn
+  static constexpr uint32_t kQOff = 0, kGOff = kTileBytes;  // Q, dO of an item; two items
+  static constexpr uint32_t kRingOff = 4 * kTileBytes;
+  static constexpr uint32_t kStatOff = kRingOff + 2 * kSlots * kHalfBytes;  // [2 items][128] {-LSE log2 e, -delta}
+  static constexpr uint32_t kBarOff = kStatOff + 2048;
+  static constexpr int kQFull = 0;                     // [2 items]
+  static constexpr int kOut = 2;                       // [2] dQ is where Q was
+  static constexpr int kFull = 4;                      // [2 streams][kSlots]
+  static constexpr int kEmpty = kFull + 2 * kSlots;    // [2][kSlots]
+  static constexpr int kSFull = kEmpty + 2 * kSlots;   // [2 streams]
+  static constexpr int kPFull = kSFull + 2;            // [2]
+  static constexpr int kDone = kPFull + 2;             // [2] an item's last product
+  static constexpr int kRead = kDone + 2;              // [2] dQ is taken out
+  static constexpr int kStat = kRead + 2;              // [2 items] LSE and delta are there
+  static constexpr int kSeen = kStat + 2;              // [2] all warps for dS have them
+  static constexpr int kDrain = kSeen + 2;             // [2 streams]
   static constexpr int kNumBars = kDrain + 2;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kMiscOff + 16;
-  // loads; products of keys [0, 64) and [64, 128); a spare; 8 warps for dS; 4
+  // Q and dO; products of keys [0, 64) and [64, 128); K and V; 8 warps for dS; 4
   // for delta and dQ
   static constexpr int kThreads = 32 * 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -78,21 +79,21 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kQFull), 1);
-    mbar_init(bar(C::kQFree), 6);
-    for (int s = 0; s < C::kSlots; ++s) {
+    for (int s = 0; s < 2 * C::kSlots; ++s) {
       mbar_init(bar(C::kFull + s), 1);
-      mbar_init(bar(C::kEmpty + s), 2);
+      mbar_init(bar(C::kEmpty + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kQFull + i), 1);
+      mbar_init(bar(C::kOut + i), 4);
       mbar_init(bar(C::kSFull + i), 1);
       mbar_init(bar(C::kPFull + i), 8);
       mbar_init(bar(C::kDone + i), 1);
       mbar_init(bar(C::kRead + i), 4);
+      mbar_init(bar(C::kStat + i), 4);
+      mbar_init(bar(C::kSeen + i), 8);
       mbar_init(bar(C::kDrain + i), 1);
     }
-    mbar_init(bar(C::kStat), 4);
-    mbar_init(bar(C::kSeen), 8);
     misc[1] = (base_u32 & 1023u) != 0;  // the tiles' swizzle counts on it
     if (misc[1] != 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
     fence_mbar_init();
@@ -119,52 +120,99 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
   pass.by = spot_of(p, gridDim.x, 1);
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- loads
+    // ------------------------------------------------------------ Q and dO an item ahead, dQ out
     if (lane == 0) {
-      const uint32_t q_bytes = (uint32_t)(3 * C::kBoxes * p.pack * p.tile_tokens) * 128u;
-      Ring<C::kSlots> r;
-      int loads = 0, asked = 0;
-      auto load = [&](const CUtensorMap* m, int row, int head, int b) -> bool {
-        if (loads >= C::kSlots && !wait(C::kEmpty + r.slot, r.parity ^ 1u, 0)) return false;
-        const uint32_t full = bar(C::kFull + r.slot);
-        mbar_arrive_expect_tx(full, C::kTileBytes);
+      const uint32_t q_bytes = (uint32_t)(2 * C::kBoxes * p.pack * p.tile_tokens) * 128u;
+      int at[2][3];  // where the items in the buffers are
+      auto out = [&](int item) -> bool {
+        const int buf = item & 1;
+        if (!wait(C::kOut + buf, (uint32_t)(item >> 1) & 1u, 0)) return false;
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_4d(base_u32 + C::kRingOff + r.slot * C::kTileBytes + bx * C::kBoxBytes, m, full, bx * 64, row, head,
-                      b);
-        r.next();
-        ++loads;
+          tma_store_4d(&p.o_map, base_u32 + buf * 2 * C::kTileBytes + bx * C::kBoxBytes, bx * 64, at[0][0], at[0][1],
+                       at[0][2]);
+        tma_store_commit_and_wait_read();
         return true;
       };
+      int item = 0;
+      bool ok = true;
+      Walk<false> c, o;
+      o.start(p, pass);
+      for (c.start(p, pass); c.more(pass); c.next(p, pass)) {
+        const Work& w = c.w;
+        if (o.more(pass)) o.next(p, pass);
+        if (w.nt == 0) continue;
+        const int buf = item & 1;
+        if (item >= 2 && !(ok = out(item - 2))) break;
+        mbar_arrive_expect_tx(bar(C::kQFull + buf), q_bytes);
+        const int c1 = query_c1(p, w, 0), c2 = query_c2(p, w, 0);
+#pragma unroll
+        for (int bx = 0; bx < C::kBoxes; ++bx) {
+          const uint32_t to = base_u32 + buf * 2 * C::kTileBytes + bx * C::kBoxBytes;
+          tma_load_4d(to + C::kGOff, &p.do_map, bar(C::kQFull + buf), bx * 64, c1, c2, w.b);
+          tma_load_4d(to + C::kQOff, &p.q_map, bar(C::kQFull + buf), bx * 64, c1, c2, w.b);
+        }
+        // O of the item after it, which the warps for delta load themselves
+        if (o.more(pass) && o.w.nt > 0) {
+#pragma unroll
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_prefetch_4d(&p.of_map, bx * 64, query_c1(p, o.w, 0), query_c2(p, o.w, 0), o.w.b);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) at[0][i] = at[1][i];
+        at[1][0] = c1, at[1][1] = c2, at[1][2] = w.b;
+        ++item;
+      }
+      if (item == 1) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) at[0][i] = at[1][i];
+      }
+      for (int k = max(0, item - 2); ok && k < item; ++k) {
+        ok = out(k);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) at[0][i] = at[1][i];
+      }
+      tma_store_wait_all();
+      if (*abort_flag)  // nothing of this block's copies may land after it
+        for (int k = max(0, item - 2); k < item; ++k)
+          wait_drain(bar(C::kQFull + (k & 1)), (uint32_t)(k >> 1) & 1u, p.err_word);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------- V, K, each stream its half
+    if (lane == 0) {
+      int loads[2] = {0, 0};
+      Ring<C::kSlots> r[2];
       bool ok = true;
       Walk<false> c;
       for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
-        if (w.nt == 0) continue;
         const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
         for (int j = 0; ok && j < w.nt; ++j) {
-          if (!(ok = load(&p.k_map, j * kTileN, head, kb))) break;
-          if (j == 0) {
-            if (asked > 0 && !(ok = wait(C::kQFree, (uint32_t)(asked - 1) & 1u, 1))) break;
-            ++asked;
-            mbar_arrive_expect_tx(bar(C::kQFull), q_bytes);
-            const int c1 = query_c1(p, w, 0), c2 = query_c2(p, w, 0);
 #pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx) {
-              const uint32_t to = base_u32 + bx * C::kBoxBytes;
-              tma_load_4d(to + C::kQOff, &p.q_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
-              tma_load_4d(to + C::kGOff, &p.do_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
-              tma_load_4d(to + C::kOOff, &p.o_map, bar(C::kQFull), bx * 64, c1, c2, w.b);
+          for (int h = 0; h < 2; ++h) {
+            if (w.keys - j * kTileN <= 64 * h) break;  // the tile ends before this half
+#pragma unroll 1
+            for (int k = 0; ok && k < 2; ++k) {  // V before K: V's slot is free first
+              const CUtensorMap* m = k == 0 ? &p.v_map : &p.k_map;
+              const int at = h * C::kSlots + r[h].slot;
+              if (loads[h] >= C::kSlots && !(ok = wait(C::kEmpty + at, r[h].parity ^ 1u, 1))) break;
+              mbar_arrive_expect_tx(bar(C::kFull + at), C::kHalfBytes);
+#pragma unroll
+              for (int bx = 0; bx < C::kBoxes; ++bx)
+                tma_load_4d(base_u32 + C::kRingOff + at * C::kHalfBytes + bx * C::kHalfBox, m, bar(C::kFull + at),
+                            bx * 64, j * kTileN + 64 * h, head, kb);
+              r[h].next();
+              ++loads[h];
             }
+            if (!ok) break;
           }
-          ok = load(&p.v_map, j * kTileN, head, kb);
         }
       }
-      if (*abort_flag) {  // nothing of this block's copies may land after it
-        for (int k = max(0, loads - C::kSlots); k < loads; ++k)
-          wait_drain(bar(C::kFull + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
-        if (asked > 0) wait_drain(bar(C::kQFull), (uint32_t)(asked - 1) & 1u, p.err_word);
-      }
+      if (*abort_flag)
+        for (int h = 0; h < 2; ++h)
+          for (int k = max(0, loads[h] - C::kSlots); k < loads[h]; ++k)
+            wait_drain(bar(C::kFull + h * C::kSlots + k % C::kSlots), (uint32_t)(k / C::kSlots) & 1u, p.err_word);
     }
     __syncwarp();
   } else if (warp < 3) {
@@ -172,79 +220,70 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const int h = warp - 1;  // keys [64 h, 64 h + 64) of every tile
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, 0);
     constexpr uint32_t idesc_q = idesc_bf16_f32(128, D, 1);
-    constexpr uint32_t kStep = C::kTileBytes >> 4;
-    constexpr uint32_t kHalf = (64u * 128u) >> 4;  // 64 rows on
+    constexpr uint32_t kStep = C::kHalfBytes >> 4;
+    const uint32_t ring = C::kRingOff + (uint32_t)h * C::kSlots * C::kHalfBytes;
     const uint64_t dq = smem_desc_sw128(base_u32 + C::kQOff, 16, 1024);
-    const uint64_t dg = smem_desc_sw128(base_u32 + C::kGOff, 16, 1024);
-    const uint64_t dk = smem_desc_sw128(base_u32 + C::kRingOff, 16, 1024);
-    const uint64_t dm = smem_desc_sw128(base_u32 + C::kRingOff, C::kBoxBytes, 1024);  // as the MN-major operand
+    const uint64_t dk = smem_desc_sw128(base_u32 + ring, 16, 1024);
+    const uint64_t dm = smem_desc_sw128(base_u32 + ring, C::kHalfBox, 1024);  // as the MN-major operand
     const uint32_t hi_k = (uint32_t)(dq >> 32), hi_mn = (uint32_t)(dm >> 32);
     const uint32_t tS = tmem + (uint32_t)h * 128u, tQ = tmem + 256u + (uint32_t)h * D;
+    const uint32_t full = C::kFull + h * C::kSlots, empty = C::kEmpty + h * C::kSlots;
     const uint32_t lead = elect_lead();
     Ring<C::kSlots> r;
-    uint32_t q_parity = 0, p_parity = 0;
-    int used = 0;
+    uint32_t p_parity = 0;
+    int used = 0, item = 0;
     bool ok = true;
     auto scores = [&](uint32_t to, uint32_t a_lo, uint32_t b_lo) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-        mma_ss_l(lead, to, make_desc(a_lo + off, hi_k), make_desc(b_lo + off, hi_k), idesc_s, kk > 0 ? 1u : 0u);
+        const uint32_t a = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4, b = ((kk >> 2) * C::kHalfBox + (kk & 3) * 32) >> 4;
+        mma_ss_l(lead, to, make_desc(a_lo + a, hi_k), make_desc(b_lo + b, hi_k), idesc_s, kk > 0 ? 1u : 0u);
       }
     };
     Walk<true> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
-      const int nt = c.w.nt, keys = c.w.keys;
-      if (!(ok = wait_warp(C::kQFull, q_parity, 2))) break;
-      q_parity ^= 1u;
-      bool begun = false;
-      for (int j = 0; ok && j < nt; ++j) {
-        const int live = keys - j * kTileN - 64 * h;  // keys of this half
-        Ring<C::kSlots> v = r;
-        v.next();
-        if (!(ok = wait_warp(C::kFull + r.slot, r.parity, 3) && wait_warp(C::kFull + v.slot, v.parity, 3))) break;
-        if (live > 0) {
-          tc_fence_after();
-          const uint32_t k0 = (uint32_t)dk + r.slot * kStep + h * kHalf, v0 = (uint32_t)dk + v.slot * kStep + h * kHalf;
-          scores(tS, (uint32_t)dq, k0);        // S = Q K^T
-          scores(tS + 64u, (uint32_t)dg, v0);  // dP = dO V^T
-          mma_commit_l(lead, bar(C::kSFull + h));
-          mma_commit_l(lead, bar(C::kEmpty + v.slot));
-          if (j + 1 == nt) mma_commit_l(lead, bar(C::kQFree));
-          const int steps = min(4, (live + 15) >> 4);  // 16 keys each
-          // keys past the sequence's end may hold anything, and 0 * NaN is NaN
-          if (__builtin_expect(steps * 16 > live, 0))
-            zero_rows<C::kBoxes>(base + C::kRingOff + r.slot * C::kTileBytes, 64 * h + live, 64 * h + steps * 16);
-          // the item before has its dQ taken out before this one's goes over it
-          if (__builtin_expect(!begun && used > 0, 0) &&
-              !(ok = wait_warp(C::kRead + h, (uint32_t)(used - 1) & 1u, 4)))
-            break;
-          if (!(ok = wait_warp(C::kPFull + h, p_parity, 5))) break;
-          p_parity ^= 1u;
-          tc_fence_after();
-          const uint32_t m0 = (uint32_t)dm + r.slot * kStep + h * kHalf;
+      const int buf = item & 1, keys = c.w.keys - 64 * h, steps_n = (keys + 127) >> 7;  // tiles with keys in this half
+      if (!(ok = wait_warp(C::kQFull + buf, (uint32_t)(item >> 1) & 1u, 2))) break;
+      const uint32_t q0 = (uint32_t)dq + buf * (2 * C::kTileBytes >> 4);
+      for (int j = 0; j < steps_n; ++j) {
+        const int live = keys - j * kTileN;
+        const int vs = r.slot;
+        if (!(ok = wait_warp(full + vs, r.parity, 3))) break;
+        r.next();
+        tc_fence_after();
+        scores(tS + 64u, q0 + (C::kTileBytes >> 4), (uint32_t)dk + vs * kStep);  // dP = dO V^T
+        mma_commit_l(lead, bar(empty + vs));
+        const int ks = r.slot;
+        if (!(ok = wait_warp(full + ks, r.parity, 3))) break;
+        r.next();
+        scores(tS, q0, (uint32_t)dk + ks * kStep);  // S = Q K^T
+        mma_commit_l(lead, bar(C::kSFull + h));
+        const int steps = min(4, (live + 15) >> 4);  // 16 keys each
+        // keys past the sequence's end may hold anything, and 0 * NaN is NaN
+        if (__builtin_expect(steps * 16 > live, 0))
+          zero_rows<C::kBoxes, C::kHalfBox>(base + ring + ks * C::kHalfBytes, live, steps * 16);
+        // the item before has its dQ taken out before this one's goes over it
+        if (__builtin_expect(j == 0 && used > 0, 0) && !(ok = wait_warp(C::kRead + h, (uint32_t)(used - 1) & 1u, 4)))
+          break;
+        if (!(ok = wait_warp(C::kPFull + h, p_parity, 5))) break;
+        p_parity ^= 1u;
+        tc_fence_after();
+        const uint32_t m0 = (uint32_t)dm + ks * kStep;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // dQ += dS K
-            if (kk < steps)
-              mma_ts_l(lead, tQ, tS + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u, make_desc(m0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_q,
-                       kk > 0 || begun ? 1u : 0u);
-          begun = true;
-          mma_commit_l(lead, bar(C::kEmpty + r.slot));
-        } else {  // the tile ends before this half
-          arrive_warp(C::kEmpty + r.slot);
-          arrive_warp(C::kEmpty + v.slot);
-          if (j + 1 == nt) arrive_warp(C::kQFree);
-        }
-        r.next();
-        r.next();
+        for (int kk = 0; kk < 4; ++kk)  // dQ += dS K
+          if (kk < steps)
+            mma_ts_l(lead, tQ, tS + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u,
+                     make_desc(m0 + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_q, j + kk > 0 ? 1u : 0u);
+        mma_commit_l(lead, bar(empty + ks));
       }
       if (!ok) break;
-      if (begun) {
+      if (steps_n > 0) {
         mma_commit_l(lead, bar(C::kDone + h));
         ++used;
       }
+      ++item;
       c.next(p, pass);
       c.seek(p, pass);
     }
@@ -253,7 +292,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       if (lane == 0) wait_drain(bar(C::kDrain + h), 0, p.err_word);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------------- dS
     // Eight warps to a step, 32 columns each: half the time of four from scores
     // to dS, which is what a stream waits for.
@@ -270,9 +309,9 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     c.seek(p, pass);
     while (ok && c.more(pass)) {
       const int nt = c.w.nt, keys = c.w.keys;
-      if (!(ok = wait_warp(C::kStat, (uint32_t)item & 1u, 6))) break;
-      const float2 st = stat[row];
-      arrive_warp(C::kSeen);
+      if (!(ok = wait_warp(C::kStat + (item & 1), (uint32_t)(item >> 1) & 1u, 6))) break;
+      const float2 st = stat[(item & 1) * 128 + row];
+      arrive_warp(C::kSeen + (item & 1));
       const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
       for (int j = 0; ok && j < nt; ++j) {
 #pragma unroll
@@ -309,51 +348,102 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       c.next(p, pass);
       c.seek(p, pass);
     }
-  } else if (warp >= 12) {
+  } else {
     // ------------------------------------------------------------ delta, dQ
+    // delta of the next item is formed while this one's products run; O comes
+    // from global memory, for there is no room for it beside two items' Q and dO.
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tQ = tmem + ((uint32_t)(quad * 32) << 16) + 256u;
     const int row_t = row / p.pack, row_g = row - row_t * p.pack;
-    float2* stat = reinterpret_cast<float2*>(base + C::kStatOff);
-    uint32_t q_parity = 0;
-    int item = 0, used[2] = {0, 0};
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of an access
+    const uint32_t inv = (65535u + (uint32_t)p.pack) / (uint32_t)p.pack;  // r * inv >> 16 = r / pack below 128
+    const int sub = lane / kLanes, col = lane % kLanes;  // 16-byte pieces
+    int used[2] = {0, 0};
     bool ok = true;
+    auto alive = [&](const Work& w) { return row_t < w.live && row_t < p.tile_tokens; };
+    auto stats = [&](const Work& w, int item) {
+      float2* stat = reinterpret_cast<float2*>(base + C::kStatOff) + (item & 1) * 128;
+      const bool live = alive(w);
+      const long long at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + w.t0 + row_t;
+      const float lse = live ? __ldg(p.LSE + at) : INFINITY;
+      if (item >= 2 && !wait_warp(C::kSeen + (item & 1), (uint32_t)((item >> 1) - 1) & 1u, 10)) return false;
+      const uint16_t* o_base = p.O + w.b * p.o_batch + w.t0 * p.o_token + w.hb * p.pack * D + col * 8;
+      const uint8_t* g_base = base + (item & 1) * 2 * C::kTileBytes + C::kGOff + (col >> 3) * C::kBoxBytes;
+#pragma unroll 1
+      for (int s0 = 0; s0 < kLanes; s0 += 8) {
+        uint4 a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = quad * 32 + (s0 + i) * kRows + sub;
+          const int rt = (int)((uint32_t)r * inv >> 16), rg = r - rt * p.pack;
+          a[i] = rt < w.live && rt < p.tile_tokens ? *reinterpret_cast<const uint4*>(o_base + rt * p.o_token + rg * D)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (s0 == 0 && !wait_warp(C::kQFull + (item & 1), (uint32_t)(item >> 1) & 1u, 8)) return false;
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = quad * 32 + (s0 + i) * kRows + sub;
+          const uint4 g = *reinterpret_cast<const uint4*>(g_base + r * 128 + (((col & 7) ^ (r & 7)) << 4));
+          const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {g.x, g.y, g.z, g.w};
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc = __ffma2_rn(make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u)),
+                             make_float2(__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xFFFF0000u)), acc);
+          d[i] = acc.x + acc.y;
+        }
+        // sums over a row's lanes, halving the rows a lane holds at each step
+        int mine = 0;
+#pragma unroll
+        for (int n = 4, bit = kLanes / 2; n > 0; n >>= 1, bit >>= 1) {
+          const bool up = lane & bit;
+          mine = 2 * mine + (up ? 1 : 0);
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const float keep = up ? d[i + n] : d[i], send = up ? d[i] : d[i + n];
+            d[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+          }
+        }
+        if (kLanes == 16) d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
+        if (kLanes == 8 || (lane & 1) == 0) stat[quad * 32 + (s0 + mine) * kRows + sub].y = -d[0];
+      }
+      __syncwarp();
+      const float nd = stat[row].y;
+      stat[row] = make_float2(live ? -lse * kLog2e : -INFINITY, live ? nd : 0.f);
+      if (live) p.delta[at] = -nd;
+      arrive_warp(C::kStat + (item & 1));
+      return true;
+    };
     Walk<true> c;
-    for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
-      const Work& w = c.w;
-      const int t = w.t0 + row_t, head = w.hb * p.pack + row_g;
-      const bool stored = row_t < p.tile_tokens && t < p.Lq, live = row_t < w.live && row_t < p.tile_tokens;
-      uint4* out = reinterpret_cast<uint4*>(p.dQ + w.b * p.dq_batch + t * p.dq_token + head * D);
-      if (w.nt == 0) {  // no query or no key
-        if (stored)
+    auto seek = [&]() {
+      while (c.more(pass) && c.w.nt == 0) {  // no query or no key
+        if (row_t < p.tile_tokens && c.w.t0 + row_t < p.Lq) {
+          uint4* out = reinterpret_cast<uint4*>(p.dQ + c.w.b * p.dq_batch + (c.w.t0 + row_t) * p.dq_token +
+                                                (c.w.hb * p.pack + row_g) * D);
 #pragma unroll 1
           for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
-        continue;
+        }
+        c.next(p, pass);
       }
-      const long long at = ((long long)w.b * p.H + head) * p.Lq + t;
-      const float lse = live ? __ldg(p.LSE + at) : INFINITY;
-      if (!(ok = wait_warp(C::kQFull, q_parity, 8))) break;
-      q_parity ^= 1u;
-      float2 acc = make_float2(0.f, 0.f);
-      const uint8_t* mine = base + row * 128;
-#pragma unroll 4
-      for (int k = 0; k < D / 8; ++k) {
-        const uint32_t off = (k >> 3) * C::kBoxBytes + (((k & 7) ^ (row & 7)) << 4);
-        const uint4 a = *reinterpret_cast<const uint4*>(mine + C::kOOff + off);
-        const uint4 b = *reinterpret_cast<const uint4*>(mine + C::kGOff + off);
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc = __ffma2_rn(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u)),
-                           make_float2(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xFFFF0000u)), acc);
+    };
+    c.start(p, pass);
+    seek();
+    bool more = c.more(pass);
+    Work w = c.w;
+#pragma unroll 1
+    for (int item = -1; ok && more; ++item) {
+      if (item >= 0) {
+        w = c.w;
+        c.next(p, pass);
+        seek();
       }
-      const float delta = acc.x + acc.y;
-      // the item before has been seen by every warp, also by those that had no step in it
-      if (item > 0 && !(ok = wait_warp(C::kSeen, (uint32_t)(item - 1) & 1u, 10))) break;
-      stat[row] = make_float2(live ? -lse * kLog2e : -INFINITY, live ? -delta : 0.f);
-      if (live) p.delta[at] = delta;
-      arrive_warp(C::kStat);
-      arrive_warp(C::kQFree);
+      const bool ahead = c.more(pass);
+      if (ahead && !(ok = stats(c.w, item + 1))) break;
+      if (item < 0) continue;
+      more = ahead;
+      const bool live = alive(w);
+      uint8_t* out = base + (item & 1) * 2 * C::kTileBytes + C::kQOff + row * 128;
       // dQ: the halves' parts
       const bool two = w.keys > 64;
       if (!(ok = wait_warp(C::kDone, (uint32_t)used[0] & 1u, 9))) break;
@@ -374,24 +464,24 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
           arrive_warp(C::kRead);
           if (two) arrive_warp(C::kRead + 1);
         }
-        if (stored) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 8 * i + 2 * k;
-              float2 x = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-              if (two) x = __fadd2_rn(x, make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])));
-              x = __fmul2_rn(x, make_float2(p.scale, p.scale));
-              o[k] = live ? pack_bf16(x.x, x.y) : 0u;
-            }
-            out[cc / 8 + i] = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int k = 0; k < 4; ++k) {
+            const int e = 8 * i + 2 * k;
+            float2 x = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+            if (two) x = __fadd2_rn(x, make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])));
+            x = __fmul2_rn(x, make_float2(p.scale, p.scale));
+            o[k] = live ? pack_bf16(x.x, x.y) : 0u;
           }
+          const int k = cc / 8 + i;
+          *reinterpret_cast<uint4*>(out + (k >> 3) * C::kBoxBytes + (((k & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
-        __syncwarp();
       }
-      ++item;
+      fence_proxy_async_smem();
+      arrive_warp(C::kOut + (item & 1));
     }
   }
   tc_fence_before();
@@ -547,8 +637,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
       mbar_arrive_expect_tx(bar(C::kRes), 2 * C::kTileBytes);
 #pragma unroll
       for (int bx = 0; bx < C::kBoxes; ++bx) {
-        tma_load_4d(base_u32 + C::kKOff + bx * C::kBoxBytes, &p.k_map, bar(C::kRes), bx * 64, k0, hk, kb);
-        tma_load_4d(base_u32 + C::kVOff + bx * C::kBoxBytes, &p.v_map, bar(C::kRes), bx * 64, k0, hk, kb);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t to = base_u32 + bx * C::kBoxBytes + h * (C::kBoxBytes / 2);
+          tma_load_4d(to + C::kKOff, &p.k_map, bar(C::kRes), bx * 64, k0 + 64 * h, hk, kb);
+          tma_load_4d(to + C::kVOff, &p.v_map, bar(C::kRes), bx * 64, k0 + 64 * h, hk, kb);
+        }
       }
     }
     const uint32_t half_bytes = (uint32_t)(2 * C::kBoxes * p.h_pack * p.h_tokens) * 128u;
@@ -562,7 +656,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     }
     Stream s = first;
     seek(s);
-    float ls[4], dl[4];  // of the tile to be loaded next, requested one tile ahead
+    float ls[4], dl[4];
+    bool has[4];  // of the tile to be loaded next, requested one tile ahead
     auto fetch = [&]() {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -571,8 +666,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
         const int t = s.iq * 2 * p.h_tokens + h * p.h_tokens + tok[i & 1];
         const int head = hk * p.group + s.hb * p.h_pack + hd[i & 1];
         const long long at = ((long long)s.b * p.H + head) * p.Lq + t;
-        ls[i] = in ? -__ldg(p.LSE + at) * kLog2e : -INFINITY;
-        dl[i] = in ? -__ldg(p.delta + at) : 0.f;
+        ls[i] = dl[i] = 0.f;
+        if (in) ls[i] = __ldg(p.LSE + at), dl[i] = __ldg(p.delta + at);
+        has[i] = in;
       }
     };
     if (s.i < s.end) fetch();
@@ -602,8 +698,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
         float* stat = reinterpret_cast<float*>(base + so + 2 * C::kTileBytes) + 64 * h;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          stat[lane + 32 * i] = ls[2 * h + i];
-          stat[128 + lane + 32 * i] = dl[2 * h + i];
+          stat[lane + 32 * i] = has[2 * h + i] ? -ls[2 * h + i] * kLog2e : -INFINITY;
+          stat[128 + lane + 32 * i] = -dl[2 * h + i];
         }
         arrive_warp(C::kFull + 2 * st + h);
         ++halves;

@@ -1228,10 +1228,10 @@ static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, in
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D) {
+static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D, int rows) {
   const long long row = (long long)H * D;
   return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
-                    (size_t)batch_of(r, B, row) * 2);
+                    (size_t)batch_of(r, B, row) * 2, rows);
 }
 
 // Heads of one tile of `rows` query rows: the number, among those that divide
@@ -1299,8 +1299,8 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.err_word = device_error_word();
   if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.o_map, O, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
-      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim) ||
-      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim))
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim, kTileN) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim, kTileN))
     return SAB_ERR_CUDA;
   return launch_cross_forward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
                                                                                               : SAB_ERR_CUDA;
@@ -1402,6 +1402,9 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.delta = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.delta_bytes);
+  p.O = static_cast<uint16_t*>(O->data);  // read
+  p.o_batch = batch_of(O, d.batch, qrow);
+  p.o_token = token_of(O, d.q_tokens, qrow);
   p.dQ = static_cast<uint16_t*>(dQ->data);
   p.dK = static_cast<uint16_t*>(dK->data);
   p.dV = static_cast<uint16_t*>(dV->data);
@@ -1414,12 +1417,13 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.err_word = device_error_word();
   const int B = d.batch, L = d.q_tokens, H = d.heads, D = d.head_dim;
   if (!encode_query_rows(&p.q_map, Q, B, L, H, D, p.pack, p.tile_tokens) ||
-      !encode_query_rows(&p.o_map, O, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.do_map, dO, B, L, H, D, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.of_map, O, B, L, H, D, p.pack, p.tile_tokens) ||
+      !encode_query_rows(&p.o_map, dQ, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.q_map_h, Q, B, L, H, D, p.h_pack, p.h_tokens) ||
       !encode_query_rows(&p.do_map_h, dO, B, L, H, D, p.h_pack, p.h_tokens) ||
-      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, D) ||
-      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, D))
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, D, 64) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, D, 64))
     return SAB_ERR_CUDA;
   return launch_cross_backward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
                                                                                                : SAB_ERR_CUDA;

@@ -324,7 +324,7 @@ struct CrossParams {
 // forward (pair 1); those that dK and dV stream have halves of h_pack heads x
 // h_tokens tokens, at most 64 rows.
 struct CrossBwdParams : CrossParams {
-  CUtensorMap do_map;             // as q_map
+  CUtensorMap do_map, of_map;     // dO and O, as q_map; o_map is dQ's; boxes of k_map and v_map have 64 rows
   CUtensorMap q_map_h, do_map_h;  // halves
   int Hk;
   int h_pack, h_tokens, h_qtiles;
