@@ -1228,10 +1228,10 @@ static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, in
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D, int rows) {
+static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D) {
   const long long row = (long long)H * D;
   return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
-                    (size_t)batch_of(r, B, row) * 2, rows);
+                    (size_t)batch_of(r, B, row) * 2);
 }
 
 // Heads of one tile of `rows` query rows: the number, among those that divide
@@ -1299,8 +1299,8 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.err_word = device_error_word();
   if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.o_map, O, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
-      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim, kTileN) ||
-      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim, kTileN))
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, d.head_dim))
     return SAB_ERR_CUDA;
   return launch_cross_forward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
                                                                                               : SAB_ERR_CUDA;
@@ -1321,18 +1321,18 @@ static int cross_shares(long long units, long long tiles) {
   return best;
 }
 struct CrossBackPlan {
-  int h_pack, h_tokens, h_qtiles, shares;
+  int pack, tile_tokens, n_qtiles, shares;
   long long units;
   size_t delta_bytes, part_bytes;
 };
 static CrossBackPlan cross_back_plan(const sab_cross_desc& d) {
   CrossBackPlan b;
   const int group = d.heads / d.kv_heads;
-  b.h_pack = cross_pack(d.q_tokens, group, 64);
-  b.h_tokens = 64 / b.h_pack;
-  b.h_qtiles = (d.q_tokens + 2 * b.h_tokens - 1) / (2 * b.h_tokens);
+  b.pack = cross_pack(d.q_tokens, group, kTileM);
+  b.tile_tokens = kTileM / b.pack;
+  b.n_qtiles = (d.q_tokens + b.tile_tokens - 1) / b.tile_tokens;
   b.units = (long long)((d.kv_tokens + kTileN - 1) / kTileN) * d.kv_heads * d.kv_batch;
-  const long long tiles = (long long)(d.batch / d.kv_batch) * (group / b.h_pack) * b.h_qtiles;
+  const long long tiles = (long long)(d.batch / d.kv_batch) * (group / b.pack) * b.n_qtiles;
   b.shares = cross_shares(b.units, tiles);
   b.delta_bytes = align_up((size_t)d.batch * d.heads * d.q_tokens * sizeof(float), kAlign);
   b.part_bytes =
@@ -1387,16 +1387,13 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.Hk = d.kv_heads;
   p.D = d.head_dim;
   p.group = d.heads / d.kv_heads;
-  p.pack = cross_pack(d.q_tokens, p.group, kTileM);
-  p.tile_tokens = kTileM / p.pack;
-  p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
+  p.pack = b.pack;
+  p.tile_tokens = b.tile_tokens;
+  p.n_qtiles = b.n_qtiles;
   p.head_blocks = d.heads / p.pack;
   p.pair = 1;
   p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
   p.splits = 1;
-  p.h_pack = b.h_pack;
-  p.h_tokens = b.h_tokens;
-  p.h_qtiles = b.h_qtiles;
   p.shares = b.shares;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1420,10 +1417,8 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
       !encode_query_rows(&p.do_map, dO, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.of_map, O, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.o_map, dQ, B, L, H, D, p.pack, p.tile_tokens) ||
-      !encode_query_rows(&p.q_map_h, Q, B, L, H, D, p.h_pack, p.h_tokens) ||
-      !encode_query_rows(&p.do_map_h, dO, B, L, H, D, p.h_pack, p.h_tokens) ||
-      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, D, 64) ||
-      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, D, 64))
+      !encode_key_rows(&p.k_map, K, d.kv_batch, d.kv_tokens, d.kv_heads, D) ||
+      !encode_key_rows(&p.v_map, V, d.kv_batch, d.kv_tokens, d.kv_heads, D))
     return SAB_ERR_CUDA;
   return launch_cross_backward(p, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAB_OK
                                                                                                : SAB_ERR_CUDA;

@@ -321,13 +321,10 @@ struct CrossParams {
 };
 
 // Its gradients (see sab_cross_attention_backward).  Query tiles of dQ as in the
-// forward (pair 1); those that dK and dV stream have halves of h_pack heads x
-// h_tokens tokens, at most 64 rows.
+// forward (pair 1), for dK and dV too.
 struct CrossBwdParams : CrossParams {
-  CUtensorMap do_map, of_map;     // dO and O, as q_map; o_map is dQ's; boxes of k_map and v_map have 64 rows
-  CUtensorMap q_map_h, do_map_h;  // halves
+  CUtensorMap do_map, of_map;     // dO and O, as q_map; o_map is dQ's
   int Hk;
-  int h_pack, h_tokens, h_qtiles;
   int shares;                     // blocks among which the queries of a key tile are cut
   float scale;
   float* delta;                   // [B, H, Lq]
