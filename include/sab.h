@@ -643,14 +643,16 @@ typedef struct {
 } sab_cross_desc;
 
 /*
- * Token rows of one tensor: token (b, t) holds heads * head_dim contiguous
- * elements at data + b * batch + t * token (strides in elements, multiples of
- * 8, at least a token's extent), so that a slice of a fused projection needs no
- * copy.  data is 16-byte aligned.  Strides of axes of one entry are not read.
+ * Token rows of one tensor: head h of token (b, t) is the head_dim contiguous
+ * elements at data + b * batch + t * token + h * head (strides in elements,
+ * multiples of 8; head 0: contiguous heads), so that neither a slice of a fused
+ * projection nor a tensor with heads before tokens needs a copy.  Heads and tokens
+ * must not overlap, nor sequences of a tensor that is written.  data is 16-byte
+ * aligned.  Strides of axes of one entry are not read.
  */
 typedef struct {
   void* data;
-  long long batch, token;
+  long long batch, token, head;
 } sab_token_rows;
 
 sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,

@@ -729,24 +729,25 @@ class CrossDesc(ctypes.Structure):
 
 
 class TokenRows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong),
+                ("head", ctypes.c_longlong)]
 
 
 _CROSS = struct.Struct("@7i")       # the layouts of CrossDesc and TokenRows, packed faster than the structures
-_TOKENS = struct.Struct("@Pqq")     # are built
+_TOKENS = struct.Struct("@Pqqq")    # are built
 
 
 def _token_rows(t, shape, name, dev):
-    """Token rows of a bf16 [B, L, H, D] tensor with contiguous heads."""
+    """Token rows of a bf16 [B, L, H, D] tensor."""
     try:
         if t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != shape:
             _refuse(t, name, dev, (torch.bfloat16,), shape)
     except AttributeError:
         _refuse(t, name, dev, (torch.bfloat16,), shape)
     b, l, h, d = t.stride()
-    if (d != 1 and shape[3] > 1) or (h != shape[3] and shape[2] > 1):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return _TOKENS.pack(t.data_ptr(), b, l)
+    if (d != 1 and shape[3] > 1) or (h == 0 and shape[2] > 1):
+        raise ValueError(f"{name}: heads must be contiguous each and apart from one another")
+    return _TOKENS.pack(t.data_ptr(), b, l, h)
 
 
 def _cross_shapes(Q, K):
@@ -764,7 +765,7 @@ def _cross_shapes(Q, K):
 
 def cross_attention(Q, K, V, softmax_scale: float, O, LSE=None, q_len=None, kv_len=None, stream=None):
     """sab_cross_attention: queries ``Q`` [B, Lq, H, D] over an encoder's ``K``,
-    ``V`` [B or 1, Lk, Hk, D] (bf16, batch and token strides free), of which the
+    ``V`` [B or 1, Lk, Hk, D] (bf16, strides of all axes but the last free), of which the
     first ``q_len`` and ``kv_len`` tokens (int32 per sequence) are real (see
     include/sab.h)."""
     dev = _device()

@@ -146,7 +146,7 @@ __device__ __noinline__ SlowSum slow_step(const CrossParams& p, uint32_t meet, v
 __device__ __noinline__ void clear_tile(const CrossParams& p, int b, int hb, int t0, int row) {
   const int row_t = row / p.pack, head = hb * p.pack + row - row_t * p.pack, t = t0 + row_t;
   if (row_t >= p.tile_tokens || t >= p.Lq) return;
-  uint4* o = reinterpret_cast<uint4*>(p.O + b * p.o_batch + t * p.o_token + head * p.D);
+  uint4* o = reinterpret_cast<uint4*>(p.O + b * p.o_batch + t * p.o_token + head * p.o_head);
 #pragma unroll 1
   for (int i = 0; i < p.D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
   if (p.LSE != nullptr) p.LSE[((long long)b * p.H + head) * p.Lq + t] = -INFINITY;
@@ -738,7 +738,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         cluster_sync_all();
         if (stored && !bad) {
           const float* all = reinterpret_cast<const float*>(base + C::kRingOff) + row * per;
-          uint16_t* out = p.O + w.b * p.o_batch + t * p.o_token + (w.hb * p.pack + row_g) * D + split * per;
+          uint16_t* out = p.O + w.b * p.o_batch + t * p.o_token + (w.hb * p.pack + row_g) * p.o_head + split * per;
           for (int cc = 0; cc < per; cc += 4) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = 0; c < p.splits; ++c) {

@@ -20,6 +20,18 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Where the n-th of a run of tile pairs is, of which one is done with before the
+// other (V before K, dO before Q): N pairs of places in turn, the one done with
+// last where the other was.
+template <int N>
+__device__ __forceinline__ int last_slot(int n) {
+  return 2 * (n % N) + ((n / N) & 1);
+}
+template <int N>
+__device__ __forceinline__ int first_slot(int n) {
+  return last_slot<N>(n) ^ 1;
+}
+
 // ------------------------------------------------------------------- dQ, delta
 
 template <int D_>
@@ -54,11 +66,6 @@ struct DqCfg {
   static constexpr int kThreads = 32 * 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
-// Where the n-th key tile's K and V are: a pair of places for the even tiles and
-// one for the odd, K where the tile two before had V, which is done with first.
-__device__ __forceinline__ int k_slot(unsigned n) { return (int)(2u * (n & 1u) + ((n >> 1) & 1u)); }
-__device__ __forceinline__ int v_slot(unsigned n) { return k_slot(n) ^ 1; }
-
 // P stays in registers, so S is free for the next tile as soon as it is read, and
 // two warps issue products: one S = Q K^T, the other dP = dO V^T and, once dS is
 // over dP, dQ += dS K.  TMEM: S, dP, and dQ of two items, one being taken out.
@@ -193,11 +200,11 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
   } else if (warp == 3) {
     // ------------------------------------------------------------------ K, V
     if (lane == 0) {
-      unsigned n[2] = {0, 0};  // K and V tiles
+      int n[2] = {0, 0};  // K and V tiles
       bool ok = true;
       auto load = [&](int which, const CUtensorMap* m, int row, int head, int b) -> bool {
-        const unsigned k = n[which];
-        const int at = which == 0 ? k_slot(k) : v_slot(k);
+        const int k = n[which];
+        const int at = which == 0 ? last_slot<2>(k) : first_slot<2>(k);
         if (k >= 2 && !wait(C::kEmpty + at, ((k >> 1) - 1) & 1u, 1)) return false;
         mbar_arrive_expect_tx(bar(C::kFull + at), C::kTileBytes);
         for (int bx = 0; bx < C::kBoxes; ++bx)
@@ -215,8 +222,8 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       }
       if (*abort_flag)
         for (int which = 0; which < 2; ++which)
-          for (unsigned k = n[which] > 2 ? n[which] - 2 : 0; k < n[which]; ++k)
-            wait_drain(bar(C::kFull + (which == 0 ? k_slot(k) : v_slot(k))), (k >> 1) & 1u, p.err_word);
+          for (int k = max(0, n[which] - 2); k < n[which]; ++k)
+            wait_drain(bar(C::kFull + (which == 0 ? last_slot<2>(k) : first_slot<2>(k))), (k >> 1) & 1u, p.err_word);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -225,8 +232,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint64_t dq = smem_desc_sw128(base_u32 + C::kQOff, 16, 1024);
     const uint32_t dk = (uint32_t)smem_desc_sw128(base_u32 + C::kRingOff, 16, 1024), hi = (uint32_t)(dq >> 32);
     const uint32_t lead = elect_lead();
-    unsigned n = 0;
-    int item = 0;
+    int n = 0, item = 0;
     bool ok = true;
     Walk<true> c;
     c.start(p, pass);
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       c.seek(p, pass);
       if (!(ok = wait_warp(C::kQFull, (uint32_t)item & 1u, 2))) break;
       for (int j = 0; j < nt; ++j, ++n) {
-        const int slot = k_slot(n);
+        const int slot = last_slot<2>(n);
         if (!(ok = wait_warp(C::kFull + slot, (n >> 1) & 1u, 3))) break;
         if (n > 0 && !(ok = wait_warp(C::kSRead, (n - 1) & 1u, 4))) break;
         tc_fence_after();
@@ -269,8 +275,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t hi_k = (uint32_t)(dg >> 32), hi_mn = (uint32_t)(dm >> 32);
     const uint32_t tG = tmem + 128u;
     const uint32_t lead = elect_lead();
-    unsigned n = 0;
-    int item = 0;
+    int n = 0, item = 0;
     bool ok = true;
     Walk<true> c;
     c.start(p, pass);
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       c.seek(p, pass);
       if (!(ok = wait_warp(C::kGFull + buf, (uint32_t)(item >> 1) & 1u, 5))) break;
       for (int j = 0; j < nt; ++j, ++n) {
-        const int ks = k_slot(n), vs = v_slot(n), live = keys - j * kTileN;
+        const int ks = last_slot<2>(n), vs = first_slot<2>(n), live = keys - j * kTileN;
         if (!(ok = wait_warp(C::kFull + vs, (n >> 1) & 1u, 6))) break;
         tc_fence_after();
 #pragma unroll
@@ -326,8 +331,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)cg * 64u, tG = tS + 128u;
     const float2* stat = reinterpret_cast<const float2*>(base + C::kStatOff);
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    unsigned n = 0;
-    int item = 0;
+    int n = 0, item = 0;
     bool ok = true;
     Walk<true> c;
     c.start(p, pass);
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       const long long at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + w.t0 + row_t;
       const float lse = live ? __ldg(p.LSE + at) : INFINITY;
       if (item >= 2 && !wait_warp(C::kSeen + (item & 1), (uint32_t)((item >> 1) - 1) & 1u, 13)) return false;
-      const uint16_t* o_base = p.O + w.b * p.o_batch + w.t0 * p.o_token + w.hb * p.pack * D + col * 8;
+      const uint16_t* o_base = p.O + w.b * p.o_batch + w.t0 * p.o_token + w.hb * p.pack * p.o_head + col * 8;
       const uint8_t* g_base = base + (item & 1) * C::kTileBytes + C::kGOff + (col >> 3) * C::kBoxBytes;
 #pragma unroll 1
       for (int s0 = 0; s0 < kLanes; s0 += 8) {
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         for (int i = 0; i < 8; ++i) {
           const int r = quad * 32 + (s0 + i) * kRows + sub;
           const int rt = (int)((uint32_t)r * inv >> 16), rg = r - rt * p.pack;
-          a[i] = rt < w.live && rt < p.tile_tokens ? *reinterpret_cast<const uint4*>(o_base + rt * p.o_token + rg * D)
+          a[i] = rt < w.live && rt < p.tile_tokens ? *reinterpret_cast<const uint4*>(o_base + rt * p.o_token + rg * p.o_head)
                                                    : make_uint4(0u, 0u, 0u, 0u);
         }
         if (s0 == 0 && !wait_warp(C::kGFull + (item & 1), (uint32_t)(item >> 1) & 1u, 14)) return false;
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       while (c.more(pass) && c.w.nt == 0) {  // no query or no key
         if (row_t < p.tile_tokens && c.w.t0 + row_t < p.Lq) {
           uint4* out = reinterpret_cast<uint4*>(p.dQ + c.w.b * p.dq_batch + (c.w.t0 + row_t) * p.dq_token +
-                                                (c.w.hb * p.pack + row_g) * D);
+                                                (c.w.hb * p.pack + row_g) * p.dq_head);
 #pragma unroll 1
           for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -529,13 +533,13 @@ struct DkvCfg {
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr uint32_t kKOff = 0, kVOff = kTileBytes;  // resident
   static constexpr uint32_t kStageOff = 2 * kTileBytes;
-  // a stage: Q, dO, then 128 of -LSE log2 e and 128 of -delta
-  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 1024;
-  static constexpr uint32_t kBarOff = kStageOff + kStages * kStageBytes;
+  static constexpr uint32_t kStatOff = kStageOff + 2 * kStages * kTileBytes;  // [kStages][2][128] -LSE log2 e, -delta
+  static constexpr uint32_t kBarOff = kStatOff + kStages * 1024;
   static constexpr int kRes = 0;
-  static constexpr int kFull = 1;                 // [kStages]
-  static constexpr int kEmpty = kFull + kStages;  // [kStages] both streams are done with it
-  static constexpr int kSFull = kEmpty + kStages; // [2 streams] S^T, dP^T
+  static constexpr int kStat = 1;                     // [kStages]
+  static constexpr int kFull = kStat + kStages;       // [2 kStages] Q and dO tiles
+  static constexpr int kEmpty = kFull + 2 * kStages;  // [2 kStages] both streams are done with it
+  static constexpr int kSFull = kEmpty + 2 * kStages; // [2 streams] S^T, dP^T
   static constexpr int kPFull = kSFull + 2;       // [2] P^T, dS^T
   static constexpr int kDone = kPFull + 2;        // [2]
   static constexpr int kDrain = kDone + 2;        // [2]
@@ -589,8 +593,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::kRes), 1);
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(C::kFull + i), 2);  // copies, LSE and delta
+    for (int i = 0; i < C::kStages; ++i) mbar_init(bar(C::kStat + i), 1);
+    for (int i = 0; i < 2 * C::kStages; ++i) {
+      mbar_init(bar(C::kFull + i), 1);
       mbar_init(bar(C::kEmpty + i), 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     const int n = (kTileM - rows) * 8;
     for (int i = threadIdx.x; i < C::kStages * 2 * C::kBoxes * n; i += blockDim.x) {
       const int box = i / n, k = i - box * n;
-      uint8_t* to = base + C::kStageOff + box / (2 * C::kBoxes) * C::kStageBytes + box % (2 * C::kBoxes) * C::kBoxBytes;
+      uint8_t* to = base + C::kStageOff + box * C::kBoxBytes;
       *reinterpret_cast<uint4*>(to + (rows + (k >> 3)) * 128 + (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
         tma_load_4d(base_u32 + C::kVOff + bx * C::kBoxBytes, &p.v_map, bar(C::kRes), bx * 64, k0, hk, kb);
       }
     }
-    const uint32_t tile_bytes = (uint32_t)(2 * C::kBoxes * rows) * 128u;
+    const uint32_t tile_bytes = (uint32_t)(C::kBoxes * rows) * 128u;
     // four rows a lane: place within the tile's heads and tokens
     int tok[4], hd[4];
 #pragma unroll
@@ -692,50 +697,55 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
       }
     };
     if (s.i < s.end) fetch();
-    int n = 0;
-    bool ok = true;
-    while (s.i < s.end) {
-      const int st = n % C::kStages;
-      const uint32_t so = C::kStageOff + st * C::kStageBytes, full = bar(C::kFull + st);
-      if (n >= C::kStages && !(ok = wait_warp(C::kEmpty + st, (uint32_t)(n / C::kStages - 1) & 1u, 0))) break;
+    int loads[2] = {0, 0};  // Q and dO tiles
+    auto load = [&](int which, const CUtensorMap* m) -> bool {
+      const int k = loads[which], at = which == 0 ? last_slot<C::kStages>(k) : first_slot<C::kStages>(k);
+      if (k >= C::kStages && !wait_warp(C::kEmpty + at, (uint32_t)(k / C::kStages - 1) & 1u, 0)) return false;
       if (lane == 0) {
         const int head = hk * p.group + s.hb * p.pack, t = s.iq * p.tile_tokens;
         const int c1 = p.pack == 1 ? t : head, c2 = p.pack == 1 ? head : t;
+        const uint32_t full = bar(C::kFull + at);
         mbar_arrive_expect_tx(full, tile_bytes);
 #pragma unroll
-        for (int bx = 0; bx < C::kBoxes; ++bx) {
-          tma_load_4d(base_u32 + so + bx * C::kBoxBytes, &p.q_map, full, bx * 64, c1, c2, s.b);
-          tma_load_4d(base_u32 + so + C::kTileBytes + bx * C::kBoxBytes, &p.do_map, full, bx * 64, c1, c2, s.b);
-        }
+        for (int bx = 0; bx < C::kBoxes; ++bx)
+          tma_load_4d(base_u32 + C::kStageOff + at * C::kTileBytes + bx * C::kBoxBytes, m, full, bx * 64, c1, c2, s.b);
       }
-      float* stat = reinterpret_cast<float*>(base + so + 2 * C::kTileBytes);
+      __syncwarp();
+      ++loads[which];
+      return true;
+    };
+    bool ok = true;
+    while (s.i < s.end) {
+      const int st = loads[0] % C::kStages;
+      if (!(ok = load(0, &p.q_map) && load(1, &p.do_map))) break;
+      float* stat = reinterpret_cast<float*>(base + C::kStatOff + st * 1024);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         stat[lane + 32 * i] = has[i] ? -ls[i] * kLog2e : -INFINITY;
         stat[128 + lane + 32 * i] = -dl[i];
       }
-      arrive_warp(C::kFull + st);
-      ++n;
+      arrive_warp(C::kStat + st);
       next(s);
       if (s.i < s.end) fetch();
     }
     if (lane == 0 && *abort_flag) {
       if (any) wait_drain(bar(C::kRes), 0, p.err_word);
-      for (int k = max(0, n - C::kStages); k < n; ++k)
-        wait_drain(bar(C::kFull + k % C::kStages), (uint32_t)(k / C::kStages) & 1u, p.err_word);
+      for (int which = 0; which < 2; ++which)
+        for (int k = max(0, loads[which] - C::kStages); k < loads[which]; ++k)
+          wait_drain(bar(C::kFull + (which == 0 ? last_slot<C::kStages>(k) : first_slot<C::kStages>(k))),
+                     (uint32_t)(k / C::kStages) & 1u, p.err_word);
     }
     __syncwarp();
   } else if (warp < 3) {
     // ------------------------------------------------- products of a stream
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, 1);
-    constexpr uint32_t kStep = C::kStageBytes >> 4, kTile = C::kTileBytes >> 4;
+    constexpr uint32_t kTile = C::kTileBytes >> 4;
     const int h = warp - 1;  // 0: S, dV; 1: dP, dK
     const uint32_t dk = (uint32_t)smem_desc_sw128(base_u32 + C::kKOff, 16, 1024) + (uint32_t)h * kTile;
     const uint64_t ds = smem_desc_sw128(base_u32 + C::kStageOff, 16, 1024);
     const uint64_t dm = smem_desc_sw128(base_u32 + C::kStageOff, C::kBoxBytes, 1024);  // as the MN-major operand
     const uint32_t hi_k = (uint32_t)(ds >> 32), hi_mn = (uint32_t)(dm >> 32);
-    const uint32_t b_k = (uint32_t)ds + (uint32_t)h * kTile, b_mn = (uint32_t)dm + (uint32_t)(1 - h) * kTile;
     const uint32_t tS = tmem + 128u * (uint32_t)h, tA = tmem + 256u + (uint32_t)(h * D);
     const uint32_t lead = elect_lead();
     Stream s = first;
@@ -743,31 +753,36 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     bool ok = first.i >= first.end || wait_warp(C::kRes, 0, 1);  // also where no query turns out live
     int n = 0;
     for (; ok && s.i < s.end; ++n) {
-      const int st = n % C::kStages;
-      if (!(ok = wait_warp(C::kFull + st, (uint32_t)(n / C::kStages) & 1u, 2))) break;
-      if (__builtin_expect(p.q_len != nullptr && s.live < p.tile_tokens, 0)) {
-        // queries past the sequence's end may hold anything, and 0 * NaN is NaN
-        uint8_t* q = base + C::kStageOff + st * C::kStageBytes;
-        zero_rows<C::kBoxes>(q, s.live * p.pack, kTileM);
-        zero_rows<C::kBoxes>(q + C::kTileBytes, s.live * p.pack, kTileM);
-      }
+      const uint32_t parity = (uint32_t)(n / C::kStages) & 1u;
+      const int qs = last_slot<C::kStages>(n), gs = first_slot<C::kStages>(n);
+      const int own = h == 0 ? qs : gs, other = h == 0 ? gs : qs;  // of the scores, of the sums
+      if (!(ok = wait_warp(C::kFull + own, parity, 2))) break;
+      const bool part = p.q_len != nullptr && s.live < p.tile_tokens;
+      const int live = s.live * p.pack;
+      // queries past the sequence's end may hold anything, and 0 * NaN is NaN
+      if (__builtin_expect(part, 0))
+        zero_rows<C::kBoxes>(base + C::kStageOff + own * C::kTileBytes, live, kTileM);
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-        mma_ss_l(lead, tS, make_desc(dk + off, hi_k), make_desc(b_k + st * kStep + off, hi_k), idesc_s,
+        mma_ss_l(lead, tS, make_desc(dk + off, hi_k), make_desc((uint32_t)ds + own * kTile + off, hi_k), idesc_s,
                  kk > 0 ? 1u : 0u);
       }
       mma_commit_l(lead, bar(C::kSFull + h));
+      mma_commit_l(lead, bar(C::kEmpty + own));
       next(s);
+      if (!(ok = wait_warp(C::kFull + other, parity, 2))) break;
+      if (__builtin_expect(part, 0))  // by both streams, whichever comes first
+        zero_rows<C::kBoxes>(base + C::kStageOff + other * C::kTileBytes, live, kTileM);
       if (!(ok = wait_warp(C::kPFull + h, (uint32_t)n & 1u, 3))) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
         mma_ts_l(lead, tA, tS + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8),
-                 make_desc(b_mn + st * kStep + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_acc,
+                 make_desc((uint32_t)dm + other * kTile + ((uint32_t)(kk * 16 * 128) >> 4), hi_mn), idesc_acc,
                  n + kk > 0 ? 1u : 0u);
-      mma_commit_l(lead, bar(C::kEmpty + st));
+      mma_commit_l(lead, bar(C::kEmpty + other));
     }
     if (ok && n > 0) mma_commit_l(lead, bar(C::kDone + h));
     if (!ok) {
@@ -787,8 +802,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     bool ok = true;
     int n = 0;
     for (; ok && s.i < s.end; ++n, next(s)) {
-      const float* stat = reinterpret_cast<const float*>(base + C::kStageOff + (n % C::kStages) * C::kStageBytes +
-                                                         2 * C::kTileBytes) + hf * 64;
+      const float* stat = reinterpret_cast<const float*>(base + C::kStatOff + (n % C::kStages) * 1024) + hf * 64;
+      if (!(ok = wait_warp(C::kStat + n % C::kStages, (uint32_t)(n / C::kStages) & 1u, 7))) break;
       float2 pr[32];
       if (!(ok = wait_warp(C::kSFull, (uint32_t)n & 1u, 4))) break;
       tc_fence_after();
@@ -840,8 +855,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
       const float mul = hf == 0 ? 1.f : p.scale;
       const uint32_t from = tmem + lane_off + 256u + (uint32_t)hf * D;
       // one share: the gradients; several: this share's part
-      uint16_t* out = hf == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * D
-                              : p.dK + kb * p.dk_batch + key * p.dk_token + hk * D;
+      uint16_t* out = hf == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * p.dv_head
+                              : p.dK + kb * p.dk_batch + key * p.dk_token + hk * p.dk_head;
       float* part = p.part + ((long long)blockIdx.x * 2 + hf) * (kTileN * D) + (long long)row * 4;
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
@@ -906,8 +921,8 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ 
       a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
     }
   }
-  uint16_t* out = which == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * D
-                             : p.dK + kb * p.dk_batch + key * p.dk_token + hk * D;
+  uint16_t* out = which == 0 ? p.dV + kb * p.dv_batch + key * p.dv_token + hk * p.dv_head
+                             : p.dK + kb * p.dk_batch + key * p.dk_token + hk * p.dk_head;
   *reinterpret_cast<uint2*>(out + 4 * c4) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
 }
 

@@ -1196,32 +1196,49 @@ static bool cross_shape_ok(const sab_cross_desc* d) {
   return (long long)d->batch * d->heads * ((d->q_tokens + 31) / 32) <= (1LL << 30) &&
          (long long)d->kv_batch * d->kv_heads * ((d->kv_tokens + 31) / 32) <= (1LL << 30);
 }
-// Rows of one [B, L, heads, D] tensor: pointer and strides that a tensor map
-// takes; tokens of a written tensor apart from one another.
-static bool token_rows_ok(const sab_token_rows* r, int B, int L, long long row, bool out) {
+// Rows of one [B, L, H, D] tensor: pointer and strides that a tensor map takes;
+// heads and tokens apart from one another, and sequences too where the tensor is
+// written.  Strides of axes of one entry say nothing.
+static long long head_of(const sab_token_rows* r, int H, int D) { return H > 1 && r->head != 0 ? r->head : D; }
+static long long token_of(const sab_token_rows* r, int L, int H, int D) { return L > 1 ? r->token : (long long)H * D; }
+static long long batch_of(const sab_token_rows* r, int B, int H, int D) { return B > 1 ? r->batch : (long long)H * D; }
+static bool token_rows_ok(const sab_token_rows* r, int B, int L, int H, int D, bool out) {
   if (r == nullptr || r->data == nullptr || !aligned16(r->data)) return false;
   constexpr long long kMost = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
-  if (L > 1 && (r->token < row || r->token > kMost || r->token % 8 != 0)) return false;
-  if (B > 1 && (r->batch < row || r->batch > kMost || r->batch % 8 != 0)) return false;
-  if (!out || B == 1 || L == 1) return true;
-  return r->batch >= (L - 1) * r->token + row || r->token >= (B - 1) * r->batch + row;
+  struct Axis {
+    long long stride, n;
+  } axes[3] = {{head_of(r, H, D), H}, {r->token, L}, {r->batch, B}};
+  for (const Axis& a : axes)
+    if (a.n > 1 && (a.stride < D || a.stride > kMost || a.stride % 8 != 0)) return false;
+  // sequences that are only read may share tokens, as windows of one run do
+  const int nested = out ? 3 : 2;
+  for (int i = 0; i < nested; ++i)  // by stride
+    for (int k = 0; k + 1 < nested; ++k)
+      if (axes[k].stride > axes[k + 1].stride) {
+        const Axis a = axes[k];
+        axes[k] = axes[k + 1];
+        axes[k + 1] = a;
+      }
+  long long extent = D;
+  for (int i = 0; i < nested; ++i) {
+    if (axes[i].n == 1) continue;
+    if (axes[i].stride < extent) return false;
+    extent += (axes[i].n - 1) * axes[i].stride;
+  }
+  return true;
 }
-// strides of axes of one entry say nothing
-static long long batch_of(const sab_token_rows* r, int B, long long row) { return B > 1 ? r->batch : row; }
-static long long token_of(const sab_token_rows* r, int L, long long row) { return L > 1 ? r->token : row; }
 
 // Query rows: a map of tiles of `pack` heads x `tokens` tokens.
 static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D, int pack,
                               int tokens) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const long long row = (long long)H * D;
+  const size_t head = (size_t)head_of(r, H, D) * 2, token = (size_t)token_of(r, L, H, D) * 2;
+  const size_t batch = (size_t)batch_of(r, B, H, D) * 2;
   if (pack == 1)  // tokens before heads
-    return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
-                      (size_t)batch_of(r, B, row) * 2, tokens);
+    return encode_map(m, r->data, D, L, H, B, token, head, batch, tokens);
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)token_of(r, L, row) * 2,
-                                 (cuuint64_t)batch_of(r, B, row) * 2};
+  const cuuint64_t strides[3] = {head, token, batch};
   const cuuint32_t box[4] = {64, (cuuint32_t)pack, (cuuint32_t)tokens, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1229,9 +1246,8 @@ static bool encode_query_rows(CUtensorMap* m, const sab_token_rows* r, int B, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 static bool encode_key_rows(CUtensorMap* m, const sab_token_rows* r, int B, int L, int H, int D) {
-  const long long row = (long long)H * D;
-  return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, row) * 2, (size_t)D * 2,
-                    (size_t)batch_of(r, B, row) * 2);
+  return encode_map(m, r->data, D, L, H, B, (size_t)token_of(r, L, H, D) * 2, (size_t)head_of(r, H, D) * 2,
+                    (size_t)batch_of(r, B, H, D) * 2);
 }
 
 // Heads of one tile of `rows` query rows: the number, among those that divide
@@ -1262,9 +1278,11 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
                                const sab_token_rows* O, float* LSE, void* stream) {
   if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
   const sab_cross_desc& d = *desc;
-  const long long qrow = (long long)d.heads * d.head_dim, krow = (long long)d.kv_heads * d.head_dim;
-  if (!token_rows_ok(Q, d.batch, d.q_tokens, qrow, false) || !token_rows_ok(K, d.kv_batch, d.kv_tokens, krow, false) ||
-      !token_rows_ok(V, d.kv_batch, d.kv_tokens, krow, false) || !token_rows_ok(O, d.batch, d.q_tokens, qrow, true))
+  const int D = d.head_dim;
+  if (!token_rows_ok(Q, d.batch, d.q_tokens, d.heads, D, false) ||
+      !token_rows_ok(K, d.kv_batch, d.kv_tokens, d.kv_heads, D, false) ||
+      !token_rows_ok(V, d.kv_batch, d.kv_tokens, d.kv_heads, D, false) ||
+      !token_rows_ok(O, d.batch, d.q_tokens, d.heads, D, true))
     return SAB_ERR_INVALID_ARG;
   if (O->data == Q->data || O->data == K->data || O->data == V->data || !aligned4(q_len) || !aligned4(kv_len) ||
       !aligned16(LSE))
@@ -1274,8 +1292,9 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.q_len = q_len;
   p.kv_len = kv_len;
   p.O = static_cast<uint16_t*>(O->data);
-  p.o_batch = batch_of(O, d.batch, qrow);
-  p.o_token = token_of(O, d.q_tokens, qrow);
+  p.o_batch = batch_of(O, d.batch, d.heads, D);
+  p.o_token = token_of(O, d.q_tokens, d.heads, D);
+  p.o_head = head_of(O, d.heads, D);
   p.LSE = LSE;
   p.B = d.batch;
   p.Bk = d.kv_batch;
@@ -1353,16 +1372,16 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
                                         void* workspace, size_t ws_bytes, void* stream) {
   if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
   const sab_cross_desc& d = *desc;
-  const long long qrow = (long long)d.heads * d.head_dim, krow = (long long)d.kv_heads * d.head_dim;
+  const int B = d.batch, L = d.q_tokens, H = d.heads, Hk = d.kv_heads, D = d.head_dim;
   const sab_token_rows* in[] = {Q, O, dO, K, V};
   const sab_token_rows* out[] = {dQ, dK, dV};
   for (int i = 0; i < 5; ++i)
-    if (!(i < 3 ? token_rows_ok(in[i], d.batch, d.q_tokens, qrow, false)
-                : token_rows_ok(in[i], d.kv_batch, d.kv_tokens, krow, false)))
+    if (!(i < 3 ? token_rows_ok(in[i], B, L, H, D, false)
+                : token_rows_ok(in[i], d.kv_batch, d.kv_tokens, Hk, D, false)))
       return SAB_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i) {
-    if (!(i < 1 ? token_rows_ok(out[i], d.batch, d.q_tokens, qrow, true)
-                : token_rows_ok(out[i], d.kv_batch, d.kv_tokens, krow, true)))
+    if (!(i < 1 ? token_rows_ok(out[i], B, L, H, D, true)
+                : token_rows_ok(out[i], d.kv_batch, d.kv_tokens, Hk, D, true)))
       return SAB_ERR_INVALID_ARG;
     for (const sab_token_rows* x : in)
       if (x->data == out[i]->data) return SAB_ERR_INVALID_ARG;
@@ -1400,19 +1419,22 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.delta = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.delta_bytes);
   p.O = static_cast<uint16_t*>(O->data);  // read
-  p.o_batch = batch_of(O, d.batch, qrow);
-  p.o_token = token_of(O, d.q_tokens, qrow);
+  p.o_batch = batch_of(O, d.batch, d.heads, D);
+  p.o_token = token_of(O, d.q_tokens, d.heads, D);
+  p.o_head = head_of(O, d.heads, D);
   p.dQ = static_cast<uint16_t*>(dQ->data);
   p.dK = static_cast<uint16_t*>(dK->data);
   p.dV = static_cast<uint16_t*>(dV->data);
-  p.dq_batch = batch_of(dQ, d.batch, qrow);
-  p.dq_token = token_of(dQ, d.q_tokens, qrow);
-  p.dk_batch = batch_of(dK, d.kv_batch, krow);
-  p.dk_token = token_of(dK, d.kv_tokens, krow);
-  p.dv_batch = batch_of(dV, d.kv_batch, krow);
-  p.dv_token = token_of(dV, d.kv_tokens, krow);
+  p.dq_batch = batch_of(dQ, B, H, D);
+  p.dq_token = token_of(dQ, L, H, D);
+  p.dq_head = head_of(dQ, H, D);
+  p.dk_batch = batch_of(dK, d.kv_batch, Hk, D);
+  p.dk_token = token_of(dK, d.kv_tokens, Hk, D);
+  p.dk_head = head_of(dK, Hk, D);
+  p.dv_batch = batch_of(dV, d.kv_batch, Hk, D);
+  p.dv_token = token_of(dV, d.kv_tokens, Hk, D);
+  p.dv_head = head_of(dV, Hk, D);
   p.err_word = device_error_word();
-  const int B = d.batch, L = d.q_tokens, H = d.heads, D = d.head_dim;
   if (!encode_query_rows(&p.q_map, Q, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.do_map, dO, B, L, H, D, p.pack, p.tile_tokens) ||
       !encode_query_rows(&p.of_map, O, B, L, H, D, p.pack, p.tile_tokens) ||

@@ -307,7 +307,7 @@ struct CrossParams {
   const int* q_len;          // [B] or null
   const int* kv_len;         // [Bk] or null
   uint16_t* O;
-  long long o_batch, o_token;
+  long long o_batch, o_token, o_head;
   float* LSE;                // [B, H, Lq] or null
   int B, Bk, Lq, Lk, H, D;
   int group;                 // heads that share a key head
@@ -330,7 +330,7 @@ struct CrossBwdParams : CrossParams {
   float* delta;                   // [B, H, Lq]
   float* part;                    // [shares][Bk][Hk][key tiles][dV, dK][D / 4][128][4] (several shares)
   uint16_t *dQ, *dK, *dV;
-  long long dq_batch, dq_token, dk_batch, dk_token, dv_batch, dv_token;
+  long long dq_batch, dq_token, dq_head, dk_batch, dk_token, dk_head, dv_batch, dv_token, dv_head;
 };
 
 // Launchers (return cudaError_t of the launch).

@@ -208,6 +208,27 @@ def test_strides_slices_and_rows_in_between():
             _check_forward(q[:, :1], k, v, 0.1, out[:, 2:3, 1:], None, None, None, "one token")
 
 
+def _heads_first(t, fill=None):
+    """The same [B, L, H, D] values (or `fill`) with heads before tokens in memory."""
+    B, L, H, D = t.shape
+    out = torch.empty((B, H, L, D), dtype=t.dtype, device=t.device)
+    return (out.copy_(t.transpose(1, 2)) if fill is None else out.fill_(fill)).transpose(1, 2)
+
+
+@gpu
+@pytest.mark.parametrize("B,Lq,Lk,H,Hk,D", [(2, 200, 150, 4, 2, 128), (3, 65, 300, 6, 2, 64), (1, 1, 1000, 4, 4, 128)])
+def test_heads_before_tokens(B, Lq, Lk, H, Hk, D):
+    q, k, v, _ = _case(B, Lq, Lk, H, Hk, D)
+    ref, lse_ref = _forward(q, k, v, 0.1)
+    o, lse = _heads_first(q, 7.0), torch.empty_like(lse_ref)
+    lens = [Lk] * (B - 1) + [0]
+    sab.cross_attention(_heads_first(q), _heads_first(k), _heads_first(v), 0.1, o, lse)
+    assert torch.equal(o, ref) and torch.equal(lse, lse_ref)
+    ref, lse_ref = _forward(q, k, v, 0.1, None, lens)
+    sab.cross_attention(_heads_first(q), k, _heads_first(v), 0.1, o, lse, kv_len=_lens(lens))
+    assert torch.equal(o, ref) and torch.equal(lse, lse_ref)
+
+
 @gpu
 def test_a_bad_value_stays_in_its_rows():
     q, k, v, _ = _case(1, 300, 200, 4, 4, 64)
@@ -271,8 +292,8 @@ def _desc(**kw):
     return sab.CrossDesc(*(d[n] for n, _ in sab.CrossDesc._fields_))
 
 
-def _rows(data=4096, batch=1 << 20, token=256):
-    return sab.TokenRows(data, batch, token)
+def _rows(data=4096, batch=1 << 20, token=256, head=0):
+    return sab.TokenRows(data, batch, token, head)
 
 
 SHAPE_REFUSALS = [dict(batch=0), dict(q_tokens=0), dict(kv_tokens=0), dict(heads=0), dict(kv_heads=0), dict(heads=5),
@@ -280,7 +301,8 @@ SHAPE_REFUSALS = [dict(batch=0), dict(q_tokens=0), dict(kv_tokens=0), dict(heads
                   dict(heads=258, kv_heads=2), dict(q_tokens=(1 << 30) + 1), dict(kv_tokens=(1 << 30) + 1),
                   dict(batch=-1, kv_batch=-1), dict(batch=1 << 30, kv_batch=1, heads=2, kv_heads=1)]
 ROW_REFUSALS = [dict(data=None), dict(data=4104), dict(token=260), dict(token=120), dict(batch=-8), dict(batch=100),
-                dict(token=1 << 39), dict(batch=1 << 39), dict(token=-256)]
+                dict(token=1 << 39), dict(batch=1 << 39), dict(token=-256), dict(head=-64), dict(head=68),
+                dict(head=56), dict(head=1 << 39), dict(head=256), dict(head=320, token=128)]
 
 
 def test_refusals_before_any_cuda_call():

@@ -16,8 +16,8 @@ import torch
 
 import streaming_attention_block_gb300 as sab
 from oracle import cross as OC
-from tests.test_gpu_cross import BF, RAGGED, ROW_REFUSALS, SHAPE_REFUSALS, SHAPES, _case, _desc, _lens, _np, _rows, \
-    _spoil
+from tests.test_gpu_cross import BF, RAGGED, ROW_REFUSALS, SHAPE_REFUSALS, SHAPES, _case, _desc, _heads_first, _lens, _np, \
+    _rows, _spoil
 
 gpu = pytest.mark.gpu
 
@@ -146,6 +146,18 @@ def test_strides_and_what_lies_between():
     assert all(torch.equal(a, b) for a, b in zip(out, ref))
     dq[:, 1:Lq + 1, 1:] = 7.0
     assert bool((dq == 7).all()) and bool((dkv[Lk:] == 7).all())
+
+
+@gpu
+@pytest.mark.parametrize("B,Lq,Lk,H,Hk,D", [(2, 200, 150, 4, 2, 128), (3, 65, 300, 6, 2, 64), (1, 900, 77, 4, 4, 128)])
+def test_heads_before_tokens(B, Lq, Lk, H, Hk, D):
+    q, k, v, do = _case(B, Lq, Lk, H, Hk, D)
+    for lens in (None, [Lk] * (B - 1) + [0]):
+        ref = _backward(q, k, v, do, 0.1, None, lens)
+        o, lse = _forward(q, k, v, 0.1, None, _lens(lens))
+        out = [_heads_first(t, 7.0) for t in (q, k, v)]
+        sab.cross_attention_backward(*(_heads_first(t) for t in (q, k, v, o, do)), lse, 0.1, *out, kv_len=_lens(lens))
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
 
 
 @gpu
