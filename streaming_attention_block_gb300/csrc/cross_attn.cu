@@ -38,11 +38,9 @@ constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p80f;
 constexpr float kRescale = 8.0f;  // running maxima: O is rescaled when one grows by more than 2^8
 constexpr int kRedoList = 64;     // query tiles a block remembers
 
-// The number of a query tile, counted one by one, from its item and stream.
-__device__ __forceinline__ uint32_t tile_of(const CrossParams& p, unsigned item, int st, int pair) {
-  const unsigned n = (unsigned)(p.n_qtiles + pair - 1) / (unsigned)pair;
-  const unsigned r = item / n;
-  return r * (unsigned)p.n_qtiles + (item - r * n) * (unsigned)pair + (unsigned)st;
+// The number of a query tile, counted one by one.
+__device__ __forceinline__ uint32_t tile_of(const CrossParams& p, const Spot& s, int st, int pair) {
+  return ((uint32_t)s.b * (uint32_t)p.head_blocks + (uint32_t)s.hb) * (uint32_t)p.n_qtiles + (uint32_t)(s.iq * pair + st);
 }
 
 // ------------------------------------------------------------------ forward
@@ -141,23 +139,13 @@ __device__ __noinline__ SlowSum slow_step(const CrossParams& p, uint32_t meet, v
   return SlowSum{m, l, true};
 }
 
-// Zeros and -inf for the tokens from t0 on of a query tile without a query or
-// without a key; a row for each thread.
-__device__ __noinline__ void clear_tile(const CrossParams& p, int b, int hb, int t0, int row) {
-  const int row_t = row / p.pack, head = hb * p.pack + row - row_t * p.pack, t = t0 + row_t;
-  if (row_t >= p.tile_tokens || t >= p.Lq) return;
-  uint4* o = reinterpret_cast<uint4*>(p.O + b * p.o_batch + t * p.o_token + head * p.o_head);
-#pragma unroll 1
-  for (int i = 0; i < p.D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (p.LSE != nullptr) p.LSE[((long long)b * p.H + head) * p.Lq + t] = -INFINITY;
-}
 // Puts a query tile on the list of those to be done again; called by each of its
 // rows that wants it (see the kernel for misc).
 __device__ __noinline__ void again_later(const CrossParams& p, uint32_t* misc, uint32_t* list, unsigned end,
-                                         unsigned item, int st, int pair) {
+                                         unsigned item, const uint32_t* seqs, int st, int pair) {
   if (atomicMax(&misc[4], end) >= end) return;  // another row has
   const uint32_t n = atomicAdd(&misc[2], 1u);
-  if (n < kRedoList) list[n] = tile_of(p, item, st, pair);
+  if (n < kRedoList) list[n] = tile_of(p, seqs != nullptr ? sorted_spot(p, seqs, item) : spot_of(p, item, pair), st, pair);
   else atomicMin(&misc[3], item);
 }
 
@@ -190,7 +178,8 @@ struct FwdCfg {
   static constexpr int kNumBars = kDrain + 2;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kListOff = kMiscOff + 32;
-  static constexpr uint32_t kSmemBytes = kListOff + kRedoList * 4;
+  static constexpr uint32_t kSeqsOff = kListOff + kRedoList * 4;  // [kMaxSorted + 1]
+  static constexpr uint32_t kSmemBytes = kSeqsOff + (kMaxSorted + 1) * 4;
   // K, V and Q; products of stream 0; the store of O; products of stream 1;
   // 8 softmax warps; 4 that end tiles
   static constexpr int kThreads = 32 * 16;
@@ -209,7 +198,7 @@ struct FwdCfg {
 // warps and a sum l each.  Four more warps take a finished O out while the next
 // tile's steps go on.  SPLIT: one item a block, its keys cut among the blocks of
 // a cluster (see the end).
-template <int D, bool PAIR, bool SPLIT>
+template <int D, bool PAIR, bool SPLIT, bool SORTED>
 __global__ void __launch_bounds__(FwdCfg<D, PAIR>::kThreads, 1)
 cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   using C = FwdCfg<D, PAIR>;
@@ -280,9 +269,16 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   pass.first = SPLIT ? blockIdx.x / (unsigned)p.splits : blockIdx.x;
   pass.step = SPLIT ? p.items : gridDim.x;
   pass.end = uniform<true>(*abort_flag) ? 0u : p.items;
-  pass.list = nullptr;
+  pass.list = pass.seqs = nullptr;
   pass.pair = PAIR ? 2 : 1;
   pass.split = split;
+  if (SORTED) {
+    uint32_t* seqs = reinterpret_cast<uint32_t*>(base + C::kSeqsOff);
+    sort_sequences(p, pass.pair, seqs, reinterpret_cast<uint32_t*>(base + C::kSumOff));
+    pass.seqs = seqs;
+    pass.end = min(pass.end, (unsigned)uniform<true>((int)(seqs[p.B] >> 6)));
+  }
+  const unsigned all = pass.end;
   pass.by = SPLIT ? Spot{0, 0, 0} : spot_of(p, gridDim.x, pass.pair);
   // To the next pass, after all roles are through with this one; false: done.
   auto next_pass = [&](int& number) -> bool {
@@ -305,7 +301,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       number = 2;
       pass.first = over;
       pass.step = gridDim.x;
-      pass.end = p.items;
+      pass.end = all;
       pass.list = nullptr;
       pass.pair = PAIR ? 2 : 1;
       return true;
@@ -339,7 +335,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           return true;
         };
         bool ok = true;
-        Walk<false> c;
+        Walk<false, SORTED> c;
         for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
           const Work& w = c.w;
           if (w.nt == 0) continue;
@@ -417,7 +413,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      Walk<true> ahead;  // the next item is looked up while the softmax works on this one
+      Walk<true, SORTED> ahead;  // the next item is looked up while the softmax works on this one
       ahead.start(p, pass);
       ahead.seek(p, pass);
       while (ahead.more(pass)) {
@@ -501,10 +497,17 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   } else if (warp == 2) {
     // ------------------------------------------------------- the store of O
     int tile = 0;
+    if (!SPLIT && !uniform<true>(*abort_flag)) {
+      if (p.q_len != nullptr || p.kv_len != nullptr) {
+        fill_zeros(base + C::kOOff, C::kTileBytes);
+        clear_tiles<C::kBoxes>(p, pass.pair, base_u32 + C::kOOff, p.LSE);
+      }
+      if (lane == 0) mbar_arrive(bar(C::kOFree));
+    }
     do {
       if (lane == 0 && !SPLIT) {
         bool ok = true;
-        Walk<false> c;
+        Walk<false, SORTED> c;
         for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
           const Work& w = c.w;
           if (w.nt == 0) continue;
@@ -584,7 +587,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     const std::integral_constant<int, 1> one;
     do {
       const bool slow = SPLIT || number > 0;
-      Walk<true> c;
+      Walk<true, SORTED> c;
       c.start(p, pass);
       c.seek(p, pass);
       while (ok && c.more(pass)) {
@@ -667,7 +670,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       if constexpr (!SPLIT) {
         const float inv = any_own ? 1.f / sum : 0.f;
         const float f[2] = {on[0] ? ex2(m[0] - top_own) * inv : 0.f, on[1] ? ex2(m[1] - top_own) * inv : 0.f};
-        if (tiles > 0 && !wait_warp(C::kOFree, (uint32_t)(tiles - 1) & 1u, 11)) return false;
+        if (!wait_warp(C::kOFree, (uint32_t)tiles & 1u, 11)) return false;
         ++tiles;
         float2 sound = make_float2(0.f, 0.f);  // stays 0 unless some value is not finite
 #pragma unroll 1
@@ -689,7 +692,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         }
         const bool again =
             number == 0 && live && !(sum >= kLeastSum && sum <= kMostSum && sound.x == 0.f && sound.y == 0.f);
-        if (__builtin_expect(again, 0)) again_later(p, misc, list, (unsigned)tiles, item, st, pass.pair);
+        if (__builtin_expect(again, 0)) again_later(p, misc, list, (unsigned)tiles, item, SORTED ? pass.seqs : nullptr, st, pass.pair);
         fence_proxy_async_smem();
         arrive_warp(C::kOReady);
         if (stored && p.LSE != nullptr) p.LSE[lse_at] = any_own ? (top_own + __log2f(sum)) * kLn2 : -INFINITY;
@@ -753,17 +756,12 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      Walk<true> c;
+      Walk<true, SORTED> c;
       for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
-        if (!SPLIT) {
-          if (w.nt == 0) clear_tile(p, w.b, w.hb, w.t0, row);
-          if (pass.pair == 2 && (w.nt == 0 || w.streams == 1) && w.t0 + p.tile_tokens < p.Lq)
-            clear_tile(p, w.b, w.hb, w.t0 + p.tile_tokens, row);
-          if (w.nt == 0) continue;
-        }
+        if (!SPLIT && w.nt == 0) continue;
 #pragma unroll 1
-        for (int st = 0; ok && st < w.streams; ++st) ok = finish(w, c.item(pass), st);
+        for (int st = 0; ok && st < w.streams; ++st) ok = finish(w, c.at, st);
         steps_before += w.nt;
       }
     } while (next_pass(number) && ok);
@@ -785,13 +783,13 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   }
 }
 
-template <int D, bool PAIR, bool SPLIT>
+template <int D, bool PAIR, bool SPLIT, bool SORTED>
 cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   using C = FwdCfg<D, PAIR>;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)C::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT, SORTED>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
@@ -808,15 +806,20 @@ cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, PAIR, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, PAIR, SPLIT, SORTED>, p);
+}
+
+template <int D>
+cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
+  if (p.splits > 1) return launch_fwd<D, false, true, false>(p, sms, s);
+  if (p.pair == 2) return p.sorted ? launch_fwd<D, true, false, true>(p, sms, s) : launch_fwd<D, true, false, false>(p, sms, s);
+  return p.sorted ? launch_fwd<D, false, false, true>(p, sms, s) : launch_fwd<D, false, false, false>(p, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_forward(const CrossParams& p, int sms, cudaStream_t s) {
-  if (p.splits > 1) return p.D == 128 ? launch_fwd<128, false, true>(p, sms, s) : launch_fwd<64, false, true>(p, sms, s);
-  if (p.pair == 2) return p.D == 128 ? launch_fwd<128, true, false>(p, sms, s) : launch_fwd<64, true, false>(p, sms, s);
-  return p.D == 128 ? launch_fwd<128, false, false>(p, sms, s) : launch_fwd<64, false, false>(p, sms, s);
+  return p.D == 128 ? forward<128>(p, sms, s) : forward<64>(p, sms, s);
 }
 
 }  // namespace sab

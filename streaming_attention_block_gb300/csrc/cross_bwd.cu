@@ -61,7 +61,8 @@ struct DqCfg {
   static constexpr int kDrain = 26;           // [2 warps with products]
   static constexpr int kNumBars = 28;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kSmemBytes = kMiscOff + 16;
+  static constexpr uint32_t kSeqsOff = kMiscOff + 16;  // [kMaxSorted + 1]
+  static constexpr uint32_t kSmemBytes = kSeqsOff + (kMaxSorted + 1) * 4;
   // Q, dO, dQ; S; dP and dQ's products; K and V; 8 warps for dS; 4 for delta and dQ
   static constexpr int kThreads = 32 * 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -69,7 +70,7 @@ struct DqCfg {
 // P stays in registers, so S is free for the next tile as soon as it is read, and
 // two warps issue products: one S = Q K^T, the other dP = dO V^T and, once dS is
 // over dP, dQ += dS K.  TMEM: S, dP, and dQ of two items, one being taken out.
-template <int D>
+template <int D, bool SORTED>
 __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const __grid_constant__ CrossBwdParams p) {
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t base[];
@@ -129,13 +130,23 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
   pass.first = blockIdx.x;
   pass.step = gridDim.x;
   pass.end = uniform<true>(*abort_flag) ? 0u : p.items;
-  pass.list = nullptr;
+  pass.list = pass.seqs = nullptr;
   pass.pair = 1;
   pass.split = 0;
+  if (SORTED) {
+    uint32_t* seqs = reinterpret_cast<uint32_t*>(base + C::kSeqsOff);
+    sort_sequences(p, 1, seqs, reinterpret_cast<uint32_t*>(base + C::kStatOff));
+    pass.seqs = seqs;
+    pass.end = min(pass.end, (unsigned)uniform<true>((int)(seqs[p.B] >> 6)));
+  }
   pass.by = spot_of(p, gridDim.x, 1);
 
   if (warp == 0) {
     // -------------------------------------------- Q, dO an item ahead, dQ out
+    if ((p.q_len != nullptr || p.kv_len != nullptr) && !uniform<true>(*abort_flag)) {
+      fill_zeros(base + C::kGOff, C::kTileBytes);
+      clear_tiles<C::kBoxes>(p, 1, base_u32 + C::kGOff, nullptr);
+    }
     if (lane == 0) {
       const uint32_t q_bytes = (uint32_t)(C::kBoxes * p.pack * p.tile_tokens) * 128u;
       int at[2][3];  // where the last two items are
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       };
       int item = 0, q_loads = 0;
       bool ok = true;
-      Walk<false> c, o;
+      Walk<false, SORTED> c, o;
       o.start(p, pass);
       for (c.start(p, pass); c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         ++n[which];
         return true;
       };
-      Walk<false> c;
+      Walk<false, SORTED> c;
       for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
         const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t lead = elect_lead();
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true> c;
+    Walk<true, SORTED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t lead = elect_lead();
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true> c;
+    Walk<true, SORTED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true> c;
+    Walk<true, SORTED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -459,20 +470,9 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       arrive_warp(C::kStat + (item & 1));
       return true;
     };
-    Walk<true> c;
-    auto seek = [&]() {
-      while (c.more(pass) && c.w.nt == 0) {  // no query or no key
-        if (row_t < p.tile_tokens && c.w.t0 + row_t < p.Lq) {
-          uint4* out = reinterpret_cast<uint4*>(p.dQ + c.w.b * p.dq_batch + (c.w.t0 + row_t) * p.dq_token +
-                                                (c.w.hb * p.pack + row_g) * p.dq_head);
-#pragma unroll 1
-          for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        c.next(p, pass);
-      }
-    };
+    Walk<true, SORTED> c;
     c.start(p, pass);
-    seek();
+    c.seek(p, pass);
     bool more = c.more(pass);
     Work w = c.w;
 #pragma unroll 1
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       if (item >= 0) {
         w = c.w;
         c.next(p, pass);
-        seek();
+        c.seek(p, pass);
       }
       const bool ahead = c.more(pass);
       if (ahead && !(ok = stats(c.w, item + 1))) break;
@@ -633,35 +633,38 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
   const bool dead = keys <= 0 || uniform<true>(*abort_flag) != 0;
 
   const int blocks = p.group / p.pack, seqs = p.Bk == 1 ? p.B : 1;
-  const long long all = (long long)seqs * blocks * p.n_qtiles;
+  // every shares-th tile, so that each share has its part of every sequence
   Stream first;
-  first.i = (int)(all * share / p.shares);
-  first.end = dead ? first.i : (int)(all * (share + 1) / p.shares);
+  first.i = share;
+  first.end = dead ? first.i : (int)((long long)seqs * blocks * p.n_qtiles);
+  const int by_r = p.shares / p.n_qtiles;
+  const int by_iq = p.shares - by_r * p.n_qtiles, by_b = by_r / blocks, by_hb = by_r - by_b * blocks;
   {
-    const int r = first.i / p.n_qtiles;
-    first.iq = first.i - r * p.n_qtiles;
+    const int r = share / p.n_qtiles;
+    first.iq = share - r * p.n_qtiles;
     first.b = (p.Bk == 1 ? 0 : kb) + r / blocks;
     first.hb = r % blocks;
   }
+  auto advance = [&](Stream& s) {
+    s.i += p.shares;
+    s.iq += by_iq;
+    s.hb += by_hb;
+    s.b += by_b;
+    if (s.iq >= p.n_qtiles) s.iq -= p.n_qtiles, ++s.hb;
+    if (s.hb >= blocks) s.hb -= blocks, ++s.b;
+  };
   // the next tile with a live query, from this one on
   auto seek = [&](Stream& s) {
-    for (; s.i < s.end; ++s.i) {
+    for (; s.i < s.end; advance(s)) {
       s.live = min(p.tile_tokens, length_of<true>(p.q_len, s.b, p.Lq) - s.iq * p.tile_tokens);
       if (s.live > 0) return;
-      if (++s.iq == p.n_qtiles) {
-        s.iq = 0;
-        if (++s.hb == blocks) s.hb = 0, ++s.b;
-      }
     }
   };
   auto next = [&](Stream& s) {
-    ++s.i;
-    if (++s.iq == p.n_qtiles) {
-      s.iq = 0;
-      if (++s.hb == blocks) s.hb = 0, ++s.b;
-    }
+    advance(s);
     seek(s);
   };
+
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
     const bool any = first.i < first.end;
@@ -945,15 +948,18 @@ template <int D>
 cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
   static bool set = false;
   if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)DqCfg<D>::kSmemBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(cross_dq_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)DqCfg<D>::kSmemBytes);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)DkvCfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     set = true;
   }
-  cudaError_t e = launch(cross_dq_kernel<D>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
+  cudaError_t e = launch(p.sorted ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
                          DqCfg<D>::kSmemBytes, p, s);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;

@@ -95,6 +95,57 @@ __device__ __noinline__ Spot spot_of(const CrossParams& p, unsigned item, int pa
   s.hb = (int)(r - (unsigned)s.b * (unsigned)p.head_blocks);
   return s;
 }
+// Items in the order of their key tiles, the most first, where lengths differ: a
+// block's items are every so many of them, so that in the order of the sequences
+// some blocks met the long ones and some the empty.  8 x 1023 x 777 tokens of
+// lengths up to that, 24 heads of 64: 40 us in the order of the sequences, MEAS1
+// so; 64 x 1 tokens over 4095 keys at most, 24/8 heads of 128: MEAS2.  Up to 64
+// sequences; with more each block meets many.
+//
+// seqs[i]: number of the first item of the i-th sequence in that order << 6 | the
+// sequence; seqs[B]: all items << 6.  For all threads of a block; scratch: 128
+// words.
+constexpr int kMaxSorted = 64;
+__device__ __noinline__ void sort_sequences(const CrossParams& p, int pair, uint32_t* seqs, uint32_t* scratch) {
+  const int t = threadIdx.x;
+  int nt = 0, tiles = 0;
+  if (t < p.B) {
+    const int ql = length_of<false>(p.q_len, t, p.Lq), kl = length_of<false>(p.kv_len, p.Bk == 1 ? 0 : t, p.Lk);
+    if (ql > 0 && kl > 0) {
+      nt = (kl + kTileN - 1) / kTileN;
+      tiles = (ql + pair * p.tile_tokens - 1) / (pair * p.tile_tokens);
+    }
+    scratch[t] = (uint32_t)nt;
+    scratch[kMaxSorted + t] = (uint32_t)tiles;
+  }
+  __syncthreads();
+  if (t < p.B) {
+    int rank = 0;
+    uint32_t before = 0;
+    for (int u = 0; u < p.B; ++u) {
+      const int other = (int)scratch[u];
+      if (other > nt || (other == nt && u < t)) ++rank, before += scratch[kMaxSorted + u];
+    }
+    seqs[rank] = (before * (uint32_t)p.head_blocks) << 6 | (uint32_t)t;
+    if (rank == p.B - 1) seqs[p.B] = ((before + (uint32_t)tiles) * (uint32_t)p.head_blocks) << 6;
+  }
+  __syncthreads();
+}
+__device__ __noinline__ Spot sorted_spot(const CrossParams& p, const uint32_t* seqs, unsigned item) {
+  int lo = 0, hi = p.B;  // the last sequence that begins at the item or before it
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((seqs[mid] >> 6) <= item) lo = mid;
+    else hi = mid;
+  }
+  const unsigned start = seqs[lo] >> 6, per = ((seqs[lo + 1] >> 6) - start) / (unsigned)p.head_blocks;
+  Spot s;
+  s.hb = (int)((item - start) / per);
+  s.iq = (int)(item - start - (unsigned)s.hb * per);
+  s.b = (int)(seqs[lo] & 63u);
+  return s;
+}
+
 // One or two query tiles (`streams`) of `pack` heads from head hb * pack on,
 // tile_tokens tokens each from t0 on, and the key tiles [first, first + nt).
 struct Work {
@@ -131,9 +182,42 @@ __device__ __forceinline__ Work work_at(const CrossParams& p, const Spot& s, int
   return w;
 }
 
+// Zeros for the rows of the block's share of query tiles without a query or
+// without a key: from `zeros`, a tile in shared memory that holds them, through
+// the copy engine (stores of 16 bytes a row took longer than the products of a
+// full tile: 8 x 2000 x 777 tokens, 12 heads of 128, half of the queries padding:
+// 55 us against 47 without padding).  lse: -inf for them, or null.  Whole warp.
+template <int BOXES>
+__device__ __noinline__ void clear_tiles(const CrossParams& p, int pair, uint32_t zeros, float* lse) {
+  const int lane = threadIdx.x & 31;
+  for (unsigned i = blockIdx.x; i < p.items; i += gridDim.x) {
+    const Work w = work_at<false>(p, spot_of(p, i, pair), 0, pair);
+    for (int t = w.nt == 0 ? 0 : w.streams; t < pair; ++t) {
+      const int t0 = w.t0 + t * p.tile_tokens;
+      if (t0 >= p.Lq) break;
+      if (lane == 0) {
+        for (int bx = 0; bx < BOXES; ++bx)
+          tma_store_4d(&p.o_map, zeros + bx * 128u * 128u, bx * 64, p.pack == 1 ? t0 : w.hb * p.pack,
+                       p.pack == 1 ? w.hb : t0, w.b);
+      }
+      const int tokens = min(p.tile_tokens, p.Lq - t0);
+      for (int g = 0; lse != nullptr && g < p.pack; ++g)
+        for (int k = lane; k < tokens; k += 32)
+          lse[((long long)w.b * p.H + w.hb * p.pack + g) * p.Lq + t0 + k] = -INFINITY;
+    }
+  }
+  if (lane == 0) tma_store_commit_and_wait_read();
+  __syncwarp();
+}
+// Such a tile (whole warp).
+__device__ __noinline__ void fill_zeros(uint8_t* tile, int bytes) {
+  for (int i = (threadIdx.x & 31) * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(tile + i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Coordinates of a query tile in its maps: head and token, or (one head a tile)
-// token and head.  The copy engine takes a plane of the first two axes at a
-// time: 128 planes of one row each took 3500 cycles a tile, one plane 1500.
+// token and head.
 __device__ __forceinline__ int query_c1(const CrossParams& p, const Work& w, int t) {
   return p.pack == 1 ? w.t0 + t * p.tile_tokens : w.hb * p.pack;
 }
@@ -147,12 +231,13 @@ __device__ __forceinline__ int query_c2(const CrossParams& p, const Work& w, int
 struct Pass {
   unsigned first, step, end;  // items, or places of the list
   const uint32_t* list;       // or null
+  const uint32_t* seqs;       // the sorted sequences of a sorted walk
   int pair, split;
   Spot by;                    // `step` items on
 };
-// The items of a pass in order.  Every role walks them by itself, by additions:
-// the divisions that find an item's place took 2000 cycles between two items.
-template <bool kUniform>
+// The items of a pass in order.  Every role walks them by itself, by additions
+// where their order is that of the tiles.
+template <bool kUniform, bool kSorted>
 struct Walk {
   unsigned at;
   Spot spot;
@@ -162,7 +247,15 @@ struct Walk {
   }
   __device__ __forceinline__ void start(const CrossParams& p, const Pass& a) {
     at = a.first;
-    if (at < a.end) place(p, a, spot_of(p, item(a), a.pair));
+    if (at < a.end) place(p, a, find(p, a));
+  }
+  __device__ __forceinline__ Spot find(const CrossParams& p, const Pass& a) const {
+    if (!kSorted || a.list != nullptr) return spot_of(p, item(a), a.pair);
+    Spot s = sorted_spot(p, a.seqs, at);
+    s.iq = uniform<kUniform>(s.iq);
+    s.hb = uniform<kUniform>(s.hb);
+    s.b = uniform<kUniform>(s.b);
+    return s;
   }
   __device__ __forceinline__ void place(const CrossParams& p, const Pass& a, const Spot& s) {
     spot = s;
@@ -172,8 +265,8 @@ struct Walk {
   __device__ __forceinline__ void next(const CrossParams& p, const Pass& a) {
     at += a.step;
     if (at >= a.end) return;
-    if (__builtin_expect(a.list != nullptr, 0)) {
-      place(p, a, spot_of(p, item(a), a.pair));
+    if (kSorted || __builtin_expect(a.list != nullptr, 0)) {
+      place(p, a, find(p, a));
       return;
     }
     const int n = (p.n_qtiles + a.pair - 1) >> (a.pair - 1);

@@ -1273,6 +1273,13 @@ static int cross_splits(unsigned items, int key_tiles) {
   return n;
 }
 
+// More than one item a block, of sequences that may differ in length; 64 of them
+// and 2^26 items at most (what the kernels' table of them holds).
+static int cross_sorted(const sab_cross_desc& d, const int* q_len, const int* kv_len, unsigned items) {
+  return (q_len != nullptr || kv_len != nullptr) && d.batch > 1 && d.batch <= 64 && (long long)items > device_sms() &&
+         items < (1u << 26);
+}
+
 sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
                                const sab_token_rows* V, const int* q_len, const int* kv_len, float softmax_scale,
                                const sab_token_rows* O, float* LSE, void* stream) {
@@ -1307,13 +1314,18 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.tile_tokens = kTileM / p.pack;
   p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.head_blocks = d.heads / p.pack;
-  // two query tiles an item where that leaves no SM without work
+  // Two query tiles an item, unless that takes the SMs over a third more tile
+  // times.  Measured alone and in pairs, 128 columns a head, 512 keys: one wave of
+  // tiles against two 11.4 and 13.2 us, two and two 16.9 and 14.4, three and four
+  // 22.2 and 21.3, eight and eight 48.7 and 37.4 (64 columns, 1500 keys: three and
+  // four 33.3 and 36.2, eight and eight 79.0 and 69.7).
   const long long columns = (long long)d.batch * p.head_blocks, sms = device_sms();
   const long long waves1 = (columns * p.n_qtiles + sms - 1) / sms;
   const long long waves2 = 2 * ((columns * ((p.n_qtiles + 1) / 2) + sms - 1) / sms);
-  p.pair = waves2 * 100 <= waves1 * 108 ? 2 : 1;
+  p.pair = 3 * waves2 <= 4 * waves1 ? 2 : 1;
   p.items = (unsigned)(columns * ((p.n_qtiles + p.pair - 1) / p.pair));
   p.splits = p.pair == 2 ? 1 : cross_splits(p.items, (d.kv_tokens + kTileN - 1) / kTileN);
+  p.sorted = cross_sorted(d, q_len, kv_len, p.items);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.err_word = device_error_word();
   if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
@@ -1413,6 +1425,7 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.pair = 1;
   p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
   p.splits = 1;
+  p.sorted = cross_sorted(d, q_len, kv_len, p.items);
   p.shares = b.shares;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;

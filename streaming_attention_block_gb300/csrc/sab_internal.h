@@ -315,6 +315,7 @@ struct CrossParams {
   int n_qtiles, head_blocks; // tiles along the tokens, and along the heads
   int pair;                  // query tiles of an item, which share their key tiles: 1 or 2
   unsigned items;
+  int sorted;                // sequences in the order of their keys (see sort_sequences)
   int splits;                // blocks of a cluster among which a tile's keys are cut
   float scale_log2;
   unsigned int* err_word;
