@@ -198,7 +198,7 @@ struct FwdCfg {
 // warps and a sum l each.  Four more warps take a finished O out while the next
 // tile's steps go on.  SPLIT: one item a block, its keys cut among the blocks of
 // a cluster (see the end).
-template <int D, bool PAIR, bool SPLIT, bool SORTED>
+template <int D, bool PAIR, bool SPLIT, bool RAGGED>
 __global__ void __launch_bounds__(FwdCfg<D, PAIR>::kThreads, 1)
 cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   using C = FwdCfg<D, PAIR>;
@@ -272,11 +272,12 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   pass.list = pass.seqs = nullptr;
   pass.pair = PAIR ? 2 : 1;
   pass.split = split;
-  if (SORTED) {
+  if (RAGGED && p.sorted) {
     uint32_t* seqs = reinterpret_cast<uint32_t*>(base + C::kSeqsOff);
     sort_sequences(p, pass.pair, seqs, reinterpret_cast<uint32_t*>(base + C::kSumOff));
     pass.seqs = seqs;
-    pass.end = min(pass.end, (unsigned)uniform<true>((int)(seqs[p.B] >> 6)));
+    const unsigned rounds = ((unsigned)uniform<true>((int)(seqs[p.B] >> 6)) + gridDim.x - 1) / gridDim.x;
+    if (pass.end > 0) pass.end = rounds * gridDim.x;
   }
   const unsigned all = pass.end;
   pass.by = SPLIT ? Spot{0, 0, 0} : spot_of(p, gridDim.x, pass.pair);
@@ -335,7 +336,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
           return true;
         };
         bool ok = true;
-        Walk<false, SORTED> c;
+        Walk<false, RAGGED> c;
         for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
           const Work& w = c.w;
           if (w.nt == 0) continue;
@@ -413,7 +414,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      Walk<true, SORTED> ahead;  // the next item is looked up while the softmax works on this one
+      Walk<true, RAGGED> ahead;  // the next item is looked up while the softmax works on this one
       ahead.start(p, pass);
       ahead.seek(p, pass);
       while (ahead.more(pass)) {
@@ -497,17 +498,15 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   } else if (warp == 2) {
     // ------------------------------------------------------- the store of O
     int tile = 0;
-    if (!SPLIT && !uniform<true>(*abort_flag)) {
-      if (p.q_len != nullptr || p.kv_len != nullptr) {
-        fill_zeros(base + C::kOOff, C::kTileBytes);
-        clear_tiles<C::kBoxes>(p, pass.pair, base_u32 + C::kOOff, p.LSE);
-      }
-      if (lane == 0) mbar_arrive(bar(C::kOFree));
+    if (RAGGED && !uniform<true>(*abort_flag)) {
+      fill_zeros(base + C::kOOff, C::kTileBytes);
+      clear_tiles<C::kBoxes>(p, pass.pair, base_u32 + C::kOOff, p.LSE);
     }
+    if (!SPLIT && lane == 0) mbar_arrive(bar(C::kOFree));
     do {
       if (lane == 0 && !SPLIT) {
         bool ok = true;
-        Walk<false, SORTED> c;
+        Walk<false, RAGGED> c;
         for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
           const Work& w = c.w;
           if (w.nt == 0) continue;
@@ -587,7 +586,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     const std::integral_constant<int, 1> one;
     do {
       const bool slow = SPLIT || number > 0;
-      Walk<true, SORTED> c;
+      Walk<true, RAGGED> c;
       c.start(p, pass);
       c.seek(p, pass);
       while (ok && c.more(pass)) {
@@ -692,7 +691,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
         }
         const bool again =
             number == 0 && live && !(sum >= kLeastSum && sum <= kMostSum && sound.x == 0.f && sound.y == 0.f);
-        if (__builtin_expect(again, 0)) again_later(p, misc, list, (unsigned)tiles, item, SORTED ? pass.seqs : nullptr, st, pass.pair);
+        if (__builtin_expect(again, 0)) again_later(p, misc, list, (unsigned)tiles, item, pass.seqs, st, pass.pair);
         fence_proxy_async_smem();
         arrive_warp(C::kOReady);
         if (stored && p.LSE != nullptr) p.LSE[lse_at] = any_own ? (top_own + __log2f(sum)) * kLn2 : -INFINITY;
@@ -756,7 +755,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
       return true;
     };
     do {
-      Walk<true, SORTED> c;
+      Walk<true, RAGGED> c;
       for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
         if (!SPLIT && w.nt == 0) continue;
@@ -783,12 +782,12 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
   }
 }
 
-template <int D, bool PAIR, bool SPLIT, bool SORTED>
+template <int D, bool PAIR, bool SPLIT, bool RAGGED>
 cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   using C = FwdCfg<D, PAIR>;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT, SORTED>,
+    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT, RAGGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set = true;
@@ -806,14 +805,15 @@ cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, PAIR, SPLIT, SORTED>, p);
+  return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, PAIR, SPLIT, RAGGED>, p);
 }
 
 template <int D>
 cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
   if (p.splits > 1) return launch_fwd<D, false, true, false>(p, sms, s);
-  if (p.pair == 2) return p.sorted ? launch_fwd<D, true, false, true>(p, sms, s) : launch_fwd<D, true, false, false>(p, sms, s);
-  return p.sorted ? launch_fwd<D, false, false, true>(p, sms, s) : launch_fwd<D, false, false, false>(p, sms, s);
+  const bool ragged = p.q_len != nullptr || p.kv_len != nullptr;
+  if (p.pair == 2) return ragged ? launch_fwd<D, true, false, true>(p, sms, s) : launch_fwd<D, true, false, false>(p, sms, s);
+  return ragged ? launch_fwd<D, false, false, true>(p, sms, s) : launch_fwd<D, false, false, false>(p, sms, s);
 }
 
 }  // namespace

@@ -70,7 +70,7 @@ struct DqCfg {
 // P stays in registers, so S is free for the next tile as soon as it is read, and
 // two warps issue products: one S = Q K^T, the other dP = dO V^T and, once dS is
 // over dP, dQ += dS K.  TMEM: S, dP, and dQ of two items, one being taken out.
-template <int D, bool SORTED>
+template <int D, bool RAGGED>
 __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const __grid_constant__ CrossBwdParams p) {
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t base[];
@@ -133,17 +133,18 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
   pass.list = pass.seqs = nullptr;
   pass.pair = 1;
   pass.split = 0;
-  if (SORTED) {
+  if (RAGGED && p.sorted) {
     uint32_t* seqs = reinterpret_cast<uint32_t*>(base + C::kSeqsOff);
     sort_sequences(p, 1, seqs, reinterpret_cast<uint32_t*>(base + C::kStatOff));
     pass.seqs = seqs;
-    pass.end = min(pass.end, (unsigned)uniform<true>((int)(seqs[p.B] >> 6)));
+    const unsigned rounds = ((unsigned)uniform<true>((int)(seqs[p.B] >> 6)) + gridDim.x - 1) / gridDim.x;
+    if (pass.end > 0) pass.end = rounds * gridDim.x;
   }
   pass.by = spot_of(p, gridDim.x, 1);
 
   if (warp == 0) {
     // -------------------------------------------- Q, dO an item ahead, dQ out
-    if ((p.q_len != nullptr || p.kv_len != nullptr) && !uniform<true>(*abort_flag)) {
+    if (RAGGED && !uniform<true>(*abort_flag)) {
       fill_zeros(base + C::kGOff, C::kTileBytes);
       clear_tiles<C::kBoxes>(p, 1, base_u32 + C::kGOff, nullptr);
     }
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       };
       int item = 0, q_loads = 0;
       bool ok = true;
-      Walk<false, SORTED> c, o;
+      Walk<false, RAGGED> c, o;
       o.start(p, pass);
       for (c.start(p, pass); c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         ++n[which];
         return true;
       };
-      Walk<false, SORTED> c;
+      Walk<false, RAGGED> c;
       for (c.start(p, pass); ok && c.more(pass); c.next(p, pass)) {
         const Work& w = c.w;
         const int head = w.hb * p.pack / p.group, kb = p.Bk == 1 ? 0 : w.b;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t lead = elect_lead();
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true, SORTED> c;
+    Walk<true, RAGGED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const uint32_t lead = elect_lead();
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true, SORTED> c;
+    Walk<true, RAGGED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     int n = 0, item = 0;
     bool ok = true;
-    Walk<true, SORTED> c;
+    Walk<true, RAGGED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       arrive_warp(C::kStat + (item & 1));
       return true;
     };
-    Walk<true, SORTED> c;
+    Walk<true, RAGGED> c;
     c.start(p, pass);
     c.seek(p, pass);
     bool more = c.more(pass);
@@ -959,7 +960,8 @@ cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set = true;
   }
-  cudaError_t e = launch(p.sorted ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
+  const bool ragged = p.q_len != nullptr || p.kv_len != nullptr;
+  cudaError_t e = launch(ragged ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
                          DqCfg<D>::kSmemBytes, p, s);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;

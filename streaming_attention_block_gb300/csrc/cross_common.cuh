@@ -97,10 +97,10 @@ __device__ __noinline__ Spot spot_of(const CrossParams& p, unsigned item, int pa
 }
 // Items in the order of their key tiles, the most first, where lengths differ: a
 // block's items are every so many of them, so that in the order of the sequences
-// some blocks met the long ones and some the empty.  8 x 1023 x 777 tokens of
-// lengths up to that, 24 heads of 64: 40 us in the order of the sequences, MEAS1
-// so; 64 x 1 tokens over 4095 keys at most, 24/8 heads of 128: MEAS2.  Up to 64
-// sequences; with more each block meets many.
+// some blocks met the long ones and some the empty.  Means of five draws of
+// lengths, in the order of the sequences and in this one: 8 x 1023 queries over 777
+// keys, 24/4 heads of 64, 40.5 and 30.6 us; 64 x 1 over 4095, 24/8 heads of 128,
+// 103.8 and 95.4 us.  Up to 64 sequences; with more each block meets many.
 //
 // seqs[i]: number of the first item of the i-th sequence in that order << 6 | the
 // sequence; seqs[B]: all items << 6.  For all threads of a block; scratch: 128
@@ -115,6 +115,8 @@ __device__ __noinline__ void sort_sequences(const CrossParams& p, int pair, uint
       nt = (kl + kTileN - 1) / kTileN;
       tiles = (ql + pair * p.tile_tokens - 1) / (pair * p.tile_tokens);
     }
+  }
+  if (t < kMaxSorted) {
     scratch[t] = (uint32_t)nt;
     scratch[kMaxSorted + t] = (uint32_t)tiles;
   }
@@ -122,16 +124,30 @@ __device__ __noinline__ void sort_sequences(const CrossParams& p, int pair, uint
   if (t < p.B) {
     int rank = 0;
     uint32_t before = 0;
-    for (int u = 0; u < p.B; ++u) {
-      const int other = (int)scratch[u];
-      if (other > nt || (other == nt && u < t)) ++rank, before += scratch[kMaxSorted + u];
+    auto count = [&](int u, uint32_t other, uint32_t its) {
+      if ((int)other > nt || ((int)other == nt && u < t)) ++rank, before += its;
+    };
+#pragma unroll 2
+    for (int u = 0; u < p.B; u += 4) {
+      const uint4 a = *reinterpret_cast<const uint4*>(scratch + u);
+      const uint4 c = *reinterpret_cast<const uint4*>(scratch + kMaxSorted + u);
+      count(u, a.x, c.x);
+      count(u + 1, a.y, c.y);
+      count(u + 2, a.z, c.z);
+      count(u + 3, a.w, c.w);
     }
     seqs[rank] = (before * (uint32_t)p.head_blocks) << 6 | (uint32_t)t;
     if (rank == p.B - 1) seqs[p.B] = ((before + (uint32_t)tiles) * (uint32_t)p.head_blocks) << 6;
   }
   __syncthreads();
 }
-__device__ __noinline__ Spot sorted_spot(const CrossParams& p, const uint32_t* seqs, unsigned item) {
+// The item of a place of a block's walk, whose every other round of gridDim.x
+// items goes backwards: who has the longest of one has the shortest of the next.
+// b < 0: there is none (the last round is not full).
+__device__ __noinline__ Spot sorted_spot(const CrossParams& p, const uint32_t* seqs, unsigned at) {
+  const unsigned round = at / gridDim.x, by = at - round * gridDim.x;
+  const unsigned item = round & 1u ? at - by + (gridDim.x - 1u - by) : at;
+  if (item >= seqs[p.B] >> 6) return Spot{0, 0, -1};
   int lo = 0, hi = p.B;  // the last sequence that begins at the item or before it
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -231,13 +247,13 @@ __device__ __forceinline__ int query_c2(const CrossParams& p, const Work& w, int
 struct Pass {
   unsigned first, step, end;  // items, or places of the list
   const uint32_t* list;       // or null
-  const uint32_t* seqs;       // the sorted sequences of a sorted walk
+  const uint32_t* seqs;       // sorted sequences, or null
   int pair, split;
   Spot by;                    // `step` items on
 };
 // The items of a pass in order.  Every role walks them by itself, by additions
 // where their order is that of the tiles.
-template <bool kUniform, bool kSorted>
+template <bool kUniform, bool kRagged>
 struct Walk {
   unsigned at;
   Spot spot;
@@ -250,7 +266,7 @@ struct Walk {
     if (at < a.end) place(p, a, find(p, a));
   }
   __device__ __forceinline__ Spot find(const CrossParams& p, const Pass& a) const {
-    if (!kSorted || a.list != nullptr) return spot_of(p, item(a), a.pair);
+    if (!kRagged || a.list != nullptr || a.seqs == nullptr) return spot_of(p, item(a), a.pair);
     Spot s = sorted_spot(p, a.seqs, at);
     s.iq = uniform<kUniform>(s.iq);
     s.hb = uniform<kUniform>(s.hb);
@@ -259,13 +275,17 @@ struct Walk {
   }
   __device__ __forceinline__ void place(const CrossParams& p, const Pass& a, const Spot& s) {
     spot = s;
+    if (kRagged && s.b < 0) {
+      w.nt = w.live = 0;
+      return;
+    }
     w = work_at<kUniform>(p, spot, a.split, a.pair);
   }
   __device__ __forceinline__ bool more(const Pass& a) const { return at < a.end; }
   __device__ __forceinline__ void next(const CrossParams& p, const Pass& a) {
     at += a.step;
     if (at >= a.end) return;
-    if (kSorted || __builtin_expect(a.list != nullptr, 0)) {
+    if ((kRagged && a.seqs != nullptr) || __builtin_expect(a.list != nullptr, 0)) {
       place(p, a, find(p, a));
       return;
     }
