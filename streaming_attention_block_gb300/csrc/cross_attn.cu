@@ -1,5 +1,5 @@
 // Cross attention: one sequence's queries over another's keys and values (an
-// encoder's states), forward and backward, for sm_103a.
+// encoder's states), for sm_103a.
 //
 // For query row i of head h and the first kv_len[b] keys of head h / (H / Hk):
 //   s_ij = scale * q_i.k_j,  O_i = sum_j softmax_j(s_ij) v_j,
@@ -40,7 +40,8 @@ constexpr int kRedoList = 64;     // query tiles a block remembers
 
 // The number of a query tile, counted one by one.
 __device__ __forceinline__ uint32_t tile_of(const CrossParams& p, const Spot& s, int st, int pair) {
-  return ((uint32_t)s.b * (uint32_t)p.head_blocks + (uint32_t)s.hb) * (uint32_t)p.n_qtiles + (uint32_t)(s.iq * pair + st);
+  const uint32_t column = (uint32_t)s.b * (uint32_t)p.head_blocks + (uint32_t)s.hb;
+  return column * (uint32_t)p.n_qtiles + (uint32_t)(s.iq * pair + st);
 }
 
 // ------------------------------------------------------------------ forward
@@ -145,8 +146,12 @@ __device__ __noinline__ void again_later(const CrossParams& p, uint32_t* misc, u
                                          unsigned item, const uint32_t* seqs, int st, int pair) {
   if (atomicMax(&misc[4], end) >= end) return;  // another row has
   const uint32_t n = atomicAdd(&misc[2], 1u);
-  if (n < kRedoList) list[n] = tile_of(p, seqs != nullptr ? sorted_spot(p, seqs, item) : spot_of(p, item, pair), st, pair);
-  else atomicMin(&misc[3], item);
+  if (n < kRedoList) {
+    const Spot s = seqs != nullptr ? sorted_spot(p, seqs, item) : spot_of(p, item, pair);
+    list[n] = tile_of(p, s, st, pair);
+  } else {
+    atomicMin(&misc[3], item);
+  }
 }
 
 template <int D_, bool PAIR>
@@ -193,7 +198,7 @@ struct FwdCfg {
 // each.  A stream has its own scores S (P goes over them), its own accumulator O
 // and its own warp that issues the products, in the order S, PV, S, PV ...: with
 // one warp for both, which has to ask some four barriers a step, the tensor cores
-// waited for that warp (1800 cycles a step for 1024 of products; 1400 with two).
+// waited for that warp (1800 cycles a step for 1024 of products; 1270 with two).
 // Softmax: the keys [0, 64) and [64, 128) of a tile are two halves with four
 // warps and a sum l each.  Four more warps take a finished O out while the next
 // tile's steps go on.  SPLIT: one item a block, its keys cut among the blocks of
@@ -785,13 +790,9 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
 template <int D, bool PAIR, bool SPLIT, bool RAGGED>
 cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
   using C = FwdCfg<D, PAIR>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, PAIR, SPLIT, RAGGED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<unsigned long long> ready;
+  const cudaError_t e = allow_smem(cross_fwd_kernel<D, PAIR, SPLIT, RAGGED>, C::kSmemBytes, ready);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(SPLIT ? p.items * (unsigned)p.splits : (p.items < (unsigned)sms ? p.items : (unsigned)sms), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
@@ -811,9 +812,9 @@ cudaError_t launch_fwd(const CrossParams& p, int sms, cudaStream_t s) {
 template <int D>
 cudaError_t forward(const CrossParams& p, int sms, cudaStream_t s) {
   if (p.splits > 1) return launch_fwd<D, false, true, false>(p, sms, s);
-  const bool ragged = p.q_len != nullptr || p.kv_len != nullptr;
-  if (p.pair == 2) return ragged ? launch_fwd<D, true, false, true>(p, sms, s) : launch_fwd<D, true, false, false>(p, sms, s);
-  return ragged ? launch_fwd<D, false, false, true>(p, sms, s) : launch_fwd<D, false, false, false>(p, sms, s);
+  if (p.q_len != nullptr || p.kv_len != nullptr)
+    return p.pair == 2 ? launch_fwd<D, true, false, true>(p, sms, s) : launch_fwd<D, false, false, true>(p, sms, s);
+  return p.pair == 2 ? launch_fwd<D, true, false, false>(p, sms, s) : launch_fwd<D, false, false, false>(p, sms, s);
 }
 
 }  // namespace

@@ -9,8 +9,8 @@
 // so that these sums are formed in the accumulators.  Key tiles are few, so the
 // queries of one are cut among several blocks, whose parts cross_sum_kernel adds
 // in order: no atomics, equal calls give equal bits.  S and dP are formed in both
-// kernels (14 D products a pair for the 10 D of one), which costs less than
-// sending dQ's parts, one for each key tile, through memory.
+// kernels: 14 D products a pair for the 10 D of one, whose dQ would go through
+// memory in fp32 parts, one for each key tile.
 #include <math.h>
 
 #include "cross_common.cuh"
@@ -432,8 +432,9 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         for (int i = 0; i < 8; ++i) {
           const int r = quad * 32 + (s0 + i) * kRows + sub;
           const int rt = (int)((uint32_t)r * inv >> 16), rg = r - rt * p.pack;
-          a[i] = rt < w.live && rt < p.tile_tokens ? *reinterpret_cast<const uint4*>(o_base + rt * p.o_token + rg * p.o_head)
-                                                   : make_uint4(0u, 0u, 0u, 0u);
+          a[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rt < w.live && rt < p.tile_tokens)
+            a[i] = *reinterpret_cast<const uint4*>(o_base + rt * p.o_token + rg * p.o_head);
         }
         if (s0 == 0 && !wait_warp(C::kGFull + (item & 1), (uint32_t)(item >> 1) & 1u, 14)) return false;
         float d[8];
@@ -918,7 +919,8 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ 
   if (key >= p.Lk) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (key < length_of<false>(p.kv_len, kb, p.Lk)) {
-    const float4* from = reinterpret_cast<const float4*>(p.part) + ((long long)unit * 2 + which) * (kTileN * D / 4) + at;
+    const float4* from =
+        reinterpret_cast<const float4*>(p.part) + ((long long)unit * 2 + which) * (kTileN * D / 4) + at;
 #pragma unroll 4
     for (int s = 0; s < p.shares; ++s) {
       const float4 x = __ldcg(from + (long long)s * units * 2 * (kTileN * D / 4));
@@ -931,7 +933,10 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ 
 }
 
 template <typename K>
-cudaError_t launch(K kernel, unsigned blocks, int threads, size_t smem, const CrossBwdParams& p, cudaStream_t s) {
+cudaError_t launch(K* kernel, unsigned blocks, int threads, size_t smem, std::atomic<unsigned long long>& ready,
+                   const CrossBwdParams& p, cudaStream_t s) {
+  const cudaError_t e = allow_smem(kernel, smem, ready);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, 1, 1);
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -947,27 +952,17 @@ cudaError_t launch(K kernel, unsigned blocks, int threads, size_t smem, const Cr
 
 template <int D>
 cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)DqCfg<D>::kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(cross_dq_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)DqCfg<D>::kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)DkvCfg<D>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  static std::atomic<unsigned long long> dq_ready[2], dkv_ready, sum_ready;
   const bool ragged = p.q_len != nullptr || p.kv_len != nullptr;
-  cudaError_t e = launch(ragged ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, p.items < (unsigned)sms ? p.items : (unsigned)sms, DqCfg<D>::kThreads,
-                         DqCfg<D>::kSmemBytes, p, s);
+  const unsigned blocks = p.items < (unsigned)sms ? p.items : (unsigned)sms;
+  cudaError_t e = launch(ragged ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, blocks, DqCfg<D>::kThreads,
+                         DqCfg<D>::kSmemBytes, dq_ready[ragged], p, s);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;
-  e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, p, s);
+  e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, dkv_ready, p,
+             s);
   if (e != cudaSuccess || p.shares == 1) return e;
-  return launch(cross_sum_kernel<D>, units * 2 * (D / 4 * kTileN / 256), 256, 0, p, s);
+  return launch(cross_sum_kernel<D>, units * 2 * (D / 4 * kTileN / 256), 256, 0, sum_ready, p, s);
 }
 
 }  // namespace

@@ -1,5 +1,8 @@
-// What the cross-attention kernels share: bounded waits, ring places, lengths.
+// What the cross-attention kernels share: bounded waits, ring places, lengths,
+// the order of the work.
 #pragma once
+
+#include <atomic>
 
 #include "ptx.cuh"
 #include "sab_internal.h"
@@ -80,6 +83,17 @@ __device__ __forceinline__ int uniform(int x) {
 template <bool kUniform>
 __device__ __forceinline__ int length_of(const int* lens, int b, int most) {
   return lens == nullptr ? most : uniform<kUniform>(min(max(__ldg(lens + b), 0), most));
+}
+
+// A kernel's shared memory limit, set once for each device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<unsigned long long>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev <= 63 && (ready.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev <= 63) ready.fetch_or(1ull << dev);
+  return e;
 }
 
 // Where an item is: its query tiles, head block and sequence.
@@ -227,7 +241,8 @@ __device__ __noinline__ void clear_tiles(const CrossParams& p, int pair, uint32_
 }
 // Such a tile (whole warp).
 __device__ __noinline__ void fill_zeros(uint8_t* tile, int bytes) {
-  for (int i = (threadIdx.x & 31) * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(tile + i) = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = (threadIdx.x & 31) * 16; i < bytes; i += 512)
+    *reinterpret_cast<uint4*>(tile + i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
 }
