@@ -58,8 +58,9 @@ struct DqCfg {
   static constexpr int kRead = 20;            // [2] dQ is taken out
   static constexpr int kStat = 22;            // [2] LSE and delta are there
   static constexpr int kSeen = 24;            // [2] all warps for dS have them
-  static constexpr int kDrain = 26;           // [2 warps with products]
-  static constexpr int kNumBars = 28;
+  static constexpr int kMeet = 26;            // [4 quadrants] the two warps of a row
+  static constexpr int kDrain = 30;           // [2 warps with products]
+  static constexpr int kNumBars = 32;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kSeqsOff = kMiscOff + 16;  // [kMaxSorted + 1]
   static constexpr uint32_t kSmemBytes = kSeqsOff + (kMaxSorted + 1) * 4;
@@ -67,10 +68,101 @@ struct DqCfg {
   static constexpr int kThreads = 32 * 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+// dS of an item with one key tile, for one warp of those for dS (64 keys): delta
+// is formed here, from all of its row, as sum_j P_ij dP_ij.  O needs not be read,
+// and with few keys its rounding showed in delta (6 keys: error of dQ 2.9e-3 of
+// its norm, 2.35e-3 so).  A function of its own: its code would lie in the way of
+// the longer items' (2 to 5 % of their time).  2 x 30720 queries over 77 keys, 12
+// heads of 128: 280 us for all gradients with O read, 248 so.
+template <int D>
+__device__ __noinline__ bool one_tile(const CrossBwdParams& p, uint32_t bars, volatile int* abort_flag, float2* stat,
+                                      uint32_t n, uint32_t item, uint32_t meets, uint32_t tS, int keys, int b, int hb,
+                                      int t0) {
+  using C = DqCfg<D>;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, cg = (int)(threadIdx.x >> 7) - 1;
+  auto wait = [&](int i, uint32_t parity, unsigned site) -> bool {
+    return __all_sync(0xffffffffu, wait_bounded(bars + 8u * (uint32_t)i, parity & 1u, abort_flag, site, p.err_word));
+  };
+  auto arrive = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8u * (uint32_t)i);
+  };
+  const uint32_t tG = tS + 128u;
+  const int hi = keys - cg * 64;  // this half's keys
+  const float lse = stat->x;
+  arrive(C::kSeen + (int)(item & 1u));
+  if (!wait(C::kSFull, n, 11) || !wait(C::kPFull, n, 12)) return false;
+  tc_fence_after();
+  // 32 columns of P and dP; zeros past the end, where they may be no numbers
+  auto take = [&](int cc, float2 (&pr)[16], uint32_t (&g)[32]) {
+    uint32_t v[32];
+    tmem_ld32(tS + 32 * cc, v);
+    tmem_ld32(tG + 32 * cc, g);
+    tmem_wait_ld();
+    const int left = hi - 32 * cc;
+    if (left < 32) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        v[k] = k < left ? v[k] : 0xff800000u;
+        g[k] = k < left ? g[k] : 0u;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
+                                  make_float2(p.scale_log2, p.scale_log2), make_float2(lse, lse));
+      pr[k] = make_float2(ex2(x.x), ex2(x.y));
+    }
+  };
+  float2 pr[16];
+  uint32_t g[32];
+  float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int cc = 0; cc < 2; ++cc) {
+    take(cc, pr, g);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      acc = __ffma2_rn(pr[k], make_float2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1])), acc);
+  }
+  // the halves of a row meet where longer items have LSE and delta, once all have read LSE
+  if (!wait(C::kSeen + (int)(item & 1u), item >> 1, 13)) return false;
+  float* meet = reinterpret_cast<float*>(stat);
+  meet[cg] = acc.x + acc.y;
+  arrive(C::kMeet + quad);
+  if (!wait(C::kMeet + quad, meets, 16)) return false;
+  const float delta = meet[0] + meet[1];
+  const float2 nd = make_float2(-delta, -delta);
+  const float one = keys == 1 ? 0.f : 1.f;  // one key: P is 1 whatever its score is
+#pragma unroll 1
+  for (int cc = 0; cc < 2; ++cc) {
+    take(cc, pr, g);
+    uint32_t o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = __fmul2_rn(
+          __fmul2_rn(pr[k], __fadd2_rn(make_float2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1])), nd)),
+          make_float2(one, one));
+      o[k] = pack_bf16(x.x, x.y);
+    }
+    tmem_st16(tG + 16 * cc, o);
+  }
+  tmem_wait_st();
+  tc_fence_before();
+  arrive(C::kSRead);
+  arrive(C::kGrad);
+  if (cg == 0 && lse > -INFINITY) {
+    const int row = quad * 32 + lane, row_t = row / p.pack, head = hb * p.pack + row - row_t * p.pack;
+    p.delta[((long long)b * p.H + head) * p.Lq + t0 + row_t] = delta;
+  }
+  __syncwarp();
+  return true;
+}
+
 // P stays in registers, so S is free for the next tile as soon as it is read, and
 // two warps issue products: one S = Q K^T, the other dP = dO V^T and, once dS is
 // over dP, dQ += dS K.  TMEM: S, dP, and dQ of two items, one being taken out.
-template <int D, bool RAGGED>
+// SHORT: items may have one key tile; RAGGED: lengths of sequences are given.
+template <int D, bool SHORT, bool RAGGED>
 __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const __grid_constant__ CrossBwdParams p) {
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t base[];
@@ -97,6 +189,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     mbar_init(bar(C::kSRead), 8);
     mbar_init(bar(C::kPFull), 1);
     mbar_init(bar(C::kGrad), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(C::kMeet + i), 2);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(C::kFull + i), 1);
       mbar_init(bar(C::kEmpty + i), 1);
@@ -187,7 +280,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         // after it is loaded by the warps for delta: both are brought near
         for (int bx = 0; bx < C::kBoxes; ++bx) {
           tma_prefetch_4d(&p.q_map, bx * 64, c1, c2, w.b);
-          if (o.more(pass) && o.w.nt > 0)
+          if (o.more(pass) && o.w.nt > (SHORT ? 1 : 0))
             tma_prefetch_4d(&p.of_map, bx * 64, query_c1(p, o.w, 0), query_c2(p, o.w, 0), o.w.b);
         }
         if (item >= 2 && !(ok = wait(C::kQFree, (uint32_t)(item - 2) & 1u, 0))) break;
@@ -341,19 +434,25 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     const int cg = (warp - 4) >> 2, quad = warp & 3;  // 64 keys each
     const int row = quad * 32 + lane;
     const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)cg * 64u, tG = tS + 128u;
-    const float2* stat = reinterpret_cast<const float2*>(base + C::kStatOff);
+    float2* stat = reinterpret_cast<float2*>(base + C::kStatOff) + row;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    int n = 0, item = 0;
+    int n = 0, item = 0, meets = 0;
     bool ok = true;
     Walk<true, RAGGED> c;
     c.start(p, pass);
     c.seek(p, pass);
     while (ok && c.more(pass)) {
-      const int nt = c.w.nt, keys = c.w.keys;
+      const int nt = c.w.nt, keys = c.w.keys, b = c.w.b, hb = c.w.hb, t0 = c.w.t0;
       c.next(p, pass);
       c.seek(p, pass);
       if (!(ok = wait_warp(C::kStat + (item & 1), (uint32_t)(item >> 1) & 1u, 10))) break;
-      const float2 st = stat[(item & 1) * 128 + row];
+      if (SHORT && nt == 1) {
+        ok = one_tile<D>(p, base_u32 + C::kBarOff, abort_flag, stat + (item & 1) * 128, (uint32_t)n, (uint32_t)item,
+                         (uint32_t)meets, tS, keys, b, hb, t0);
+        ++n, ++item, ++meets;
+        continue;
+      }
+      const float2 st = stat[(item & 1) * 128];
       arrive_warp(C::kSeen + (item & 1));
       const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
       for (int j = 0; j < nt; ++j, ++n) {
@@ -423,6 +522,11 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       const long long at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + w.t0 + row_t;
       const float lse = live ? __ldg(p.LSE + at) : INFINITY;
       if (item >= 2 && !wait_warp(C::kSeen + (item & 1), (uint32_t)((item >> 1) - 1) & 1u, 13)) return false;
+      if (SHORT && w.nt == 1) {  // delta comes from P and dP
+        stat[row].x = live ? -lse * kLog2e : -INFINITY;
+        arrive_warp(C::kStat + (item & 1));
+        return true;
+      }
       const uint16_t* o_base = p.O + w.b * p.o_batch + w.t0 * p.o_token + w.hb * p.pack * p.o_head + col * 8;
       const uint8_t* g_base = base + (item & 1) * C::kTileBytes + C::kGOff + (col >> 3) * C::kBoxBytes;
 #pragma unroll 1
@@ -856,7 +960,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
     const int key = k0 + row;
     if (ok && key - row < p.Lk) {  // half 0 has dV, half 1 dK
       tc_fence_after();
-      const bool live = row < keys && n > 0;
+      const bool live = row < keys && n > 0 && (hf == 0 || keys + k0 > 1);  // one key's softmax has no gradient
       const float mul = hf == 0 ? 1.f : p.scale;
       const uint32_t from = tmem + lane_off + 256u + (uint32_t)hf * D;
       // one share: the gradients; several: this share's part
@@ -952,11 +1056,13 @@ cudaError_t launch(K* kernel, unsigned blocks, int threads, size_t smem, std::at
 
 template <int D>
 cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
-  static std::atomic<unsigned long long> dq_ready[2], dkv_ready, sum_ready;
-  const bool ragged = p.q_len != nullptr || p.kv_len != nullptr;
+  static std::atomic<unsigned long long> dq_ready[3], dkv_ready, sum_ready;
   const unsigned blocks = p.items < (unsigned)sms ? p.items : (unsigned)sms;
-  cudaError_t e = launch(ragged ? cross_dq_kernel<D, true> : cross_dq_kernel<D, false>, blocks, DqCfg<D>::kThreads,
-                         DqCfg<D>::kSmemBytes, dq_ready[ragged], p, s);
+  const int kind = p.q_len != nullptr || p.kv_len != nullptr ? 2 : p.Lk <= kTileN ? 1 : 0;
+  cudaError_t e = launch(kind == 2   ? cross_dq_kernel<D, true, true>
+                         : kind == 1 ? cross_dq_kernel<D, true, false>
+                                     : cross_dq_kernel<D, false, false>,
+                         blocks, DqCfg<D>::kThreads, DqCfg<D>::kSmemBytes, dq_ready[kind], p, s);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;
   e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, dkv_ready, p,

@@ -97,6 +97,35 @@ def test_more_tiles_to_be_done_again_than_a_block_remembers(lens, low):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shared", [False, True])
+def test_one_key_has_no_gradient_but_its_value(D, shared):
+    """The softmax over one key is 1: dQ and dK are 0, not a rounding."""
+    q, k, v, do = _case(3, 200, 1, 6, 2, D, 1 if shared else None)
+    dq, dk, dv = _backward(q, k, v, do, 0.3)
+    assert bool((dq == 0).all()) and bool((dk == 0).all())
+    _check(q, k, v, do, 0.3, (dq, dk, dv), None, None, "one key")
+    q, k, v, do = _case(3, 200, 140, 6, 2, D, 1 if shared else None)
+    lens = [1] if shared else [1, 140, 1]
+    dq, dk, dv = _backward(q, k, v, do, 0.3, None, lens)
+    for b in ([0, 1, 2] if shared else [0, 2]):
+        assert bool((dq[b] == 0).all()) and bool((dk[0 if shared else b] == 0).all())
+    _check(q, k, v, do, 0.3, (dq, dk, dv), None, lens, "a length of one")
+
+
+@gpu
+@pytest.mark.parametrize("Lk", [2, 3, 6, 20, 128])
+def test_few_keys_and_scores_of_all_sizes(Lk):
+    """delta from P and dP; sharp and flat softmaxes, query tiles of several items."""
+    for q_scale in (0.0, 1.0, 30.0):
+        q, k, v, do = _case(4, 1100, Lk, 10, 2, 64, q_scale=q_scale)
+        grads = _backward(q, k, v, do, 0.125, [1100, 3, 0, 700], None)
+        for t in (q, do):
+            t.nan_to_num_(0.0)
+        _check(q, k, v, do, 0.125, grads, [1100, 3, 0, 700], None, f"{Lk} keys, {q_scale}")
+
+
+@gpu
 def test_lengths_change_between_replays():
     """A captured call reads the lengths of each replay."""
     B, Lq, Lk, H, D = 6, 400, 260, 8, 64
