@@ -13,6 +13,8 @@
 // one read to its write, so the variance is taken about the mean (a second pass
 // over registers, not E[x^2] - mean^2, which loses all digits of rows far off
 // centre).  Sums, moments and the weight's gradients are fp32.
+// 61440 x 1536 bf16 of 40 groups: 62 us, 0.90 of the copy rate, and 103, 0.81;
+// 4095 x 1001 fp32, accesses of 4 bytes: 11.8 and 17.7 (4.8 and 7.3 at that rate).
 #include <algorithm>
 #include <atomic>
 
@@ -464,31 +466,42 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_back_kernel(const __grid_cons
   }
 }
 
-// Sum of a group's partial rows: part [groups][splits][2][C].  32 channels x 8
+// Sum of a group's partial rows: part [groups][splits][2][C].  32 V channels x S
 // shares of the splits a block; the shares are added in their order.
-__global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float sm[8][33];
+template <int V, int S>
+__global__ void __launch_bounds__(32 * S) norm_sums_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[S][V][32];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-  const int blocks = (p.C + 31) / 32;
+  const int blocks = (p.C + 32 * V - 1) / (32 * V);
   const long long unit = blockIdx.x / blocks;  // group and tensor
-  const int c = (int)(blockIdx.x - unit * blocks) * 32 + lane;
+  const int c = ((int)(blockIdx.x - unit * blocks) * 32 + lane) * V;
   const long long group = unit >> 1;
   const int t = (int)(unit & 1);
   float* to = t == 0 ? p.dweight : p.dbias;
   if (to == nullptr) return;
   const float* from = p.part + (group * p.splits * 2 + t) * (long long)p.C + c;
-  float a = 0.f;
+  float a[V] = {};
   if (c < p.C)
 #pragma unroll 8
-    for (int s = share; s < p.splits; s += 8) a += from[(long long)s * 2 * p.C];
-  sm[share][lane] = a;
-  __syncthreads();
-  if (share == 0 && c < p.C) {
+    for (int s = share; s < p.splits; s += S) {
+      float x[V];
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from + (long long)s * 2 * p.C);
+      else
+        x[0] = from[(long long)s * 2 * p.C];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) a += sm[k][lane];
-    to[group * p.C + c] = a;
+      for (int v = 0; v < V; ++v) a[v] += x[v];
+    }
+#pragma unroll
+  for (int v = 0; v < V; ++v) sm[share][v][lane] = a[v];
+  __syncthreads();
+  if (share < V && c < p.C) {  // warp v adds the v-th of each lane's channels
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < S; ++k) sum += sm[k][share][lane];
+    to[group * p.C + c + share] = sum;
   }
 }
 
@@ -562,7 +575,11 @@ cudaError_t backward(NormParams& p, int sms, cudaStream_t s) {
   cut(p, (long long)slots * K, h.load(), sms, p.splits);
   const cudaError_t e = launch(kernel, p.groups * p.splits, threads, smem, p, s);
   if (e != cudaSuccess || p.splits == 1 || (p.dweight == nullptr && p.dbias == nullptr)) return e;
-  return launch(norm_sums_kernel, p.groups * 2 * ((p.C + 31) / 32), 256, 0, p, s);
+  // 20000 x 1536 bf16 of one group: 46.3 us with 8 shares, 40.3 with 32; 61440 x 1536
+  // of 40 groups, 15 ranges each: 105.4 us with a channel a lane, 103.0 with four
+  if (p.splits > 16) return launch(norm_sums_kernel<1, 32>, p.groups * 2 * ((p.C + 31) / 32), 1024, 0, p, s);
+  if (p.C % 4 == 0) return launch(norm_sums_kernel<4, 8>, p.groups * 2 * ((p.C + 127) / 128), 256, 0, p, s);
+  return launch(norm_sums_kernel<1, 8>, p.groups * 2 * ((p.C + 31) / 32), 256, 0, p, s);
 }
 
 // Which instance: what counts is bytes in flight an SM against the cost of a
