@@ -625,7 +625,7 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
  *           LSE = -inf.
  * LSE       device fp32 [batch, heads, q_tokens] or NULL.
  * O overlaps no input.  heads is a multiple of kv_heads, at most 128 times it;
- * head_dim 64 or 128; softmax_scale > 0.  One token per sequence (q_tokens 1)
+ * head_dim 64 or 128; kv_tokens at most 2^26; softmax_scale > 0.  One token per sequence (q_tokens 1)
  * is the form for decoding; there is no workspace: where a call has fewer query
  * tiles than the GPU has SMs, the keys of a tile are cut among the blocks of a
  * thread-block cluster, which join their parts through shared memory.
@@ -662,12 +662,13 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
 /*
  * Gradients of sab_cross_attention for a loss with gradient dO with respect to
  * O, from the forward's O and LSE (both needed).  With P recomputed from LSE and
- * delta_i = sum_d dO_id O_id:
+ * delta_i = sum_d dO_id O_id (of at most 128 keys: sum_j P_ij <dO_i, v_j>, which
+ * is the same without O's rounding):
  *   dV = P^T dO,  dS = P * (dO V^T - delta),
  *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
  * dK and dV summed over the query heads of a key head and, where kv_batch is 1,
  * over the sequences.  Padded queries and keys get zero gradients and, whatever
- * they hold, give none.
+ * they hold, give none; where a sequence has one key, its dQ and dK are 0.
  * dQ as Q, dK and dV as K: bf16 rows that overlap no input and not one another.
  * workspace  device scratch of sab_cross_attention_backward_workspace bytes,
  *            256-byte aligned, no zero-fill needed; calls that can overlap on the
@@ -747,9 +748,9 @@ sab_status sab_get_last_device_error(void* stream);
  * boundary), the scale entry of an 8-bit append, every key run of an
  * attention CTA against the rows of its source, the FP8 scale entries it
  * reads, its workspace tile and counter, the row ranges of the backward
- * tiles, and the places of the decay attention's carried states.  (The rotary
- * and single-token kernels form no index but from their block and the checked
- * shape.)  The checks are uniform over a CTA: a CTA that fails one records
+ * tiles, the query tiles of cross attention, and the places of the decay
+ * attention's carried states.  (The rotary, layer norm and single-token kernels
+ * form no index but from their block and the checked shape.)  The checks are uniform over a CTA: a CTA that fails one records
  * SAB_ERR_BOUNDS in the device error word and leaves through the same path as
  * a CTA whose wait gave up (no copy, no store; split-merge counters still
  * return to zero).  Nothing traps.  Release builds compile the checks out.

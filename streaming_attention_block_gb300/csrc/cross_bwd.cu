@@ -150,9 +150,10 @@ __device__ __noinline__ bool one_tile(const CrossBwdParams& p, uint32_t bars, vo
   tc_fence_before();
   arrive(C::kSRead);
   arrive(C::kGrad);
-  if (cg == 0 && lse > -INFINITY) {
+  if (cg == 0) {
     const int row = quad * 32 + lane, row_t = row / p.pack, head = hb * p.pack + row - row_t * p.pack;
-    p.delta[((long long)b * p.H + head) * p.Lq + t0 + row_t] = delta;
+    if (row_t < p.tile_tokens && t0 + row_t < p.Lq)
+      p.delta[((long long)b * p.H + head) * p.Lq + t0 + row_t] = delta;
   }
   __syncwarp();
   return true;

@@ -13,8 +13,8 @@
 // one read to its write, so the variance is taken about the mean (a second pass
 // over registers, not E[x^2] - mean^2, which loses all digits of rows far off
 // centre).  Sums, moments and the weight's gradients are fp32.
-// 61440 x 1536 bf16 of 40 groups: 62 us, 0.90 of the copy rate, and 103, 0.81;
-// 4095 x 1001 fp32, accesses of 4 bytes: 11.8 and 17.7 (4.8 and 7.3 at that rate).
+// 61440 x 1536 bf16 of 40 groups: 63 us, 0.89 of the copy rate, and 103, 0.81;
+// 4095 x 1001 fp32, accesses of 4 bytes: 13 and 18 (4.8 and 7.3 at that rate).
 #include <algorithm>
 #include <atomic>
 

@@ -298,7 +298,7 @@ def _rows(data=4096, batch=1 << 20, token=256, head=0):
 
 SHAPE_REFUSALS = [dict(batch=0), dict(q_tokens=0), dict(kv_tokens=0), dict(heads=0), dict(kv_heads=0), dict(heads=5),
                   dict(kv_batch=3), dict(kv_batch=0), dict(head_dim=32), dict(head_dim=96), dict(head_dim=256),
-                  dict(heads=258, kv_heads=2), dict(q_tokens=(1 << 30) + 1), dict(kv_tokens=(1 << 30) + 1),
+                  dict(heads=258, kv_heads=2), dict(q_tokens=(1 << 30) + 1), dict(kv_tokens=(1 << 26) + 1),
                   dict(batch=-1, kv_batch=-1), dict(batch=1 << 30, kv_batch=1, heads=2, kv_heads=1)]
 ROW_REFUSALS = [dict(data=None), dict(data=4104), dict(token=260), dict(token=120), dict(batch=-8), dict(batch=100),
                 dict(token=1 << 39), dict(batch=1 << 39), dict(token=-256), dict(head=-64), dict(head=68),
