@@ -350,8 +350,11 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       if (!(ok = wait_warp(C::kQFull, (uint32_t)item & 1u, 2))) break;
       for (int j = 0; j < nt; ++j, ++n) {
         const int slot = last_slot<2>(n);
-        if (!(ok = wait_warp(C::kFull + slot, (n >> 1) & 1u, 3))) break;
+        // In this order: V of the tile two before was in K's place, and this warp
+        // does not wait for V.  Once S of the tile before is read, that V's product
+        // is done, and the parity cannot be taken for that of the fill before it.
         if (n > 0 && !(ok = wait_warp(C::kSRead, (n - 1) & 1u, 4))) break;
+        if (!(ok = wait_warp(C::kFull + slot, (n >> 1) & 1u, 3))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {

@@ -126,6 +126,33 @@ def test_few_keys_and_scores_of_all_sizes(Lk):
 
 
 @gpu
+@pytest.mark.parametrize("B, Lq, Lk, H, Hk, D", [(6, 3100, 809, 4, 4, 64), (3, 2500, 1100, 6, 2, 128),
+                                                 (6, 3100, 300, 4, 4, 64), (4, 3000, 100, 4, 4, 128)])
+def test_equal_bits_while_copies_hold_up_the_loads(B, Lq, Lk, H, Hk, D):
+    """Each wait is for its own copy, however late that one is: calls of a cold
+    cache beside copies of another stream give the bits of calls left alone."""
+    q, k, v, do = _case(B, Lq, Lk, H, Hk, D)
+    o, lse = _forward(q, k, v, 0.1)
+    ref = [o, lse, *_backward(q, k, v, do, 0.1)]
+    _check_forward(q[:1], k[:1], v[:1], 0.1, o[:1], lse[:1], None, None, "alone")
+    _check(q[:1], k[:1], v[:1], do[:1], 0.1, [g[:1] for g in ref[2:]], None, None, "alone")
+    out = [torch.empty_like(t) for t in ref]
+    ws = torch.empty(sab.cross_attention_backward_workspace(B, Lq, Lk, H, Hk, D), dtype=torch.uint8, device="cuda")
+    big = torch.empty((2, 1 << 28), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    for i in range(12):
+        big[1].fill_(i)  # nothing of the call is left in L2
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(1 + i % 3):
+                big[0].copy_(big[1])
+        sab.cross_attention(q, k, v, 0.1, *out[:2])
+        sab.cross_attention_backward(q, k, v, out[0], do, out[1], 0.1, *out[2:], workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref)), i
+
+
+@gpu
 def test_lengths_change_between_replays():
     """A captured call reads the lengths of each replay."""
     B, Lq, Lk, H, D = 6, 400, 260, 8, 64
