@@ -41,26 +41,27 @@ struct DqCfg {
   static constexpr uint32_t kBoxBytes = 128u * 128u;
   static constexpr uint32_t kTileBytes = kBoxBytes * kBoxes;
   static constexpr uint32_t kQOff = 0, kGOff = kTileBytes;  // Q of an item, dO of two
-  static constexpr uint32_t kRingOff = 3 * kTileBytes;      // two K and two V tiles
-  static constexpr uint32_t kStatOff = kRingOff + 4 * kTileBytes;  // [2 items][128] {-LSE log2 e, -delta}
+  static constexpr int kPairs = D == 128 ? 2 : 4;           // of K and V tiles
+  static constexpr uint32_t kRingOff = 3 * kTileBytes;
+  static constexpr uint32_t kStatOff = kRingOff + 2 * kPairs * kTileBytes;  // [2 items][128] {-LSE log2 e, -delta}
   static constexpr uint32_t kBarOff = kStatOff + 2048;
   static constexpr int kQFull = 0;
   static constexpr int kQFree = 1;            // an item's last scores are done
   static constexpr int kGFull = 2;            // [2 items] dO
   static constexpr int kOut = 4;              // [2] dQ is where dO was
-  static constexpr int kFull = 6;             // [4]
-  static constexpr int kEmpty = 10;           // [4]
-  static constexpr int kSFull = 14;           // S
-  static constexpr int kSRead = 15;           // S is read
-  static constexpr int kPFull = 16;           // dP
-  static constexpr int kGrad = 17;            // dS
-  static constexpr int kDone = 18;            // [2 items] the last product
-  static constexpr int kRead = 20;            // [2] dQ is taken out
-  static constexpr int kStat = 22;            // [2] LSE and delta are there
-  static constexpr int kSeen = 24;            // [2] all warps for dS have them
-  static constexpr int kMeet = 26;            // [4 quadrants] the two warps of a row
-  static constexpr int kDrain = 30;           // [2 warps with products]
-  static constexpr int kNumBars = 32;
+  static constexpr int kSFull = 6;            // S
+  static constexpr int kSRead = 7;            // S is read
+  static constexpr int kPFull = 8;            // dP
+  static constexpr int kGrad = 9;             // dS
+  static constexpr int kDone = 10;            // [2 items] the last product
+  static constexpr int kRead = 12;            // [2] dQ is taken out
+  static constexpr int kStat = 14;            // [2] LSE and delta are there
+  static constexpr int kSeen = 16;            // [2] all warps for dS have them
+  static constexpr int kMeet = 18;            // [4 quadrants] the two warps of a row
+  static constexpr int kDrain = 22;           // [2 warps with products]
+  static constexpr int kFull = 24;            // [2 kPairs]
+  static constexpr int kEmpty = kFull + 2 * kPairs;  // [2 kPairs]
+  static constexpr int kNumBars = kEmpty + 2 * kPairs;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kSeqsOff = kMiscOff + 16;  // [kMaxSorted + 1]
   static constexpr uint32_t kSmemBytes = kSeqsOff + (kMaxSorted + 1) * 4;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
     mbar_init(bar(C::kPFull), 1);
     mbar_init(bar(C::kGrad), 8);
     for (int i = 0; i < 4; ++i) mbar_init(bar(C::kMeet + i), 2);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * C::kPairs; ++i) {
       mbar_init(bar(C::kFull + i), 1);
       mbar_init(bar(C::kEmpty + i), 1);
     }
@@ -310,8 +311,8 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       bool ok = true;
       auto load = [&](int which, const CUtensorMap* m, int row, int head, int b) -> bool {
         const int k = n[which];
-        const int at = which == 0 ? last_slot<2>(k) : first_slot<2>(k);
-        if (k >= 2 && !wait(C::kEmpty + at, ((k >> 1) - 1) & 1u, 1)) return false;
+        const int at = which == 0 ? last_slot<C::kPairs>(k) : first_slot<C::kPairs>(k);
+        if (k >= C::kPairs && !wait(C::kEmpty + at, (uint32_t)(k / C::kPairs - 1) & 1u, 1)) return false;
         mbar_arrive_expect_tx(bar(C::kFull + at), C::kTileBytes);
         for (int bx = 0; bx < C::kBoxes; ++bx)
           tma_load_4d(base_u32 + C::kRingOff + at * C::kTileBytes + bx * C::kBoxBytes, m, bar(C::kFull + at), bx * 64,
@@ -328,8 +329,9 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       }
       if (*abort_flag)
         for (int which = 0; which < 2; ++which)
-          for (int k = max(0, n[which] - 2); k < n[which]; ++k)
-            wait_drain(bar(C::kFull + (which == 0 ? last_slot<2>(k) : first_slot<2>(k))), (k >> 1) & 1u, p.err_word);
+          for (int k = max(0, n[which] - C::kPairs); k < n[which]; ++k)
+            wait_drain(bar(C::kFull + (which == 0 ? last_slot<C::kPairs>(k) : first_slot<C::kPairs>(k))),
+                       (uint32_t)(k / C::kPairs) & 1u, p.err_word);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -349,12 +351,12 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       c.seek(p, pass);
       if (!(ok = wait_warp(C::kQFull, (uint32_t)item & 1u, 2))) break;
       for (int j = 0; j < nt; ++j, ++n) {
-        const int slot = last_slot<2>(n);
+        const int slot = last_slot<C::kPairs>(n);
         // In this order: V of the tile two before was in K's place, and this warp
         // does not wait for V.  Once S of the tile before is read, that V's product
         // is done, and the parity cannot be taken for that of the fill before it.
         if (n > 0 && !(ok = wait_warp(C::kSRead, (n - 1) & 1u, 4))) break;
-        if (!(ok = wait_warp(C::kFull + slot, (n >> 1) & 1u, 3))) break;
+        if (!(ok = wait_warp(C::kFull + slot, (uint32_t)(n / C::kPairs) & 1u, 3))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -396,8 +398,8 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       c.seek(p, pass);
       if (!(ok = wait_warp(C::kGFull + buf, (uint32_t)(item >> 1) & 1u, 5))) break;
       for (int j = 0; j < nt; ++j, ++n) {
-        const int ks = last_slot<2>(n), vs = first_slot<2>(n), live = keys - j * kTileN;
-        if (!(ok = wait_warp(C::kFull + vs, (n >> 1) & 1u, 6))) break;
+        const int ks = last_slot<C::kPairs>(n), vs = first_slot<C::kPairs>(n), live = keys - j * kTileN;
+        if (!(ok = wait_warp(C::kFull + vs, (uint32_t)(n / C::kPairs) & 1u, 6))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
         mma_commit_l(lead, bar(C::kEmpty + vs));
         // the item two before has its dQ taken out before this one's goes over it
         if (j == 0 && item >= 2 && !(ok = wait_warp(C::kRead + buf, (uint32_t)((item >> 1) - 1) & 1u, 7))) break;
-        if (!(ok = wait_warp(C::kFull + ks, (n >> 1) & 1u, 8))) break;
+        if (!(ok = wait_warp(C::kFull + ks, (uint32_t)(n / C::kPairs) & 1u, 8))) break;
         const int steps = min(8, (live + 15) >> 4);  // 16 keys each
         // keys past the sequence's end may hold anything, and 0 * NaN is NaN
         if (__builtin_expect(steps * 16 > live, 0))
