@@ -752,15 +752,19 @@ def _token_rows(t, shape, name, dev):
 
 def _cross_shapes(Q, K):
     """(query shape, key shape, description) of a call."""
-    for t, name in ((Q, "Q"), (K, "K")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise TypeError(f"{name}: expected a [B, L, H, D] torch tensor")
-    x, y = Q.shape, K.shape
-    if max(*x, *y) > 0x7FFFFFFF:  # would be cut to 32 bits on the way to the library
-        raise SabError(1, "cross_attention")
-    if y[3] != x[3]:
-        raise ValueError(f"K: expected a head dimension of {x[3]}, got {y[3]}")
-    return x, y, _CROSS.pack(x[0], x[1], y[0], y[1], x[2], y[2], x[3])
+    try:
+        x, y = Q.shape, K.shape
+        B, Lq, H, D = x
+        Bk, Lk, Hk, Dk = y
+    except (AttributeError, TypeError, ValueError):
+        name = "Q" if not isinstance(Q, torch.Tensor) or Q.dim() != 4 else "K"
+        raise TypeError(f"{name}: expected a [B, L, H, D] torch tensor") from None
+    if Dk != D:
+        raise ValueError(f"K: expected a head dimension of {D}, got {Dk}")
+    try:
+        return x, y, _CROSS.pack(B, Lq, Bk, Lk, H, Hk, D)
+    except struct.error:  # beyond 32 bits
+        raise SabError(1, "cross_attention") from None
 
 
 def cross_attention(Q, K, V, softmax_scale: float, O, LSE=None, q_len=None, kv_len=None, stream=None):
@@ -821,17 +825,19 @@ def _norm_rows(t, like, name, dev):
     axis: all leading axes as one, with one stride between rows."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in _DTYPES:
         _refuse(t, name, dev, tuple(_DTYPES))
-    if t.dim() == 0 or t.numel() == 0:
-        raise ValueError(f"{name}: expected [..., channels] with at least one row and channel")
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+    shape = t.shape
+    if like is None:
+        if not shape or 0 in shape:
+            raise ValueError(f"{name}: expected [..., channels] with at least one row and channel")
+    elif t.dtype != like.dtype or shape != like.shape:
         raise ValueError(f"{name}: expected the shape and type of X, {tuple(like.shape)} {like.dtype}, got "
-                         f"{tuple(t.shape)} {t.dtype}")
+                         f"{tuple(shape)} {t.dtype}")
     if t.is_contiguous():
-        return t.data_ptr(), t.shape[-1]
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        return t.data_ptr(), shape[-1]
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: a row's channels must be contiguous")
     step = span = None  # stride of the innermost leading axis, and what the next one has to have
-    for n, st in reversed(tuple(zip(t.shape[:-1], t.stride()[:-1]))):
+    for n, st in reversed(tuple(zip(shape[:-1], t.stride()[:-1]))):
         if n == 1:
             continue
         if step is None:
@@ -839,7 +845,7 @@ def _norm_rows(t, like, name, dev):
         elif st != span:
             raise ValueError(f"{name}: rows must be one stride apart")
         span = st * n
-    return t.data_ptr(), t.shape[-1] if step is None else step
+    return t.data_ptr(), shape[-1] if step is None else step
 
 
 def _norm_desc(X, group_rows, weight_offset, eps):
@@ -848,6 +854,8 @@ def _norm_desc(X, group_rows, weight_offset, eps):
     group_rows = rows if group_rows is None else int(group_rows)
     if group_rows < 1:
         raise SabError(1, "layer_norm: group_rows")
+    if C > 0x7FFFFFFF:  # would not fit on the way to the library
+        raise SabError(1, "layer_norm")
     groups = -(-rows // group_rows)
     return _NORM.pack(rows, C, group_rows, float(weight_offset), float(eps), _DTYPES[X.dtype]), rows, C, groups
 

@@ -69,6 +69,7 @@ struct DqCfg {
   static constexpr int kThreads = 32 * 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+
 // dS of an item with one key tile, for one warp of those for dS (64 keys): delta
 // is formed here, from all of its row, as sum_j P_ij dP_ij.  O needs not be read,
 // and with few keys its rounding showed in delta (6 keys: error of dQ 2.9e-3 of
