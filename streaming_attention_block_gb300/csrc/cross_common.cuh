@@ -51,12 +51,12 @@ __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, unsigned*
 }
 
 // Zero the rows [from, to) of a tile in shared memory (whole warp).
-template <int BOXES, int BOX_BYTES = 128 * 128>
+template <int BOXES>
 __device__ __noinline__ void zero_rows(uint8_t* tile, int from, int to) {
   const int lane = threadIdx.x & 31, n = (to - from) * 8;  // 16-byte pieces a box of 64 columns
   for (int i = lane; i < n * BOXES; i += 32) {
     const int bx = i >= n ? 1 : 0, k = i - bx * n;
-    *reinterpret_cast<uint4*>(tile + bx * BOX_BYTES + (from + (k >> 3)) * 128 + (k & 7) * 16) =
+    *reinterpret_cast<uint4*>(tile + bx * 128 * 128 + (from + (k >> 3)) * 128 + (k & 7) * 16) =
         make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
