@@ -29,12 +29,14 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 // P = 2^(s - m) in bf16 has fp32's exponents and is summed in fp32, so the
-// reference m need not be the row's maximum: any m that keeps the sum l within
-// 2^80 of 1 gives the same digits (nothing overflows, and what ftz drops is
-// below 2^-46 of the sum).  Rows take m = 0, without looking for a maximum, which
-// scores below 55 in size never need; a tile with a row whose l leaves the range,
-// or whose O is not finite, is done again with its running maxima.
-constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p80f;
+// reference m need not be the row's maximum: any m that keeps the row's sum l from
+// 2^-24 to 2^80 gives the same digits.  Nothing overflows below; a key whose P ftz
+// drops has less than 2^-102 of the sum, and products P V below 2^-126 lose at most
+// 2^-126 a key of O (a least sum of 2^-80 lost values of 2^-60 and below).  Rows
+// take m = 0, without looking for a maximum; their sums are in that range where the
+// largest score is between -16.6 and 55.4 - ln(keys).  A tile with a row whose l is
+// not, or whose O is not finite, is done again with its running maxima.
+constexpr float kLeastSum = 0x1p-24f, kMostSum = 0x1p80f;
 constexpr float kRescale = 8.0f;  // running maxima: O is rescaled when one grows by more than 2^8
 constexpr int kRedoList = 64;     // query tiles a block remembers
 
