@@ -621,8 +621,8 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
  * q_len     device int32 [batch] or NULL (all q_tokens), kv_len: device int32
  *           [kv_batch] or NULL (all kv_tokens); clamped on the device.  Tokens
  *           past them are padding: never used, whatever they hold.  Padded
- *           queries, and all queries of a sequence without keys, get O = 0 and
- *           LSE = -inf.
+ *           queries, all queries of a sequence without keys and those whose
+ *           scores all overflow to -inf get O = 0 and LSE = -inf.
  * LSE       device fp32 [batch, heads, q_tokens] or NULL.
  * O overlaps no input.  heads is a multiple of kv_heads, at most 128 times it;
  * head_dim 64 or 128; kv_tokens at most 2^26; softmax_scale > 0.  One token per sequence (q_tokens 1)
@@ -668,7 +668,8 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
  *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
  * dK and dV summed over the query heads of a key head and, where kv_batch is 1,
  * over the sequences.  Padded queries and keys get zero gradients and, whatever
- * they hold, give none; where a sequence has one key, its dQ and dK are 0.
+ * they hold, give none, nor does a query whose LSE is -inf; where a sequence has
+ * one key, its dQ and dK are 0.
  * dQ as Q, dK and dV as K: bf16 rows that overlap no input and not one another.
  * workspace  device scratch of sab_cross_attention_backward_workspace bytes,
  *            256-byte aligned, no zero-fill needed; calls that can overlap on the

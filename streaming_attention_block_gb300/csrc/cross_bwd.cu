@@ -20,6 +20,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// What is added to a row's scores for P, from its LSE.  -inf: P is 0, also where
+// all scores were -inf (they and an infinity would be no number, and that of every
+// key's gradient).
+__device__ __forceinline__ float minus_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
 // Where the n-th of a run of tile pairs is, of which one is done with before the
 // other (V before K, dO before Q): N pairs of places in turn, the one done with
 // last where the other was.
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       const float lse = live ? __ldg(p.LSE + at) : INFINITY;
       if (item >= 2 && !wait_warp(C::kSeen + (item & 1), (uint32_t)((item >> 1) - 1) & 1u, 13)) return false;
       if (SHORT && w.nt == 1) {  // delta comes from P and dP
-        stat[row].x = live ? -lse * kLog2e : -INFINITY;
+        stat[row].x = live ? minus_lse(lse) : -INFINITY;
         arrive_warp(C::kStat + (item & 1));
         return true;
       }
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       }
       __syncwarp();
       const float nd = stat[row].y;
-      stat[row] = make_float2(live ? -lse * kLog2e : -INFINITY, live ? nd : 0.f);
+      stat[row] = make_float2(live ? minus_lse(lse) : -INFINITY, live ? nd : 0.f);
       if (live) p.delta[at] = -nd;
       arrive_warp(C::kStat + (item & 1));
       return true;
@@ -837,7 +842,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
       float* stat = reinterpret_cast<float*>(base + C::kStatOff + st * 1024);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        stat[lane + 32 * i] = has[i] ? -ls[i] * kLog2e : -INFINITY;
+        stat[lane + 32 * i] = has[i] ? minus_lse(ls[i]) : -INFINITY;
         stat[128 + lane + 32 * i] = -dl[i];
       }
       arrive_warp(C::kStat + st);
