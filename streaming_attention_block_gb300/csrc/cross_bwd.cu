@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1) cross_dq_kernel(const _
       float2* stat = reinterpret_cast<float2*>(base + C::kStatOff) + (item & 1) * 128;
       const bool live = alive(w);
       const long long at = ((long long)w.b * p.H + w.hb * p.pack + row_g) * p.Lq + w.t0 + row_t;
-      const float lse = live ? __ldg(p.LSE + at) : INFINITY;
+      const float lse = live ? ld_global(p.LSE + at) : INFINITY;
       if (item >= 2 && !wait_warp(C::kSeen + (item & 1), (uint32_t)((item >> 1) - 1) & 1u, 13)) return false;
       if (SHORT && w.nt == 1) {  // delta comes from P and dP
         stat[row].x = live ? minus_lse(lse) : -INFINITY;
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
         const long long at = ((long long)s.b * p.H + head) * p.Lq + t;
         has[i] = tok[i] < s.live && lane + 32 * i < rows;
         ls[i] = dl[i] = 0.f;
-        if (has[i]) ls[i] = __ldg(p.LSE + at), dl[i] = __ldg(p.delta + at);
+        if (has[i]) ls[i] = ld_global(p.LSE + at), dl[i] = ld_global(p.delta + at);
       }
     };
     if (s.i < s.end) fetch();

@@ -82,7 +82,7 @@ __device__ __forceinline__ int uniform(int x) {
 }
 template <bool kUniform>
 __device__ __forceinline__ int length_of(const int* lens, int b, int most) {
-  return lens == nullptr ? most : uniform<kUniform>(min(max(__ldg(lens + b), 0), most));
+  return lens == nullptr ? most : uniform<kUniform>(min(max(ld_global(lens + b), 0), most));
 }
 
 // A kernel's shared memory limit, set once for each device.

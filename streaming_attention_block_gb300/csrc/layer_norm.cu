@@ -116,17 +116,18 @@ __device__ __forceinline__ void forget(uint32_t& r) { asm volatile("" : "+r"(r))
 __device__ __forceinline__ void forget(uint16_t& r) { asm volatile("" : "+h"(r)); }
 __device__ __forceinline__ void forget(float& r) { asm volatile("" : "+f"(r)); }
 
-// the values of a weight row that belong to an access
+// The values of a weight row that belong to an access (plain loads: the kernel
+// before this one in the stream may have written them).
 __device__ __forceinline__ void load_f32(const float* p, float2 (&f)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 __device__ __forceinline__ void load_f32(const float* p, float2 (&f)[2]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 a = *reinterpret_cast<const float4*>(p);
   f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
 }
-__device__ __forceinline__ void load_f32(const float* p, float2 (&f)[1]) { f[0] = make_float2(__ldg(p), __ldg(p + 1)); }
-__device__ __forceinline__ void load_f32(const float* p, float (&f)[1]) { f[0] = __ldg(p); }
+__device__ __forceinline__ void load_f32(const float* p, float2 (&f)[1]) { f[0] = make_float2(p[0], p[1]); }
+__device__ __forceinline__ void load_f32(const float* p, float (&f)[1]) { f[0] = p[0]; }
 __device__ __forceinline__ void store_f32(float* p, const float2 (&f)[4]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
@@ -351,8 +352,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_back_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const long long r = base + a.slot + (long long)k * a.slots;
-      nm[k] = r < a.r1 ? __ldg(p.mean + r) : 0.f;
-      nr[k] = r < a.r1 ? __ldg(p.rstd + r) : 0.f;
+      nm[k] = r < a.r1 ? ld_global(p.mean + r) : 0.f;
+      nr[k] = r < a.r1 ? ld_global(p.rstd + r) : 0.f;
     }
   };
   fetch(a.r0);
