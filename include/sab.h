@@ -749,12 +749,15 @@ sab_status sab_get_last_device_error(void* stream);
  * boundary), the scale entry of an 8-bit append, every key run of an
  * attention CTA against the rows of its source, the FP8 scale entries it
  * reads, its workspace tile and counter, the row ranges of the backward
- * tiles, the query tiles of cross attention, and the places of the decay
- * attention's carried states.  (The rotary, layer norm and single-token kernels
- * form no index but from their block and the checked shape.)  The checks are uniform over a CTA: a CTA that fails one records
- * SAB_ERR_BOUNDS in the device error word and leaves through the same path as
- * a CTA whose wait gave up (no copy, no store; split-merge counters still
- * return to zero).  Nothing traps.  Release builds compile the checks out.
+ * tiles, the query tiles of cross attention and the blocks and query tiles of
+ * its key gradients, and the places of the decay attention's carried states.
+ * (The rotary, layer norm and single-token kernels form no index but from their
+ * block and the checked shape.)  The checks are uniform over a CTA: a CTA that
+ * fails one records SAB_ERR_BOUNDS in the device error word and leaves through
+ * the same path as a CTA whose wait gave up (no copy, no store; split-merge
+ * counters still return to zero); one that walks the query tiles of cross
+ * attention leaves out the tile that failed and goes on.  Nothing traps.
+ * Release builds compile the checks out.
  *
  * sab_debug_bounds_enabled: 1 in a debug build, 0 otherwise.
  * sab_debug_inject_bounds_error: makes the next launch of the named kind
@@ -762,15 +765,17 @@ sab_status sab_get_last_device_error(void* stream);
  * (the forged index points inside memory the caller owns in the forms the
  * self-test uses: one slot past the ring rows for an append, one slot past
  * the ring for an attention key run, one tile fewer than the workspace holds
- * for a split tile).  what: SAB_DEBUG_INJECT_APPEND_SLOT,
- * SAB_DEBUG_INJECT_KEY_ROW or SAB_DEBUG_INJECT_WS_TILE; 0 cancels a pending
- * injection.  Host-side only: nothing is launched.  Errors: UNSUPPORTED in a
+ * for a split tile, one sequence of queries and one block of the key gradients
+ * too many for cross attention).  what: SAB_DEBUG_INJECT_APPEND_SLOT,
+ * SAB_DEBUG_INJECT_KEY_ROW, SAB_DEBUG_INJECT_WS_TILE or
+ * SAB_DEBUG_INJECT_CROSS_ITEM; 0 cancels a pending injection.  Host-side only: nothing is launched.  Errors: UNSUPPORTED in a
  * release build, INVALID_ARG for another `what`.
  */
 enum {
   SAB_DEBUG_INJECT_APPEND_SLOT = 1, /* next ring append (BF16 or 8-bit) */
   SAB_DEBUG_INJECT_KEY_ROW = 2,     /* next streaming chunk attention */
-  SAB_DEBUG_INJECT_WS_TILE = 3      /* next split (num_splits >= 2) chunk attention */
+  SAB_DEBUG_INJECT_WS_TILE = 3,     /* next split (num_splits >= 2) chunk attention */
+  SAB_DEBUG_INJECT_CROSS_ITEM = 4   /* next cross attention, or its gradients */
 };
 int sab_debug_bounds_enabled(void);
 sab_status sab_debug_inject_bounds_error(int what);

@@ -26,6 +26,7 @@ ERR_BOUNDS = 7
 DEBUG_INJECT_APPEND_SLOT = 1
 DEBUG_INJECT_KEY_ROW = 2
 DEBUG_INJECT_WS_TILE = 3
+DEBUG_INJECT_CROSS_ITEM = 4
 
 
 class SabError(RuntimeError):

@@ -624,6 +624,7 @@ cross_fwd_kernel(const __grid_constant__ CrossParams p) {
     bool ok = pass.end > 0;
     int used[2] = {0, 0}, tiles = 0;
     auto finish = [&](const Work& w, unsigned item, int st) -> bool {
+      if (kDebugBounds && w.b < 0) return false;  // a part of a cluster: none of its blocks stores
       const int t = w.t0 + st * p.tile_tokens + row_t;
       const bool stored = row_t < p.tile_tokens && t < p.Lq;  // this row has an O and an LSE
       const bool live = row_t < p.tile_tokens && st * p.tile_tokens + row_t < w.live;

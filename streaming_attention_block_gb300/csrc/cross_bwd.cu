@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
       mbar_init(bar(C::kDone + i), 1);
       mbar_init(bar(C::kDrain + i), 1);
     }
-    misc[1] = (base_u32 & 1023u) != 0;
+    misc[1] = (base_u32 & 1023u) != 0 || (kDebugBounds && share >= p.shares);
     if (misc[1] != 0 && p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
     fence_mbar_init();
   }
@@ -774,6 +774,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1) cross_dkv_kernel(const
   // the next tile with a live query, from this one on
   auto seek = [&](Stream& s) {
     for (; s.i < s.end; advance(s)) {
+      if constexpr (kDebugBounds) {
+        if (s.b >= p.B || s.hb >= blocks || s.iq >= p.n_qtiles) {
+          if (p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
+          *abort_flag = 1;
+          s.i = s.end;
+          return;
+        }
+      }
       s.live = min(p.tile_tokens, length_of<true>(p.q_len, s.b, p.Lq) - s.iq * p.tile_tokens);
       if (s.live > 0) return;
     }
@@ -1077,7 +1085,7 @@ cudaError_t backward(const CrossBwdParams& p, int sms, cudaStream_t s) {
                          blocks, DqCfg<D>::kThreads, DqCfg<D>::kSmemBytes, dq_ready[kind], p, s);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)((p.Lk + kTileN - 1) / kTileN) * (unsigned)p.Hk * (unsigned)p.Bk;
-  e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, dkv_ready, p,
+  e = launch(cross_dkv_kernel<D>, units * (unsigned)p.shares + p.forged, DkvCfg<D>::kThreads, DkvCfg<D>::kSmemBytes, dkv_ready, p,
              s);
   if (e != cudaSuccess || p.shares == 1) return e;
   return launch(cross_sum_kernel<D>, units * 2 * (D / 4 * kTileN / 256), 256, 0, sum_ready, p, s);

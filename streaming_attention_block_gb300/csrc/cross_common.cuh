@@ -179,7 +179,7 @@ __device__ __noinline__ Spot sorted_spot(const CrossParams& p, const uint32_t* s
 // One or two query tiles (`streams`) of `pack` heads from head hb * pack on,
 // tile_tokens tokens each from t0 on, and the key tiles [first, first + nt).
 struct Work {
-  int b, hb, t0;
+  int b, hb, t0;    // b < 0: an index that a debug build has refused
   int live;         // tokens from t0 on that are inside q_len
   int streams;
   int first, nt;
@@ -191,12 +191,23 @@ __device__ __forceinline__ Work work_at(const CrossParams& p, const Spot& s, int
   w.t0 = s.iq * pair * p.tile_tokens;
   w.b = s.b;
   w.hb = s.hb;
+  w.live = 0;
+  w.streams = 1;
+  w.first = w.nt = w.keys = 0;
+  // (a refused item has nothing, and its rows are not taken for dead ones)
+  if constexpr (kDebugBounds) {
+    if ((unsigned)w.b >= (unsigned)p.B || (unsigned)w.hb >= (unsigned)p.head_blocks ||
+        (unsigned)w.t0 >= (unsigned)p.Lq) {
+      if (p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
+      w.b = -1;
+      return w;
+    }
+  }
   w.live = length_of<kUniform>(p.q_len, w.b, p.Lq) - w.t0;
   w.streams = pair == 2 && w.live > p.tile_tokens ? 2 : 1;
   const int kl = w.live > 0 ? length_of<kUniform>(p.kv_len, p.Bk == 1 ? 0 : w.b, p.Lk) : 0;
   const int total = (kl + kTileN - 1) / kTileN;
   int last = total;
-  w.first = 0;
   if (p.splits > 1) {
     w.first = (int)((long long)total * split / p.splits);
     last = (int)((long long)total * (split + 1) / p.splits);
@@ -204,9 +215,10 @@ __device__ __forceinline__ Work work_at(const CrossParams& p, const Spot& s, int
   w.nt = last - w.first;
   w.keys = min(kl, last * kTileN) - w.first * kTileN;
   if constexpr (kDebugBounds) {
-    if (w.b >= p.B || w.hb >= p.head_blocks || w.t0 >= p.Lq || w.first < 0 || last * kTileN - kTileN >= p.Lk) {
+    if (w.first < 0 || last * kTileN - kTileN >= p.Lk) {
       if (p.err_word != nullptr) atomicOr(p.err_word, kErrBoundsBit);
       w.nt = w.live = 0;
+      w.b = -1;
     }
   }
   return w;
@@ -222,6 +234,7 @@ __device__ __noinline__ void clear_tiles(const CrossParams& p, int pair, uint32_
   const int lane = threadIdx.x & 31;
   for (unsigned i = blockIdx.x; i < p.items; i += gridDim.x) {
     const Work w = work_at<false>(p, spot_of(p, i, pair), 0, pair);
+    if (kDebugBounds && w.b < 0) continue;
     for (int t = w.nt == 0 ? 0 : w.streams; t < pair; ++t) {
       const int t0 = w.t0 + t * p.tile_tokens;
       if (t0 >= p.Lq) break;

@@ -1281,6 +1281,13 @@ static int cross_sorted(const sab_cross_desc& d, const int* q_len, const int* kv
          items < (1u << 26);
 }
 
+// Debug builds: the items of a sequence past the last.
+static bool forge_items(CrossParams& p) {
+  if (!take_injection(SAB_DEBUG_INJECT_CROSS_ITEM)) return false;
+  p.items += (unsigned)(p.head_blocks * ((p.n_qtiles + p.pair - 1) / p.pair));
+  return true;
+}
+
 sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
                                const sab_token_rows* V, const int* q_len, const int* kv_len, float softmax_scale,
                                const sab_token_rows* O, float* LSE, void* stream) {
@@ -1327,6 +1334,7 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.items = (unsigned)(columns * ((p.n_qtiles + p.pair - 1) / p.pair));
   p.splits = p.pair == 2 ? 1 : cross_splits(p.items, (d.kv_tokens + kTileN - 1) / kTileN);
   p.sorted = cross_sorted(d, q_len, kv_len, p.items);
+  forge_items(p);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.err_word = device_error_word();
   if (!encode_query_rows(&p.q_map, Q, d.batch, d.q_tokens, d.heads, d.head_dim, p.pack, p.tile_tokens) ||
@@ -1427,6 +1435,7 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.items = (unsigned)((long long)d.batch * p.head_blocks * p.n_qtiles);
   p.splits = 1;
   p.sorted = cross_sorted(d, q_len, kv_len, p.items);
+  p.forged = forge_items(p) ? 1 : 0;
   p.shares = b.shares;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1614,7 +1623,7 @@ int sab_debug_bounds_enabled(void) { return kDebugBounds ? 1 : 0; }
 
 sab_status sab_debug_inject_bounds_error(int what) {
   if (!kDebugBounds) return SAB_ERR_UNSUPPORTED;
-  if (what < 0 || what > SAB_DEBUG_INJECT_WS_TILE) return SAB_ERR_INVALID_ARG;
+  if (what < 0 || what > SAB_DEBUG_INJECT_CROSS_ITEM) return SAB_ERR_INVALID_ARG;
   g_inject.store(what);
   return SAB_OK;
 }

@@ -327,6 +327,7 @@ struct CrossBwdParams : CrossParams {
   CUtensorMap do_map, of_map;     // dO and O, as q_map; o_map is dQ's
   int Hk;
   int shares;                     // blocks among which the queries of a key tile are cut
+  unsigned forged;                // debug builds: blocks past the last (dK and dV)
   float scale;
   float* delta;                   // [B, H, Lq]
   float* part;                    // [shares][Bk][Hk][key tiles][dV, dK][D / 4][128][4] (several shares)
