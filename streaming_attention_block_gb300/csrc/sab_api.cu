@@ -1274,6 +1274,14 @@ static int cross_splits(unsigned items, int key_tiles) {
   return n;
 }
 
+// Query tiles of a call whose sequences may differ in length: 2^26 at most.  A
+// block first clears its rows without a query or key, in 1.1 (gradients 1.6) us a
+// tile of one token, and its other warps wait for that 2 s at most: 0.5 (0.7) s of
+// 2^26 tiles on 152 SMs; those of 2^28 ran out.
+static bool cross_tiles_ok(const sab_cross_desc& d, const int* q_len, const int* kv_len, long long tiles) {
+  return (q_len == nullptr && kv_len == nullptr) || d.batch * tiles <= (1LL << 26);
+}
+
 // More than one item a block, of sequences that may differ in length; 64 of them
 // and 2^26 items at most (what the kernels' table of them holds).
 static int cross_sorted(const sab_cross_desc& d, const int* q_len, const int* kv_len, unsigned items) {
@@ -1322,6 +1330,7 @@ sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows*
   p.tile_tokens = kTileM / p.pack;
   p.n_qtiles = (d.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.head_blocks = d.heads / p.pack;
+  if (!cross_tiles_ok(d, q_len, kv_len, (long long)p.head_blocks * p.n_qtiles)) return SAB_ERR_INVALID_ARG;
   // Two query tiles an item, unless that takes the SMs over a third more tile
   // times.  Measured alone and in pairs, 128 columns a head, 512 keys: one wave of
   // tiles against two 11.4 and 13.2 us, two and two 16.9 and 14.4, three and four
@@ -1411,6 +1420,7 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   }
   if (LSE == nullptr || !aligned16(LSE) || !aligned4(q_len) || !aligned4(kv_len)) return SAB_ERR_INVALID_ARG;
   const CrossBackPlan b = cross_back_plan(d);
+  if (!cross_tiles_ok(d, q_len, kv_len, (long long)(H / b.pack) * b.n_qtiles)) return SAB_ERR_INVALID_ARG;
   if (workspace == nullptr || ws_bytes < b.delta_bytes + b.part_bytes ||
       (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0)
     return SAB_ERR_WORKSPACE;
