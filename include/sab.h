@@ -627,8 +627,8 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
  * O overlaps no input.  heads is a multiple of kv_heads, at most 128 times it;
  * head_dim 64 or 128; kv_tokens at most 2^26; with q_len or kv_len at most 2^26
  * query tiles (of 128 rows: tokens of the heads that share a key head);
- * softmax_scale > 0.  One token per sequence (q_tokens 1) is the form for
- * decoding; there is no workspace: where a call has fewer query tiles than the
+ * softmax_scale > 0, at most 2^127.  One token per sequence (q_tokens 1) is the
+ * form for decoding; there is no workspace: where a call has fewer query tiles than the
  * GPU has SMs, the keys of a tile are cut among the blocks of a thread-block
  * cluster, which join their parts through shared memory.
  * Scores and sums are fp32; P is rounded to bf16 for its product.

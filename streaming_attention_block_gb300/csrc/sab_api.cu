@@ -1197,6 +1197,9 @@ static bool cross_shape_ok(const sab_cross_desc* d) {
   return (long long)d->batch * d->heads * ((d->q_tokens + 31) / 32) <= (1LL << 30) &&
          (long long)d->kv_batch * d->kv_heads * ((d->kv_tokens + 31) / 32) <= (1LL << 30);
 }
+// The kernels' scale, of exponents to base 2, has to be finite too: with an
+// infinite one a score of 0 is no number.
+static bool cross_scale_ok(float scale) { return scale > 0.f && isfinite(scale * 1.4426950408889634f); }
 // Rows of one [B, L, H, D] tensor: pointer and strides that a tensor map takes;
 // heads and tokens apart from one another, and sequences too where the tensor is
 // written.  Strides of axes of one entry say nothing.
@@ -1299,7 +1302,7 @@ static bool forge_items(CrossParams& p) {
 sab_status sab_cross_attention(const sab_cross_desc* desc, const sab_token_rows* Q, const sab_token_rows* K,
                                const sab_token_rows* V, const int* q_len, const int* kv_len, float softmax_scale,
                                const sab_token_rows* O, float* LSE, void* stream) {
-  if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
+  if (!cross_shape_ok(desc) || !cross_scale_ok(softmax_scale)) return SAB_ERR_INVALID_ARG;
   const sab_cross_desc& d = *desc;
   const int D = d.head_dim;
   if (!token_rows_ok(Q, d.batch, d.q_tokens, d.heads, D, false) ||
@@ -1400,7 +1403,7 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
                                         const float* LSE, const int* q_len, const int* kv_len, float softmax_scale,
                                         const sab_token_rows* dQ, const sab_token_rows* dK, const sab_token_rows* dV,
                                         void* workspace, size_t ws_bytes, void* stream) {
-  if (!cross_shape_ok(desc) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return SAB_ERR_INVALID_ARG;
+  if (!cross_shape_ok(desc) || !cross_scale_ok(softmax_scale)) return SAB_ERR_INVALID_ARG;
   const sab_cross_desc& d = *desc;
   const int B = d.batch, L = d.q_tokens, H = d.heads, Hk = d.kv_heads, D = d.head_dim;
   const sab_token_rows* in[] = {Q, O, dO, K, V};

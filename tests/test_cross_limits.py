@@ -31,3 +31,10 @@ def _status(d, ql, kl, back, scale=0.1):
 def test_more_query_tiles_of_unequal_sequences_than_are_cleared_in_time(back, kw):
     for ql, kl in ((P(4096), None), (None, P(4096)), (P(4096), P(8192))):
         assert _status(_desc(**kw), ql, kl, back) == 1
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_scales_that_are_infinite_to_base_2(back):
+    """3e38 log2 e is no fp32 number, and 0 times it none at all."""
+    for scale in (3.0e38, 2.4e38, float("inf")):
+        assert _status(_desc(), None, None, back, scale) == 1
