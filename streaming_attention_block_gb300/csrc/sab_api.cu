@@ -1458,12 +1458,8 @@ sab_status sab_cross_attention_backward(const sab_cross_desc* desc, const sab_to
   p.o_batch = batch_of(O, d.batch, d.heads, D);
   p.o_token = token_of(O, d.q_tokens, d.heads, D);
   p.o_head = head_of(O, d.heads, D);
-  p.dQ = static_cast<uint16_t*>(dQ->data);
   p.dK = static_cast<uint16_t*>(dK->data);
   p.dV = static_cast<uint16_t*>(dV->data);
-  p.dq_batch = batch_of(dQ, B, H, D);
-  p.dq_token = token_of(dQ, L, H, D);
-  p.dq_head = head_of(dQ, H, D);
   p.dk_batch = batch_of(dK, d.kv_batch, Hk, D);
   p.dk_token = token_of(dK, d.kv_tokens, Hk, D);
   p.dk_head = head_of(dK, Hk, D);

@@ -331,8 +331,8 @@ struct CrossBwdParams : CrossParams {
   float scale;
   float* delta;                   // [B, H, Lq]
   float* part;                    // [shares][Bk][Hk][key tiles][dV, dK][D / 4][128][4] (several shares)
-  uint16_t *dQ, *dK, *dV;
-  long long dq_batch, dq_token, dq_head, dk_batch, dk_token, dk_head, dv_batch, dv_token, dv_head;
+  uint16_t *dK, *dV;              // (dQ goes out through o_map)
+  long long dk_batch, dk_token, dk_head, dv_batch, dv_token, dv_head;
 };
 
 // Launchers (return cudaError_t of the launch).
