@@ -623,7 +623,8 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
  *           past them are padding: never used, whatever they hold.  Padded
  *           queries, all queries of a sequence without keys and those whose
  *           scores all overflow to -inf get O = 0 and LSE = -inf.
- * LSE       device fp32 [batch, heads, q_tokens] or NULL.
+ * LSE       device fp32 [batch, heads, q_tokens] or NULL;
+ *           16-byte aligned (a slice of its sequences may not be).
  * O overlaps no input.  heads is a multiple of kv_heads, at most 128 times it;
  * head_dim 64 or 128; kv_tokens at most 2^26; with q_len or kv_len at most 2^26
  * query tiles (of 128 rows: tokens of the heads that share a key head);
@@ -632,6 +633,11 @@ sab_status sab_decay_attention_backward(const void* Q, const void* K, const void
  * GPU has SMs, the keys of a tile are cut among the blocks of a thread-block
  * cluster, which join their parts through shared memory.
  * Scores and sums are fp32; P is rounded to bf16 for its product.
+ * Time goes by the scores too: a tile of 128 query rows is computed a second time,
+ * with a running maximum, where the sum of a row's exp(s_ij) leaves 2^-24 .. 2^80
+ * (its largest score is below -16.6 or above 55 - ln(keys) then) or its O is not
+ * finite; a call of such tiles alone takes 2 to 4 times as long (not where the
+ * keys of a tile are cut among a cluster).
  * Errors: INVALID_ARG, CUDA.
  */
 typedef struct {

@@ -35,7 +35,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 2^-126 a key of O (a least sum of 2^-80 lost values of 2^-60 and below).  Rows
 // take m = 0, without looking for a maximum; their sums are in that range where the
 // largest score is between -16.6 and 55.4 - ln(keys).  A tile with a row whose l is
-// not, or whose O is not finite, is done again with its running maxima.
+// not, or whose O is not finite, is done again with its running maxima, two tiles
+// an item one by one.  2 x 30720 queries over 512 keys, 12 heads of 128: 142 us, with
+// a row of it in every seventh tile 235, with all tiles done again 472; one chunk of
+// 1536 queries 11 and 22; 16384 over 8192 keys, 8 heads, 331, 554 and 1265.
 constexpr float kLeastSum = 0x1p-24f, kMostSum = 0x1p80f;
 constexpr float kRescale = 8.0f;  // running maxima: O is rescaled when one grows by more than 2^8
 constexpr int kRedoList = 64;     // query tiles a block remembers

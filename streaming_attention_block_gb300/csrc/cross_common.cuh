@@ -114,7 +114,10 @@ __device__ __noinline__ Spot spot_of(const CrossParams& p, unsigned item, int pa
 // some blocks met the long ones and some the empty.  Means of five draws of
 // lengths, in the order of the sequences and in this one: 8 x 1023 queries over 777
 // keys, 24/4 heads of 64, 40.5 and 30.6 us; 64 x 1 over 4095, 24/8 heads of 128,
-// 103.8 and 95.4 us.  Up to 64 sequences; with more each block meets many.
+// 103.8 and 95.4 us.  Up to 64 sequences, which is what the table holds; more are
+// taken as they come, which costs 13 to 19 % forward and 9 to 22 % in the gradients
+// (65 to 128 x up to 512 over up to 777 keys against 64 of them), and 30, 14 and 5 %
+// for 65, 80 and 128 x 1 over up to 4095, 24/4 heads of 64.
 //
 // seqs[i]: number of the first item of the i-th sequence in that order << 6 | the
 // sequence; seqs[B]: all items << 6.  For all threads of a block; scratch: 128

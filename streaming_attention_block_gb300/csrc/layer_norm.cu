@@ -150,7 +150,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int lanes, int warps, flo
     return;
   }
   // each step halves the lanes of a value or, while there are several, the
-  // values of a lane: K + 3 exchanges instead of 5 K (K = 8: 9 for 40)
+  // values of a lane: K + 4 - log2 K exchanges instead of 5 K (K = 8: 9 for 40)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int idx = 0;
   float t[K];

@@ -1192,7 +1192,8 @@ static bool cross_shape_ok(const sab_cross_desc* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return false;
   if (d->heads % d->kv_heads != 0 || d->heads / d->kv_heads > kTileM) return false;
   if (d->kv_batch != 1 && d->kv_batch != d->batch) return false;
-  // a query tile over 2^26 keys takes up to 0.8 s; its end is waited for 2 s at most
+  // a query tile over 2^26 keys takes up to 1.1 s (2.2 us a key tile with running
+  // maxima); its end is waited for 2 s at most
   if (d->q_tokens > (1 << 30) || d->kv_tokens > (1 << 26) || d->heads > (1 << 20)) return false;
   return (long long)d->batch * d->heads * ((d->q_tokens + 31) / 32) <= (1LL << 30) &&
          (long long)d->kv_batch * d->kv_heads * ((d->kv_tokens + 31) / 32) <= (1LL << 30);
