@@ -418,7 +418,7 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // orders these loads behind those writes; it does not order the read-only path
 // (__ldg), which is for data that nothing writes while the kernel runs, its early
 // start included.  The compiler keeps them where they stand, and no more than they:
-// as plain loads they cost the gradients of cross attention 4 % and layer norm's 3 %.
+// as plain loads they cost the gradients of cross attention 5 % and layer norm's 3 %.
 __device__ __forceinline__ float ld_global(const float* a) {
   float x;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(a));

@@ -1280,8 +1280,8 @@ static int cross_splits(unsigned items, int key_tiles) {
 
 // Query tiles of a call whose sequences may differ in length: 2^26 at most.  A
 // block first clears its rows without a query or key, in 1.1 (gradients 1.6) us a
-// tile of one token, and its other warps wait for that 2 s at most: 0.5 (0.7) s of
-// 2^26 tiles on 152 SMs; those of 2^28 ran out.
+// tile of one token (measured up to 2^20), and its other warps wait for that 2 s at
+// most.  On 152 SMs 2^26 tiles make 0.5 (0.7) s, 2^28 would 1.9 (2.8).
 static bool cross_tiles_ok(const sab_cross_desc& d, const int* q_len, const int* kv_len, long long tiles) {
   return (q_len == nullptr && kv_len == nullptr) || d.batch * tiles <= (1LL << 26);
 }
